@@ -575,6 +575,117 @@ tim_status tim_logprob_noalloc(const void *hidden, const void *gamma, const void
                                int32_t *out_top1, int32_t *out_status, tim_stream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Operators on a logits matrix.
+ *
+ * The calls above never store the logits; the next ones are for programs that
+ * have them: an engine at the moment it samples, a trainer that distils.
+ * logits is [T, V], row stride ld >= V elements (ld <= 2^31), any element-aligned
+ * address, of one of the types below; 1 <= T <= 2^31 - 1, 1 <= V <=
+ * TIM_LOGITS_MAX_V.  -inf is a token that cannot occur.  A row's results do not
+ * depend on T or on the other rows; the float results of the same row at another
+ * address modulo 16 bytes may differ in their last bits.
+ * The workspace of these calls holds the status word alone: 1024 bytes, zero-
+ * initialised once, and one workspace serves any number of calls at any sizes,
+ * on one stream at a time.
+ * ------------------------------------------------------------------------ */
+typedef enum tim_dtype { TIM_F32 = 0, TIM_BF16 = 1, TIM_F16 = 2 } tim_dtype;
+#define TIM_LOGITS_MAX_V 393216
+
+/* ------------------------------------------------------------------------ *
+ * Sampling.
+ *
+ * Draws the tokens whose score tim_processed_logprob defines, from given uniform
+ * numbers, and returns that score (the generation score A of tim_compare).  Per
+ * row, with s_v = z_v / temperature and the tokens ordered by (z descending, lower
+ * id first):
+ *   top-k   the first top_k tokens, the set K (top_k <= 0 or >= V: all);
+ *   top-p   q = softmax of s over K; a token is kept when the q-mass of the tokens
+ *           before it is < top_p (the first always is; top_p >= 1: all of K);
+ *   min-p   of these, the ones with exp(s_v - s_max) >= min_p (0: all);
+ *   out_ids[t]      smallest v with sum_{kept w <= v} exp(s_w) > u_t S, where
+ *                   S = sum_{kept} exp(s_w);
+ *   out_logprob[t]  = s_x - ln S for the token x drawn;
+ *   out_lse_kept[t] = ln S;   out_kept[t] = number of kept tokens (-inf is never
+ *                   kept).
+ * temperature = 0 is the greedy choice: the first token of the order, logprob 0,
+ * out_lse_kept its logit, one token kept.
+ * Sums are held in 64-bit integers of weights exact to 2^-33, so a token differs
+ * from exact arithmetic's only if a border lies within about 1e-11 of the row's
+ * mass.
+ *
+ * params  host memory, read during the call.  row_* are device arrays [T] that
+ *         take the place of the scalar beside them, or NULL.  temperature is 0 or
+ *         in [1e-6, 1e6]; top_p > 0; 0 <= min_p <= 1.
+ * uniform float32 [T] in [0, 1).
+ * Errors: TIM_ERR_INVALID_ARG, TIM_ERR_SHAPE, TIM_ERR_WORKSPACE,
+ *   TIM_ERR_UNSUPPORTED_DEVICE, TIM_ERR_CUDA (immediate).  Via tim_status_sync:
+ *   TIM_ERR_INVALID_ARG (a row's uniform number or setting out of range) and
+ *   TIM_ERR_NONFINITE (a NaN or +inf logit, or a row of -inf alone); such a row gets
+ *   id -1, NaN, NaN and 0, the others are as always.
+ * ------------------------------------------------------------------------ */
+typedef struct tim_sample_params {
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+  const float *row_temperature;
+  const int32_t *row_top_k;
+  const float *row_top_p;
+  const float *row_min_p;
+} tim_sample_params;
+
+tim_status tim_sample(const void *logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                      const float *uniform, const tim_sample_params *params, int32_t *out_ids,
+                      float *out_logprob, float *out_lse_kept, int32_t *out_kept, void *workspace,
+                      size_t workspace_bytes, tim_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * Distillation from a teacher's top logits.
+ *
+ * Per row, with s_v = z_v / temperature, p = softmax(s), and the teacher's head:
+ * K entries (teacher_ids[t, k], teacher_logprob[t, k] = ln q_k), as
+ * tim_processed_logprob_head returns them.  An entry with id -1 or logprob -inf is
+ * none; the others form H.  Q = sum_H q_k, P = sum_H p_k.  With tail = 1 the tokens
+ * outside H are one more bucket, p_r = 1 - P (summed directly) and q_r = 1 - Q; it
+ * is left out where q_r <= 2^-20 (the rounding of the teacher's own numbers) or
+ * where no token outside H has any mass.
+ *   TIM_DISTILL_FORWARD_KL  loss = sum_H q_k (ln q_k - ln p_k) [+ q_r (ln q_r - ln p_r)]
+ *   TIM_DISTILL_REVERSE_KL  loss = sum_H p_k (ln p_k - ln q_k) [+ p_r (ln p_r - ln q_r)]
+ *   out_lse[t] = ln sum_v exp(s_v)
+ * A row whose H is empty (the rows of a prompt) has loss 0, lse 0 and gradient 0,
+ * and its logits are not read.
+ *
+ * tim_distill_backward: out_dlogits = grad_loss[t] * d loss_t / d z_t, of the type of
+ * logits, row stride ldd; rows with grad_loss 0 get zeros.  saved is the forward's
+ * out_saved for the same arguments.
+ *
+ * teacher_ids  int32 [T, K]; teacher_logprob float32 [T, K]; 1 <= K <=
+ *              TIM_DISTILL_MAX_K.  temperature in [1e-6, 1e6].
+ * out_saved    float32 [T, TIM_DISTILL_SAVED].
+ * out_dlogits  must not meet the memory of logits.
+ * Errors: as tim_sample.  Via tim_status_sync: TIM_ERR_TOKEN_RANGE (an id below -1 or
+ *   from V up), TIM_ERR_INVALID_ARG (an id twice in a row, a logprob that is NaN or
+ *   above 1), TIM_ERR_NONFINITE (a NaN or +inf logit, or a loss that is not finite).
+ *   A row of the first two kinds has NaN loss and gradients (zeros where grad_loss is 0).
+ * ------------------------------------------------------------------------ */
+#define TIM_DISTILL_MAX_K 1024
+#define TIM_DISTILL_SAVED 8
+#define TIM_DISTILL_FORWARD_KL 0
+#define TIM_DISTILL_REVERSE_KL 1
+
+tim_status tim_distill(const void *logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                       const int32_t *teacher_ids, const float *teacher_logprob, int32_t K,
+                       float temperature, int32_t kind, int32_t tail, float *out_loss,
+                       float *out_lse, float *out_saved, void *workspace, size_t workspace_bytes,
+                       tim_stream_t stream);
+
+tim_status tim_distill_backward(const void *logits, int32_t dtype, int64_t ld, int64_t T,
+                                int32_t V, const int32_t *teacher_ids,
+                                const float *teacher_logprob, int32_t K, float temperature,
+                                int32_t kind, const float *saved, const float *grad_loss,
+                                void *out_dlogits, int64_t ldd, tim_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Self-test of the bounded waits (the pages have no counterpart: it exercises
  * this library's own failure detection).  Every mbarrier wait in the LM-head
  * kernel gives up after a time limit, records TIM_ERR_TIMEOUT in the status

@@ -45,3 +45,4 @@ from .backward import logit_grad, oracle_logprob_backward, rmsnorm_backward  # n
 from .diag import (  # noqa: F401
     QUANTILES, oracle_diag, oracle_diag_lenient, quantile_linear,
 )
+from .logits_ops import distill_row, sample_row  # noqa: E402,F401

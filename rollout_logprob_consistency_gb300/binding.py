@@ -106,6 +106,23 @@ _SIGNATURES = {
                                     _f32, _f32, _vp, _vp, _sz, _vp]),
 }
 
+
+
+class _SampleParams(_c.Structure):
+    _fields_ = [("temperature", _f32), ("top_k", _i32), ("top_p", _f32), ("min_p", _f32),
+                ("row_temperature", _vp), ("row_top_k", _vp), ("row_top_p", _vp),
+                ("row_min_p", _vp)]
+
+
+_SIGNATURES.update({
+    "tim_sample": (_c.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _c.POINTER(_SampleParams), _vp,
+                              _vp, _vp, _vp, _vp, _sz, _vp]),
+    "tim_distill": (_c.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _i32, _vp,
+                               _vp, _vp, _vp, _sz, _vp]),
+    "tim_distill_backward": (_c.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _i32,
+                                        _vp, _vp, _vp, _i64, _vp]),
+})
+
 _lib = None
 
 
@@ -629,6 +646,237 @@ def processed_logprob(hidden, gamma, W, token_ids, temperature: float, eps: floa
     if check:
         workspace.check("tim_processed_logprob", stream)
     return (*out, hid_ids, hid_lp) if head else out
+
+
+# ----------------------------------------------------------------------------- logits operators
+
+LOGITS_WORKSPACE_BYTES = 1024
+DISTILL_SAVED = 8
+DISTILL_KINDS = {"forward": 0, "reverse": 1}
+
+
+def _logits_args(t, name):
+    """(T, V, dtype code, row stride) of a [T, V] CUDA tensor whose rows are contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    T, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if T > 1 else V
+    if ld < V:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return T, V, code, ld
+
+
+def _at(dev, stream):
+    """The context of a call: its device, and its stream where one is given, so that what the
+    call allocates belongs to the stream that uses it."""
+    torch = _torch()
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev)
+
+
+def _on_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+
+
+def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, out=None,
+           workspace: Optional[Workspace] = None, stream=None, check: bool = True):
+    """Draw one token a row from ``logits`` [T, V] (float32, bfloat16 or float16 CUDA tensor,
+    rows contiguous, any row stride) with the uniform numbers ``uniform`` float32 [T] in
+    [0, 1) (tim_sample).  Returns (ids i32 [T], logprob f32 [T], lse_kept f32 [T], kept i32
+    [T]); logprob is the processed score of the token drawn.
+
+    ``temperature`` (0: greedy), ``top_k`` (<= 0: off), ``top_p`` (>= 1: off) and ``min_p``
+    (0: off) are numbers, or [T] tensors (float32, top_k int32) with a setting a row.
+    ``out`` = the four result tensors to write.
+    """
+    torch = _torch()
+    T, V, code, ld = _logits_args(logits, "logits")
+    dev = logits.device
+    _need(uniform, torch.float32, "uniform", 1)
+    tensors = {"uniform": uniform}
+    p = _SampleParams(1.0, 0, 1.0, 0.0, None, None, None, None)
+    for name, value, dtype in (("temperature", temperature, torch.float32),
+                               ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                               ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            _need(value, dtype, name, 1)
+            tensors[name] = value
+            setattr(p, "row_" + name, value.data_ptr())
+        else:
+            setattr(p, name, int(value) if name == "top_k" else float(value))
+    if out is not None:
+        for t, dtype, name in zip(out, (torch.int32, torch.float32, torch.float32, torch.int32),
+                                  ("out ids", "out logprob", "out lse_kept", "out kept")):
+            _need(t, dtype, name, 1)
+            tensors[name] = t
+    for name, t in tensors.items():
+        if t.shape[0] != T:
+            raise ValueError(f"{name} must have one value a row")
+    _on_device(dev, **tensors)
+    with _at(dev, stream):
+        if out is None:
+            out = (torch.empty(T, dtype=torch.int32, device=dev),
+                   torch.empty(T, dtype=torch.float32, device=dev),
+                   torch.empty(T, dtype=torch.float32, device=dev),
+                   torch.empty(T, dtype=torch.int32, device=dev))
+        if workspace is None:
+            workspace = Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        status = lib().tim_sample(_ptr(logits), code, ld, T, V, _ptr(uniform), _c.byref(p),
+                                  _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
+                                  workspace.ptr, workspace.nbytes, _stream_ptr(stream))
+        _check(status, "tim_sample")
+        if check:
+            workspace.check("tim_sample", stream)
+    return out
+
+
+def _distill_args(logits, teacher_ids, teacher_logprob, kind):
+    torch = _torch()
+    T, V, code, ld = _logits_args(logits, "logits")
+    _need(teacher_ids, torch.int32, "teacher_ids", 2)
+    _need(teacher_logprob, torch.float32, "teacher_logprob", 2)
+    if teacher_ids.shape[0] != T or teacher_logprob.shape != teacher_ids.shape:
+        raise ValueError("teacher_ids and teacher_logprob must both be [T, K]")
+    if kind not in DISTILL_KINDS:
+        raise ValueError(f"kind must be one of {sorted(DISTILL_KINDS)}")
+    _on_device(logits.device, teacher_ids=teacher_ids, teacher_logprob=teacher_logprob)
+    return T, V, code, ld, teacher_ids.shape[1], DISTILL_KINDS[kind]
+
+
+def distill(logits, teacher_ids, teacher_logprob, temperature: float = 1.0, *,
+            kind: str = "forward", tail: bool = False, out=None,
+            workspace: Optional[Workspace] = None, stream=None, check: bool = True):
+    """Per-row distillation loss of ``logits`` [T, V] against a teacher's top logits
+    (tim_distill).  teacher_ids int32 [T, K] and teacher_logprob float32 [T, K] as
+    ``processed_logprob(..., head=True)`` returns them; entries with id -1 or logprob -inf
+    are none, and a row without entries has loss 0.  ``kind`` "forward" is KL(teacher ||
+    student) over the head, "reverse" KL(student || teacher); ``tail`` adds the other
+    tokens as one bucket.  Returns (loss f32 [T], lse f32 [T], saved f32 [T, 8] for
+    ``distill_backward``)."""
+    torch = _torch()
+    T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
+    dev = logits.device
+    if out is not None:
+        for t, shape, name in zip(out, ((T,), (T,), (T, DISTILL_SAVED)),
+                                  ("out loss", "out lse", "out saved")):
+            _need(t, torch.float32, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        _on_device(dev, loss=out[0], lse=out[1], saved=out[2])
+    with _at(dev, stream):
+        if out is None:
+            out = (torch.empty(T, dtype=torch.float32, device=dev),
+                   torch.empty(T, dtype=torch.float32, device=dev),
+                   torch.empty(T, DISTILL_SAVED, dtype=torch.float32, device=dev))
+        if workspace is None:
+            workspace = Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        _check(lib().tim_distill(_ptr(logits), code, ld, T, V, _ptr(teacher_ids),
+                                 _ptr(teacher_logprob), K, float(temperature), kd,
+                                 int(bool(tail)), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
+                                 workspace.ptr, workspace.nbytes, _stream_ptr(stream)),
+               "tim_distill")
+        if check:
+            workspace.check("tim_distill", stream)
+    return out
+
+
+def _dlogits_out(logits, out):
+    torch = _torch()
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _, _, _, ldd = _logits_args(out, "out_dlogits")
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out_dlogits must have the shape and type of logits")
+    _on_device(logits.device, out_dlogits=out)
+    return out, ldd
+
+
+def distill_backward(logits, teacher_ids, teacher_logprob, saved, grad_loss,
+                     temperature: float = 1.0, *, kind: str = "forward", out_dlogits=None,
+                     stream=None):
+    """Gradient of sum_t grad_loss[t] loss[t] with respect to ``logits``
+    (tim_distill_backward), in the type of ``logits``.  ``saved`` is ``distill``'s third
+    result for the same arguments; grad_loss float32 [T]."""
+    torch = _torch()
+    T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
+    _need(saved, torch.float32, "saved", 2)
+    _need(grad_loss, torch.float32, "grad_loss", 1)
+    if tuple(saved.shape) != (T, DISTILL_SAVED) or grad_loss.shape[0] != T:
+        raise ValueError("saved must be [T, 8] and grad_loss [T]")
+    _on_device(logits.device, saved=saved, grad_loss=grad_loss)
+    with _at(logits.device, stream):
+        out, ldd = _dlogits_out(logits, out_dlogits)
+        _check(lib().tim_distill_backward(_ptr(logits), code, ld, T, V, _ptr(teacher_ids),
+                                          _ptr(teacher_logprob), K, float(temperature), kd,
+                                          _ptr(saved), _ptr(grad_loss), _ptr(out), ldd,
+                                          _stream_ptr(stream)), "tim_distill_backward")
+    return out
+
+
+def distill_grad(logits, teacher_ids, teacher_logprob, grad_loss, temperature: float = 1.0, *,
+                 kind: str = "forward", tail: bool = False, out_dlogits=None,
+                 workspace: Optional[Workspace] = None, stream=None, check: bool = True):
+    """The loss of ``distill`` and the gradient of ``distill_backward`` for row weights
+    ``grad_loss`` float32 [T] that are known beforehand.  Returns (loss f32 [T], dlogits)."""
+    loss, _, saved = distill(logits, teacher_ids, teacher_logprob, temperature, kind=kind,
+                             tail=tail, workspace=workspace, stream=stream, check=check)
+    return loss, distill_backward(logits, teacher_ids, teacher_logprob, saved, grad_loss,
+                                  temperature, kind=kind, out_dlogits=out_dlogits, stream=stream)
+
+
+def _distill_function():
+    torch = _torch()
+
+    class Distill(torch.autograd.Function):
+        """loss[t] of tim_distill with the gradient of tim_distill_backward."""
+
+        @staticmethod
+        def forward(ctx, logits, teacher_ids, teacher_logprob, temperature, kind, tail,
+                    workspace, check):
+            loss, _, saved = distill(logits, teacher_ids, teacher_logprob, temperature, kind=kind,
+                                     tail=tail, workspace=workspace, check=check)
+            ctx.save_for_backward(logits, teacher_ids, teacher_logprob, saved)
+            ctx.temperature, ctx.kind = float(temperature), kind
+            return loss
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_loss):
+            logits, ids, lp, saved = ctx.saved_tensors
+            g = grad_loss.contiguous().float()
+            d = distill_backward(logits, ids, lp, saved, g, ctx.temperature, kind=ctx.kind)
+            return (d, None, None, None, None, None, None, None)
+
+    return Distill
+
+
+_DISTILL = None
+
+
+def distill_loss(logits, teacher_ids, teacher_logprob, temperature: float = 1.0, *,
+                 kind: str = "forward", tail: bool = False,
+                 workspace: Optional[Workspace] = None, check: bool = True):
+    """Differentiable per-row distillation loss f32 [T] (gradient with respect to ``logits``
+    alone, once): ``distill`` forward, ``distill_backward`` backward.  Runs on the current
+    stream."""
+    global _DISTILL
+    if _DISTILL is None:
+        _DISTILL = _distill_function()
+    return _DISTILL.apply(logits, teacher_ids, teacher_logprob, temperature, kind, tail,
+                          workspace, check)
 
 
 # ----------------------------------------------------------------------------- vocab-parallel

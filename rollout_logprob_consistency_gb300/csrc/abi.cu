@@ -82,6 +82,18 @@ cudaError_t launch_seg_diag(const float* A, const float* B, const float* C, cons
                             float mis_hi, tim_seq_diag* out, void* workspace,
                             cudaStream_t stream);
 size_t diag_workspace_bytes(int64_t T, int n_seq);
+cudaError_t launch_sample(const void* logits, int dtype, int64_t ld, int64_t T, int V,
+                          const float* uniform, const tim_sample_params& p, int32_t* ids,
+                          float* logprob, float* lse, int32_t* kept, int* status,
+                          cudaStream_t stream);
+cudaError_t launch_distill(const void* logits, int dtype, int64_t ld, int64_t T, int V,
+                           const int32_t* ids, const float* lp, int K, float temperature, int kind,
+                           int tail, float* loss, float* lse, float* saved, int* status,
+                           cudaStream_t stream);
+cudaError_t launch_distill_backward(const void* logits, int dtype, int64_t ld, int64_t T, int V,
+                                    const int32_t* ids, const float* lp, int K, float temperature,
+                                    int kind, const float* saved, const float* grad, void* dlogits,
+                                    int64_t ldd, cudaStream_t stream);
 
 namespace {
 
@@ -223,6 +235,44 @@ BwdLayout backward_layout(int64_t T, int32_t d, int32_t V) {
   B.g_off = align_up(B.y_off + static_cast<size_t>(B.Tp) * dd * 2, 1024);
   B.total = align_up(B.g_off + static_cast<size_t>(B.Tp) * static_cast<size_t>(B.Vp) * 2, 1024);
   return B;
+}
+
+size_t dtype_bytes(int32_t dtype) {
+  return dtype == TIM_F32 ? 4 : dtype == TIM_BF16 || dtype == TIM_F16 ? 2 : 0;
+}
+
+// A [T, V] matrix of logits (or of their gradients) with row stride ld elements.
+tim_status check_logits(const void* p, int32_t dtype, int64_t ld, int64_t T, int32_t V) {
+  const size_t es = dtype_bytes(dtype);
+  if (p == nullptr || es == 0 || !aligned(p, es)) return TIM_ERR_INVALID_ARG;
+  if (T < 1 || T > INT32_MAX || V < 1 || V > TIM_LOGITS_MAX_V) return TIM_ERR_SHAPE;
+  if (ld < V || ld > (static_cast<int64_t>(1) << 31)) return TIM_ERR_SHAPE;
+  return TIM_OK;
+}
+
+// Whether the byte ranges of two such matrices meet.
+bool matrices_meet(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t dtype,
+                   int64_t T, int32_t V) {
+  const uintptr_t es = dtype_bytes(dtype);
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + static_cast<uintptr_t>((T - 1) * lda + V) * es;
+  const uintptr_t b1 = b0 + static_cast<uintptr_t>((T - 1) * ldb + V) * es;
+  return a0 < b1 && b0 < a1;
+}
+
+tim_status check_distill(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                         const int32_t* ids, const float* lp, int32_t K, float temperature,
+                         int32_t kind, int32_t tail) {
+  tim_status s = check_logits(logits, dtype, ld, T, V);
+  if (s != TIM_OK) return s;
+  if (ids == nullptr || lp == nullptr || !aligned(ids, 4) || !aligned(lp, 4))
+    return TIM_ERR_INVALID_ARG;
+  if (K < 1 || K > TIM_DISTILL_MAX_K) return TIM_ERR_SHAPE;
+  if (!(std::isfinite(temperature) && temperature >= 1e-6f && temperature <= 1e6f))
+    return TIM_ERR_INVALID_ARG;
+  if (kind != TIM_DISTILL_FORWARD_KL && kind != TIM_DISTILL_REVERSE_KL) return TIM_ERR_INVALID_ARG;
+  if (tail != 0 && tail != 1) return TIM_ERR_INVALID_ARG;
+  return TIM_OK;
 }
 
 bool valid_shard(int32_t G, int32_t g) {
@@ -782,6 +832,69 @@ tim_status tim_compare_diag(const float* lp_gen, const float* lp_replay, const f
   return from_cuda(launch_seg_diag(lp_gen, lp_replay, lp_train, top1_gen, top1_replay, top1_train,
                                    seq_offsets, n_seq, mask, T, tis_cap, mis_lo, mis_hi, out_diag,
                                    workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tim_status tim_sample(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                      const float* uniform, const tim_sample_params* params, int32_t* out_ids,
+                      float* out_logprob, float* out_lse_kept, int32_t* out_kept, void* workspace,
+                      size_t workspace_bytes, tim_stream_t stream) {
+  tim_status s = check_logits(logits, dtype, ld, T, V);
+  if (s != TIM_OK) return s;
+  if (uniform == nullptr || params == nullptr || out_ids == nullptr || out_logprob == nullptr ||
+      out_lse_kept == nullptr || out_kept == nullptr)
+    return TIM_ERR_INVALID_ARG;
+  const tim_sample_params& p = *params;
+  if (!aligned(uniform, 4) || !aligned(out_ids, 4) || !aligned(out_logprob, 4) ||
+      !aligned(out_lse_kept, 4) || !aligned(out_kept, 4) || !aligned(p.row_temperature, 4) ||
+      !aligned(p.row_top_k, 4) || !aligned(p.row_top_p, 4) || !aligned(p.row_min_p, 4))
+    return TIM_ERR_INVALID_ARG;
+  if (p.row_temperature == nullptr && p.temperature != 0.f &&
+      !(p.temperature >= 1e-6f && p.temperature <= 1e6f))
+    return TIM_ERR_INVALID_ARG;
+  if (p.row_top_p == nullptr && !(p.top_p > 0.f)) return TIM_ERR_INVALID_ARG;
+  if (p.row_min_p == nullptr && !(p.min_p >= 0.f && p.min_p <= 1.f)) return TIM_ERR_INVALID_ARG;
+  if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  return from_cuda(launch_sample(logits, dtype, ld, T, V, uniform, p, out_ids, out_logprob,
+                                 out_lse_kept, out_kept, static_cast<int*>(workspace),
+                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tim_status tim_distill(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                       const int32_t* teacher_ids, const float* teacher_logprob, int32_t K,
+                       float temperature, int32_t kind, int32_t tail, float* out_loss,
+                       float* out_lse, float* out_saved, void* workspace, size_t workspace_bytes,
+                       tim_stream_t stream) {
+  tim_status s = check_distill(logits, dtype, ld, T, V, teacher_ids, teacher_logprob, K,
+                               temperature, kind, tail);
+  if (s != TIM_OK) return s;
+  if (out_loss == nullptr || out_lse == nullptr || out_saved == nullptr || !aligned(out_loss, 4) ||
+      !aligned(out_lse, 4) || !aligned(out_saved, 4))
+    return TIM_ERR_INVALID_ARG;
+  if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  return from_cuda(launch_distill(logits, dtype, ld, T, V, teacher_ids, teacher_logprob, K,
+                                  temperature, kind, tail, out_loss, out_lse, out_saved,
+                                  static_cast<int*>(workspace),
+                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tim_status tim_distill_backward(const void* logits, int32_t dtype, int64_t ld, int64_t T,
+                                int32_t V, const int32_t* teacher_ids,
+                                const float* teacher_logprob, int32_t K, float temperature,
+                                int32_t kind, const float* saved, const float* grad_loss,
+                                void* out_dlogits, int64_t ldd, tim_stream_t stream) {
+  tim_status s =
+      check_distill(logits, dtype, ld, T, V, teacher_ids, teacher_logprob, K, temperature, kind, 0);
+  if (s != TIM_OK) return s;
+  if ((s = check_logits(out_dlogits, dtype, ldd, T, V)) != TIM_OK) return s;
+  if (saved == nullptr || grad_loss == nullptr || !aligned(saved, 4) || !aligned(grad_loss, 4))
+    return TIM_ERR_INVALID_ARG;
+  if (matrices_meet(logits, ld, out_dlogits, ldd, dtype, T, V)) return TIM_ERR_INVALID_ARG;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  return from_cuda(launch_distill_backward(logits, dtype, ld, T, V, teacher_ids, teacher_logprob,
+                                           K, temperature, kind, saved, grad_loss, out_dlogits,
+                                           ldd, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
