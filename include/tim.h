@@ -659,6 +659,9 @@ tim_status tim_sample(const void *logits, int32_t dtype, int64_t ld, int64_t T, 
  * logits, row stride ldd; rows with grad_loss 0 get zeros.  saved is the forward's
  * out_saved for the same arguments.
  *
+ * tim_distill_grad: out_loss of tim_distill and out_dlogits of tim_distill_backward in
+ * one call, for weights grad_loss that are known beforehand: logits is read once.
+ *
  * teacher_ids  int32 [T, K]; teacher_logprob float32 [T, K]; 1 <= K <=
  *              TIM_DISTILL_MAX_K.  temperature in [1e-6, 1e6].
  * out_saved    float32 [T, TIM_DISTILL_SAVED].
@@ -678,6 +681,12 @@ tim_status tim_distill(const void *logits, int32_t dtype, int64_t ld, int64_t T,
                        float temperature, int32_t kind, int32_t tail, float *out_loss,
                        float *out_lse, float *out_saved, void *workspace, size_t workspace_bytes,
                        tim_stream_t stream);
+
+tim_status tim_distill_grad(const void *logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                            const int32_t *teacher_ids, const float *teacher_logprob, int32_t K,
+                            float temperature, int32_t kind, int32_t tail, const float *grad_loss,
+                            float *out_loss, void *out_dlogits, int64_t ldd, void *workspace,
+                            size_t workspace_bytes, tim_stream_t stream);
 
 tim_status tim_distill_backward(const void *logits, int32_t dtype, int64_t ld, int64_t T,
                                 int32_t V, const int32_t *teacher_ids,

@@ -119,6 +119,8 @@ _SIGNATURES.update({
                               _vp, _vp, _vp, _vp, _sz, _vp]),
     "tim_distill": (_c.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _i32, _vp,
                                _vp, _vp, _vp, _sz, _vp]),
+    "tim_distill_grad": (_c.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _i32, _i32,
+                                    _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
     "tim_distill_backward": (_c.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _i32,
                                         _vp, _vp, _vp, _i64, _vp]),
 })
@@ -830,11 +832,28 @@ def distill_grad(logits, teacher_ids, teacher_logprob, grad_loss, temperature: f
                  kind: str = "forward", tail: bool = False, out_dlogits=None,
                  workspace: Optional[Workspace] = None, stream=None, check: bool = True):
     """The loss of ``distill`` and the gradient of ``distill_backward`` for row weights
-    ``grad_loss`` float32 [T] that are known beforehand.  Returns (loss f32 [T], dlogits)."""
-    loss, _, saved = distill(logits, teacher_ids, teacher_logprob, temperature, kind=kind,
-                             tail=tail, workspace=workspace, stream=stream, check=check)
-    return loss, distill_backward(logits, teacher_ids, teacher_logprob, saved, grad_loss,
-                                  temperature, kind=kind, out_dlogits=out_dlogits, stream=stream)
+    ``grad_loss`` float32 [T] that are known beforehand (tim_distill_grad): ``logits`` is read
+    once.  Returns (loss f32 [T], dlogits)."""
+    torch = _torch()
+    T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
+    _need(grad_loss, torch.float32, "grad_loss", 1)
+    if grad_loss.shape[0] != T:
+        raise ValueError("grad_loss must be [T]")
+    dev = logits.device
+    _on_device(dev, grad_loss=grad_loss)
+    with _at(dev, stream):
+        out, ldd = _dlogits_out(logits, out_dlogits)
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        _check(lib().tim_distill_grad(_ptr(logits), code, ld, T, V, _ptr(teacher_ids),
+                                      _ptr(teacher_logprob), K, float(temperature), kd,
+                                      int(bool(tail)), _ptr(grad_loss), _ptr(loss), _ptr(out), ldd,
+                                      workspace.ptr, workspace.nbytes, _stream_ptr(stream)),
+               "tim_distill_grad")
+        if check:
+            workspace.check("tim_distill_grad", stream)
+    return loss, out
 
 
 def _distill_function():

@@ -90,6 +90,10 @@ cudaError_t launch_distill(const void* logits, int dtype, int64_t ld, int64_t T,
                            const int32_t* ids, const float* lp, int K, float temperature, int kind,
                            int tail, float* loss, float* lse, float* saved, int* status,
                            cudaStream_t stream);
+cudaError_t launch_distill_grad(const void* logits, int dtype, int64_t ld, int64_t T, int V,
+                                const int32_t* ids, const float* lp, int K, float temperature,
+                                int kind, int tail, const float* grad, float* loss, void* dlogits,
+                                int64_t ldd, int* status, cudaStream_t stream);
 cudaError_t launch_distill_backward(const void* logits, int dtype, int64_t ld, int64_t T, int V,
                                     const int32_t* ids, const float* lp, int K, float temperature,
                                     int kind, const float* saved, const float* grad, void* dlogits,
@@ -877,6 +881,27 @@ tim_status tim_distill(const void* logits, int32_t dtype, int64_t ld, int64_t T,
                                   temperature, kind, tail, out_loss, out_lse, out_saved,
                                   static_cast<int*>(workspace),
                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tim_status tim_distill_grad(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
+                            const int32_t* teacher_ids, const float* teacher_logprob, int32_t K,
+                            float temperature, int32_t kind, int32_t tail, const float* grad_loss,
+                            float* out_loss, void* out_dlogits, int64_t ldd, void* workspace,
+                            size_t workspace_bytes, tim_stream_t stream) {
+  tim_status s = check_distill(logits, dtype, ld, T, V, teacher_ids, teacher_logprob, K,
+                               temperature, kind, tail);
+  if (s != TIM_OK) return s;
+  if ((s = check_logits(out_dlogits, dtype, ldd, T, V)) != TIM_OK) return s;
+  if (grad_loss == nullptr || out_loss == nullptr || !aligned(grad_loss, 4) ||
+      !aligned(out_loss, 4))
+    return TIM_ERR_INVALID_ARG;
+  if (matrices_meet(logits, ld, out_dlogits, ldd, dtype, T, V)) return TIM_ERR_INVALID_ARG;
+  if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  return from_cuda(launch_distill_grad(logits, dtype, ld, T, V, teacher_ids, teacher_logprob, K,
+                                       temperature, kind, tail, grad_loss, out_loss, out_dlogits,
+                                       ldd, static_cast<int*>(workspace),
+                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
 tim_status tim_distill_backward(const void* logits, int32_t dtype, int64_t ld, int64_t T,

@@ -129,6 +129,179 @@ struct Row {
 };
 
 // ---------------------------------------------------------------------------
+// Two fp32 operations in one instruction.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 ex2x2(F2 a) {
+  const float2 t = unpack2(a);
+  return f2(ex2_approx(t.x), ex2_approx(t.y));
+}
+
+// ---------------------------------------------------------------------------
+// A row over a cluster of CTAs.  Each CTA holds one contiguous slice of the row's vectors in
+// shared memory, brought there by one asynchronous bulk copy, so a row is read from memory
+// once whatever is done with it.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* smem, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(smem)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The slice of CTA `rank` of `size`: vectors j0 .. j0 + n - 1 of the row.
+struct Slice {
+  int j0, n;
+};
+__device__ __forceinline__ Slice slice_of(int nvec, int rank, int size) {
+  const int per = (nvec + size - 1) / size;
+  const int j0 = min(nvec, rank * per);
+  return Slice{j0, min(nvec, j0 + per) - j0};
+}
+
+// Starts the slice's copy into `dst` (called by one thread; `bar` counts one arrival).  The
+// row's first and last vectors may hold bytes that are not the row's: those are left to
+// load_slice_edges.
+template <int kDtype>
+__device__ __forceinline__ void load_slice(const Row<kDtype>& r, const Slice& s, uint4* dst,
+                                           uint64_t* bar) {
+  int a = s.j0, b = s.j0 + s.n;
+  if (a < b && !r.whole(a)) ++a;
+  if (a < b && !r.whole(b - 1)) --b;
+  const uint32_t bytes = static_cast<uint32_t>(b - a) * 16u;
+  mbar_arrive_expect_tx(bar, bytes);
+  if (bytes != 0)
+    bulk_load(dst + (a - s.j0), r.p - r.shift + static_cast<int64_t>(a) * Elem<kDtype>::kVec,
+              bytes, bar);
+}
+template <int kDtype>
+__device__ __forceinline__ void load_slice_edges(const Row<kDtype>& r, const Slice& s, uint4* dst) {
+  if (threadIdx.x < 2 && s.n > 0) {
+    const int j = threadIdx.x == 0 ? s.j0 : s.j0 + s.n - 1;
+    if (!r.whole(j)) dst[j - s.j0] = r.load_edge(j);
+  }
+}
+
+// How a row of V elements is spread: CTAs a row and threads a CTA, from the size of a row alone,
+// so that a row is split the same way in every batch.
+struct RowPlan {
+  int cluster, threads;
+  uint32_t slice_bytes;
+};
+inline RowPlan plan_row(int V, int elem_bytes) {
+  const int64_t vecs = (static_cast<int64_t>(V) * elem_bytes + 15) / 16 + 1;
+  RowPlan p;
+  p.cluster = 1;
+  while (p.cluster < 8 && (vecs + p.cluster - 1) / p.cluster * 16 > 40960) p.cluster *= 2;
+  const int64_t per = (vecs + p.cluster - 1) / p.cluster;
+  p.slice_bytes = static_cast<uint32_t>(per * 16);
+  p.threads = p.slice_bytes > 40960 ? 512 : 256;
+  return p;
+}
+
+// T rows, a cluster of `cluster` CTAs each.
+template <class Args>
+inline cudaError_t launch_clusters(void (*kernel)(const Args), int64_t T, int cluster, int threads,
+                                   size_t smem, cudaStream_t stream, const Args& a) {
+  if (T * cluster > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// ---------------------------------------------------------------------------
+// Pairs of floats (value h + l, |l| at most half a step of h): about 2^-45.  A row's few
+// scalars are computed in these: the fp64 units of this part are so few that a hundred fp64
+// operations a row cost more than streaming the row.
+struct Df {
+  float h, l;
+};
+__device__ __forceinline__ Df two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Df quick_two_sum(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Df two_prod(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+// An infinite or NaN h stays what it is.
+__device__ __forceinline__ Df renorm(float h, float l) {
+  const Df r = quick_two_sum(h, l);
+  return fabsf(r.h) < INFINITY ? r : Df{r.h, 0.f};
+}
+__device__ __forceinline__ Df df(float a) { return {a, 0.f}; }
+__device__ __forceinline__ Df operator-(Df a) { return {-a.h, -a.l}; }
+__device__ __forceinline__ Df operator+(Df a, Df b) {
+  const Df s = two_sum(a.h, b.h);
+  return fabsf(s.h) < INFINITY ? renorm(s.h, s.l + (a.l + b.l)) : Df{s.h, 0.f};
+}
+__device__ __forceinline__ Df operator-(Df a, Df b) { return a + (-b); }
+__device__ __forceinline__ Df operator*(Df a, Df b) {
+  const Df p = two_prod(a.h, b.h);
+  return fabsf(p.h) < INFINITY ? renorm(p.h, fmaf(a.h, b.l, fmaf(a.l, b.h, p.l))) : Df{p.h, 0.f};
+}
+__device__ __forceinline__ Df reciprocal(Df a) {
+  const float r = 1.f / a.h;
+  return renorm(r, r * fmaf(-r, a.l, fmaf(-r, a.h, 1.f)));
+}
+
+// ---------------------------------------------------------------------------
 // 2^x in fixed point.
 //
 // x = z * K with K = Kh + Kl (a float and its remainder).  z * Kh is taken exactly as
@@ -173,22 +346,15 @@ constexpr Pow2Table make_pow2_table() {
 
 constexpr int kPow2Bits = 8;
 
-// What a row's logits are raised with: 2^((z - c) K), c = 0 or the row's largest logit.
+// What a row's logits are raised with: 2^((z - c) K), where c is subtracted only if `recentre`.
 struct Pow2Row {
-  float kh, kl;   // K = log2(e) / temperature
-  float c;        // subtracted first when `recentre`
-  int recentre;   // |max K| is too large for the split of z K itself
+  float kh, kl;  // K = log2(e) / temperature
+  float c;
+  bool recentre;
 };
 
-__device__ __forceinline__ Pow2Row pow2_row(float temperature, float zmax) {
-  const double K = 1.4426950408889634 / static_cast<double>(temperature);
-  Pow2Row r;
-  r.kh = static_cast<float>(K);
-  r.kl = static_cast<float>(K - static_cast<double>(r.kh));
-  r.recentre = !(fabs(static_cast<double>(zmax) * K) < 8192.0);
-  r.c = r.recentre ? zmax : 0.f;
-  return r;
-}
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596299e-8f;  // log2(e) as a pair
+constexpr float kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;    // ln 2 as a pair
 
 // w and n with 2^((z - c) K) = w 2^(n - 62).  |(z - c) K| must be below 2^14.
 __device__ __forceinline__ unsigned long long pow2_fixed(float z, const Pow2Row& k,
@@ -216,15 +382,38 @@ __device__ __forceinline__ unsigned long long pow2_fixed(float z, const Pow2Row&
                                              __float2int_rn(p));
 }
 
-// The same as a double, for x above -900.
-__device__ __forceinline__ double pow2_double(float z, const Pow2Row& k,
-                                              const unsigned long long* table) {
-  int n;
-  const unsigned long long w = pow2_fixed(z, k, table, n);
-  return static_cast<double>(w) * __longlong_as_double(static_cast<long long>(n - 62 + 1023) << 52);
-}
-
 // The table, one copy a translation unit.
 static __device__ const Pow2Table g_pow2_table = make_pow2_table();
+
+// 2^((z - c) K) as a pair of floats; 0 below 2^-126, so that the caller need not care about
+// pow2_fixed's range.  (z - c) K must be at most 100.
+__device__ __forceinline__ Df pow2_df(float z, const Pow2Row& k) {
+  const float x = (k.recentre ? z - k.c : z) * k.kh;
+  if (!(x > -126.f)) return {x <= -126.f ? 0.f : __int_as_float(0x7FC00000), 0.f};  // NaN stays
+  int n;
+  const unsigned long long w = pow2_fixed(z, k, g_pow2_table.t, n);
+  // the top 48 of w's 62 or 63 bits, 24 in each part
+  const float scale = __int_as_float((n + 127) << 23);
+  const float h = static_cast<float>(static_cast<uint32_t>(w >> 39)) * (scale * 0x1p-23f);
+  const float l = static_cast<float>(static_cast<uint32_t>(w >> 15) & 0xFFFFFFu) * (scale * 0x1p-47f);
+  return renorm(h, l);
+}
+
+// e^x
+__device__ __forceinline__ Df exp_df(float x) {
+  return pow2_df(x, Pow2Row{kLog2eHi, kLog2eLo, 0.f, false});
+}
+
+// ln a for a positive finite a: l = ln of the leading bits in fp32, then
+// ln a = l + ln(a e^-l) with the small second term from its series.
+__device__ __forceinline__ Df log_df(Df a) {
+  const int e = static_cast<int>(__float_as_uint(a.h) >> 23) - 127;  // subnormals are not met
+  const float s = __int_as_float((127 - e) << 23);
+  const Df f = {a.h * s, a.l * s};
+  const float l = __logf(f.h);
+  const Df r = f * exp_df(-l) - df(1.f);
+  const Df ln = df(l) + renorm(r.h, r.l - 0.5f * r.h * r.h);
+  return Df{kLn2Hi, kLn2Lo} * df(static_cast<float>(e)) + ln;
+}
 
 }  // namespace tim

@@ -47,6 +47,16 @@ struct SampleArgs {
   int* status;
 };
 
+__device__ __forceinline__ Pow2Row pow2_row(float temperature, float zmax) {
+  const double K = 1.4426950408889634 / static_cast<double>(temperature);
+  Pow2Row r;
+  r.kh = static_cast<float>(K);
+  r.kl = static_cast<float>(K - static_cast<double>(r.kh));
+  r.recentre = !(fabs(static_cast<double>(zmax) * K) < 8192.0);  // too large for the split of z K
+  r.c = r.recentre ? zmax : 0.f;
+  return r;
+}
+
 // Monotone map of float bits to unsigned (larger float -> larger key; -0 and +0 are one).
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t f = __float_as_uint(z + 0.f);

@@ -162,6 +162,24 @@ def test_distill_backward_refusals(tim, kw, code):
     assert _backward(tim, **kw) == code
 
 
+def _grad(tim, **kw):
+    a = dict(logits=P, dtype=1, ld=64, T=4, V=64, ids=P, lp=P, K=8, temperature=1.0, kind=0, tail=0,
+             grad=P, loss=P, out=2 * P, ldd=64, ws=P, nbytes=1024)
+    a.update(kw)
+    return tim.lib().tim_distill_grad(a["logits"], a["dtype"], a["ld"], a["T"], a["V"], a["ids"],
+                                      a["lp"], a["K"], a["temperature"], a["kind"], a["tail"],
+                                      a["grad"], a["loss"], a["out"], a["ldd"], a["ws"],
+                                      a["nbytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", DISTILL_BAD + [
+    (dict(tail=-1), ARG), (dict(grad=None), ARG), (dict(loss=None), ARG), (dict(loss=P + 1), ARG),
+    (dict(out=None), ARG), (dict(ldd=63), SHAPE), (dict(out=P), ARG), (dict(ws=None), WORKSPACE),
+    (dict(nbytes=1023), WORKSPACE)])
+def test_distill_grad_refusals(tim, kw, code):
+    assert _grad(tim, **kw) == code
+
+
 def test_binding_refuses_wrong_tensors(tim):
     torch = pytest.importorskip("torch")
     z = torch.zeros(2, 8)
