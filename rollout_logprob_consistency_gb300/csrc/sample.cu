@@ -6,14 +6,28 @@
 //   top-p   q = softmax of s over K; a token is kept while the q-mass before it is < p
 //   min-p   exp(s - s_max) >= min_p
 //   token   the smallest id v with  sum_{kept w <= v} exp(s_w) > u * sum_kept exp(s)
-// What is kept is "key above a border key, or equal to it with an id up to a border id",
-// so a row is described by two numbers and is never sorted.
 //
 // A token drawn, or the last one that top-p keeps, is decided by sums of up to hundreds of
 // thousands of exponentials against a border: rounding them to 32 bits would move the
-// border past tokens.  Every weight is therefore taken to 2^-33 (pow2_fixed) and summed as a
-// 64-bit integer at a scale fixed by an approximate first sum, so that the row's total is
-// near 2^60: the sums are exact in that scale and do not depend on the order or the split.
+// border past tokens.  Every weight that decides is therefore taken to 2^-33 (pow2_fixed) and
+// summed as a 64-bit integer, at a scale that puts the row's total between 2^53 and 2^60: the
+// sums are exact in that scale and do not depend on the order or the split.
+//
+// A row is held in shared memory by a cluster of CTAs (one read of memory), a slice each.  A
+// thread's largest logits of its part of the slice bound everything else:
+//  - sum over the threads of (largest weight x elements) bounds the row's total: the scale;
+//  - the k-th largest of the threads' maxima is a bound that every top-k logit meets (they
+//    are k different logits), found to 1/256 of their range by a histogram of them;
+//  - only threads whose maximum meets the bound look at their elements again.
+// Two ways follow:
+//  few   the tokens above the bound (top-k's; for top-p the logit below which all tokens
+//        together hold less than 1 - p; min-p's own) fit a list of kCap: rank 0 sorts it and
+//        decides alone.  Top-p without top-k needs the row's total: a sum in fp32 with a proven
+//        error decides unless the border lies within that error.
+//  wide  everything else, the unfiltered row first of all: what is kept is "key above a border
+//        key, or equal to it with an id up to a border id", found digit by digit with
+//        histograms of counts or integer weights, and the token by running sums over chunks.
+// Both give the same token: the weights and sums are the same integers.
 #include <cmath>
 
 #include "logits_row.cuh"
@@ -22,15 +36,18 @@ namespace tim {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 256;
+constexpr int kMaxCluster = 8;
+constexpr int kCap = 512;      // tokens of the list
+constexpr int kListK = 256;    // largest top-k that the list serves
+constexpr float kSumError = 0x1p-17f;  // of the fp32 sum, see approximate_sum
 using u64 = unsigned long long;
 
 struct SampleArgs {
   const void* logits;
   int64_t ld;
   int V;
+  int cluster;
   const float* uniform;
   float temperature;
   int top_k;
@@ -47,16 +64,6 @@ struct SampleArgs {
   int* status;
 };
 
-__device__ __forceinline__ Pow2Row pow2_row(float temperature, float zmax) {
-  const double K = 1.4426950408889634 / static_cast<double>(temperature);
-  Pow2Row r;
-  r.kh = static_cast<float>(K);
-  r.kl = static_cast<float>(K - static_cast<double>(r.kh));
-  r.recentre = !(fabs(static_cast<double>(zmax) * K) < 8192.0);  // too large for the split of z K
-  r.c = r.recentre ? zmax : 0.f;
-  return r;
-}
-
 // Monotone map of float bits to unsigned (larger float -> larger key; -0 and +0 are one).
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t f = __float_as_uint(z + 0.f);
@@ -67,212 +74,630 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 constexpr uint32_t kNegInfKey = 0x007FFFFFu;  // key_of(-inf)
 
+// Levels of 8 bits after which a key of the type is known: the bits below are its sign's.
+template <int kDtype>
+constexpr int kLevels = kDtype == TIM_F32 ? 4 : kDtype == TIM_F16 ? 3 : 2;
+
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+__device__ __forceinline__ u64 warp_scan(u64 v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
 
-struct Shared {
-  u64 table[256];
-  u64 mass[kBins];
-  uint32_t count[kBins];
-  u64 warp[kWarps];
-  float warpf[kWarps];
-  u64 pick_acc;
-  u64 pick_in;
-  uint32_t pick_digit;
-  int pick_all;
-  int found;
-  int bad;
-};
+__device__ __forceinline__ uint32_t remote_load(const void* smem, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(smem, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t remote_add(void* smem, uint32_t rank, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+               : "=r"(r)
+               : "r"(cluster_addr(smem, rank)), "r"(v)
+               : "memory");
+  return r;
+}
 
+// Elementwise maximum of two vectors' elements, NaN if either is.
+template <int kDtype>
+__device__ __forceinline__ uint4 max_vec(uint4 a, const uint4& b) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&a);
+  const uint32_t* y = reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kDtype == TIM_F32)
+      asm("max.NaN.f32 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+    else if constexpr (kDtype == TIM_BF16)
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+    else
+      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+  }
+  return a;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Everything of a row that all its CTAs agree on.
 struct RowState {
   Pow2Row pw;
-  int top;      // weights are w 2^(n - top) at the row's scale: shift = top - n
+  Df inv_tau;
+  float M;      // largest logit
+  int top;      // a weight w 2^(n - 62) of pow2_fixed is w >> (top - n)
+  float zlow;   // logits below have weight 0 and are raised to this one
   uint32_t kc;  // kept: key > kc, or key == kc and id <= idc
   int idc;
 };
 
-// The integer weight of a logit at the row's scale.
 __device__ __forceinline__ u64 weight(float z, const RowState& s, const u64* table) {
   int n;
+  if (s.pw.recentre) {
+    // logits so far apart that a float's step can be many octaves
+    if (!((z - s.pw.c) * s.pw.kh > static_cast<float>(s.top) - 62.5f)) return 0;
+  } else {
+    z = fmaxf(z, s.zlow);
+  }
   const u64 w = pow2_fixed(z, s.pw, table, n);
   return w >> min(s.top - n, 63);
 }
-
 __device__ __forceinline__ bool keeps(uint32_t key, int id, const RowState& s) {
   return key > s.kc || (key == s.kc && id <= s.idc);
 }
 
-// Calls f(id, z) for the row's elements in this warp's contiguous slice, lane order being id
-// order within each step of 32 vectors.
-template <int kDtype, class F>
-__device__ __forceinline__ void for_slice(const Row<kDtype>& r, int warp, F&& f) {
+struct Select {  // the wide way's histograms
+  uint32_t count[2][kBins], lo[2][kBins], hi[2][kBins];
+};
+struct List {
+  u64 key[kCap];  // key << 32 | ~id: larger comes first
+  u64 w[kCap];
+};
+
+template <int kThreads>
+struct Shared {
+  u64 table[256];
+  union {
+    Select sel;
+    List list;
+  };
+  u64 xch[2][kMaxCluster][3];
+  uint32_t hist[kBins];  // of the threads' maxima, all CTAs'
+  u64 warp[kThreads / 32];
+  uint32_t warpu[kThreads / 32];
+  uint32_t warpv[kThreads / 32];
+  float warpf[kThreads / 32];
+  u64 acc;
+  u64 cta_sum;
+  uint32_t digit, in;
+  uint32_t list_n;
+  int all, found, count_lo, count_hi;
+  uint64_t bar;
+};
+
+template <int kDtype, int kThreads>
+struct Sampler {
   using E = Elem<kDtype>;
-  const int nvec = r.nvec();
-  const int per = (nvec + kWarps * 32 - 1) / (kWarps * 32) * 32;
-  const int j0 = warp * per, j1 = min(nvec, j0 + per);
-  for (int jj = j0; jj < j1; jj += 32) {
-    const int j = jj + (threadIdx.x & 31);
-    float v[E::kVec];
-    if (j < j1) {
-      E::unpack(r.load(j), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E::kVec; ++i) v[i] = -INFINITY;
-    }
-    f(j * E::kVec - r.shift, v);
-  }
-}
+  static constexpr int kVec = E::kVec;
+  static constexpr int kWarps = kThreads / 32;
 
-// Border of the tokens whose measure before them, in (key descending, id ascending) order,
-// is below `target`; measure 1 (kMass false) or the weight.  Only tokens that `s` keeps
-// count.  On return s.kc / s.idc hold the border; digits of 8 bits from the top.
-template <int kDtype, bool kMass>
-__device__ void select_border(const Row<kDtype>& r, RowState& s, float zlow, u64 target,
-                              Shared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t prefix = 0;
-  u64 acc = 0, in = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      sh.mass[i] = 0;
-      sh.count[i] = 0;
-    }
-    __syncthreads();
-    for_slice(r, warp, [&](int id0, const auto& v) {
-#pragma unroll
-      for (int i = 0; i < Elem<kDtype>::kVec; ++i) {
-        const uint32_t key = key_of(v[i]);
-        if (shift < 24 && (key >> (shift + 8)) != prefix) continue;
-        if (!keeps(key, id0 + i, s)) continue;
-        const int d = (key >> shift) & 255;
-        atomicAdd(&sh.count[d], 1u);
-        if (kMass && v[i] >= zlow) atomicAdd(&sh.mass[d], weight(v[i], s, sh.table));
-      }
-    });
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 a = acc;
-      int d = 255;
-      for (; d > 0; --d) {
-        const u64 h = kMass ? sh.mass[d] : static_cast<u64>(sh.count[d]);
-        if (a + h >= target) break;
-        a += h;
-      }
-      sh.pick_digit = d;
-      sh.pick_all = d == 0 && a + (kMass ? sh.mass[0] : static_cast<u64>(sh.count[0])) < target;
-      sh.pick_acc = a;
-      sh.pick_in = sh.count[d];
-    }
-    __syncthreads();
-    if (sh.pick_all) return;  // fewer than the target: every one of them stays
-    prefix = (prefix << 8) | sh.pick_digit;
-    acc = sh.pick_acc;
-    in = sh.pick_in;
-    __syncthreads();
-  }
-  // the border key's tokens have equal measures: how many of them, in id order
-  u64 w = 1;
-  if (kMass) {
-    const float z = key_value(prefix);
-    w = z >= zlow ? weight(z, s, sh.table) : 0;
-    if (w == 0) w = 1;
-  }
-  const u64 want = (target - acc + w - 1) / w;
-  if (want >= in) {
-    if (prefix != s.kc) {
-      s.kc = prefix;
-      s.idc = INT32_MAX;
-    }
-    return;
-  }
-  // the id of the want-th of them
-  u64 mine = 0;
-  for_slice(r, warp, [&](int id0, const auto& v) {
-#pragma unroll
-    for (int i = 0; i < Elem<kDtype>::kVec; ++i)
-      mine += key_of(v[i]) == prefix && keeps(prefix, id0 + i, s) ? 1 : 0;
-  });
-  mine = warp_sum(mine);
-  if (lane == 0) sh.warp[warp] = mine;
-  __syncthreads();
-  u64 before = 0;
-  for (int i = 0; i < warp; ++i) before += sh.warp[i];
-  if (before < want && want <= before + mine) {
-    u64 run = before;
-    for_slice(r, warp, [&](int id0, const auto& v) {
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < Elem<kDtype>::kVec; ++i)
-        c += key_of(v[i]) == prefix && keeps(prefix, id0 + i, s) ? 1 : 0;
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      u64 at = run + incl - c;
-      if (at < want && want <= at + c) {
-#pragma unroll
-        for (int i = 0; i < Elem<kDtype>::kVec; ++i)
-          if (key_of(v[i]) == prefix && keeps(prefix, id0 + i, s) && ++at == want)
-            sh.found = id0 + i;
-      }
-      run += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    });
-  }
-  __syncthreads();
-  s.kc = prefix;
-  s.idc = sh.found;
-  __syncthreads();
-}
+  const SampleArgs& a;
+  Shared<kThreads>& sh;
+  const uint4* slice;
+  u64* chunk;  // a sum for each 32 vectors of the slice
+  Row<kDtype> r;
+  Slice s;
+  int rank, tid, warp, lane, phase;
+  RowState st;
 
+  // ---- among the CTAs of the row: every CTA's three numbers to every CTA
+  __device__ __forceinline__ void exchange(u64 x, u64 y, u64 z) {  // called by all, the values of thread 0..31
+    if (warp == 0 && lane < a.cluster) {
+      cluster_store(cluster_addr(&sh.xch[phase & 1][rank][0], lane), x);
+      cluster_store(cluster_addr(&sh.xch[phase & 1][rank][1], lane), y);
+      cluster_store(cluster_addr(&sh.xch[phase & 1][rank][2], lane), z);
+    }
+    cluster_arrive();
+    cluster_wait();
+    ++phase;
+  }
+  __device__ __forceinline__ u64 got(int rank_, int i) const { return sh.xch[(phase - 1) & 1][rank_][i]; }
+
+  // id of slot i of the slice's vector j
+  __device__ __forceinline__ int id_of(int j, int i) const { return (s.j0 + j) * kVec + i - r.shift; }
+  __device__ __forceinline__ bool in_row(int id) const { return id >= 0 && id < a.V; }
+
+  // ---- sums over the slice.  f(z, key, id) is a token's number; the slice goes by chunks of 32
+  // vectors, chunk c to warp c mod kWarps; chunk[] gets their sums.  Returns the CTA's.
+  template <class F>
+  __device__ __forceinline__ u64 chunk_sums(F&& f) {
+    const int chunks = (s.n + 31) / 32;
+    u64 mine = 0;
+    for (int c = warp; c < chunks; c += kWarps) {
+      const int j = c * 32 + lane;
+      u64 sum = 0;
+      if (j < s.n) {
+        float v[kVec];
+        E::unpack(slice[j], v);
+        const int id0 = id_of(j, 0);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sum += f(v[i], id0 + i);
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) chunk[c] = sum;
+      mine += sum;
+    }
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = mine;
+    __syncthreads();
+    u64 t = 0;
+    for (int i = 0; i < kWarps; ++i) t += sh.warp[i];
+    return t;
+  }
+  // The token at which the running sum of f first exceeds `target` (below the CTA's sum);
+  // warp 0, after chunk_sums(f).  -1 in the other warps.
+  template <class F>
+  __device__ __forceinline__ int locate(u64 target, F&& f) {
+    const int chunks = (s.n + 31) / 32;
+    u64 run = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      const u64 x = c0 + lane < chunks ? chunk[c0 + lane] : 0;
+      const u64 incl = run + warp_scan(x);
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, incl > target);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        u64 at = __shfl_sync(0xFFFFFFFFu, incl - x, l);
+        const int j = (c0 + l) * 32 + lane;
+        u64 w[kVec], sum = 0;
+        float v[kVec];
+        const int id0 = id_of(j, 0);
+        if (j < s.n) E::unpack(slice[j], v);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          w[i] = j < s.n ? f(v[i], id0 + i) : 0;
+          sum += w[i];
+        }
+        at += warp_scan(sum) - sum;
+        int id = -1;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          if (at <= target && target < at + w[i]) id = id0 + i;
+          at += w[i];
+        }
+        return __reduce_max_sync(0xFFFFFFFFu, id);
+      }
+      run = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    return -1;
+  }
+
+  // ---- the wide way's border.  Among the tokens that the state keeps: the last one before which
+  // the measure (1, or with kMass the weight) is below `target`; the state then keeps up to it.
+  template <bool kMass>
+  __device__ void select_border(u64 target) {
+    uint32_t prefix = 0, in = 0;
+    u64 acc = 0;
+    const uint32_t kc = st.kc;
+    const int idc = st.idc;
+    for (int level = 0; level < kLevels<kDtype>; ++level) {
+      const int shift = 24 - 8 * level, b = level & 1;
+      for (int i = tid; i < kBins; i += kThreads)
+        sh.sel.count[b][i] = sh.sel.lo[b][i] = sh.sel.hi[b][i] = 0;
+      __syncthreads();
+      for (int j = tid; j < s.n; j += kThreads) {
+        float v[kVec];
+        E::unpack(slice[j], v);
+        const int id0 = id_of(j, 0);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const uint32_t key = key_of(v[i]);
+          if (level > 0 && (key >> (shift + 8)) != prefix) continue;
+          if (!(key > kc || (key == kc && id0 + i <= idc))) continue;
+          const int d = (key >> shift) & 255;
+          atomicAdd(&sh.sel.count[b][d], 1u);
+          if (kMass) {  // a 64-bit sum from two 32-bit ones
+            const u64 w = weight(v[i], st, sh.table);
+            const uint32_t wl = static_cast<uint32_t>(w);
+            const uint32_t old = atomicAdd(&sh.sel.lo[b][d], wl);
+            const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
+            if (wh != 0) atomicAdd(&sh.sel.hi[b][d], wh);
+          }
+        }
+      }
+      cluster_arrive();
+      cluster_wait();
+      // digit 255 - tid, all CTAs'; their running sums from the top
+      uint32_t cnt = 0;
+      u64 h = 0;
+      if (tid < kBins) {
+        const int d = 255 - tid;
+        for (int c = 0; c < a.cluster; ++c) {
+          const uint32_t n = remote_load(&sh.sel.count[b][d], c);
+          cnt += n;
+          if (!kMass)
+            h += n;
+          else if (n != 0)
+            h += (static_cast<u64>(remote_load(&sh.sel.hi[b][d], c)) << 32) +
+                 remote_load(&sh.sel.lo[b][d], c);
+        }
+      }
+      const u64 incl = warp_scan(h);
+      if (lane == 31) sh.warp[warp] = incl;
+      if (tid == 0) sh.all = 1;
+      __syncthreads();
+      u64 before = acc + incl - h;
+      for (int i = 0; i < min(warp, kBins / 32); ++i) before += sh.warp[i];
+      if (tid < kBins && before < target && target <= before + h) {
+        sh.digit = 255 - tid;
+        sh.acc = before;
+        sh.in = cnt;
+        sh.all = 0;
+      }
+      __syncthreads();
+      const bool all = sh.all != 0;  // fewer than the target: every one of them stays
+      prefix = (prefix << 8) | sh.digit;
+      acc = sh.acc;
+      in = sh.in;
+      __syncthreads();
+      if (all) return;
+    }
+    const int rest = 32 - 8 * kLevels<kDtype>;
+    uint32_t key = rest == 0 ? prefix : prefix << rest;
+    if (rest != 0 && !(key & 0x80000000u)) key |= (1u << rest) - 1u;  // a negative number's
+    // the border key's tokens have equal measures: how many of them, in id order
+    const u64 w = kMass ? max(weight(key_value(key), st, sh.table), 1ull) : 1ull;
+    const u64 want = (target - acc + w - 1) / w;
+    if (want >= in) {
+      if (key != kc) {
+        st.kc = key;
+        st.idc = INT32_MAX;
+      }
+      return;
+    }
+    auto tie = [&](float z, int id) -> u64 {
+      return key_of(z) == key && (key > kc || id <= idc) && in_row(id) ? 1 : 0;
+    };
+    const u64 mine = chunk_sums(tie);
+    exchange(mine, 0, 0);
+    u64 before = 0;
+    int owner = 0;
+    for (; owner < a.cluster - 1 && before + got(owner, 0) < want; ++owner) before += got(owner, 0);
+    int id = 0;
+    if (rank == owner && warp == 0) id = locate(want - 1 - before, tie);
+    exchange(static_cast<u64>(id), 0, 0);
+    st.kc = key;
+    st.idc = static_cast<int>(got(owner, 0));
+  }
+
+  __device__ __forceinline__ u64 kept_weight(float z, int id) const {
+    return keeps(key_of(z), id, st) && in_row(id) ? weight(z, st, sh.table) : 0;
+  }
+
+  // total: kept weights' sum; x: logit of the token; one thread
+  __device__ void write_row(int64_t row, int id, float x, u64 total, int n) {
+    // ln total as a pair: the leading 48 bits, and the scale
+    const int lz = __clzll(static_cast<long long>(total));
+    const u64 t = total << lz;
+    const Df f = renorm(static_cast<float>(static_cast<uint32_t>(t >> 40)) * 0x1p-24f,
+                        static_cast<float>(static_cast<uint32_t>(t >> 16) & 0xFFFFFFu) * 0x1p-48f);
+    const float e = static_cast<float>(64 - lz + st.top - 62);
+    const Df ln = log_df(f) + Df{kLn2Hi, kLn2Lo} * df(e);
+    const float base = st.pw.recentre ? st.pw.c : 0.f;
+    const Df lse = ln + df(base) * st.inv_tau;
+    a.ids[row] = id;
+    a.logprob[row] = n == 1 ? 0.f : ((df(x) - df(base)) * st.inv_tau - ln).h;
+    a.lse[row] = n == 1 ? (df(st.M) * st.inv_tau).h : lse.h;
+    a.kept[row] = n;
+  }
+
+  // ---- the wide way, by all CTAs
+  __device__ void wide(int64_t row, float u, int k, float top_p, uint32_t kmin) {
+    st.kc = kNegInfKey;
+    st.idc = INT32_MIN;
+    auto kept = [&](float z, int id) { return kept_weight(z, id); };
+    if (k > 0 && k < a.V) select_border<false>(static_cast<u64>(k));
+    auto total_of = [&](u64 mine, u64 n) {
+      exchange(mine, n, 0);
+      u64 t = 0;
+      for (int c = 0; c < a.cluster; ++c) t += got(c, 0);
+      return t;
+    };
+    if (top_p < 1.f) {
+      const u64 total = total_of(chunk_sums(kept), 0);
+      const u64 target =
+          static_cast<u64>(ceil(static_cast<double>(total) * static_cast<double>(top_p)));
+      select_border<true>(max(target, 1ull));
+    }
+    if (kmin > st.kc) {
+      st.kc = kmin;
+      st.idc = INT32_MAX;
+    }
+    // the number kept
+    uint32_t n = 0;
+    for (int j = tid; j < s.n; j += kThreads) {
+      float v[kVec];
+      E::unpack(slice[j], v);
+      const int id0 = id_of(j, 0);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        n += keeps(key_of(v[i]), id0 + i, st) && in_row(id0 + i) ? 1 : 0;
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    __syncthreads();
+    if (lane == 0) sh.warpu[warp] = n;
+    const u64 mine = chunk_sums(kept);
+    n = 0;
+    for (int i = 0; i < kWarps; ++i) n += sh.warpu[i];
+    const u64 total = total_of(mine, n);
+    const u64 target = static_cast<u64>(static_cast<double>(total) * static_cast<double>(u));
+    u64 before = 0;
+    uint32_t all = 0;
+    for (int c = 0; c < a.cluster; ++c) {
+      all += static_cast<uint32_t>(got(c, 1));
+      if (c < rank) before += got(c, 0);
+    }
+    if (warp == 0 && before <= target && target < before + mine) {
+      const int id = locate(target - before, kept);
+      if (lane == 0) write_row(row, id, r.at(id), total, static_cast<int>(all));
+    }
+  }
+
+  // ---- the few way: rank 0 with the list of n tokens; `complete`: it holds all that min-p keeps.
+  // False: the row's total is not known well enough (only with a positive `sum`, the fp32 total in
+  // units of 2^(max K)).
+  __device__ bool few(int64_t row, float u, int n, int k, float top_p, uint32_t kmin,
+                      bool complete, float sum) {
+    List& L = sh.list;
+    constexpr int kPer = (kCap + kThreads - 1) / kThreads;
+    // sorted by counting how many come before
+    u64 mine[kPer];
+    int at[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = tid + q * kThreads;
+      at[q] = 0;
+      mine[q] = i < n ? L.key[i] : 0;
+      if (i < n)
+        for (int j = 0; j < n; ++j) at[q] += L.key[j] > mine[q] ? 1 : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (tid + q * kThreads < n) L.key[at[q]] = mine[q];
+    if (tid == 0) sh.count_lo = sh.count_hi = 0;
+    __syncthreads();
+    if (k > 0) n = min(n, k);
+    // weights in order, kPer a thread, and their running sum
+    u64 w[kPer], sum_w = 0;
+    uint32_t key[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = tid * kPer + q;
+      key[q] = i < n ? static_cast<uint32_t>(L.key[i] >> 32) : 0u;
+      w[q] = i < n ? weight(key_value(key[q]), st, sh.table) : 0;
+      sum_w += w[q];
+      if (i < n) L.w[i] = w[q];
+    }
+    const u64 incl = warp_scan(sum_w);
+    if (lane == 31) sh.warp[warp] = incl;
+    __syncthreads();
+    u64 before = incl - sum_w, total = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += sh.warp[i];
+      total += sh.warp[i];
+    }
+    u64 lo = ~0ull, hi = ~0ull;  // top-p keeps a token while the sum before it is below
+    if (top_p < 1.f) {
+      const double p = static_cast<double>(top_p);
+      if (sum > 0.f) {
+        // the total in the weights' unit: 2^(max K - top + 62)
+        const Df mk = st.pw.recentre ? df(0.f) : df(st.M) * Df{st.pw.kh, st.pw.kl};
+        const float whole = rintf(mk.h), frac = (mk.h - whole) + mk.l;
+        const double unit =
+            static_cast<double>(pow2_df(frac, Pow2Row{1.f, 0.f, 0.f, false}).h) *
+            __longlong_as_double(static_cast<long long>(static_cast<int>(whole) - st.top + 62 + 1023) << 52);
+        const double P = p * static_cast<double>(sum) * unit;
+        lo = static_cast<u64>(P * (1.0 - static_cast<double>(kSumError)));
+        hi = static_cast<u64>(P * (1.0 + static_cast<double>(kSumError))) + 1;
+        if (hi > total && !complete) lo = 0;  // the list may not reach the border
+      } else {
+        lo = hi = max(static_cast<u64>(ceil(static_cast<double>(total) * p)), 1ull);
+      }
+    }
+    int c_lo = 0, c_hi = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      if (tid * kPer + q < n) {
+        const bool min_ok = key[q] >= kmin;
+        c_lo += before < lo && min_ok ? 1 : 0;
+        c_hi += before < hi && min_ok ? 1 : 0;
+      }
+      before += w[q];
+    }
+    if (c_lo != 0) atomicAdd(&sh.count_lo, c_lo);
+    if (c_hi != 0) atomicAdd(&sh.count_hi, c_hi);
+    __syncthreads();
+    const int m = sh.count_lo;
+    if (m != sh.count_hi) return false;
+    // the draw, by id: what the kept tokens of lower ids weigh
+    u64 kept = 0, below[kPer];
+    int id[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = tid + q * kThreads;
+      below[q] = 0;
+      id[q] = i < m ? static_cast<int>(~static_cast<uint32_t>(L.key[i])) : -1;
+    }
+    if (tid - lane < m) {  // this warp has tokens
+      for (int j = 0; j < m; ++j) {
+        const u64 wj = L.w[j];
+        const int idj = static_cast<int>(~static_cast<uint32_t>(L.key[j]));
+        kept += wj;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) below[q] += idj < id[q] ? wj : 0;
+      }
+      const u64 target = static_cast<u64>(static_cast<double>(kept) * static_cast<double>(u));
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int i = tid + q * kThreads;
+        if (i < m && below[q] <= target && target < below[q] + L.w[i])
+          write_row(row, id[q], key_value(static_cast<uint32_t>(L.key[i] >> 32)), kept, m);
+      }
+    }
+    return true;
+  }
+};
+
+// fp32 sum of 2^((z - c) K) over a thread's vectors.  A term's argument carries two roundings of
+// 2^-24 (below 40 octaves: 3.3e-6 of the term; terms further down are below 2^-40 of the
+// largest), the exponential 2^-22, and the sum of up to 100 terms in four partial sums 2^-24 a
+// term: together below kSumError = 7.6e-6 of the row's sum.
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__device__ __forceinline__ float approximate_sum(const uint4* slice, int n, int first, int step,
+                                                 float c, float k) {
   using E = Elem<kDtype>;
-  __shared__ Shared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
+  const F2 ref = f2(-c, -c), kk = f2(k, k);
+  F2 acc = f2(0.f, 0.f), acc2 = acc;
+#pragma unroll 4
+  for (int j = first; j < n; j += step) {
+    float v[E::kVec];
+    E::unpack(slice[j], v);
+#pragma unroll
+    for (int i = 0; i < E::kVec; i += 4) {
+      acc = add2(acc, ex2x2(mul2(add2(f2(v[i], v[i + 1]), ref), kk)));
+      acc2 = add2(acc2, ex2x2(mul2(add2(f2(v[i + 2], v[i + 3]), ref), kk)));
+    }
+  }
+  const float2 t = unpack2(add2(acc, acc2));
+  return t.x + t.y;
+}
+
+template <int kDtype, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
+    sample_kernel(const SampleArgs a) {
+  using E = Elem<kDtype>;
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ uint4 slice_mem[];
+  __shared__ Shared<kThreads> sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x / a.cluster;
+  const int rank = static_cast<int>(cluster_rank());
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
-  const float u = a.uniform[row];
-  float tau = a.row_temperature ? a.row_temperature[row] : a.temperature;
-  int k = a.row_top_k ? a.row_top_k[row] : a.top_k;
-  const float top_p = a.row_top_p ? a.row_top_p[row] : a.top_p;
-  const float min_p = a.row_min_p ? a.row_min_p[row] : a.min_p;
-  const bool args_ok = u >= 0.f && u < 1.f && (tau == 0.f || (tau >= 1e-6f && tau <= 1e6f)) &&
-                       top_p > 0.f && min_p >= 0.f && min_p <= 1.f;
+  const Slice s = slice_of(r.nvec(), rank, a.cluster);
+
+  cluster_arrive();
+  if (tid == 0) {
+    mbar_init(&sh.bar, 1);
+    fence_mbarrier_init();
+    load_slice(r, s, slice_mem, &sh.bar);
+    sh.list_n = 0;
+  }
+  load_slice_edges(r, s, slice_mem);
+  for (int i = tid; i < 256; i += kThreads) {
+    sh.table[i] = __ldg(&g_pow2_table.t[i]);
+    sh.hist[i] = 0;
+  }
+  const float u = __ldg(a.uniform + row);
+  float tau = a.row_temperature ? __ldg(a.row_temperature + row) : a.temperature;
+  int k = a.row_top_k ? __ldg(a.row_top_k + row) : a.top_k;
+  const float top_p = a.row_top_p ? __ldg(a.row_top_p + row) : a.top_p;
+  const float min_p = a.row_min_p ? __ldg(a.row_min_p + row) : a.min_p;
+  int bad = u >= 0.f && u < 1.f && (tau == 0.f || (tau >= 1e-6f && tau <= 1e6f)) && top_p > 0.f &&
+                    min_p >= 0.f && min_p <= 1.f
+                ? 0
+                : TIM_ERR_INVALID_ARG;
   if (tau == 0.f) {
     tau = 1.f;
     k = 1;
   }
-  for (int i = threadIdx.x; i < 256; i += kThreads) sh.table[i] = g_pow2_table.t[i];
-  if (threadIdx.x == 0) {
-    sh.bad = args_ok ? 0 : TIM_ERR_INVALID_ARG;
-    sh.found = -1;
+  if (k >= a.V) k = 0;
+  Sampler<kDtype, kThreads> S{a, sh, slice_mem, reinterpret_cast<u64*>(slice_mem + s.n), r, s, rank,
+                              tid, warp, lane, 0, {}};
+  RowState& st = S.st;
+  st.inv_tau = reciprocal(df(tau));
+  const Df K = Df{kLog2eHi, kLog2eLo} * st.inv_tau;
+  st.pw.kh = K.h;
+  st.pw.kl = K.l;
+
+  const int never = 0;
+  __syncthreads();  // the barrier, the edges, the table
+  if (!mbar_wait(&sh.bar, 0, &never)) set_status(a.status, TIM_ERR_TIMEOUT);
+
+  // ---- the largest logit of each thread, and of the CTA
+  float tmax = -INFINITY;
+  if (tid < s.n) {
+    uint4 m = slice_mem[tid];
+#pragma unroll 4
+    for (int j = tid + kThreads; j < s.n; j += kThreads) m = max_vec<kDtype>(m, slice_mem[j]);
+    float v[E::kVec];
+    E::unpack(m, v);
+    tmax = v[0];
+#pragma unroll
+    for (int i = 1; i < E::kVec; ++i) tmax = max_nan(tmax, v[i]);
+  }
+  const bool nan = !(tmax < INFINITY);
+  const uint32_t mykey = nan ? 0xFFFFFFFFu : key_of(tmax);
+  {
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, mykey);
+    const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, mykey > kNegInfKey ? mykey : 0xFFFFFFFFu);
+    if (lane == 0) {
+      sh.warpu[warp] = hi;
+      sh.warpv[warp] = lo;
+    }
   }
   __syncthreads();
-
-  float m = -INFINITY;
-  bool nan = false;
-  for_slice(r, warp, [&](int, const auto& v) {
+  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+  for (int i = 0; i < kWarps; ++i) {
+    hi = max(hi, sh.warpu[i]);
+    lo = min(lo, sh.warpv[i]);
+  }
+  const bool list_k = k > 0 && k <= kListK;
+  const bool need_sum = !list_k && top_p < 1.f && k == 0;
+  const bool cta_ok = hi > kNegInfKey && hi != 0xFFFFFFFFu;
+  const float cmax = cta_ok ? key_value(hi) : 0.f;
+  // sums relative to the CTA's largest: of all weights, and of the threads' largest
+  float sum = 0.f, cover = 0.f;
+  if (cta_ok) {
+    if (need_sum) sum = approximate_sum<kDtype>(slice_mem, s.n, tid, kThreads, cmax, K.h);
+    cover = ex2_approx((tmax - cmax) * K.h);
+  }
 #pragma unroll
-    for (int i = 0; i < E::kVec; ++i) {
-      m = fmaxf(m, v[i]);
-      nan |= !(v[i] < INFINITY);
-    }
-  });
-  if (nan) sh.bad = TIM_ERR_NONFINITE;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if (lane == 0) sh.warpf[warp] = m;
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    cover += __shfl_xor_sync(0xFFFFFFFFu, cover, o);
+  }
   __syncthreads();
-  for (int i = 0; i < kWarps; ++i) m = fmaxf(m, sh.warpf[i]);
-  int bad = sh.bad;
-  if (bad == 0 && m == -INFINITY) bad = TIM_ERR_NONFINITE;
-  if (bad != 0) {
-    if (threadIdx.x == 0) {
+  if (lane == 0) {
+    sh.warpf[warp] = sum;
+    sh.warpu[warp] = __float_as_uint(cover);
+  }
+  __syncthreads();
+  sum = cover = 0.f;
+  for (int i = 0; i < kWarps; ++i) {
+    sum += sh.warpf[i];
+    cover += __uint_as_float(sh.warpu[i]);
+  }
+  cluster_wait();  // every CTA of the row runs
+  S.exchange((static_cast<u64>(hi) << 32) | lo,
+             (static_cast<u64>(__float_as_uint(sum)) << 32) | __float_as_uint(cover), 0);
+  hi = 0;
+  lo = 0xFFFFFFFFu;
+  for (int c = 0; c < a.cluster; ++c) {
+    hi = max(hi, static_cast<uint32_t>(S.got(c, 0) >> 32));
+    lo = min(lo, static_cast<uint32_t>(S.got(c, 0)));
+  }
+  if (bad == 0 && (hi == 0xFFFFFFFFu || hi <= kNegInfKey)) bad = TIM_ERR_NONFINITE;
+  if (bad != 0) {  // the same in every CTA of the row
+    if (rank == 0 && tid == 0) {
       set_status(a.status, bad);
       a.ids[row] = -1;
       a.logprob[row] = a.lse[row] = __int_as_float(0x7FC00000);
@@ -280,125 +705,147 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
     return;
   }
-  __syncthreads();
-
-  // approximate total, relative to the largest
-  const float k2 = static_cast<float>(1.4426950408889634 / static_cast<double>(tau));
-  float sum = 0.f;
-  for_slice(r, warp, [&](int, const auto& v) {
-#pragma unroll
-    for (int i = 0; i < E::kVec; ++i) sum += ex2_approx((v[i] - m) * k2);
-  });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) sh.warpf[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int i = 0; i < kWarps; ++i) sum += sh.warpf[i];
-  __syncthreads();
-
-  RowState s;
-  s.pw = pow2_row(tau, m);
-  // weights relative to 2^N >= the largest; the total near 2^60
-  const double K = 1.4426950408889634 / static_cast<double>(tau);
-  const double mk = s.pw.recentre ? 0.0 : static_cast<double>(m) * K;
-  const int N = static_cast<int>(ceil(mk));
-  const int scale = 60 - ilogbf(sum);
-  s.top = N + 62 - scale;
-  s.kc = kNegInfKey;
-  s.idc = INT32_MIN;
-  // below this a weight is 0: the first bound keeps 2^x within pow2_fixed's range
-  const float zlow = static_cast<float>(
-      fmax(static_cast<double>(m) - 80.0 / K, -3.4028234663852886e38));
-
-  if (k > 0 && k < a.V) select_border<kDtype, false>(r, s, zlow, static_cast<u64>(k), sh);
-  auto kept_mass = [&]() {
-    u64 mine = 0;
-    for_slice(r, warp, [&](int id0, const auto& v) {
-#pragma unroll
-      for (int i = 0; i < E::kVec; ++i)
-        if (v[i] >= zlow && keeps(key_of(v[i]), id0 + i, s)) mine += weight(v[i], s, sh.table);
-    });
-    mine = warp_sum(mine);
-    __syncthreads();
-    if (lane == 0) sh.warp[warp] = mine;
-    __syncthreads();
-    u64 t = 0;
-    for (int i = 0; i < kWarps; ++i) t += sh.warp[i];
-    return t;
-  };
-  if (top_p < 1.f) {
-    const u64 total = kept_mass();
-    u64 target = static_cast<u64>(ceil(static_cast<double>(total) * static_cast<double>(top_p)));
-    target = max(target, 1ull);
-    __syncthreads();
-    select_border<kDtype, true>(r, s, zlow, target, sh);
+  const float M = key_value(hi);
+  st.M = M;
+  sum = cover = 0.f;
+  for (int c = 0; c < a.cluster; ++c) {
+    const uint32_t ch = static_cast<uint32_t>(S.got(c, 0) >> 32);
+    if (ch <= kNegInfKey) continue;
+    const float f = ex2_approx((key_value(ch) - M) * K.h);
+    sum += f * __uint_as_float(static_cast<uint32_t>(S.got(c, 1) >> 32));
+    cover += f * __uint_as_float(static_cast<uint32_t>(S.got(c, 1)));
   }
+  // ---- the scale.  The weights relative to the largest sum up to at most `cover` x (elements a
+  // thread), and to at least `cover`; N bounds the largest, so the total is below 2^61.
+  {
+    const Df mk = df(M) * K;
+    st.pw.recentre = !(fabsf(mk.h) < 8192.f);  // too large to split z K itself
+    st.pw.c = st.pw.recentre ? M : 0.f;
+    const int N = st.pw.recentre ? 0 : static_cast<int>(ceilf(mk.h));
+    const int most = ((r.nvec() + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
+    const int e = ilogbf(cover * static_cast<float>(most * E::kVec)) + 1;
+    st.top = N + 2 + e;
+    // top - n <= 63 for all logits from here up
+    st.zlow = (df(static_cast<float>(st.top) - 62.5f) * reciprocal(K)).h;
+  }
+  // ---- a bound for the list
+  uint32_t kmin = kNegInfKey + 1;  // min-p keeps from here up
   if (min_p > 0.f) {
-    const double cut = static_cast<double>(m) + static_cast<double>(tau) * log(static_cast<double>(min_p));
-    const uint32_t kmin = key_of(__double2float_ru(cut));
-    if (kmin > s.kc) {
-      s.kc = kmin;
-      s.idc = INT32_MAX;
-    }
+    const bool tiny = min_p < 0x1p-126f;
+    const Df ln = log_df(df(tiny ? min_p * 0x1p64f : min_p)) -
+                  (tiny ? Df{kLn2Hi, kLn2Lo} * df(64.f) : df(0.f));
+    const Df cut = df(M) + df(tau) * ln;
+    kmin = key_of(cut.h) + (cut.l > 0.f ? 1u : 0u);  // the first float that is not below
+    kmin = max(kmin, kNegInfKey + 1);
   }
-  const u64 total = kept_mass();
-  const u64 target = static_cast<u64>(static_cast<double>(total) * static_cast<double>(u));
-  // the first token whose running sum exceeds the target, and the number kept
-  u64 mine = sh.warp[warp];
-  u64 before = 0;
-  for (int i = 0; i < warp; ++i) before += sh.warp[i];
-  __syncthreads();
-  u64 n_kept = 0;
-  for_slice(r, warp, [&](int id0, const auto& v) {
-#pragma unroll
-    for (int i = 0; i < E::kVec; ++i) n_kept += keeps(key_of(v[i]), id0 + i, s) ? 1 : 0;
-  });
-  n_kept = warp_sum(n_kept);
-  if (lane == 0) sh.mass[warp] = n_kept;
-  if (before <= target && target < before + mine) {
-    u64 run = before;
-    for_slice(r, warp, [&](int id0, const auto& v) {
-      u64 w[E::kVec], c = 0;
-#pragma unroll
-      for (int i = 0; i < E::kVec; ++i) {
-        w[i] = v[i] >= zlow && keeps(key_of(v[i]), id0 + i, s) ? weight(v[i], s, sh.table) : 0;
-        c += w[i];
-      }
-      u64 incl = c;
+  // the list holds all tokens from the key `bound` up
+  uint32_t bound = kNegInfKey + 1;
+  bool listed = min_p > 0.f && top_p >= 1.f;
+  if (listed) bound = kmin;
+  if (list_k) {
+    uint32_t b = hi;
+    if (k > 1) {
+      // the threads' maxima in 256 bins from the largest down to the lowest, or over 64 octaves
+      // or units where they reach further: then the last bin bounds nothing
+      const float most = fmaxf(64.f, 64.f / K.h);
+      const float whole = M - key_value(lo), range = fminf(whole, most);
+      const float per_bin = range * (1.f / 255.f), inv = per_bin > 0.f ? 1.f / per_bin : 0.f;
+      if (mykey > kNegInfKey)
+        atomicAdd(&sh.hist[static_cast<int>(fminf((M - tmax) * inv, 255.f))], 1u);
+      cluster_arrive();
+      cluster_wait();
+      uint32_t incl = 0;
+      if (tid < kBins)
+        for (int c = 0; c < a.cluster; ++c) incl += remote_load(&sh.hist[tid], c);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const u64 up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += up;
       }
-      u64 at = run + incl - c;
-      if (at <= target && target < at + c) {
+      if (lane == 31) sh.warpv[warp] = incl;
+      if (tid == 0) sh.digit = kBins;
+      __syncthreads();
+      for (int i = 0; i < warp; ++i) incl += sh.warpv[i];
+      if (tid < kBins && incl >= static_cast<uint32_t>(k)) atomicMin(&sh.digit, tid);
+      __syncthreads();
+      const uint32_t bin = sh.digit;
+      // every maximum of the bins up to this one is above the bin's lower end
+      const float low = M - (static_cast<float>(bin) + 1.01f) * per_bin;
+      b = bin < 255u || (bin == 255u && range == whole && whole < INFINITY)
+              ? max(key_of(low), kNegInfKey + 1)
+              : kNegInfKey + 1;
+    }
+    listed = listed || b > kNegInfKey + 1;
+    bound = max(bound, b);
+  } else if (need_sum) {
+    // the tokens below this hold less than 1 - p of the mass, were there V of them
+    const float share = (1.f - top_p) * sum * (1.f - 0x1p-10f) / static_cast<float>(a.V);
+    if (share > 0.f) {
+      const float low = M + (__log2f(share) - 0x1p-10f) / K.h;
+      bound = max(max(key_of(low), kmin), kNegInfKey + 1);
+      listed = true;
+    }
+  }
+  if (listed) {
+    const float least = key_value(bound);
+    if (tmax >= least) {
+      for (int j = tid; j < s.n; j += kThreads) {
+        float v[E::kVec];
+        E::unpack(slice_mem[j], v);
 #pragma unroll
         for (int i = 0; i < E::kVec; ++i) {
-          if (at <= target && target < at + w[i]) sh.found = id0 + i;
-          at += w[i];
+          if (v[i] >= least) {
+            const uint32_t at = remote_add(&sh.list_n, 0, 1u);
+            if (at < kCap)
+              cluster_store(cluster_addr(&sh.list.key[at], 0),
+                            (static_cast<u64>(key_of(v[i])) << 32) |
+                                static_cast<uint32_t>(~static_cast<uint32_t>(S.id_of(j, i))));
+          }
         }
       }
-      run += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    });
+    }
+    cluster_arrive();
+    cluster_wait();
+    const uint32_t n = remote_load(&sh.list_n, 0);
+    if (n <= kCap) {
+      bool done = true;
+      if (rank == 0)
+        done = S.few(row, u, static_cast<int>(n), k, top_p, kmin, bound == kmin,
+                     need_sum ? sum : 0.f);
+      if (!need_sum) {
+        // the others have nothing left to do; rank 0's memory was read before this
+        cluster_arrive();
+        if (rank == 0) cluster_wait();
+        return;
+      }
+      S.exchange(done ? 1 : 0, 0, 0);
+      if (S.got(0, 0) != 0) return;
+    } else {
+      cluster_arrive();  // rank 0's list is read no more: its memory serves the histograms
+      cluster_wait();
+    }
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int id = sh.found;
-    u64 n = 0;
-    for (int i = 0; i < kWarps; ++i) n += sh.mass[i];
-    const double base = s.pw.recentre ? static_cast<double>(m) : 0.0;
-    const double inv_tau = 1.0 / static_cast<double>(tau);
-    // ln sum = ln(total) in the weights' unit
-    const double ls = log(static_cast<double>(total)) +
-                      static_cast<double>(s.top - 62) * 0.6931471805599453;
-    const double x = (static_cast<double>(r.at(id)) - base) * inv_tau;
-    a.ids[row] = id;
-    a.logprob[row] = n == 1 ? 0.f : static_cast<float>(x - ls);
-    a.lse[row] = n == 1 ? static_cast<float>(static_cast<double>(m) * inv_tau)
-                        : static_cast<float>(base * inv_tau + ls);
-    a.kept[row] = static_cast<int32_t>(n);
-  }
+  S.wide(row, u, k, top_p, kmin);
+  cluster_arrive();  // the others may still read this CTA's memory
+  cluster_wait();
+}
+
+template <int kDtype, int kThreads>
+cudaError_t launch_rows(const SampleArgs& a, int64_t T, const RowPlan& p, cudaStream_t stream) {
+  // the slice and a sum for each 32 of its vectors
+  const size_t smem = p.slice_bytes + (p.slice_bytes / 16 / 32 + 2) * 8;
+  auto* kernel = sample_kernel<kDtype, kThreads>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_clusters(kernel, T, p.cluster, kThreads, smem, stream, a);
+}
+template <int kDtype>
+cudaError_t launch_type(SampleArgs a, int64_t T, cudaStream_t stream) {
+  const RowPlan p = plan_row(a.V, sizeof(typename Elem<kDtype>::raw));
+  a.cluster = p.cluster;
+  return p.threads == 256 ? launch_rows<kDtype, 256>(a, T, p, stream)
+                          : launch_rows<kDtype, 512>(a, T, p, stream);
 }
 
 }  // namespace
@@ -407,17 +854,12 @@ cudaError_t launch_sample(const void* logits, int dtype, int64_t ld, int64_t T, 
                           const float* uniform, const tim_sample_params& p, int32_t* ids,
                           float* logprob, float* lse, int32_t* kept, int* status,
                           cudaStream_t stream) {
-  const SampleArgs a = {logits, ld, V, uniform, p.temperature, p.top_k, p.top_p, p.min_p,
+  const SampleArgs a = {logits, ld, V, 1, uniform, p.temperature, p.top_k, p.top_p, p.min_p,
                         p.row_temperature, p.row_top_k, p.row_top_p, p.row_min_p, ids, logprob,
                         lse, kept, status};
-  const unsigned g = static_cast<unsigned>(T);
-  if (dtype == TIM_F32)
-    sample_kernel<TIM_F32><<<g, kThreads, 0, stream>>>(a);
-  else if (dtype == TIM_BF16)
-    sample_kernel<TIM_BF16><<<g, kThreads, 0, stream>>>(a);
-  else
-    sample_kernel<TIM_F16><<<g, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return dtype == TIM_F32    ? launch_type<TIM_F32>(a, T, stream)
+         : dtype == TIM_BF16 ? launch_type<TIM_BF16>(a, T, stream)
+                             : launch_type<TIM_F16>(a, T, stream);
 }
 
 }  // namespace tim
