@@ -655,14 +655,17 @@ def processed_logprob(hidden, gamma, W, token_ids, temperature: float, eps: floa
 LOGITS_WORKSPACE_BYTES = 1024
 DISTILL_SAVED = 8
 DISTILL_KINDS = {"forward": 0, "reverse": 1}
+_DTYPE_CODES = {}
 
 
 def _logits_args(t, name):
     """(T, V, dtype code, row stride) of a [T, V] CUDA tensor whose rows are contiguous."""
     torch = _torch()
+    if not _DTYPE_CODES:
+        _DTYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    code = _DTYPE_CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if not t.is_cuda:
@@ -670,27 +673,37 @@ def _logits_args(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     T, V = t.shape
-    if V > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if V > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if T > 1 else V
+    if T <= 1:
+        ld = V
     if ld < V:
         raise ValueError(f"{name} must have rows that do not overlap")
     return T, V, code, ld
 
 
-def _at(dev, stream):
-    """The context of a call: its device, and its stream where one is given, so that what the
+def _vector(t, dtype, T, dev, name):
+    """A contiguous [T] tensor of ``dtype`` on ``dev``; its address."""
+    _need(t, dtype, name, 1)
+    if t.shape[0] != T:
+        raise ValueError(f"{name} must have one value a row")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return t.data_ptr()
+
+
+def _run(dev, stream, call):
+    """call(raw stream) with ``dev`` current and, where a stream is given, on it, so that what the
     call allocates belongs to the stream that uses it."""
     torch = _torch()
     if stream is not None:
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev)
-
-
-def _on_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream or None)
+    if torch.cuda.current_device() == dev.index:
+        return call(torch._C._cuda_getCurrentRawStream(dev.index) or None)
+    with torch.cuda.device(dev):
+        return call(torch._C._cuda_getCurrentRawStream(dev.index) or None)
 
 
 def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, out=None,
@@ -707,42 +720,43 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, o
     torch = _torch()
     T, V, code, ld = _logits_args(logits, "logits")
     dev = logits.device
-    _need(uniform, torch.float32, "uniform", 1)
-    tensors = {"uniform": uniform}
+    f32, i32 = torch.float32, torch.int32
+    u = _vector(uniform, f32, T, dev, "uniform")
     p = _SampleParams(1.0, 0, 1.0, 0.0, None, None, None, None)
-    for name, value, dtype in (("temperature", temperature, torch.float32),
-                               ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
-                               ("min_p", min_p, torch.float32)):
-        if isinstance(value, torch.Tensor):
-            _need(value, dtype, name, 1)
-            tensors[name] = value
-            setattr(p, "row_" + name, value.data_ptr())
-        else:
-            setattr(p, name, int(value) if name == "top_k" else float(value))
+    if isinstance(temperature, torch.Tensor):
+        p.row_temperature = _vector(temperature, f32, T, dev, "temperature")
+    else:
+        p.temperature = temperature
+    if isinstance(top_k, torch.Tensor):
+        p.row_top_k = _vector(top_k, i32, T, dev, "top_k")
+    else:
+        p.top_k = int(top_k)
+    if isinstance(top_p, torch.Tensor):
+        p.row_top_p = _vector(top_p, f32, T, dev, "top_p")
+    else:
+        p.top_p = top_p
+    if isinstance(min_p, torch.Tensor):
+        p.row_min_p = _vector(min_p, f32, T, dev, "min_p")
+    else:
+        p.min_p = min_p
     if out is not None:
-        for t, dtype, name in zip(out, (torch.int32, torch.float32, torch.float32, torch.int32),
-                                  ("out ids", "out logprob", "out lse_kept", "out kept")):
-            _need(t, dtype, name, 1)
-            tensors[name] = t
-    for name, t in tensors.items():
-        if t.shape[0] != T:
-            raise ValueError(f"{name} must have one value a row")
-    _on_device(dev, **tensors)
-    with _at(dev, stream):
-        if out is None:
-            out = (torch.empty(T, dtype=torch.int32, device=dev),
-                   torch.empty(T, dtype=torch.float32, device=dev),
-                   torch.empty(T, dtype=torch.float32, device=dev),
-                   torch.empty(T, dtype=torch.int32, device=dev))
-        if workspace is None:
-            workspace = Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
-        status = lib().tim_sample(_ptr(logits), code, ld, T, V, _ptr(uniform), _c.byref(p),
-                                  _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
-                                  workspace.ptr, workspace.nbytes, _stream_ptr(stream))
-        _check(status, "tim_sample")
+        for t, dtype, name in zip(out, (i32, f32, f32, i32), ("ids", "logprob", "lse_kept", "kept")):
+            _vector(t, dtype, T, dev, "out " + name)
+
+    def call(sp):
+        o = out
+        if o is None:
+            o = (torch.empty(T, dtype=i32, device=dev), torch.empty(T, dtype=f32, device=dev),
+                 torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=i32, device=dev))
+        ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        _check(lib().tim_sample(logits.data_ptr(), code, ld, T, V, u, _c.byref(p), o[0].data_ptr(),
+                                o[1].data_ptr(), o[2].data_ptr(), o[3].data_ptr(), ws.ptr,
+                                ws.nbytes, sp), "tim_sample")
         if check:
-            workspace.check("tim_sample", stream)
-    return out
+            ws.check("tim_sample", stream)
+        return o
+
+    return _run(dev, stream, call)
 
 
 def _distill_args(logits, teacher_ids, teacher_logprob, kind):
@@ -750,12 +764,14 @@ def _distill_args(logits, teacher_ids, teacher_logprob, kind):
     T, V, code, ld = _logits_args(logits, "logits")
     _need(teacher_ids, torch.int32, "teacher_ids", 2)
     _need(teacher_logprob, torch.float32, "teacher_logprob", 2)
+    K = teacher_ids.shape[1]
     if teacher_ids.shape[0] != T or teacher_logprob.shape != teacher_ids.shape:
         raise ValueError("teacher_ids and teacher_logprob must both be [T, K]")
     if kind not in DISTILL_KINDS:
         raise ValueError(f"kind must be one of {sorted(DISTILL_KINDS)}")
-    _on_device(logits.device, teacher_ids=teacher_ids, teacher_logprob=teacher_logprob)
-    return T, V, code, ld, teacher_ids.shape[1], DISTILL_KINDS[kind]
+    if teacher_ids.device != logits.device or teacher_logprob.device != logits.device:
+        raise ValueError(f"teacher_ids and teacher_logprob must be on {logits.device}")
+    return T, V, code, ld, K, DISTILL_KINDS[kind]
 
 
 def distill(logits, teacher_ids, teacher_logprob, temperature: float = 1.0, *,
@@ -770,40 +786,37 @@ def distill(logits, teacher_ids, teacher_logprob, temperature: float = 1.0, *,
     ``distill_backward``)."""
     torch = _torch()
     T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
-    dev = logits.device
+    dev, f32 = logits.device, torch.float32
     if out is not None:
-        for t, shape, name in zip(out, ((T,), (T,), (T, DISTILL_SAVED)),
-                                  ("out loss", "out lse", "out saved")):
-            _need(t, torch.float32, name)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-        _on_device(dev, loss=out[0], lse=out[1], saved=out[2])
-    with _at(dev, stream):
-        if out is None:
-            out = (torch.empty(T, dtype=torch.float32, device=dev),
-                   torch.empty(T, dtype=torch.float32, device=dev),
-                   torch.empty(T, DISTILL_SAVED, dtype=torch.float32, device=dev))
-        if workspace is None:
-            workspace = Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
-        _check(lib().tim_distill(_ptr(logits), code, ld, T, V, _ptr(teacher_ids),
-                                 _ptr(teacher_logprob), K, float(temperature), kd,
-                                 int(bool(tail)), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
-                                 workspace.ptr, workspace.nbytes, _stream_ptr(stream)),
-               "tim_distill")
+        _vector(out[0], f32, T, dev, "out loss")
+        _vector(out[1], f32, T, dev, "out lse")
+        _need(out[2], f32, "out saved", 2)
+        if tuple(out[2].shape) != (T, DISTILL_SAVED) or out[2].device != dev:
+            raise ValueError(f"out saved must be [T, {DISTILL_SAVED}] on {dev}")
+
+    def call(sp):
+        o = out
+        if o is None:
+            o = (torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev),
+                 torch.empty(T, DISTILL_SAVED, dtype=f32, device=dev))
+        ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        _check(lib().tim_distill(logits.data_ptr(), code, ld, T, V, teacher_ids.data_ptr(),
+                                 teacher_logprob.data_ptr(), K, temperature, kd, int(bool(tail)),
+                                 o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), ws.ptr,
+                                 ws.nbytes, sp), "tim_distill")
         if check:
-            workspace.check("tim_distill", stream)
-    return out
+            ws.check("tim_distill", stream)
+        return o
+
+    return _run(dev, stream, call)
 
 
-def _dlogits_out(logits, out):
-    torch = _torch()
-    if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+def _dlogits_stride(logits, out):
+    """Row stride of the caller's gradient tensor."""
     _, _, _, ldd = _logits_args(out, "out_dlogits")
-    if out.shape != logits.shape or out.dtype != logits.dtype:
-        raise ValueError("out_dlogits must have the shape and type of logits")
-    _on_device(logits.device, out_dlogits=out)
-    return out, ldd
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out_dlogits must have the shape, type and device of logits")
+    return ldd
 
 
 def distill_backward(logits, teacher_ids, teacher_logprob, saved, grad_loss,
@@ -814,18 +827,24 @@ def distill_backward(logits, teacher_ids, teacher_logprob, saved, grad_loss,
     result for the same arguments; grad_loss float32 [T]."""
     torch = _torch()
     T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
+    dev = logits.device
     _need(saved, torch.float32, "saved", 2)
-    _need(grad_loss, torch.float32, "grad_loss", 1)
-    if tuple(saved.shape) != (T, DISTILL_SAVED) or grad_loss.shape[0] != T:
-        raise ValueError("saved must be [T, 8] and grad_loss [T]")
-    _on_device(logits.device, saved=saved, grad_loss=grad_loss)
-    with _at(logits.device, stream):
-        out, ldd = _dlogits_out(logits, out_dlogits)
-        _check(lib().tim_distill_backward(_ptr(logits), code, ld, T, V, _ptr(teacher_ids),
-                                          _ptr(teacher_logprob), K, float(temperature), kd,
-                                          _ptr(saved), _ptr(grad_loss), _ptr(out), ldd,
-                                          _stream_ptr(stream)), "tim_distill_backward")
-    return out
+    if tuple(saved.shape) != (T, DISTILL_SAVED) or saved.device != dev:
+        raise ValueError(f"saved must be [T, {DISTILL_SAVED}] on {dev}")
+    g = _vector(grad_loss, torch.float32, T, dev, "grad_loss")
+    ldd = V if out_dlogits is None else _dlogits_stride(logits, out_dlogits)
+
+    def call(sp):
+        o = out_dlogits
+        if o is None:
+            o = torch.empty(T, V, dtype=logits.dtype, device=dev)
+        _check(lib().tim_distill_backward(logits.data_ptr(), code, ld, T, V,
+                                          teacher_ids.data_ptr(), teacher_logprob.data_ptr(), K,
+                                          temperature, kd, saved.data_ptr(), g, o.data_ptr(), ldd,
+                                          sp), "tim_distill_backward")
+        return o
+
+    return _run(dev, stream, call)
 
 
 def distill_grad(logits, teacher_ids, teacher_logprob, grad_loss, temperature: float = 1.0, *,
@@ -836,24 +855,25 @@ def distill_grad(logits, teacher_ids, teacher_logprob, grad_loss, temperature: f
     once.  Returns (loss f32 [T], dlogits)."""
     torch = _torch()
     T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
-    _need(grad_loss, torch.float32, "grad_loss", 1)
-    if grad_loss.shape[0] != T:
-        raise ValueError("grad_loss must be [T]")
     dev = logits.device
-    _on_device(dev, grad_loss=grad_loss)
-    with _at(dev, stream):
-        out, ldd = _dlogits_out(logits, out_dlogits)
+    g = _vector(grad_loss, torch.float32, T, dev, "grad_loss")
+    ldd = V if out_dlogits is None else _dlogits_stride(logits, out_dlogits)
+
+    def call(sp):
+        o = out_dlogits
+        if o is None:
+            o = torch.empty(T, V, dtype=logits.dtype, device=dev)
         loss = torch.empty(T, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
-        _check(lib().tim_distill_grad(_ptr(logits), code, ld, T, V, _ptr(teacher_ids),
-                                      _ptr(teacher_logprob), K, float(temperature), kd,
-                                      int(bool(tail)), _ptr(grad_loss), _ptr(loss), _ptr(out), ldd,
-                                      workspace.ptr, workspace.nbytes, _stream_ptr(stream)),
-               "tim_distill_grad")
+        ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        _check(lib().tim_distill_grad(logits.data_ptr(), code, ld, T, V, teacher_ids.data_ptr(),
+                                      teacher_logprob.data_ptr(), K, temperature, kd,
+                                      int(bool(tail)), g, loss.data_ptr(), o.data_ptr(), ldd,
+                                      ws.ptr, ws.nbytes, sp), "tim_distill_grad")
         if check:
-            workspace.check("tim_distill_grad", stream)
-    return loss, out
+            ws.check("tim_distill_grad", stream)
+        return loss, o
+
+    return _run(dev, stream, call)
 
 
 def _distill_function():

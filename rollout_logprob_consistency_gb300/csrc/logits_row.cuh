@@ -153,6 +153,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 __device__ __forceinline__ F2 ex2x2(F2 a) {
   const float2 t = unpack2(a);
   return f2(ex2_approx(t.x), ex2_approx(t.y));
@@ -180,6 +185,10 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* smem, uint32_t rank
 }
 __device__ __forceinline__ void cluster_store(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+__device__ __forceinline__ void cluster_store32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -304,9 +313,9 @@ __device__ __forceinline__ Df reciprocal(Df a) {
 // ---------------------------------------------------------------------------
 // 2^x in fixed point.
 //
-// x = z * K with K = Kh + Kl (a float and its remainder).  z * Kh is taken exactly as
-// ph + pl; ph is split at multiples of 1/256 into n + j/256 + g, |g| <= 2^-9 plus the
-// small pl, and
+// x = z * K with K = Kh + Kl (a float and its remainder) is split at the multiple of 1/256
+// next to z Kh (the sum with a number whose last place is 1/256) into n + j/256 + g, where
+// one multiply-add gives z Kh less that multiple with one rounding, |g| <= 2^-9, and
 //   2^x = 2^n * T[j] * (1 + p),  p = 2^g - 1 = g ln2 + g^2 ln2^2/2 + g^3 ln2^3/6
 // (the next term is below 2^-41).  T is a table at scale 2^62 and p is taken at scale
 // 2^32, so T[j] (1 + p) is one 32 x 32 -> 64-bit multiply-add.  The largest error is the
@@ -357,29 +366,47 @@ constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596299e-8f;  // log2(e) a
 constexpr float kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;    // ln 2 as a pair
 
 // w and n with 2^((z - c) K) = w 2^(n - 62).  |(z - c) K| must be below 2^14.
+constexpr float kPow2Magic = 49152.f;  // 1.5 * 2^15: a sum's last place is 1/256
 __device__ __forceinline__ unsigned long long pow2_fixed(float z, const Pow2Row& k,
                                                          const unsigned long long* table, int& n) {
-  constexpr float kMagic = 49152.f;  // 1.5 * 2^15: the sum's last place is 1/256
-  float ph, pl;
+  float t, g;
   if (k.recentre) {
     // z - c = d + e exactly
     const float d = z - k.c, b = d - z;
     const float e = (z - (d - b)) + (-k.c - b);
-    ph = d * k.kh;
-    pl = fmaf(e, k.kh, fmaf(d, k.kl, fmaf(d, k.kh, -ph)));
+    t = fmaf(d, k.kh, kPow2Magic);
+    g = fmaf(e, k.kh, fmaf(d, k.kl, fmaf(d, k.kh, kPow2Magic - t)));
   } else {
-    ph = z * k.kh;
-    pl = fmaf(z, k.kl, fmaf(z, k.kh, -ph));
+    t = fmaf(z, k.kh, kPow2Magic);
+    g = fmaf(z, k.kl, fmaf(z, k.kh, kPow2Magic - t));
   }
-  const float t = ph + kMagic;
-  const float g = (ph - (t - kMagic)) + pl;
-  const int ti = __float_as_int(t) - __float_as_int(kMagic);
+  const int ti = __float_as_int(t) - __float_as_int(kPow2Magic);
   // p at scale 2^32
   const float p = g * fmaf(g, fmaf(g, 238388336.0f, 1031764992.0f), 2977044472.0f);
   const unsigned long long T = table[ti & 255];
-  n = ti >> kPow2Bits;
+  n = ti >> 8;
   return T + static_cast<unsigned long long>(static_cast<long long>(static_cast<int>(T >> 32)) *
                                              __float2int_rn(p));
+}
+// Two at once without recentring, as right shifts of `top` - n.
+struct Pow2Pair {
+  F2 kh, kl;
+  uint32_t top;  // top + (bits of kPow2Magic >> 8)
+};
+__device__ __forceinline__ void pow2_shifted(F2 z, const Pow2Pair& k, const unsigned long long* table,
+                                             unsigned long long& w0, unsigned long long& w1) {
+  const F2 magic = f2(kPow2Magic, kPow2Magic);
+  const F2 t = fma2(z, k.kh, magic);
+  const F2 g = fma2(z, k.kl, fma2(z, k.kh, fma2(t, f2(-1.f, -1.f), magic)));
+  const F2 p = mul2(g, fma2(g, fma2(g, f2(238388336.0f, 238388336.0f), f2(1031764992.0f, 1031764992.0f)),
+                            f2(2977044472.0f, 2977044472.0f)));
+  const float2 tt = unpack2(t), pp = unpack2(p);
+  const uint32_t b0 = __float_as_uint(tt.x), b1 = __float_as_uint(tt.y);
+  const unsigned long long T0 = table[b0 & 255u], T1 = table[b1 & 255u];
+  const long long q0 = static_cast<long long>(static_cast<int>(T0 >> 32)) * __float2int_rn(pp.x);
+  const long long q1 = static_cast<long long>(static_cast<int>(T1 >> 32)) * __float2int_rn(pp.y);
+  w0 = (T0 + static_cast<unsigned long long>(q0)) >> (k.top - (b0 >> 8));
+  w1 = (T1 + static_cast<unsigned long long>(q1)) >> (k.top - (b1 >> 8));
 }
 
 // The table, one copy a translation unit.

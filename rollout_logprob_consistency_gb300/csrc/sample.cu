@@ -40,6 +40,7 @@ constexpr int kBins = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kCap = 512;      // tokens of the list
 constexpr int kListK = 256;    // largest top-k that the list serves
+constexpr int kMaxSteps = 64;  // 32-vector steps of a warp's part: at most 24580 vectors over 16 warps
 constexpr float kSumError = 0x1p-17f;  // of the fp32 sum, see approximate_sum
 using u64 = unsigned long long;
 
@@ -123,6 +124,21 @@ __device__ __forceinline__ uint4 max_vec(uint4 a, const uint4& b) {
   }
   return a;
 }
+template <int kDtype>
+__device__ __forceinline__ uint4 min_vec(uint4 a, const uint4& b) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&a);
+  const uint32_t* y = reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kDtype == TIM_F32)
+      asm("min.f32 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+    else if constexpr (kDtype == TIM_BF16)
+      asm("min.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+    else
+      asm("min.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(y[i]));
+  }
+  return a;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -170,15 +186,16 @@ struct Shared {
     Select sel;
     List list;
   };
-  u64 xch[2][kMaxCluster][3];
-  uint32_t hist[kBins];  // of the threads' maxima, all CTAs'
+  u64 xch[2][kMaxCluster][2];
+  // of every warp of every CTA: largest key, and a sum relative to it
+  uint32_t gkey[kMaxCluster * kThreads / 32];
+  float gsum[kMaxCluster * kThreads / 32];
+  uint32_t hist[kBins];  // of the threads' maxima
   u64 warp[kThreads / 32];
   uint32_t warpu[kThreads / 32];
-  uint32_t warpv[kThreads / 32];
-  float warpf[kThreads / 32];
+  u64 step[kMaxSteps];  // sums over 32 vectors each, of one warp's part
   u64 acc;
-  u64 cta_sum;
-  uint32_t digit, in;
+  uint32_t digit, in, bound;
   uint32_t list_n;
   int all, found, count_lo, count_hi;
   uint64_t bar;
@@ -193,18 +210,16 @@ struct Sampler {
   const SampleArgs& a;
   Shared<kThreads>& sh;
   const uint4* slice;
-  u64* chunk;  // a sum for each 32 vectors of the slice
   Row<kDtype> r;
   Slice s;
   int rank, tid, warp, lane, phase;
   RowState st;
 
-  // ---- among the CTAs of the row: every CTA's three numbers to every CTA
-  __device__ __forceinline__ void exchange(u64 x, u64 y, u64 z) {  // called by all, the values of thread 0..31
+  // ---- among the CTAs of the row: every CTA's two numbers to every CTA
+  __device__ __forceinline__ void exchange(u64 x, u64 y) {  // called by all; warp 0's values
     if (warp == 0 && lane < a.cluster) {
       cluster_store(cluster_addr(&sh.xch[phase & 1][rank][0], lane), x);
       cluster_store(cluster_addr(&sh.xch[phase & 1][rank][1], lane), y);
-      cluster_store(cluster_addr(&sh.xch[phase & 1][rank][2], lane), z);
     }
     cluster_arrive();
     cluster_wait();
@@ -216,68 +231,70 @@ struct Sampler {
   __device__ __forceinline__ int id_of(int j, int i) const { return (s.j0 + j) * kVec + i - r.shift; }
   __device__ __forceinline__ bool in_row(int id) const { return id >= 0 && id < a.V; }
 
-  // ---- sums over the slice.  f(z, key, id) is a token's number; the slice goes by chunks of 32
-  // vectors, chunk c to warp c mod kWarps; chunk[] gets their sums.  Returns the CTA's.
+  // ---- sums over the slice.  A warp has a contiguous part of it, in steps of 32 vectors.
+  __device__ __forceinline__ int part_steps() const { return (s.n + kThreads - 1) / kThreads; }
+  __device__ __forceinline__ int part_start(int w) const { return w * part_steps() * 32; }
+
+  // The sum of f(z, id) over the slice; sh.warp[] gets the parts' sums.  f(v, id0, ends) is the sum
+  // of a vector.
   template <class F>
-  __device__ __forceinline__ u64 chunk_sums(F&& f) {
-    const int chunks = (s.n + 31) / 32;
-    u64 mine = 0;
-    for (int c = warp; c < chunks; c += kWarps) {
-      const int j = c * 32 + lane;
-      u64 sum = 0;
-      if (j < s.n) {
-        float v[kVec];
-        E::unpack(slice[j], v);
-        const int id0 = id_of(j, 0);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) sum += f(v[i], id0 + i);
-      }
-      sum = warp_sum(sum);
-      if (lane == 0) chunk[c] = sum;
-      mine += sum;
+  __device__ __forceinline__ u64 slice_sum(F&& f) {
+    const int j0 = part_start(warp), j1 = min(s.n, j0 + part_steps() * 32);
+    u64 sum = 0;
+    for (int j = j0 + lane; j < j1; j += 32) {
+      float v[kVec];
+      E::unpack(slice[j], v);
+      sum += f(v, id_of(j, 0));
     }
+    sum = warp_sum(sum);
     __syncthreads();
-    if (lane == 0) sh.warp[warp] = mine;
+    if (lane == 0) sh.warp[warp] = sum;
     __syncthreads();
     u64 t = 0;
     for (int i = 0; i < kWarps; ++i) t += sh.warp[i];
     return t;
   }
-  // The token at which the running sum of f first exceeds `target` (below the CTA's sum);
-  // warp 0, after chunk_sums(f).  -1 in the other warps.
-  template <class F>
-  __device__ __forceinline__ int locate(u64 target, F&& f) {
-    const int chunks = (s.n + 31) / 32;
-    u64 run = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 32) {
-      const u64 x = c0 + lane < chunks ? chunk[c0 + lane] : 0;
-      const u64 incl = run + warp_scan(x);
-      const unsigned past = __ballot_sync(0xFFFFFFFFu, incl > target);
-      if (past != 0) {
-        const int l = __ffs(past) - 1;
-        u64 at = __shfl_sync(0xFFFFFFFFu, incl - x, l);
-        const int j = (c0 + l) * 32 + lane;
-        u64 w[kVec], sum = 0;
+  // The token at which the running sum first exceeds `target` (below the CTA's sum), in every
+  // thread; after slice_sum(f), by the whole CTA.  one(z, id) is a token's number.
+  template <class F, class G>
+  __device__ __forceinline__ int locate(u64 target, F&& f, G&& one) {
+    int w = 0;
+    for (; w < kWarps - 1 && target >= sh.warp[w]; ++w) target -= sh.warp[w];
+    const int j0 = part_start(w), j1 = min(s.n, j0 + part_steps() * 32);
+    for (int i = warp; j0 + i * 32 < j1; i += kWarps) {
+      const int j = j0 + i * 32 + lane;
+      u64 sum = 0;
+      if (j < j1) {
         float v[kVec];
-        const int id0 = id_of(j, 0);
-        if (j < s.n) E::unpack(slice[j], v);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          w[i] = j < s.n ? f(v[i], id0 + i) : 0;
-          sum += w[i];
-        }
-        at += warp_scan(sum) - sum;
-        int id = -1;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          if (at <= target && target < at + w[i]) id = id0 + i;
-          at += w[i];
-        }
-        return __reduce_max_sync(0xFFFFFFFFu, id);
+        E::unpack(slice[j], v);
+        sum = f(v, id_of(j, 0));
       }
-      run = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      sum = warp_sum(sum);
+      if (lane == 0) sh.step[i] = sum;
     }
-    return -1;
+    __syncthreads();
+    int i = 0;
+    for (; j0 + (i + 1) * 32 < j1 && target >= sh.step[i]; ++i) target -= sh.step[i];
+    if (warp == 0) {
+      const int j = j0 + i * 32 + lane;
+      u64 x[kVec], sum = 0;
+      float v[kVec];
+      const int id0 = id_of(j, 0);
+      if (j < j1) E::unpack(slice[j], v);
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) {
+        x[q] = j < j1 ? one(v[q], id0 + q) : 0;
+        sum += x[q];
+      }
+      u64 at = warp_scan(sum) - sum;
+#pragma unroll
+      for (int q = 0; q < kVec; ++q) {
+        if (at <= target && target < at + x[q]) sh.found = id0 + q;
+        at += x[q];
+      }
+    }
+    __syncthreads();
+    return sh.found;
   }
 
   // ---- the wide way's border.  Among the tokens that the state keeps: the last one before which
@@ -366,14 +383,20 @@ struct Sampler {
     auto tie = [&](float z, int id) -> u64 {
       return key_of(z) == key && (key > kc || id <= idc) && in_row(id) ? 1 : 0;
     };
-    const u64 mine = chunk_sums(tie);
-    exchange(mine, 0, 0);
+    auto ties = [&](const float(&v)[kVec], int id0) {
+      u64 n = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) n += tie(v[i], id0 + i);
+      return n;
+    };
+    const u64 mine = slice_sum(ties);
+    exchange(mine, 0);
     u64 before = 0;
     int owner = 0;
     for (; owner < a.cluster - 1 && before + got(owner, 0) < want; ++owner) before += got(owner, 0);
     int id = 0;
-    if (rank == owner && warp == 0) id = locate(want - 1 - before, tie);
-    exchange(static_cast<u64>(id), 0, 0);
+    if (rank == owner) id = locate(want - 1 - before, ties, tie);
+    exchange(static_cast<u64>(id), 0);
     st.kc = key;
     st.idc = static_cast<int>(got(owner, 0));
   }
@@ -399,20 +422,67 @@ struct Sampler {
     a.kept[row] = n;
   }
 
+  // The scale: N bounds the largest weight and 2^e the sum of all relative to it, so the row's
+  // total is below 2^60.
+  __device__ __forceinline__ void set_scale(float most) {
+    const Df mk = df(st.M) * Df{st.pw.kh, st.pw.kl};
+    st.pw.recentre = !(fabsf(mk.h) < 8192.f);  // too large to split z K itself
+    st.pw.c = st.pw.recentre ? st.M : 0.f;
+    const int N = st.pw.recentre ? 0 : static_cast<int>(ceilf(mk.h));
+    st.top = N + 3 + ilogbf(most);
+    // top - n <= 63 for all logits from here up
+    st.zlow = ((static_cast<float>(st.top) - 62.5f) / st.pw.kh);
+  }
+
+  // Sum and count of the whole row from every CTA's.
+  __device__ __forceinline__ u64 total_of(u64 mine, u64 n, u64& all) {
+    exchange(mine, n);
+    u64 t = 0;
+    all = 0;
+    for (int c = 0; c < a.cluster; ++c) {
+      t += got(c, 0);
+      all += got(c, 1);
+    }
+    return t;
+  }
+
+  // The draw, f and one being the kept tokens' weights and n their number in the slice.
+  template <class F, class G>
+  __device__ __forceinline__ void draw(int64_t row, float u, uint32_t n, F&& f, G&& one) {
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    __syncthreads();
+    if (lane == 0) sh.warpu[warp] = n;
+    const u64 mine = slice_sum(f);
+    n = 0;
+    for (int i = 0; i < kWarps; ++i) n += sh.warpu[i];
+    u64 all;
+    const u64 total = total_of(mine, n, all);
+    const u64 target = static_cast<u64>(static_cast<double>(total) * static_cast<double>(u));
+    u64 before = 0;
+    for (int c = 0; c < rank; ++c) before += got(c, 0);
+    if (before <= target && target < before + mine) {  // one CTA of the row
+      const int id = locate(target - before, f, one);
+      if (tid == 0) write_row(row, id, r.at(id), total, static_cast<int>(all));
+    }
+  }
+
   // ---- the wide way, by all CTAs
   __device__ void wide(int64_t row, float u, int k, float top_p, uint32_t kmin) {
     st.kc = kNegInfKey;
     st.idc = INT32_MIN;
-    auto kept = [&](float z, int id) { return kept_weight(z, id); };
-    if (k > 0 && k < a.V) select_border<false>(static_cast<u64>(k));
-    auto total_of = [&](u64 mine, u64 n) {
-      exchange(mine, n, 0);
+    for (int i = tid; i < 256; i += kThreads) sh.table[i] = __ldg(&g_pow2_table.t[i]);
+    __syncthreads();
+    auto one = [&](float z, int id) { return kept_weight(z, id); };
+    auto kept = [&](const float(&v)[kVec], int id0) {
       u64 t = 0;
-      for (int c = 0; c < a.cluster; ++c) t += got(c, 0);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) t += one(v[i], id0 + i);
       return t;
     };
+    u64 all;
+    if (k > 0) select_border<false>(static_cast<u64>(k));
     if (top_p < 1.f) {
-      const u64 total = total_of(chunk_sums(kept), 0);
+      const u64 total = total_of(slice_sum(kept), 0, all);
       const u64 target =
           static_cast<u64>(ceil(static_cast<double>(total) * static_cast<double>(top_p)));
       select_border<true>(max(target, 1ull));
@@ -421,7 +491,6 @@ struct Sampler {
       st.kc = kmin;
       st.idc = INT32_MAX;
     }
-    // the number kept
     uint32_t n = 0;
     for (int j = tid; j < s.n; j += kThreads) {
       float v[kVec];
@@ -431,23 +500,56 @@ struct Sampler {
       for (int i = 0; i < kVec; ++i)
         n += keeps(key_of(v[i]), id0 + i, st) && in_row(id0 + i) ? 1 : 0;
     }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    __syncthreads();
-    if (lane == 0) sh.warpu[warp] = n;
-    const u64 mine = chunk_sums(kept);
-    n = 0;
-    for (int i = 0; i < kWarps; ++i) n += sh.warpu[i];
-    const u64 total = total_of(mine, n);
-    const u64 target = static_cast<u64>(static_cast<double>(total) * static_cast<double>(u));
-    u64 before = 0;
-    uint32_t all = 0;
-    for (int c = 0; c < a.cluster; ++c) {
-      all += static_cast<uint32_t>(got(c, 1));
-      if (c < rank) before += got(c, 0);
+    draw(row, u, n, kept, one);
+  }
+
+  // ---- the unfiltered row, by all CTAs
+  __device__ void plain(int64_t row, float u) {
+    for (int i = tid; i < 256; i += kThreads) sh.table[i] = __ldg(&g_pow2_table.t[i]);
+    // all tokens but those of -inf are kept: only a thread that meets one counts
+    uint4 low = make_uint4(0, 0, 0, 0);
+    uint32_t n = 0;
+    if (tid < s.n) {
+      low = slice[tid];
+      for (int j = tid + kThreads; j < s.n; j += kThreads) low = min_vec<kDtype>(low, slice[j]);
+      float v[kVec];
+      E::unpack(low, v);
+      bool some = false;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) some |= v[i] == -INFINITY;
+      if (!some) {
+        n = static_cast<uint32_t>((s.n - tid + kThreads - 1) / kThreads) * kVec;
+      } else {
+        for (int j = tid; j < s.n; j += kThreads) {
+          E::unpack(slice[j], v);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) n += v[i] > -INFINITY ? 1 : 0;
+        }
+      }
     }
-    if (warp == 0 && before <= target && target < before + mine) {
-      const int id = locate(target - before, kept);
-      if (lane == 0) write_row(row, id, r.at(id), total, static_cast<int>(all));
+    __syncthreads();
+    auto one = [&](float z, int) { return weight(z, st, sh.table); };
+    if (st.pw.recentre) {
+      draw(row, u, n, [&](const float(&v)[kVec], int) {
+        u64 t = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) t += one(v[i], 0);
+        return t;
+      }, one);
+    } else {
+      const Pow2Pair k = {f2(st.pw.kh, st.pw.kh), f2(st.pw.kl, st.pw.kl),
+                          static_cast<uint32_t>(st.top) + (__float_as_uint(kPow2Magic) >> 8)};
+      const float zlow = st.zlow;
+      draw(row, u, n, [&](const float(&v)[kVec], int) {
+        u64 t = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2) {
+          u64 w0, w1;
+          pow2_shifted(f2(fmaxf(v[i], zlow), fmaxf(v[i + 1], zlow)), k, sh.table, w0, w1);
+          t += w0 + w1;
+        }
+        return t;
+      }, one);
     }
   }
 
@@ -483,7 +585,7 @@ struct Sampler {
     for (int q = 0; q < kPer; ++q) {
       const int i = tid * kPer + q;
       key[q] = i < n ? static_cast<uint32_t>(L.key[i] >> 32) : 0u;
-      w[q] = i < n ? weight(key_value(key[q]), st, sh.table) : 0;
+      w[q] = i < n ? weight(key_value(key[q]), st, g_pow2_table.t) : 0;
       sum_w += w[q];
       if (i < n) L.w[i] = w[q];
     }
@@ -600,12 +702,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
     fence_mbarrier_init();
     load_slice(r, s, slice_mem, &sh.bar);
     sh.list_n = 0;
+    sh.bound = 0;
   }
   load_slice_edges(r, s, slice_mem);
-  for (int i = tid; i < 256; i += kThreads) {
-    sh.table[i] = __ldg(&g_pow2_table.t[i]);
-    sh.hist[i] = 0;
-  }
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
   const float u = __ldg(a.uniform + row);
   float tau = a.row_temperature ? __ldg(a.row_temperature + row) : a.temperature;
   int k = a.row_top_k ? __ldg(a.row_top_k + row) : a.top_k;
@@ -619,20 +719,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
     tau = 1.f;
     k = 1;
   }
-  if (k >= a.V) k = 0;
-  Sampler<kDtype, kThreads> S{a, sh, slice_mem, reinterpret_cast<u64*>(slice_mem + s.n), r, s, rank,
-                              tid, warp, lane, 0, {}};
+  k = k <= 0 || k >= a.V ? 0 : k;
+  Sampler<kDtype, kThreads> S{a, sh, slice_mem, r, s, rank, tid, warp, lane, 0, {}};
   RowState& st = S.st;
   st.inv_tau = reciprocal(df(tau));
   const Df K = Df{kLog2eHi, kLog2eLo} * st.inv_tau;
   st.pw.kh = K.h;
   st.pw.kl = K.l;
-
+  const bool list_k = k > 0 && k <= kListK;
+  const bool need_sum = k == 0 && top_p < 1.f;
+  const bool all_kept = k == 0 && top_p >= 1.f && min_p == 0.f;
   const int never = 0;
-  __syncthreads();  // the barrier, the edges, the table
+  __syncthreads();  // the barrier and the edges
   if (!mbar_wait(&sh.bar, 0, &never)) set_status(a.status, TIM_ERR_TIMEOUT);
 
-  // ---- the largest logit of each thread, and of the CTA
+  // ---- the largest logit of each thread; of each warp, to every CTA of the row
   float tmax = -INFINITY;
   if (tid < s.n) {
     uint4 m = slice_mem[tid];
@@ -644,57 +745,33 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
 #pragma unroll
     for (int i = 1; i < E::kVec; ++i) tmax = max_nan(tmax, v[i]);
   }
-  const bool nan = !(tmax < INFINITY);
-  const uint32_t mykey = nan ? 0xFFFFFFFFu : key_of(tmax);
-  {
-    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, mykey);
-    const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, mykey > kNegInfKey ? mykey : 0xFFFFFFFFu);
-    if (lane == 0) {
-      sh.warpu[warp] = hi;
-      sh.warpv[warp] = lo;
+  const uint32_t mykey = !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
+  const uint32_t wkey = __reduce_max_sync(0xFFFFFFFFu, mykey);
+  float sum = 0.f;
+  if (wkey > kNegInfKey && wkey != 0xFFFFFFFFu) {
+    // relative to the warp's largest: all its weights, or the threads' largest
+    const float wmax = key_value(wkey);
+    if (need_sum)
+      sum = approximate_sum<kDtype>(slice_mem, s.n, tid, kThreads, wmax, K.h);
+    else if (!list_k)
+      sum = ex2_approx((tmax - wmax) * K.h);
+    if (!list_k) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     }
   }
-  __syncthreads();
-  uint32_t hi = 0, lo = 0xFFFFFFFFu;
-  for (int i = 0; i < kWarps; ++i) {
-    hi = max(hi, sh.warpu[i]);
-    lo = min(lo, sh.warpv[i]);
-  }
-  const bool list_k = k > 0 && k <= kListK;
-  const bool need_sum = !list_k && top_p < 1.f && k == 0;
-  const bool cta_ok = hi > kNegInfKey && hi != 0xFFFFFFFFu;
-  const float cmax = cta_ok ? key_value(hi) : 0.f;
-  // sums relative to the CTA's largest: of all weights, and of the threads' largest
-  float sum = 0.f, cover = 0.f;
-  if (cta_ok) {
-    if (need_sum) sum = approximate_sum<kDtype>(slice_mem, s.n, tid, kThreads, cmax, K.h);
-    cover = ex2_approx((tmax - cmax) * K.h);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    cover += __shfl_xor_sync(0xFFFFFFFFu, cover, o);
-  }
-  __syncthreads();
-  if (lane == 0) {
-    sh.warpf[warp] = sum;
-    sh.warpu[warp] = __float_as_uint(cover);
-  }
-  __syncthreads();
-  sum = cover = 0.f;
-  for (int i = 0; i < kWarps; ++i) {
-    sum += sh.warpf[i];
-    cover += __uint_as_float(sh.warpu[i]);
-  }
   cluster_wait();  // every CTA of the row runs
-  S.exchange((static_cast<u64>(hi) << 32) | lo,
-             (static_cast<u64>(__float_as_uint(sum)) << 32) | __float_as_uint(cover), 0);
-  hi = 0;
-  lo = 0xFFFFFFFFu;
-  for (int c = 0; c < a.cluster; ++c) {
-    hi = max(hi, static_cast<uint32_t>(S.got(c, 0) >> 32));
-    lo = min(lo, static_cast<uint32_t>(S.got(c, 0)));
+  if (lane < a.cluster) {
+    const int g = rank * kWarps + warp;
+    cluster_store32(cluster_addr(&sh.gkey[g], lane), wkey);
+    if (!list_k) cluster_store32(cluster_addr(&sh.gsum[g], lane), __float_as_uint(sum));
   }
+  cluster_arrive();
+  cluster_wait();
+  const int groups = a.cluster * kWarps;
+  uint32_t hi = 0;
+  for (int g = lane; g < groups; g += 32) hi = max(hi, sh.gkey[g]);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
   if (bad == 0 && (hi == 0xFFFFFFFFu || hi <= kNegInfKey)) bad = TIM_ERR_NONFINITE;
   if (bad != 0) {  // the same in every CTA of the row
     if (rank == 0 && tid == 0) {
@@ -707,27 +784,26 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   }
   const float M = key_value(hi);
   st.M = M;
-  sum = cover = 0.f;
-  for (int c = 0; c < a.cluster; ++c) {
-    const uint32_t ch = static_cast<uint32_t>(S.got(c, 0) >> 32);
-    if (ch <= kNegInfKey) continue;
-    const float f = ex2_approx((key_value(ch) - M) * K.h);
-    sum += f * __uint_as_float(static_cast<uint32_t>(S.got(c, 1) >> 32));
-    cover += f * __uint_as_float(static_cast<uint32_t>(S.got(c, 1)));
+  // the groups' sums relative to the row's largest
+  auto row_sum = [&]() {
+    float t = 0.f;
+    for (int g = lane; g < groups; g += 32) {
+      const uint32_t key = sh.gkey[g];
+      if (key > kNegInfKey) t += sh.gsum[g] * ex2_approx((key_value(key) - M) * K.h);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    return t;
+  };
+  // the elements of a thread, at most
+  const float of_thread = static_cast<float>(
+      ((r.nvec() + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads * E::kVec);
+  if (all_kept) {
+    S.set_scale(row_sum() * of_thread);
+    S.plain(row, u);
+    return;
   }
-  // ---- the scale.  The weights relative to the largest sum up to at most `cover` x (elements a
-  // thread), and to at least `cover`; N bounds the largest, so the total is below 2^61.
-  {
-    const Df mk = df(M) * K;
-    st.pw.recentre = !(fabsf(mk.h) < 8192.f);  // too large to split z K itself
-    st.pw.c = st.pw.recentre ? M : 0.f;
-    const int N = st.pw.recentre ? 0 : static_cast<int>(ceilf(mk.h));
-    const int most = ((r.nvec() + a.cluster - 1) / a.cluster + kThreads - 1) / kThreads;
-    const int e = ilogbf(cover * static_cast<float>(most * E::kVec)) + 1;
-    st.top = N + 2 + e;
-    // top - n <= 63 for all logits from here up
-    st.zlow = (df(static_cast<float>(st.top) - 62.5f) * reciprocal(K)).h;
-  }
+
   // ---- a bound for the list
   uint32_t kmin = kNegInfKey + 1;  // min-p keeps from here up
   if (min_p > 0.f) {
@@ -735,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
     const Df ln = log_df(df(tiny ? min_p * 0x1p64f : min_p)) -
                   (tiny ? Df{kLn2Hi, kLn2Lo} * df(64.f) : df(0.f));
     const Df cut = df(M) + df(tau) * ln;
-    kmin = key_of(cut.h) + (cut.l > 0.f ? 1u : 0u);  // the first float that is not below
-    kmin = max(kmin, kNegInfKey + 1);
+    kmin = max(key_of(cut.h) + (cut.l > 0.f ? 1u : 0u),  // the first float that is not below
+               kNegInfKey + 1);
   }
   // the list holds all tokens from the key `bound` up
   uint32_t bound = kNegInfKey + 1;
@@ -744,12 +820,27 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   if (listed) bound = kmin;
   if (list_k) {
     uint32_t b = hi;
-    if (k > 1) {
-      // the threads' maxima in 256 bins from the largest down to the lowest, or over 64 octaves
-      // or units where they reach further: then the last bin bounds nothing
-      const float most = fmaxf(64.f, 64.f / K.h);
-      const float whole = M - key_value(lo), range = fminf(whole, most);
-      const float per_bin = range * (1.f / 255.f), inv = per_bin > 0.f ? 1.f / per_bin : 0.f;
+    if (k > 1 && k <= groups) {
+      // the k-th largest of the warps' largest: four threads a key, counting those before it
+      const int g = tid >> 2;
+      int before = 0;
+      if (g < groups) {
+        const uint32_t mine = sh.gkey[g];
+        for (int i = tid & 3; i < groups; i += 4) {
+          const uint32_t other = sh.gkey[i];
+          before += other > mine || (other == mine && i < g) ? 1 : 0;
+        }
+      }
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+      if (g < groups && before == k - 1) sh.bound = sh.gkey[g];
+      __syncthreads();
+      b = max(sh.bound, kNegInfKey + 1);
+    } else if (k > 1) {
+      // more than there are warps: the threads' maxima in 256 bins from the largest down, over 64
+      // octaves or units; the last bin bounds nothing
+      const float range = fmaxf(64.f, 64.f / K.h);
+      const float per_bin = range * (1.f / 255.f), inv = 1.f / per_bin;
       if (mykey > kNegInfKey)
         atomicAdd(&sh.hist[static_cast<int>(fminf((M - tmax) * inv, 255.f))], 1u);
       cluster_arrive();
@@ -762,22 +853,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
         const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += up;
       }
-      if (lane == 31) sh.warpv[warp] = incl;
+      if (lane == 31) sh.warpu[warp] = incl;
       if (tid == 0) sh.digit = kBins;
       __syncthreads();
-      for (int i = 0; i < warp; ++i) incl += sh.warpv[i];
+      for (int i = 0; i < warp; ++i) incl += sh.warpu[i];
       if (tid < kBins && incl >= static_cast<uint32_t>(k)) atomicMin(&sh.digit, tid);
       __syncthreads();
       const uint32_t bin = sh.digit;
       // every maximum of the bins up to this one is above the bin's lower end
-      const float low = M - (static_cast<float>(bin) + 1.01f) * per_bin;
-      b = bin < 255u || (bin == 255u && range == whole && whole < INFINITY)
-              ? max(key_of(low), kNegInfKey + 1)
-              : kNegInfKey + 1;
+      b = bin < 255u ? max(key_of(M - (static_cast<float>(bin) + 1.01f) * per_bin), kNegInfKey + 1)
+                     : kNegInfKey + 1;
     }
     listed = listed || b > kNegInfKey + 1;
     bound = max(bound, b);
   } else if (need_sum) {
+    sum = row_sum();
     // the tokens below this hold less than 1 - p of the mass, were there V of them
     const float share = (1.f - top_p) * sum * (1.f - 0x1p-10f) / static_cast<float>(a.V);
     if (share > 0.f) {
@@ -808,23 +898,43 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
     cluster_wait();
     const uint32_t n = remote_load(&sh.list_n, 0);
     if (n <= kCap) {
-      bool done = true;
-      if (rank == 0)
-        done = S.few(row, u, static_cast<int>(n), k, top_p, kmin, bound == kmin,
-                     need_sum ? sum : 0.f);
       if (!need_sum) {
         // the others have nothing left to do; rank 0's memory was read before this
         cluster_arrive();
-        if (rank == 0) cluster_wait();
+        if (rank != 0) return;
+        S.set_scale(static_cast<float>(kCap));
+        S.few(row, u, static_cast<int>(n), k, top_p, kmin, bound == kmin, 0.f);
+        cluster_wait();
         return;
       }
-      S.exchange(done ? 1 : 0, 0, 0);
+      bool done = true;
+      if (rank == 0) {
+        S.set_scale(sum);
+        done = S.few(row, u, static_cast<int>(n), k, top_p, kmin, bound == kmin, sum);
+      }
+      S.exchange(done ? 1 : 0, 0);
       if (S.got(0, 0) != 0) return;
     } else {
       cluster_arrive();  // rank 0's list is read no more: its memory serves the histograms
       cluster_wait();
     }
   }
+  if (list_k) {  // the groups' sums were not taken
+    sum = ex2_approx((tmax - M) * K.h);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    __syncthreads();
+    if (lane == 0) sh.warpu[warp] = __float_as_uint(sum);
+    __syncthreads();
+    sum = 0.f;
+    for (int i = 0; i < kWarps; ++i) sum += __uint_as_float(sh.warpu[i]);
+    S.exchange(__float_as_uint(sum), 0);
+    sum = 0.f;
+    for (int c = 0; c < a.cluster; ++c) sum += __uint_as_float(static_cast<uint32_t>(S.got(c, 0)));
+  } else if (!need_sum) {
+    sum = row_sum();
+  }
+  S.set_scale(need_sum ? sum : sum * of_thread);
   S.wide(row, u, k, top_p, kmin);
   cluster_arrive();  // the others may still read this CTA's memory
   cluster_wait();
@@ -832,8 +942,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
 
 template <int kDtype, int kThreads>
 cudaError_t launch_rows(const SampleArgs& a, int64_t T, const RowPlan& p, cudaStream_t stream) {
-  // the slice and a sum for each 32 of its vectors
-  const size_t smem = p.slice_bytes + (p.slice_bytes / 16 / 32 + 2) * 8;
+  const size_t smem = p.slice_bytes;
   auto* kernel = sample_kernel<kDtype, kThreads>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
