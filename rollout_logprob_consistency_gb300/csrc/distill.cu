@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kBackThreads = 256;
 constexpr int kMaxWarps = 16;
-constexpr int kMaxCluster = 8;
 constexpr float kTailFloor = 0x1p-20f;  // a teacher's tail up to this is rounding
 constexpr float kTailLeast = 0x1p-100f;  // below this share of the mass the student has no tail
 
@@ -43,7 +42,7 @@ struct DistillArgs {
   float inv_h, inv_l;  // 1 / temperature as a pair
   int kind;
   int tail;
-  int cluster;
+  int parts;  // backward: CTAs a row
   float* loss;
   float* lse;    // forward only
   float* saved;  // forward only: [T][TIM_DISTILL_SAVED]
@@ -93,6 +92,56 @@ __device__ __forceinline__ void gradient_vector(float (&v)[kVec], F2 ref, F2 k, 
     v[i] = t.x;
     v[i + 1] = t.y;
   }
+}
+
+// The gradient of a slice's tokens, c 2^((z - M) log2e / tau), or zeros without a read.
+constexpr int kGradUnroll = 4;  // vectors of a thread in flight
+template <int kDtype, int kThreads>
+__device__ __forceinline__ void gradient_slice(const DistillArgs& a, const Row<kDtype>& r,
+                                               const Slice& s, typename Elem<kDtype>::raw* out,
+                                               float M, float c, bool zero) {
+  using E = Elem<kDtype>;
+  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
+  // the vectors that are one load and one store each
+  int j0 = 0, j1 = 0;
+  if (same && s.n > 0) {
+    j0 = r.whole(s.j0) ? 0 : 1;
+    j1 = max(j0, r.whole(s.j0 + s.n - 1) ? s.n : s.n - 1);
+  }
+  const F2 ref = f2(-M, -M), kk = f2(a.kh, a.kh), cc = f2(c, c);
+  const int64_t at = static_cast<int64_t>(s.j0) * E::kVec - r.shift;
+  const uint4* from = reinterpret_cast<const uint4*>(r.p + at);
+  uint4* to = reinterpret_cast<uint4*>(out + at);
+  if (zero) {
+    for (int j = j0 + threadIdx.x; j < j1; j += kThreads) to[j] = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int j = j0 + threadIdx.x; j < j1; j += kGradUnroll * kThreads) {
+      uint4 u[kGradUnroll];
+#pragma unroll
+      for (int n = 0; n < kGradUnroll; ++n)
+        if (j + n * kThreads < j1) u[n] = __ldcs(from + j + n * kThreads);
+#pragma unroll
+      for (int n = 0; n < kGradUnroll; ++n) {
+        if (j + n * kThreads < j1) {
+          float v[E::kVec];
+          E::unpack(u[n], v);
+          gradient_vector(v, ref, kk, cc);
+          __stcs(to + j + n * kThreads, E::pack(v));
+        }
+      }
+    }
+  }
+  // the others: the row's ends, or all where the output lies otherwise
+  auto edge = [&](int j) {
+    float v[E::kVec] = {};
+    if (!zero) {
+      E::unpack(r.load(s.j0 + j), v);
+      gradient_vector(v, ref, kk, cc);
+    }
+    store_vector<kDtype>(out, r, s.j0 + j, same, v);
+  };
+  if (static_cast<int>(threadIdx.x) < j0) edge(threadIdx.x);
+  for (int j = j1 + threadIdx.x; j < s.n; j += kThreads) edge(j);
 }
 
 // One entry's gradient with respect to s, M the row's maximum.
@@ -193,54 +242,38 @@ __device__ __forceinline__ void merge(float& m, float& sum, float m2, float s2, 
   m = mm;
 }
 
-// Loss of a row by a cluster of CTAs, and with kGrad its gradient for a known grad[row].
-//
-// Each CTA holds its slice of the row in shared memory, so the gradient costs one write and no
-// second read.  While the slice is on its way every CTA does the head's terms (the same in all
-// of them: no second exchange is needed), then sums its slice's other tokens relative to the
-// head's maximum, sends the sum to the others and all combine them in rank order.  Nothing
-// else has to be known before the sum: a weight relative to the head's maximum only overflows
-// if a token lies 2^127 above the whole head, and then that slice is summed again with a running
-// maximum.
-// 256 threads a CTA: five CTAs an SM, as many as 40 KB slices fit.
-template <int kDtype, bool kGrad, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) distill_kernel(const DistillArgs a) {
+// Loss of a row by one CTA that streams it, and with kGrad the gradient in a second pass, which
+// finds the row in L2: a CTA's fixed work is spread over a whole row, and a row's bits cannot
+// depend on the batch.
+template <bool kGrad>
+constexpr int kRowThreads = kGrad ? 512 : 256;
+constexpr int kRowUnroll = 4;  // vectors of a thread in flight, and as many being summed
+template <int kDtype, bool kGrad>
+__global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
+    distill_kernel(const DistillArgs a) {
   using E = Elem<kDtype>;
   using raw = typename E::raw;
-  extern __shared__ uint4 slice_mem[];
+  constexpr int kThreads = kRowThreads<kGrad>, warps = kThreads / 32, U = kRowUnroll;
+  extern __shared__ uint4 marks_mem[];  // a byte a vector: which of its tokens are the head's
   __shared__ HeadSums red[kMaxWarps];
-  __shared__ float redm[kMaxWarps], reds[kMaxWarps];
-  __shared__ float s_hmax[kMaxWarps];
-  __shared__ uint64_t part[kMaxCluster][2];  // (reference, sum) and the error code of every CTA
-  __shared__ uint64_t head_part[kMaxCluster][4];
+  __shared__ float redm[kMaxWarps], reds[kMaxWarps], s_hmax[kMaxWarps];
   __shared__ RowConstants s_terms;
   __shared__ float s_M;
   __shared__ int s_bad;
-  __shared__ uint64_t bar;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int warps = kThreads / 32;
-  const int64_t row = blockIdx.x / a.cluster;
-  const int rank = static_cast<int>(cluster_rank());
+  const int64_t row = blockIdx.x;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
-  const Slice s = slice_of(r.nvec(), rank, a.cluster);
-  uint8_t* marks = reinterpret_cast<uint8_t*>(slice_mem + s.n);  // a byte a vector: ids met
+  const int nvec = r.nvec();
+  uint8_t* marks = reinterpret_cast<uint8_t*>(marks_mem);
   const int32_t* ids = a.ids + row * a.K;
   const float* lp = a.lp + row * a.K;
   raw* out = nullptr;
   if constexpr (kGrad) out = static_cast<raw*>(a.dlogits) + row * a.ldd;
 
-  cluster_arrive();  // this CTA runs: the others may write to its memory after their wait
-  if (tid == 0) {
-    s_bad = 0;
-    mbar_init(&bar, 1);
-    fence_mbarrier_init();
-  }
-  for (int i = tid; i < (s.n + 3) / 4; i += kThreads)
-    reinterpret_cast<uint32_t*>(marks)[i] = 0u;
-  // Calls f(id, ln q, z) for this thread's entries that are in the head; the first one's values
-  // are loaded once.
   const int id0 = tid < a.K ? __ldg(ids + tid) : -1;
   const float lq0 = tid < a.K ? __ldg(lp + tid) : 0.f;
+  if (tid == 0) s_bad = 0;
+  for (int i = tid; i < (nvec + 15) / 16; i += kThreads) marks_mem[i] = make_uint4(0, 0, 0, 0);
   auto usable = [&](int id, float lq) { return in_head(id, lq) && id < a.V && lq <= 1.f; };
   const float z0 = usable(id0, lq0) ? r.at(id0) : 0.f;
   auto for_head = [&](auto&& f) {
@@ -262,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) distill_ker
     else if (in_head(id, lq))
       any = 1;
   }
-  if (!__syncthreads_or(any | bad)) {  // the same in every CTA of the row: no entries
-    if (rank == 0 && tid == 0) {
+  if (!__syncthreads_or(any | bad)) {  // no entries
+    if (tid == 0) {
       a.loss[row] = 0.f;
       if constexpr (!kGrad) {
         a.lse[row] = 0.f;
@@ -273,80 +306,84 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) distill_ker
     }
     if constexpr (kGrad) {
       const Row<kDtype> o(out, 0, 0, a.V);  // the output's own vectors
-      const Slice so = slice_of(o.nvec(), rank, a.cluster);
       const float zeros[E::kVec] = {};
-      for (int j = so.j0 + tid; j < so.j0 + so.n; j += kThreads)
+      for (int j = tid; j < o.nvec(); j += kThreads)
         store_vector<kDtype>(out, o, j, true, zeros);
     }
-    cluster_wait();
     return;
   }
-  if (tid == 0) load_slice(r, s, slice_mem, &bar);
-  load_slice_edges(r, s, slice_mem);
-
-  // ---- the head, while the slice is on its way
+  // the first vectors are on their way while the head is done
+  uint4 u[U];
+#pragma unroll
+  for (int n = 0; n < U; ++n) {
+    const int j = tid + n * kThreads;
+    if (j < nvec) u[n] = r.load(j);
+  }
   float hmax = -INFINITY;
   for_head([&](int id, float, float z) {
     hmax = fmaxf(hmax, z);
-    const int slot = id + r.shift - s.j0 * E::kVec;
-    if (slot >= 0 && slot < s.n * E::kVec) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(marks) + slot / E::kVec / 4;
-      const uint32_t bit = 1u << (slot / E::kVec % 4 * 8 + slot % E::kVec);
-      if ((atomicOr(w, bit) & bit) && bad == 0) bad = TIM_ERR_INVALID_ARG;  // an id twice
-    }
+    const int slot = id + r.shift;
+    uint32_t* w = reinterpret_cast<uint32_t*>(marks) + slot / E::kVec / 4;
+    const uint32_t bit = 1u << (slot / E::kVec % 4 * 8 + slot % E::kVec);
+    if ((atomicOr(w, bit) & bit) && bad == 0) bad = TIM_ERR_INVALID_ARG;  // an id twice
   });
   if (bad != 0) atomicMax(&s_bad, bad);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) hmax = fmaxf(hmax, __shfl_xor_sync(0xFFFFFFFFu, hmax, o));
   if (lane == 0) s_hmax[warp] = hmax;
   __syncthreads();
-  for (int i = 0; i < min(warps, (a.K + 31) / 32); ++i) hmax = fmaxf(hmax, s_hmax[i]);
+  const int head_warps = min(warps, (a.K + 31) / 32);
+  for (int i = 0; i < head_warps; ++i) hmax = fmaxf(hmax, s_hmax[i]);
   const float href = hmax == -INFINITY ? 0.f : hmax;
-  // entry rank + cluster i is thread i's
-  const int head_n = (a.K - rank + a.cluster - 1) / a.cluster, head_warps = (head_n + 31) / 32;
-  if (tid < head_warps * 32) {
+  if (warp < head_warps) {
     HeadSums h = {};
-    const int k = rank + a.cluster * tid;
-    if (k < a.K) {
-      const int id = __ldg(ids + k);
-      const float lq = __ldg(lp + k);
-      if (usable(id, lq)) {
-        const float z = r.at(id);
-        const Df t = df(lq) - scaled(z, href, a);
-        h.e = pow2_df(z, Pow2Row{a.kh, a.kl, href, true});
-        h.q = exp_df(lq);
-        if (h.q.h != 0.f) h.qx = h.q * t;
-        if (h.e.h != 0.f) h.ex = -(h.e * t);
-      }
-    }
+    for_head([&](int, float lq, float z) {
+      const Df t = df(lq) - scaled(z, href, a);
+      const Df e = pow2_df(z, Pow2Row{a.kh, a.kl, href, true}), q = exp_df(lq);
+      h.e = h.e + e;
+      h.q = h.q + q;
+      if (q.h != 0.f) h.qx = h.qx + q * t;
+      if (e.h != 0.f) h.ex = h.ex - e * t;
+    });
     h = warp_sum(h, 16);
     if (lane == 0) red[warp] = h;
   }
 
-  // ---- the slice: sum of 2^((z - reference) log2e / tau) outside the head
+  // ---- sum of 2^((z - reference) log2e / tau) outside the head
   const float k2 = a.kh;
-  const int never = 0;
-  if (!mbar_wait(&bar, 0, &never)) set_status(a.status, TIM_ERR_TIMEOUT);
-  // the head's tokens leave the slice: 2^-inf = 0 in the sum, and their gradients come later
-  for_head([&](int id, float, float) {
-    const int slot = id + r.shift - s.j0 * E::kVec;
-    if (slot >= 0 && slot < s.n * E::kVec)
-      reinterpret_cast<raw*>(slice_mem)[slot] = E::narrow(-INFINITY);
-  });
-  __syncthreads();
+  auto unmarked = [&](const uint4& x, int j, float(&v)[E::kVec]) {
+    E::unpack(x, v);
+    const uint32_t mk = marks[j];
+    if (mk != 0) {
+#pragma unroll
+      for (int i = 0; i < E::kVec; ++i)
+        if ((mk >> i) & 1u) v[i] = -INFINITY;
+    }
+  };
   float m = href, sum;
   {
     const F2 ref = f2(-href, -href), kk = f2(k2, k2);
     F2 acc = f2(0.f, 0.f), acc2 = acc;
-    const uint4* end = slice_mem + s.n;
-#pragma unroll 4
-    for (const uint4* p = slice_mem + tid; p < end; p += kThreads) {
-      float v[E::kVec];
-      E::unpack(*p, v);
+    for (int j0 = tid; j0 < nvec; j0 += U * kThreads) {
+      uint4 w[U];
 #pragma unroll
-      for (int i = 0; i < E::kVec; i += 4) {
-        acc = add2(acc, ex2x2(mul2(add2(f2(v[i], v[i + 1]), ref), kk)));
-        acc2 = add2(acc2, ex2x2(mul2(add2(f2(v[i + 2], v[i + 3]), ref), kk)));
+      for (int n = 0; n < U; ++n) {
+        const int j = j0 + (U + n) * kThreads;
+        if (j < nvec) w[n] = r.load(j);
+      }
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        const int j = j0 + n * kThreads;
+        if (j < nvec) {
+          float v[E::kVec];
+          unmarked(u[n], j, v);
+#pragma unroll
+          for (int i = 0; i < E::kVec; i += 4) {
+            acc = add2(acc, ex2x2(mul2(add2(f2(v[i], v[i + 1]), ref), kk)));
+            acc2 = add2(acc2, ex2x2(mul2(add2(f2(v[i + 2], v[i + 3]), ref), kk)));
+          }
+        }
+        u[n] = w[n];
       }
     }
     const float2 t = unpack2(add2(acc, acc2));
@@ -366,9 +403,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) distill_ker
   if (__syncthreads_or(!(sum < INFINITY) || hmax == -INFINITY)) {
     m = -INFINITY;
     sum = 0.f;
-    for (int j = tid; j < s.n; j += kThreads) {
+    for (int j = tid; j < nvec; j += kThreads) {
       float v[E::kVec];
-      E::unpack(slice_mem[j], v);
+      unmarked(r.load(j), j, v);
       float vm = m;
 #pragma unroll
       for (int i = 0; i < E::kVec; ++i) vm = fmaxf(vm, v[i]);
@@ -383,192 +420,81 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) distill_ker
     publish();
     __syncthreads();
   }
-  cluster_wait();
-  // the loss alone is rank 0's work
-  const int readers = kGrad ? a.cluster : 1;
+  const float nan = __int_as_float(0x7FC00000);
+  HeadSums hs = {};
+  float M = 0.f;
   if (warp == 0) {
     m = lane < warps ? redm[lane] : -INFINITY;
     sum = lane < warps ? reds[lane] : 0.f;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
       merge(m, sum, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, sum, o), k2);
-    if (lane < readers) {
-      cluster_store(cluster_addr(&part[rank][0], lane),
-                    (static_cast<uint64_t>(__float_as_uint(sum)) << 32) | __float_as_uint(m));
-      cluster_store(cluster_addr(&part[rank][1], lane), static_cast<uint64_t>(s_bad));
-    }
-  } else if (warp == 1) {
-    HeadSums h = {};
-    if (lane < head_warps) h = red[lane];
-    if (head_warps > 1) h = warp_sum(h, 8);
-    const Df out[4] = {h.e, h.q, h.qx, h.ex};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const Df v = bcast(out[i]);
-      if (lane < readers)
-        cluster_store(cluster_addr(&head_part[rank][i], lane),
-                      (static_cast<uint64_t>(__float_as_uint(v.l)) << 32) | __float_as_uint(v.h));
-    }
-  }
-  cluster_arrive();
-  if (!kGrad && rank != 0) return;  // having arrived
-  cluster_wait();
-  // all parts, combined in rank order by a whole warp; every lane has the result
-  struct Combined {
-    float M, rest;
-    int code;
-    HeadSums h;
-  };
-  auto combine = [&]() {
-    const bool mine = lane < a.cluster;
-    const float mi = mine ? __uint_as_float(static_cast<uint32_t>(part[lane][0])) : -INFINITY;
-    float rest = mine ? __uint_as_float(static_cast<uint32_t>(part[lane][0] >> 32)) : 0.f;
-    Combined t = {};
-    t.code = __reduce_max_sync(0xFFFFFFFFu, mine ? static_cast<int>(part[lane][1]) : 0);
-    HeadSums h = {};
-    if (mine) {
-      Df* d[4] = {&h.e, &h.q, &h.qx, &h.ex};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t u = head_part[lane][i];
-        *d[i] = Df{__uint_as_float(static_cast<uint32_t>(u)),
-                   __uint_as_float(static_cast<uint32_t>(u >> 32))};
-      }
-    }
-    if (a.cluster > 1) h = warp_sum(h, 4);
-    float M = fmaxf(hmax, mi);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    // a part of -inf alone has sum 0, one with a NaN has NaN
-    if (mi != -INFINITY) rest *= ex2_approx((mi - M) * k2);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-    t.M = __shfl_sync(0xFFFFFFFFu, M, 0);
-    t.rest = __shfl_sync(0xFFFFFFFFu, rest, 0);
-    t.h = HeadSums{bcast(h.e), bcast(h.q), bcast(h.qx), bcast(h.ex)};
-    return t;
-  };
-  const float nan = __int_as_float(0x7FC00000);
-  auto write_loss = [&](const Combined& t) {
-    const RowLoss v = row_loss(a, t.M, hmax, t.rest, t.h);
+    m = __shfl_sync(0xFFFFFFFFu, m, 0);
+    sum = __shfl_sync(0xFFFFFFFFu, sum, 0);
+    if (lane < head_warps) hs = red[lane];
+    if (head_warps > 1) hs = warp_sum(hs, 8);
+    hs = HeadSums{bcast(hs.e), bcast(hs.q), bcast(hs.qx), bcast(hs.ex)};
+    M = fmaxf(hmax, m);
+    if (m != -INFINITY) sum *= ex2_approx((m - M) * k2);
     if (lane == 0) {
-      if (t.code != 0)
-        set_status(a.status, t.code);
-      else if (!(isfinite(v.lse) && isfinite(v.loss)))
-        set_status(a.status, TIM_ERR_NONFINITE);
-      a.loss[row] = t.code != 0 ? nan : v.loss;
-      if constexpr (!kGrad) a.lse[row] = t.code != 0 ? nan : v.lse;
-    }
-  };
-  if (warp == 0) {
-    const Combined t = combine();
-    if (lane == 0) {
-      RowConstants c = row_constants(a, t.M, hmax, t.rest, t.h);
-      if (t.code != 0) c.c_rest = c.c_head = nan;
+      RowConstants c = row_constants(a, M, hmax, sum, hs);
+      if (s_bad != 0) c.c_rest = c.c_head = nan;
       s_terms = c;
-      s_M = t.M;
+      s_M = M;
       if constexpr (!kGrad) {
         float* saved = a.saved + row * TIM_DISTILL_SAVED;
-        saved[kMax] = t.M;
+        saved[kMax] = M;
         saved[kInvSum] = c.inv;
         saved[kLogSum] = c.logS;
         saved[kRest] = c.c_rest;
         saved[kHead] = c.c_head;
-        saved[kLive] = t.code != 0 ? nan : 1.f;
+        saved[kLive] = s_bad != 0 ? nan : 1.f;
         saved[kLive + 1] = saved[kLive + 2] = 0.f;
       }
     }
     __syncwarp();
-    if (!kGrad) write_loss(t);
   }
-  if constexpr (!kGrad) return;
-
-  // ---- the gradient, from the slice in shared memory
-  __syncthreads();
-  const float w = __ldg(a.grad + row);
-  const float g = w * a.inv_h;
-  const RowConstants t = s_terms;
-  const float M = s_M;
-  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
-  if (w == 0.f) {
-    const float zeros[E::kVec] = {};
-    for (int j = tid; j < s.n; j += kThreads) store_vector<kDtype>(out, r, s.j0 + j, same, zeros);
-    if (rank == 0 && warp == 0) write_loss(combine());
-    return;
+  if (kGrad) __syncthreads();
+  if (warp == 0) {  // nothing waits for the loss
+    const RowLoss v = row_loss(a, M, hmax, sum, hs);
+    if (lane == 0) {
+      if (s_bad != 0)
+        set_status(a.status, s_bad);
+      else if (!(isfinite(v.lse) && isfinite(v.loss)))
+        set_status(a.status, TIM_ERR_NONFINITE);
+      a.loss[row] = s_bad != 0 ? nan : v.loss;
+      if constexpr (!kGrad) a.lse[row] = s_bad != 0 ? nan : v.lse;
+    }
   }
-  const float c = t.c_rest * t.inv * g;
-  const F2 ref = f2(-M, -M), kk = f2(k2, k2), cc = f2(c, c);
-  int j0 = 0, j1 = 0;  // the vectors that are one store each
-  if (same && s.n > 0) {
-    j0 = r.whole(s.j0) ? 0 : 1;
-    j1 = max(j0, r.whole(s.j0 + s.n - 1) ? s.n : s.n - 1);
-  }
-  uint4* const to = reinterpret_cast<uint4*>(out - r.shift + static_cast<int64_t>(s.j0) * E::kVec);
-#pragma unroll 4
-  for (int j = j0 + tid; j < j1; j += kThreads) {
-    float v[E::kVec];
-    E::unpack(slice_mem[j], v);
-    gradient_vector(v, ref, kk, cc);
-    to[j] = E::pack(v);
-  }
-  // the others: the row's ends, or all where the output lies otherwise
-  auto store_edge = [&](int j) {
-    float v[E::kVec];
-    E::unpack(slice_mem[j], v);
-    gradient_vector(v, ref, kk, cc);
-    store_vector<kDtype>(out, r, s.j0 + j, same, v);
-  };
-  if (tid < j0) store_edge(tid);
-  for (int j = j1 + tid; j < s.n; j += kThreads) store_edge(j);
-  if (rank == 0 && warp == warps - 1) write_loss(combine());  // nothing waits for the loss
-  __syncthreads();  // the head's tokens are written again, after the whole slice
-  for_head([&](int id, float lq, float z) {
-    const int slot = id + r.shift - s.j0 * E::kVec;
-    if (slot >= 0 && slot < s.n * E::kVec)
+  if constexpr (kGrad) {
+    const float w = __ldg(a.grad + row), g = w * a.inv_h;
+    const RowConstants t = s_terms;
+    gradient_slice<kDtype, kThreads>(a, r, Slice{0, nvec}, out, s_M, t.c_rest * t.inv * g, w == 0.f);
+    if (w == 0.f) return;
+    __syncthreads();  // the head's tokens are written again, after the whole row
+    M = s_M;
+    for_head([&](int id, float lq, float z) {
       out[id] = E::narrow(head_gradient(a, z, lq, M, t.logS, t.inv, t.c_head) * g);
-  });
+    });
+  }
 }
 
 // The gradient alone, from what the forward saved: a CTA a slice of a row, reading and writing
 // it once; the head's tokens are written again after the slice.
-constexpr int kBackUnroll = 4;  // vectors of a thread in flight
 template <int kDtype>
 __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const DistillArgs a) {
   using E = Elem<kDtype>;
   using raw = typename E::raw;
-  const int64_t row = blockIdx.x / a.cluster;
+  const int64_t row = blockIdx.x / a.parts;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
-  const Slice s = slice_of(r.nvec(), blockIdx.x % a.cluster, a.cluster);
+  const Slice s = slice_of(r.nvec(), blockIdx.x % a.parts, a.parts);
   raw* out = static_cast<raw*>(a.dlogits) + row * a.ldd;
-  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
   const float* saved = a.saved + row * TIM_DISTILL_SAVED;
   const float w = __ldg(a.grad + row), live = saved[kLive], g = w * a.inv_h;
   const bool zero = live == 0.f || w == 0.f;
-  const float k2 = a.kh;
   const float M = saved[kMax], inv = saved[kInvSum];
-  const float c = live * saved[kRest] * inv * g;  // NaN for a row the forward refused
-  for (int j0 = threadIdx.x; j0 < s.n; j0 += kBackUnroll * kBackThreads) {
-    uint4 u[kBackUnroll];
-#pragma unroll
-    for (int n = 0; n < kBackUnroll; ++n) {
-      const int j = j0 + n * kBackThreads;
-      if (!zero && j < s.n) u[n] = r.load(s.j0 + j);
-    }
-#pragma unroll
-    for (int n = 0; n < kBackUnroll; ++n) {
-      const int j = j0 + n * kBackThreads;
-      if (j >= s.n) break;
-      float v[E::kVec];
-      if (zero) {
-#pragma unroll
-        for (int i = 0; i < E::kVec; ++i) v[i] = 0.f;
-      } else {
-        E::unpack(u[n], v);
-        gradient_vector(v, f2(-M, -M), f2(k2, k2), f2(c, c));
-      }
-      store_vector<kDtype>(out, r, s.j0 + j, same, v);
-    }
-  }
+  // NaN for a row the forward refused
+  gradient_slice<kDtype, kBackThreads>(a, r, s, out, M, live * saved[kRest] * inv * g, zero);
   if (zero || live != live) return;
   __syncthreads();
   const float logS = saved[kLogSum];
@@ -591,29 +517,23 @@ void set_temperature(DistillArgs& a, float temperature) {
   a.inv_l = static_cast<float>(inv - static_cast<double>(a.inv_h));
 }
 
-template <int kDtype, bool kGrad, int kThreads>
-cudaError_t launch_rows(const DistillArgs& a, int64_t T, const RowPlan& p, cudaStream_t stream) {
-  const size_t smem = p.slice_bytes + p.slice_bytes / 16 + 16;  // the slice and its marks
-  auto* kernel = distill_kernel<kDtype, kGrad, kThreads>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int kDtype, bool kGrad>
+cudaError_t launch_rows(const DistillArgs& a, int64_t T, cudaStream_t stream) {
+  const size_t smem = (static_cast<size_t>(a.V) * sizeof(typename Elem<kDtype>::raw) / 16 + 2 + 31) / 16 * 16;
+  cudaError_t e = cudaFuncSetAttribute(distill_kernel<kDtype, kGrad>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_clusters(kernel, T, p.cluster, kThreads, smem, stream, a);
-}
-template <int kDtype, bool kGrad>
-cudaError_t launch_rows(DistillArgs a, int64_t T, cudaStream_t stream) {
-  const RowPlan p = plan_row(a.V, sizeof(typename Elem<kDtype>::raw));
-  a.cluster = p.cluster;
-  return p.threads == 256 ? launch_rows<kDtype, kGrad, 256>(a, T, p, stream)
-                          : launch_rows<kDtype, kGrad, 512>(a, T, p, stream);
+  distill_kernel<kDtype, kGrad><<<static_cast<unsigned>(T), kRowThreads<kGrad>, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <int kDtype>
 cudaError_t launch_back(DistillArgs a, int64_t T, cudaStream_t stream) {
-  a.cluster = plan_row(a.V, sizeof(typename Elem<kDtype>::raw)).cluster;
-  if (T * a.cluster > INT32_MAX) return cudaErrorInvalidValue;
+  a.parts = plan_row(a.V, sizeof(typename Elem<kDtype>::raw)).cluster;
+  if (T * a.parts > INT32_MAX) return cudaErrorInvalidValue;
   distill_backward_kernel<kDtype>
-      <<<static_cast<unsigned>(T * a.cluster), kBackThreads, 0, stream>>>(a);
+      <<<static_cast<unsigned>(T * a.parts), kBackThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
