@@ -85,7 +85,7 @@ size_t diag_workspace_bytes(int64_t T, int n_seq);
 cudaError_t launch_sample(const void* logits, int dtype, int64_t ld, int64_t T, int V,
                           const float* uniform, const tim_sample_params& p, int32_t* ids,
                           float* logprob, float* lse, int32_t* kept, int* status,
-                          cudaStream_t stream);
+                          cudaStream_t stream, int num_sms);
 cudaError_t launch_distill(const void* logits, int dtype, int64_t ld, int64_t T, int V,
                            const int32_t* ids, const float* lp, int K, float temperature, int kind,
                            int tail, float* loss, float* lse, float* saved, int* status,
@@ -858,10 +858,11 @@ tim_status tim_sample(const void* logits, int32_t dtype, int64_t ld, int64_t T, 
   if (p.row_top_p == nullptr && !(p.top_p > 0.f)) return TIM_ERR_INVALID_ARG;
   if (p.row_min_p == nullptr && !(p.min_p >= 0.f && p.min_p <= 1.f)) return TIM_ERR_INVALID_ARG;
   if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
-  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  int sms = 0;
+  if ((s = check_device(&sms)) != TIM_OK) return s;
   return from_cuda(launch_sample(logits, dtype, ld, T, V, uniform, p, out_ids, out_logprob,
                                  out_lse_kept, out_kept, static_cast<int*>(workspace),
-                                 reinterpret_cast<cudaStream_t>(stream)));
+                                 reinterpret_cast<cudaStream_t>(stream), sms));
 }
 
 tim_status tim_distill(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,

@@ -253,20 +253,30 @@ inline RowPlan plan_row(int V, int elem_bytes) {
 // T rows, a cluster of `cluster` CTAs each.
 template <class Args>
 inline cudaError_t launch_clusters(void (*kernel)(const Args), int64_t T, int cluster, int threads,
-                                   size_t smem, cudaStream_t stream, const Args& a) {
+                                   size_t smem, cudaStream_t stream, const Args& a,
+                                   bool programmatic = false) {
   if (T * cluster > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (programmatic) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -414,11 +424,12 @@ static __device__ const Pow2Table g_pow2_table = make_pow2_table();
 
 // 2^((z - c) K) as a pair of floats; 0 below 2^-126, so that the caller need not care about
 // pow2_fixed's range.  (z - c) K must be at most 100.
-__device__ __forceinline__ Df pow2_df(float z, const Pow2Row& k) {
+__device__ __forceinline__ Df pow2_df(float z, const Pow2Row& k,
+                                      const unsigned long long* table = g_pow2_table.t) {
   const float x = (k.recentre ? z - k.c : z) * k.kh;
   if (!(x > -126.f)) return {x <= -126.f ? 0.f : __int_as_float(0x7FC00000), 0.f};  // NaN stays
   int n;
-  const unsigned long long w = pow2_fixed(z, k, g_pow2_table.t, n);
+  const unsigned long long w = pow2_fixed(z, k, table, n);
   // the top 48 of w's 62 or 63 bits, 24 in each part
   const float scale = __int_as_float((n + 127) << 23);
   const float h = static_cast<float>(static_cast<uint32_t>(w >> 39)) * (scale * 0x1p-23f);
@@ -427,18 +438,18 @@ __device__ __forceinline__ Df pow2_df(float z, const Pow2Row& k) {
 }
 
 // e^x
-__device__ __forceinline__ Df exp_df(float x) {
-  return pow2_df(x, Pow2Row{kLog2eHi, kLog2eLo, 0.f, false});
+__device__ __forceinline__ Df exp_df(float x, const unsigned long long* table = g_pow2_table.t) {
+  return pow2_df(x, Pow2Row{kLog2eHi, kLog2eLo, 0.f, false}, table);
 }
 
 // ln a for a positive finite a: l = ln of the leading bits in fp32, then
 // ln a = l + ln(a e^-l) with the small second term from its series.
-__device__ __forceinline__ Df log_df(Df a) {
+__device__ __forceinline__ Df log_df(Df a, const unsigned long long* table = g_pow2_table.t) {
   const int e = static_cast<int>(__float_as_uint(a.h) >> 23) - 127;  // subnormals are not met
   const float s = __int_as_float((127 - e) << 23);
   const Df f = {a.h * s, a.l * s};
   const float l = __logf(f.h);
-  const Df r = f * exp_df(-l) - df(1.f);
+  const Df r = f * exp_df(-l, table) - df(1.f);
   const Df ln = df(l) + renorm(r.h, r.l - 0.5f * r.h * r.h);
   return Df{kLn2Hi, kLn2Lo} * df(static_cast<float>(e)) + ln;
 }
