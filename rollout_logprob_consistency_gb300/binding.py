@@ -745,7 +745,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, o
 
     def call(sp):
         o = out
-        if o is None:
+        if o is None:  # views of one allocation would take the host longer than four
             o = (torch.empty(T, dtype=i32, device=dev), torch.empty(T, dtype=f32, device=dev),
                  torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=i32, device=dev))
         ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)

@@ -313,6 +313,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
     return;
   }
   // the first vectors are on their way while the head is done
+  const uint4* const vec = r.vec();
+  const int w1 = r.w1();
   uint4 u[U];
 #pragma unroll
   for (int n = 0; n < U; ++n) {
@@ -369,7 +371,10 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
 #pragma unroll
       for (int n = 0; n < U; ++n) {
         const int j = j0 + (U + n) * kThreads;
-        if (j < nvec) w[n] = r.load(j);
+        if (j < w1)
+          w[n] = __ldg(vec + j);
+        else if (j < nvec)
+          w[n] = r.load_edge(j);
       }
 #pragma unroll
       for (int n = 0; n < U; ++n) {
@@ -519,11 +524,13 @@ void set_temperature(DistillArgs& a, float temperature) {
 
 template <int kDtype, bool kGrad>
 cudaError_t launch_rows(const DistillArgs& a, int64_t T, cudaStream_t stream) {
-  const size_t smem = (static_cast<size_t>(a.V) * sizeof(typename Elem<kDtype>::raw) / 16 + 2 + 31) / 16 * 16;
-  cudaError_t e = cudaFuncSetAttribute(distill_kernel<kDtype, kGrad>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  auto marks = [](int64_t V) {
+    return static_cast<size_t>(V * sizeof(typename Elem<kDtype>::raw) / 16 + 2 + 31) / 16 * 16;
+  };
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(distill_kernel<kDtype, kGrad>, marks(TIM_LOGITS_MAX_V), allowed);
   if (e != cudaSuccess) return e;
+  const size_t smem = marks(a.V);
   distill_kernel<kDtype, kGrad><<<static_cast<unsigned>(T), kRowThreads<kGrad>, smem, stream>>>(a);
   return cudaGetLastError();
 }

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "tim_common.cuh"
@@ -126,7 +127,27 @@ struct Row {
     return E::pack(v);
   }
   __device__ __forceinline__ float at(int i) const { return E::widen(p[i]); }
+  // vector j itself, and the vectors w0 <= j < w1 that are whole
+  __device__ __forceinline__ const uint4* vec() const {
+    return reinterpret_cast<const uint4*>(p - shift);
+  }
+  __device__ __forceinline__ int w0() const { return shift != 0 ? 1 : 0; }
+  __device__ __forceinline__ int w1() const { return (shift + V) / E::kVec; }
 };
+
+// Lets a kernel use `bytes` of dynamic shared memory, once a device: `done` has a bit for each.
+template <class Kernel>
+inline cudaError_t allow_smem(Kernel* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---------------------------------------------------------------------------
 // Two fp32 operations in one instruction.

@@ -14,7 +14,7 @@
 // sums are exact in that scale and do not depend on the order or the split.
 //
 // This kernel decides the rows that few tokens decide, one CTA a row, reading it once: while
-// it streams, every thread keeps the largest logits of four blocks of its vectors (and, for
+// it streams, every thread notes the largest logits of blocks of its vectors (and, for
 // top-p alone, a running sum in fp32).  They bound the tokens that can be kept:
 //  - the k-th largest of the threads' (or groups of threads') maxima is met by every top-k
 //    logit, they being k different logits;
@@ -37,18 +37,24 @@ namespace {
 
 constexpr int kCap = 1024;     // tokens of the list
 constexpr int kListK = 256;    // largest top-k that the list serves
-constexpr int kCount = 256;    // orders by counting up to here
+constexpr int kBins = 256;
+constexpr int kCount = 512;    // orders by counting up to here
 constexpr int kUnroll = 4;     // vectors of a thread in flight, and as many being looked at
-constexpr int kBlocks = 4;     // maxima a thread keeps
+constexpr int kMaxima = 5120;  // of blocks of the row, kept while it streams
 constexpr float kSumError = 0x1p-16f;  // of the fp32 sum, see its place
 
 template <int kThreads>
 struct Shared {
   u64 table[256];
-  u64 key[kCap];  // key << 32 | ~id: larger comes first
-  u64 w[kCap];
-  uint32_t group[kThreads];
-  uint16_t item[kThreads * kBlocks];  // blocks to be read again: thread * kBlocks + block
+  union {
+    float top[kMaxima];  // of block b of thread t: top[b kThreads + t]
+    struct {
+      u64 key[kCap];  // key << 32 | ~id: larger comes first
+      u64 w[kCap];
+    };
+  };
+  uint32_t group[kThreads > kBins ? kThreads : kBins];
+  uint16_t item[kCap];  // blocks to be read again: the places of their maxima
   u64 warp[kThreads / 32];
   uint32_t warpu[kThreads / 32];
   float warpf[kThreads / 32];
@@ -81,17 +87,30 @@ template <int kThreads>
 __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>& sh, int64_t row,
                        float u, int n, int k, float top_p, uint32_t kmin, bool complete,
                        float sum) {
-  constexpr int kPer = kCap / kThreads > 0 ? kCap / kThreads : 1;
+  constexpr int kRank = kCount > kThreads ? kCount / kThreads : 1;
   const int tid = threadIdx.x, lane = tid & 31;
   if (n <= kCount) {
-    const int each = sharers<kThreads>(n), i = tid / each;
-    const u64 mine = i < n ? sh.key[i] : 0;
-    int at = 0;
-    if (i < n)
-      for (int j = tid & (each - 1); j < n; j += each) at += sh.key[j] > mine ? 1 : 0;
-    for (int o = 1; o < each; o <<= 1) at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
+    const int each = sharers<kThreads>(n), first = tid / each;
+    u64 mine[kRank];
+    int at[kRank];
+#pragma unroll
+    for (int q = 0; q < kRank; ++q) {
+      const int i = first + q * kThreads;
+      mine[q] = i < n ? sh.key[i] : 0;
+      at[q] = 0;
+    }
+    if ((tid - lane) / each < n) {
+      for (int j = tid & (each - 1); j < n; j += each) {
+        const u64 x = sh.key[j];
+#pragma unroll
+        for (int q = 0; q < kRank; ++q) at[q] += x > mine[q] ? 1 : 0;
+      }
+    }
+    for (int o = 1; o < each; o <<= 1) at[0] += __shfl_xor_sync(0xFFFFFFFFu, at[0], o);
     __syncthreads();
-    if (i < n && (tid & (each - 1)) == 0) sh.key[at] = mine;
+#pragma unroll
+    for (int q = 0; q < kRank; ++q)
+      if (first + q * kThreads < n && (tid & (each - 1)) == 0) sh.key[at[q]] = mine[q];
   } else {
     int n2 = 2 * kCount;
     while (n2 < n) n2 <<= 1;
@@ -102,19 +121,16 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
   if (tid == 0) sh.count_lo = sh.count_hi = 0;
   __syncthreads();
   if (k > 0) n = min(n, k);
-  // weights in order, kPer a thread, and their running sum
-  u64 w[kPer], part = 0;
-  uint32_t key[kPer];
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = tid * kPer + q;
-    key[q] = i < n ? static_cast<uint32_t>(sh.key[i] >> 32) : 0u;
-    w[q] = i < n ? weight(key_value(key[q]), st, sh.table) : 0;
-    part += w[q];
-    if (i < n) sh.w[i] = w[q];
+  // weights in order, and their running sum: a thread has `per` of them in a row
+  const int per = (n + kThreads - 1) / kThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  u64 part = 0;
+  for (int i = i0; i < i1; ++i) {
+    const u64 w = weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
+    sh.w[i] = w;
+    part += w;
   }
   u64 total;
-  u64 before = block_scan<kThreads>(part, sh.warp, (n + 32 * kPer - 1) / (32 * kPer), total);
+  u64 before = block_scan<kThreads>(part, sh.warp, (n + 32 * per - 1) / (32 * per), total);
   u64 lo = ~0ull, hi = ~0ull;  // top-p keeps a token while the sum before it is below
   if (top_p < 1.f) {
     if (sum > 0.f) {
@@ -131,16 +147,13 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
     }
   }
   int c_lo = 0, c_hi = 0;
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    if (tid * kPer + q < n) {
-      const bool min_ok = key[q] >= kmin;
-      c_lo += before < lo && min_ok ? 1 : 0;
-      c_hi += before < hi && min_ok ? 1 : 0;
-    }
-    before += w[q];
+  for (int i = i0; i < i1; ++i) {
+    const bool min_ok = static_cast<uint32_t>(sh.key[i] >> 32) >= kmin;
+    c_lo += before < lo && min_ok ? 1 : 0;
+    c_hi += before < hi && min_ok ? 1 : 0;
+    before += sh.w[i];
   }
-  if ((tid - lane) * kPer < n) {  // this warp has tokens
+  if ((tid - lane) * per < n) {  // this warp has tokens
     c_lo = __reduce_add_sync(0xFFFFFFFFu, c_lo);
     c_hi = __reduce_add_sync(0xFFFFFFFFu, c_hi);
     if (lane == 0 && (c_lo | c_hi) != 0) {
@@ -154,22 +167,34 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
   // the draw, by id
   if (m <= kCount) {
     // what the kept tokens of lower ids weigh
-    const int each = sharers<kThreads>(m), i = tid / each;
+    const int each = sharers<kThreads>(m), first = tid / each;
     if ((tid - lane) / each >= m) return true;  // a warp without tokens
-    const int id = i < m ? static_cast<int>(~static_cast<uint32_t>(sh.key[i])) : -1;
-    u64 kept = 0, below = 0;
+    int id[kRank];
+    u64 kept = 0, below[kRank];
+#pragma unroll
+    for (int q = 0; q < kRank; ++q) {
+      const int i = first + q * kThreads;
+      id[q] = i < m ? static_cast<int>(~static_cast<uint32_t>(sh.key[i])) : -1;
+      below[q] = 0;
+    }
     for (int j = tid & (each - 1); j < m; j += each) {
-      const u64 wj = sh.w[j];
-      kept += wj;
-      below += static_cast<int>(~static_cast<uint32_t>(sh.key[j])) < id ? wj : 0;
+      const u64 w = sh.w[j];
+      const int other = static_cast<int>(~static_cast<uint32_t>(sh.key[j]));
+      kept += w;
+#pragma unroll
+      for (int q = 0; q < kRank; ++q) below[q] += other < id[q] ? w : 0;
     }
     for (int o = 1; o < each; o <<= 1) {
       kept += __shfl_xor_sync(0xFFFFFFFFu, kept, o);
-      below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
+      below[0] += __shfl_xor_sync(0xFFFFFFFFu, below[0], o);
     }
     const u64 target = draw_target(kept, u);
-    if (i < m && (tid & (each - 1)) == 0 && below <= target && target < below + sh.w[i])
-      write_row(a, st, sh.table, row, id, key_value(static_cast<uint32_t>(sh.key[i] >> 32)), kept, m);
+#pragma unroll
+    for (int q = 0; q < kRank; ++q) {
+      const int i = first + q * kThreads;
+      if (i < m && (tid & (each - 1)) == 0 && below[q] <= target && target < below[q] + sh.w[i])
+        write_row(a, st, sh.table, row, id[q], key_value(static_cast<uint32_t>(sh.key[i] >> 32)), kept, m);
+    }
     return true;
   }
   // sorted once more, by id: the low word on top descends as the id ascends
@@ -181,37 +206,34 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
   }
   __syncthreads();
   sort_desc<kThreads>(sh.key, n2);
+  const int each = (m + kThreads - 1) / kThreads, j0 = min(m, tid * each), j1 = min(m, j0 + each);
   part = 0;
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = tid * kPer + q;
-    w[q] = i < m ? weight(key_value(static_cast<uint32_t>(sh.key[i])), st, sh.table) : 0;
-    part += w[q];
-  }
-  before = block_scan<kThreads>(part, sh.warp, (m + 32 * kPer - 1) / (32 * kPer), total);
+  for (int i = j0; i < j1; ++i)
+    part += weight(key_value(static_cast<uint32_t>(sh.key[i])), st, sh.table);
+  before = block_scan<kThreads>(part, sh.warp, (m + 32 * each - 1) / (32 * each), total);
   const u64 target = draw_target(total, u);
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    if (before <= target && target < before + w[q]) {
-      const u64 x = sh.key[tid * kPer + q];
+  for (int i = j0; i < j1; ++i) {
+    const u64 x = sh.key[i], w = weight(key_value(static_cast<uint32_t>(x)), st, sh.table);
+    if (before <= target && target < before + w)
       write_row(a, st, sh.table, row, static_cast<int>(~static_cast<uint32_t>(x >> 32)),
                 key_value(static_cast<uint32_t>(x)), total, m);
-    }
-    before += w[q];
+    before += w;
   }
   return true;
 }
 
 template <int kDtype, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    sample_list_kernel(const SampleArgs a) {
   using E = Elem<kDtype>;
   constexpr int kWarps = kThreads / 32;
   __shared__ Shared<kThreads> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
+  pdl_launch_dependents();  // the wide kernel's CTAs may come as these go; it waits for all of them
   const Settings set = settings_of(a, row);
-  const bool list_k = set.k > 0 && set.k <= kListK && set.k <= kThreads * 3 / 4;
+  const bool list_k = set.k > 0 && set.k <= kListK;
   const bool need_sum = set.k == 0 && set.top_p < 1.f;
   const bool list_min = set.min_p > 0.f && set.top_p >= 1.f;
   if (set.bad == 0 && !list_k && !need_sum && !list_min) {
@@ -226,9 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(
   // ---- one pass: the largest logit of each of the thread's blocks, and the fp32 sum
   const int nvec = r.nvec();
   const int steps = (nvec + kThreads - 1) / kThreads;  // vectors of a thread
-  // steps of a block: whole groups of kUnroll
-  const int block = ((steps + kBlocks - 1) / kBlocks + kUnroll - 1) / kUnroll * kUnroll;
-  float top[kBlocks], tmax = -INFINITY, run = -INFINITY;
+  // steps of a block: whole groups of kUnroll, as few as there is room for their maxima
+  const int block = (steps + kMaxima / kThreads * kUnroll - 1) / (kMaxima / kThreads * kUnroll) * kUnroll;
+  const int blocks = (steps + block - 1) / block;
+  float tmax = -INFINITY, run = -INFINITY;
   // The sum is relative to the thread's running maximum.  A term's argument carries two roundings
   // of 2^-24 and the remainder of K, 2^-25 (together below 4.1e-6 of the term for 40 octaves;
   // terms further down are below 2^-40 of the largest), its exponential 2^-22; the partial sums
@@ -236,60 +259,80 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(
   // the threads' sums 2^-22, the product in decide() 2^-21: together below kSumError = 1.5e-5.
   F2 acc = f2(0.f, 0.f), acc2 = acc;
   const F2 kk = f2(st.pw.kh, st.pw.kh);
+  // The row's first and last vectors may be partly others': the first is loaded apart, the last
+  // counts in after the loop.
+  const uint4* const vec = r.vec();
+  const int w1 = r.w1();
   uint4 x[kUnroll];
 #pragma unroll
-  for (int n = 0; n < kUnroll; ++n) x[n] = tid + n * kThreads < nvec ? r.load(tid + n * kThreads) : neg_inf_vec<kDtype>();
+  for (int n = 0; n < kUnroll; ++n) {
+    const int j = tid + n * kThreads;
+    x[n] = j < w1 ? (j >= r.w0() ? __ldg(vec + j) : r.load_edge(j)) : neg_inf_vec<kDtype>();
+  }
+  auto add_vec = [&](const uint4& u, F2 ref) {
+    float v[E::kVec];
+    E::unpack(u, v);
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) {
+    for (int q = 0; q < E::kVec; q += 4) {
+      acc = add2(acc, ex2x2(mul2(add2(f2(v[q], v[q + 1]), ref), kk)));
+      acc2 = add2(acc2, ex2x2(mul2(add2(f2(v[q + 2], v[q + 3]), ref), kk)));
+    }
+  };
+  auto raise = [&](float most) {
+    if (most > run) {
+      const float f = ex2_approx((run - most) * st.pw.kh);
+      acc = mul2(acc, f2(f, f));
+      acc2 = mul2(acc2, f2(f, f));
+      run = most;
+    }
+    const float from = run == -INFINITY ? 0.f : -run;
+    return f2(from, from);
+  };
+  for (int b = 0; b < blocks; ++b) {
     float bmax = -INFINITY;
-    for (int i = b * block; i < min(steps, (b + 1) * block); i += kUnroll) {
+    const int end = min(steps, (b + 1) * block);
+    for (int i = b * block; i < end; i += kUnroll) {
       uint4 y[kUnroll];
+      const int j0 = tid + (i + kUnroll) * kThreads;
 #pragma unroll
-      for (int n = 0; n < kUnroll; ++n) {
-        const int j = tid + (i + kUnroll + n) * kThreads;
-        y[n] = j < nvec ? r.load(j) : neg_inf_vec<kDtype>();
-      }
+      for (int n = 0; n < kUnroll; ++n)
+        y[n] = j0 + n * kThreads < w1 ? __ldg(vec + j0 + n * kThreads) : neg_inf_vec<kDtype>();
       uint4 m = x[0];
 #pragma unroll
       for (int n = 1; n < kUnroll; ++n) m = max_vec<kDtype>(m, x[n]);
       const float most = max_of<kDtype>(m);
       bmax = max_nan(bmax, most);
       if (need_sum) {
-        if (most > run) {
-          const float f = ex2_approx((run - most) * st.pw.kh);
-          acc = mul2(acc, f2(f, f));
-          acc2 = mul2(acc2, f2(f, f));
-          run = most;
-        }
-        const float from = run == -INFINITY ? 0.f : -run;
-        const F2 ref = f2(from, from);
+        const F2 ref = raise(most);
 #pragma unroll
-        for (int n = 0; n < kUnroll; ++n) {
-          float v[E::kVec];
-          E::unpack(x[n], v);
-#pragma unroll
-          for (int q = 0; q < E::kVec; q += 4) {
-            acc = add2(acc, ex2x2(mul2(add2(f2(v[q], v[q + 1]), ref), kk)));
-            acc2 = add2(acc2, ex2x2(mul2(add2(f2(v[q + 2], v[q + 3]), ref), kk)));
-          }
-        }
+        for (int n = 0; n < kUnroll; ++n) add_vec(x[n], ref);
       }
 #pragma unroll
       for (int n = 0; n < kUnroll; ++n) x[n] = y[n];
     }
-    top[b] = bmax;
+    sh.top[b * kThreads + tid] = bmax;
     tmax = max_nan(tmax, bmax);
+  }
+  if (w1 < nvec && tid == w1 % kThreads) {
+    const uint4 u = r.load_edge(w1);
+    const float most = max_of<kDtype>(u);
+    float& t = sh.top[w1 / kThreads / block * kThreads + tid];
+    t = max_nan(t, most);
+    tmax = max_nan(tmax, most);
+    if (need_sum) add_vec(u, raise(most));
   }
   // ---- the row's largest
   const uint32_t mykey = !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
   uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, mykey);
   if (lane == 0) sh.warpu[warp] = hi;
-  // The k-th largest is looked for among groups of 2^shift threads, at least twice as many as k
-  // where there are: about 1.4 k tokens then meet it, and a group's threads share its count.
+  // The k-th largest is looked for among groups of 2^shift threads, at least twice as many as k:
+  // about 1.4 k tokens then meet it, and a group's threads share its count.  Where there are not
+  // that many threads, among all blocks, by a histogram.
   int shift = 5;
   while (shift > 0 && (kThreads >> shift) < 2 * set.k) --shift;
   const int each = 1 << shift;
-  if (list_k) {
+  const bool by_group = list_k && (kThreads >> shift) >= 2 * set.k;
+  if (by_group) {
     uint32_t g = mykey;
     for (int o = 1; o < each; o <<= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
     if ((tid & (each - 1)) == 0) sh.group[tid >> shift] = g;
@@ -319,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(
   // ---- the list holds all tokens from the key `bound` up
   const uint32_t kmin = min_p_key(M, set.tau, set.min_p);
   uint32_t bound = list_min ? kmin : kNegInfKey + 1;
-  if (list_k) {
+  if (by_group) {
     const int groups = kThreads >> shift, g = tid >> shift;
     const uint32_t mine = sh.group[g];
     int before = 0;
@@ -329,6 +372,47 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(
     }
     for (int o = 1; o < each; o <<= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     if (before == set.k - 1) sh.bound = mine;
+    __syncthreads();
+    bound = max(bound, sh.bound);
+  } else if (list_k) {
+    // in 256 bins from the largest logit down, over as much as the threads' maxima span, 64 octaves
+    // or units at most; a logit further down is in the last bin, which bounds nothing
+    for (int i = tid; i < kBins; i += kThreads) sh.group[i] = 0;
+    uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, mykey > kNegInfKey ? mykey : 0xFFFFFFFFu);
+    if (lane == 0) sh.warpu[warp] = lo;
+    __syncthreads();
+    lo = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? sh.warpu[lane] : 0xFFFFFFFFu);
+    const float range = fminf(M - key_value(lo), fmaxf(64.f, 64.f / st.pw.kh));
+    const float per_bin = range * (1.f / 254.f), inv = per_bin > 0.f ? 1.f / per_bin : 0.f;
+    for (int b = 0; b < blocks; ++b) {
+      const float t = sh.top[b * kThreads + tid];
+      if (t > -INFINITY) atomicAdd(&sh.group[static_cast<int>(fminf((M - t) * inv, 255.f))], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // a lane has eight bins; the first at which k maxima are reached
+      uint32_t count[8], part = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part += count[i] = sh.group[lane * 8 + i];
+      uint32_t at = part;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        if (lane >= o) at += up;
+      }
+      at -= part;
+      const uint32_t k = static_cast<uint32_t>(set.k);
+      if (lane == 0) sh.bound = kNegInfKey + 1;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int bin = lane * 8 + i;
+        // every maximum of the bins up to this one is above its lower end
+        if (at < k && k <= at + count[i] && bin < 255)
+          sh.bound = max(key_of(M - (static_cast<float>(bin) + 1.01f) * per_bin), kNegInfKey + 1);
+        at += count[i];
+      }
+    }
     __syncthreads();
     bound = max(bound, sh.bound);
   } else if (need_sum) {
@@ -342,50 +426,56 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(
   if (done) {
     // the blocks to be read again
     const float least = key_value(bound);
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const bool again = top[b] >= least;
+    for (int b = 0; b < blocks; ++b) {
+      const bool again = tmax >= least && sh.top[b * kThreads + tid] >= least;
       const unsigned who = __ballot_sync(0xFFFFFFFFu, again);
+      if (who == 0) continue;
       int at = 0;
-      if (lane == 0 && who != 0) at = atomicAdd(&sh.items, __popc(who));
-      at = __shfl_sync(0xFFFFFFFFu, at, 0);
-      if (again) sh.item[at + __popc(who & ((1u << lane) - 1u))] = static_cast<uint16_t>(tid * kBlocks + b);
+      if (lane == 0) at = atomicAdd(&sh.items, __popc(who));
+      at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1u));
+      if (again && at < kCap) sh.item[at] = static_cast<uint16_t>(b * kThreads + tid);
     }
     __syncthreads();
     const int items = sh.items <= kCap ? sh.items : 0;  // a block has a token at least
     if (tid == 0 && sh.items > kCap) sh.n = kCap + 1;
-    // a warp takes eight vectors of four blocks at a time
-    constexpr int kAtOnce = 4;
-    for (int i0 = warp * kAtOnce; i0 < items; i0 += kWarps * kAtOnce) {
-      const int i = i0 + (lane >> 3);
-      if (i < items) {
-        const int it = sh.item[i], t = it / kBlocks, b = it % kBlocks;
-        // nothing more is looked for once the list is full
-        const int end = *static_cast<volatile int*>(&sh.n) > kCap ? 0 : min(steps, (b + 1) * block);
-        for (int q = b * block + (lane & 7); q < end; q += 8) {
-          const int j = t + q * kThreads;
-          if (j >= nvec) continue;
-          const uint4 u = r.load(j);
-          if (!(max_of<kDtype>(u) >= least)) continue;
-          float v[E::kVec];
-          E::unpack(u, v);
+    // all their vectors at once, kUnroll of a thread in flight; the scale meanwhile
+    const int vecs = items * block;
+    for (int i0 = tid; i0 < vecs; i0 += kUnroll * kThreads) {
+      int at[kUnroll];
 #pragma unroll
-          for (int e = 0; e < E::kVec; ++e) {
-            if (v[e] >= least) {
-              const int at = atomicAdd(&sh.n, 1);
-              if (at < kCap)
-                sh.key[at] = (static_cast<u64>(key_of(v[e])) << 32) |
-                             static_cast<uint32_t>(~static_cast<uint32_t>(j * E::kVec + e - r.shift));
-            }
+      for (int n = 0; n < kUnroll; ++n) {
+        const int i = i0 + n * kThreads;
+        at[n] = -1;
+        if (i < vecs) {
+          const int q = i / block, it = sh.item[q];
+          const int step = it / kThreads * block + (i - q * block);
+          const int j = it % kThreads + step * kThreads;
+          if (step < steps && j < nvec) at[n] = j;
+        }
+        if (at[n] >= 0) x[n] = r.load(at[n]);
+      }
+      if (*static_cast<volatile int*>(&sh.n) > kCap) break;  // full: nothing more is looked for
+#pragma unroll
+      for (int n = 0; n < kUnroll; ++n) {
+        if (at[n] < 0 || !(max_of<kDtype>(x[n]) >= least)) continue;
+        float v[E::kVec];
+        E::unpack(x[n], v);
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e) {
+          if (v[e] >= least) {
+            const int to = atomicAdd(&sh.n, 1);
+            if (to < kCap)
+              sh.key[to] = (static_cast<u64>(key_of(v[e])) << 32) |
+                           static_cast<uint32_t>(~static_cast<uint32_t>(at[n] * E::kVec + e - r.shift));
           }
         }
       }
     }
+    set_scale(st, need_sum ? sum : static_cast<float>(kCap));
     __syncthreads();
     const int n = sh.n;
     done = n <= kCap;
     if (done) {
-      set_scale(st, need_sum ? sum : static_cast<float>(kCap));
       done = decide<kThreads>(a, st, sh, row, set.u, n, set.k, set.top_p, kmin, bound == kmin,
                               need_sum ? sum : 0.f);
     }
@@ -395,13 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_list_kernel(
 
 template <int kDtype>
 cudaError_t launch_list(const SampleArgs& a, int64_t T, cudaStream_t stream, int num_sms) {
+  // As few threads a row as let all rows run at once: a row's stream then lasts as long as all of
+  // them need the memory, and what follows it comes once, not once a wave.
   const unsigned g = static_cast<unsigned>(T);
   if (T <= num_sms)
     sample_list_kernel<kDtype, 1024><<<g, 1024, 0, stream>>>(a);
   else if (T <= 2 * num_sms)
     sample_list_kernel<kDtype, 512><<<g, 512, 0, stream>>>(a);
-  else
+  else if (T <= 4 * num_sms)
     sample_list_kernel<kDtype, 256><<<g, 256, 0, stream>>>(a);
+  else
+    sample_list_kernel<kDtype, 128><<<g, 128, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

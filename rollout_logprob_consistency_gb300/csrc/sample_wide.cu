@@ -773,6 +773,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   const int rank = static_cast<int>(cluster_rank());
   const int64_t clusters = gridDim.x / a.cluster, first = blockIdx.x / a.cluster;
 
+  pdl_wait();  // what the list kernel decided
+  if constexpr (!kPlain) {
+    // Nothing to be done is the usual case.  All CTAs of a cluster see the same: none writes a row
+    // before the others have come to the first barrier.
+    bool any = false;
+    for (int64_t row = first + tid * clusters; row < a.T; row += kThreads * clusters)
+      any |= __ldcg(a.kept + row) == kUndecided;
+    if (!__syncthreads_or(any)) return;
+  }
   cluster_arrive();
   if (tid == 0) {
     mbar_init(&sh.bar, 1);
@@ -781,7 +790,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   for (int i = tid; i < 256; i += kThreads) sh.table[i] = __ldg(&g_pow2_table.t[i]);
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
-  pdl_wait();      // what the list kernel decided
   uint32_t parity = 0;
   int phase = 0;
   for (int64_t base = first; base < a.T; base += 32 * clusters) {
@@ -874,8 +882,8 @@ template <int kDtype, int kThreads, bool kPlain>
 cudaError_t launch_rows(WideArgs a, const RowPlan& p, cudaStream_t stream, int num_sms) {
   const size_t smem = p.slice_bytes;
   auto* kernel = sample_wide_kernel<kDtype, kThreads, kPlain>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kernel, plan_row(TIM_LOGITS_MAX_V, sizeof(typename Elem<kDtype>::raw)).slice_bytes, allowed);
   if (e != cudaSuccess) return e;
   a.cluster = p.cluster;
   // a cluster a row, or where rows are to be looked for among the decided ones as many clusters
