@@ -39,7 +39,7 @@ constexpr int kCap = 1024;     // tokens of the list
 constexpr int kListK = 256;    // largest top-k that the list serves
 constexpr int kBins = 256;
 constexpr int kCount = 512;    // orders by counting up to here
-constexpr int kUnroll = 4;     // vectors of a thread in flight, and as many being looked at
+constexpr int kUnroll = 4;     // vectors of a thread in flight
 constexpr int kMaxima = 5120;  // of blocks of the row, kept while it streams
 constexpr float kSumError = 0x1p-16f;  // of the fp32 sum, see its place
 
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const bool need_sum = set.k == 0 && set.top_p < 1.f;
   const bool list_min = set.min_p > 0.f && set.top_p >= 1.f;
   if (set.bad == 0 && !list_k && !need_sum && !list_min) {
-    if (tid == 0) a.kept[row] = kUndecided;
+    if (tid == 0) leave_undecided(a, row);
     return;
   }
   if (tid == 0) sh.items = sh.n = 0;
@@ -259,16 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   // the threads' sums 2^-22, the product in decide() 2^-21: together below kSumError = 1.5e-5.
   F2 acc = f2(0.f, 0.f), acc2 = acc;
   const F2 kk = f2(st.pw.kh, st.pw.kh);
-  // The row's first and last vectors may be partly others': the first is loaded apart, the last
-  // counts in after the loop.
-  const uint4* const vec = r.vec();
-  const int w1 = r.w1();
+  const uint4* const vec = r.vec() + tid;
+  const int w0 = r.w0(), w1 = r.w1(), full = w1 / kThreads;  // steps that all threads have whole
   uint4 x[kUnroll];
-#pragma unroll
-  for (int n = 0; n < kUnroll; ++n) {
-    const int j = tid + n * kThreads;
-    x[n] = j < w1 ? (j >= r.w0() ? __ldg(vec + j) : r.load_edge(j)) : neg_inf_vec<kDtype>();
-  }
   auto add_vec = [&](const uint4& u, F2 ref) {
     float v[E::kVec];
     E::unpack(u, v);
@@ -292,11 +285,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     float bmax = -INFINITY;
     const int end = min(steps, (b + 1) * block);
     for (int i = b * block; i < end; i += kUnroll) {
-      uint4 y[kUnroll];
-      const int j0 = tid + (i + kUnroll) * kThreads;
+      const uint4* p = vec + i * kThreads;
+      if (i >= w0 && i + kUnroll <= full) {
 #pragma unroll
-      for (int n = 0; n < kUnroll; ++n)
-        y[n] = j0 + n * kThreads < w1 ? __ldg(vec + j0 + n * kThreads) : neg_inf_vec<kDtype>();
+        for (int n = 0; n < kUnroll; ++n) x[n] = __ldg(p + n * kThreads);
+      } else {  // the row's ends, which may be partly others'
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+          const int j = tid + (i + n) * kThreads;
+          x[n] = j < w0 || j >= w1 ? (j < nvec ? r.load_edge(j) : neg_inf_vec<kDtype>()) : __ldg(p + n * kThreads);
+        }
+      }
       uint4 m = x[0];
 #pragma unroll
       for (int n = 1; n < kUnroll; ++n) m = max_vec<kDtype>(m, x[n]);
@@ -307,19 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 #pragma unroll
         for (int n = 0; n < kUnroll; ++n) add_vec(x[n], ref);
       }
-#pragma unroll
-      for (int n = 0; n < kUnroll; ++n) x[n] = y[n];
     }
     sh.top[b * kThreads + tid] = bmax;
     tmax = max_nan(tmax, bmax);
-  }
-  if (w1 < nvec && tid == w1 % kThreads) {
-    const uint4 u = r.load_edge(w1);
-    const float most = max_of<kDtype>(u);
-    float& t = sh.top[w1 / kThreads / block * kThreads + tid];
-    t = max_nan(t, most);
-    tmax = max_nan(tmax, most);
-    if (need_sum) add_vec(u, raise(most));
   }
   // ---- the row's largest
   const uint32_t mykey = !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
@@ -480,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
                               need_sum ? sum : 0.f);
     }
   }
-  if (!done && tid == 0) a.kept[row] = kUndecided;
+  if (!done && tid == 0) leave_undecided(a, row);
 }
 
 template <int kDtype>

@@ -31,8 +31,14 @@ struct SampleArgs {
   int* status;
 };
 
-// out_kept of a row that the list could not decide: the wide kernel's.
+// A row that the list could not decide is the wide kernel's: its out_kept is kUndecided less the
+// number of such rows before it, in no particular order, so that they can be shared out evenly.
+// The rows are counted in the workspace, beside the status word; the wide kernel clears the count.
 constexpr int kUndecided = -1;
+constexpr int kCountWord = 16;
+__device__ __forceinline__ void leave_undecided(const SampleArgs& a, int64_t row) {
+  a.kept[row] = kUndecided - (atomicAdd(a.status + kCountWord, 1) & 0x3FFFFFFF);
+}
 
 // Monotone map of float bits to unsigned (larger float -> larger key; -0 and +0 are one).
 __device__ __forceinline__ uint32_t key_of(float z) {

@@ -6,7 +6,7 @@
 // The border is found in three passes over the slices.  The first counts the tokens in bins of
 // 1/32 octave of their weight: the counts place the border in one bin (top-k) or, a bin's weights
 // being within 2.2% of one another, in a few (top-p).  The second sums the integer weights of all
-// and of those above these bins, and counts and sums in bins of 1/256 octave within them: the border's is then known exactly.  The third lists the tokens of that one; rank 0 sorts
+// and of those above these bins, and counts and sums in bins of 1/256 octave (or more) within them: the border's is then known exactly.  The third lists the tokens of that one; rank 0 sorts
 // the list and walks it.  Where the list would be too long (thousands of tokens of one value) or
 // the border lies among tokens without weight, the border is found digit by digit of the
 // keys with histograms of counts or integer weights, which serves every row.
@@ -25,7 +25,7 @@ namespace {
 constexpr int kBins = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kCoarse = 2048;  // bins of 1/32 octave
-constexpr int kFine = 1024;    // bins of 1/256 octave
+constexpr int kFine = 1024;    // bins of 1/256 octave and more
 constexpr int kCap = 1024;     // tokens of one fine bin
 constexpr int kMaxSteps = 64;  // 32-vector steps of a warp's part: at most 24580 vectors over 16 warps
 
@@ -73,7 +73,7 @@ struct Shared : std::conditional_t<kPlain, NoBorder, Border> {
   uint32_t gkey[kMaxCluster * kThreads / 32];
   float gsum[kMaxCluster * kThreads / 32];
   u64 warp[kThreads / 32];
-  uint32_t warpu[kThreads / 32];
+  uint32_t warpu[kThreads / 32], warpv[kThreads / 32];
   u64 step[kMaxSteps];  // sums over 32 vectors each, of one warp's part
   int found;
   uint64_t bar;
@@ -481,7 +481,7 @@ struct Sampler {
     }
     __syncthreads();
     const int lo = sh.bin_lo, hi = kMass ? sh.bin_hi : lo;
-    if (hi >= low || hi - lo >= kFine / 8) return false;  // the same in every CTA
+    if (hi >= low) return false;  // the same in every CTA
     c_at = c_first;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -491,6 +491,8 @@ struct Sampler {
 
     // ---- the weights of all and of those above, and the fine bins within
     const int first = 8 * lo, last = 8 * hi + 7;
+    int shift = 0;  // 1/256 octave a fine bin, or as much as lets them cover those bins
+    while (((last - first) >> shift) >= kFine) ++shift;
     u64 mine = 0, above = 0;
     for (int j = tid; j < s.n; j += kThreads) {
       float v[kVec];
@@ -499,9 +501,9 @@ struct Sampler {
       for (int i = 0; i < kVec; ++i) {
         const int at = place_of(v[i], base);
         if (at >= first && at <= last) {
-          atomicAdd(&sh.fine.count[at - first], 1u);
-          if (kMass)
-            add_weight(&sh.fine.lo[at - first], &sh.fine.hi[at - first], weight(v[i], st, sh.table));
+          const int b = (at - first) >> shift;
+          atomicAdd(&sh.fine.count[b], 1u);
+          if (kMass) add_weight(&sh.fine.lo[b], &sh.fine.hi[b], weight(v[i], st, sh.table));
         }
       }
       if (kMass) {
@@ -554,7 +556,7 @@ struct Sampler {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       if (before < target && target <= before + m[i]) {
-        sh.digit = first + tid * kEach + i;
+        sh.digit = tid * kEach + i;
         sh.acc = before;
         sh.in = n[i];
         sh.all = 0;
@@ -564,30 +566,71 @@ struct Sampler {
     __syncthreads();
     // none: the bounds of the bins' mass did not hold; or too many of one value
     if (sh.all != 0 || sh.in > kCap) return false;
-    const int place = static_cast<int>(sh.digit), len = static_cast<int>(sh.in);
+    const int place = first + (static_cast<int>(sh.digit) << shift), len = static_cast<int>(sh.in);
     acc = sh.acc;
 
-    // ---- its tokens, to rank 0: behind the lists of the ranks before, its own being in place
+    // ---- its tokens, and whether they are all of one value
+    uint32_t key_lo = 0xFFFFFFFFu, key_hi = 0;
     for (int j = tid; j < s.n; j += kThreads) {
       float v[kVec];
       kept_vector(j, zc, whole, v);
+      uint32_t in = 0;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        if (place_of(v[i], base) == place)
-          sh.list[atomicAdd(&sh.list_n, 1u)] =
-              (static_cast<u64>(key_of(v[i])) << 32) |
-              static_cast<uint32_t>(~static_cast<uint32_t>(id_of(j, i)));
+      for (int i = 0; i < kVec; ++i) in |= (place_of(v[i], base) - place) >> shift == 0 ? 1u << i : 0u;
+      for (; in != 0; in &= in - 1) {
+        const int i = __ffs(in) - 1;
+        const uint32_t key = key_of(E::widen(reinterpret_cast<const typename E::raw*>(slice + j)[i]));
+        key_lo = min(key_lo, key);
+        key_hi = max(key_hi, key);
+        sh.list[atomicAdd(&sh.list_n, 1u)] =
+            (static_cast<u64>(key) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(id_of(j, i)));
       }
     }
+    key_lo = __reduce_min_sync(0xFFFFFFFFu, key_lo);
+    key_hi = __reduce_max_sync(0xFFFFFFFFu, key_hi);
     __syncthreads();
+    if (lane == 0) {
+      sh.warpu[warp] = key_lo;
+      sh.warpv[warp] = key_hi;
+    }
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) {
+      key_lo = min(key_lo, sh.warpu[i]);
+      key_hi = max(key_hi, sh.warpv[i]);
+    }
     const int listed = static_cast<int>(sh.list_n);
-    exchange(static_cast<u64>(listed), 0);
-    if (rank != 0) {
-      int at = 0;
-      for (int c = 0; c < rank; ++c) at += static_cast<int>(got(c, 0));
+    exchange(static_cast<u64>(listed), (static_cast<u64>(key_hi) << 32) | key_lo);
+    int at = 0;  // in the lists of the ranks before
+    for (int c = 0; c < a.cluster; ++c) {
+      if (c < rank) at += static_cast<int>(got(c, 0));
+      key_lo = min(key_lo, static_cast<uint32_t>(got(c, 1)));
+      key_hi = max(key_hi, static_cast<uint32_t>(got(c, 1) >> 32));
+    }
+    if (key_lo == key_hi) {
+      // equal weights: so many of them by id; the one that is last is in one CTA's list
+      const u64 w = kMass ? weight(key_value(key_lo), st, sh.table) : 1;
+      const int want = static_cast<int>((target - acc + w - 1) / w) - 1 - at;
+      if (tid == 0) sh.found = -1;
+      __syncthreads();
+      if (want >= 0 && want < listed) {
+        for (int i = tid; i < listed; i += kThreads) {
+          const u64 mine = sh.list[i];
+          int before = 0;
+          for (int q = 0; q < listed; ++q) before += sh.list[q] > mine ? 1 : 0;
+          if (before == want) sh.found = static_cast<int>(~static_cast<uint32_t>(mine));
+        }
+      }
+      __syncthreads();
+      exchange(static_cast<u64>(static_cast<int64_t>(sh.found)), 0);
+      st.kc = key_lo;
+      for (int c = 0; c < a.cluster; ++c)
+        if (static_cast<int>(got(c, 0)) >= 0) st.idc = static_cast<int>(got(c, 0));
+      return true;
+    }
+    // to rank 0: behind the lists of the ranks before, its own being in place
+    if (rank != 0)
       for (int i = tid; i < listed; i += kThreads)
         cluster_store(cluster_addr(&sh.list[at + i], 0), sh.list[i]);
-    }
     cluster_arrive();
     cluster_wait();
     u64 border = 0;
@@ -762,6 +805,11 @@ struct Sampler {
   }
 };
 
+// Whether the mark of a row is that of an undecided one of this cluster.
+__device__ __forceinline__ bool is_mine(int kept, int64_t cluster, int64_t clusters) {
+  return kept <= kUndecided && (kUndecided - kept) % static_cast<int>(clusters) == static_cast<int>(cluster);
+}
+
 template <int kDtype, int kThreads, bool kPlain>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
     sample_wide_kernel(const WideArgs a) {
@@ -775,11 +823,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
 
   pdl_wait();  // what the list kernel decided
   if constexpr (!kPlain) {
-    // Nothing to be done is the usual case.  All CTAs of a cluster see the same: none writes a row
-    // before the others have come to the first barrier.
+    if (blockIdx.x == 0 && tid == 0) a.status[kCountWord] = 0;
+    // Nothing to be done is the usual case.  All CTAs of a cluster see the same: only they write
+    // their rows, and none does before the others have come to the first barrier.
     bool any = false;
-    for (int64_t row = first + tid * clusters; row < a.T; row += kThreads * clusters)
-      any |= __ldcg(a.kept + row) == kUndecided;
+    for (int64_t row = tid; row < a.T; row += kThreads) any |= is_mine(__ldcg(a.kept + row), first, clusters);
     if (!__syncthreads_or(any)) return;
   }
   cluster_arrive();
@@ -792,17 +840,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   cluster_wait();  // every CTA of the cluster runs
   uint32_t parity = 0;
   int phase = 0;
-  for (int64_t base = first; base < a.T; base += 32 * clusters) {
-    // the next 32 rows of this cluster: which of them are to be done
-    const int64_t mine = base + lane * clusters;
-    unsigned todo = __ballot_sync(0xFFFFFFFFu, mine < a.T && (kPlain || __ldcg(a.kept + mine) == kUndecided));
-    // a CTA that is behind must not see what this one writes of a row that it has still to test
-    if (!kPlain && todo != 0) {
+  for (int64_t base = 0; base < a.T; base += kPlain ? a.T : 32) {
+    // which of the next rows are this cluster's; unfiltered rows are one a cluster
+    unsigned todo = 1;
+    if constexpr (!kPlain) {
+      const int64_t row = base + lane;
+      todo = __ballot_sync(0xFFFFFFFFu, row < a.T && is_mine(__ldcg(a.kept + row), first, clusters));
+      if (todo == 0) continue;
+      // a CTA that is behind must not see what this one writes of a row that it has still to test
       cluster_arrive();
       cluster_wait();
     }
     for (; todo != 0; todo &= todo - 1) {
-      const int64_t row = base + (__ffs(todo) - 1) * clusters;
+      const int64_t row = kPlain ? first : base + (__ffs(todo) - 1);
       const Row<kDtype> r(a.logits, row, a.ld, a.V);
       const Slice s = slice_of(r.nvec(), rank, a.cluster);
       if (tid == 0) load_slice(r, s, slice_mem, &sh.bar);
