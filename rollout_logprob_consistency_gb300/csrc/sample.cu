@@ -78,17 +78,42 @@ __device__ __forceinline__ int sharers(int n) {
 }
 
 // The row's token from the list of n tokens in sh.key, by the whole CTA; `complete`: the list
-// holds all that min-p keeps.  `sum` > 0: the row's fp32 total in units of 2^(max K), for top-p
-// without top-k.  False: that total is not known well enough.
+// holds all that min-p keeps.  For top-p without top-k, `sum` > 0 is the row's fp32 total in units
+// of 2^(max K), and `exact` > 0 its integer one.
 //
 // Up to kCount tokens the orders are found by counting: a token's comparisons are shared by as many
 // threads as there are, with no barrier between them; above it the squares cost more than a sort.
+enum Decided { kDone = 0, kUnsure, kTooShort };  // unsure: the fp32 total does not do
 template <int kThreads>
-__device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>& sh, int64_t row,
+__device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThreads>& sh, int64_t row,
                        float u, int n, int k, float top_p, uint32_t kmin, bool complete,
-                       float sum) {
+                       float sum, u64 exact) {
   constexpr int kRank = kCount > kThreads ? kCount / kThreads : 1;
   const int tid = threadIdx.x, lane = tid & 31;
+  u64 lo = ~0ull, hi = ~0ull;  // top-p keeps a token while the sum before it is below
+  if (sum > 0.f || exact > 0) {
+    if (exact > 0) {
+      lo = hi = top_p_target(exact, top_p);
+    } else {
+      // the total in the weights' unit: 2^(max K - top + 62)
+      const Df mk = st.pw.recentre ? df(0.f) : df(st.M) * Df{st.pw.kh, st.pw.kl};
+      const float whole = rintf(mk.h), frac = (mk.h - whole) + mk.l;
+      const float P = top_p * sum * pow2_df(frac, Pow2Row{1.f, 0.f, 0.f, false}, sh.table).h;
+      const int e = static_cast<int>(whole) - st.top + 62;
+      lo = scaled_up(P * (1.f - kSumError), e);
+      hi = scaled_up(P * (1.f + kSumError), e) + 1;
+    }
+    if (!complete) {  // whether the list reaches the border, before any order is looked for
+      u64 listed = 0;
+      for (int i = tid; i < n; i += kThreads)
+        listed += weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
+      u64 all;
+      block_scan<kThreads>(listed, sh.warp, kThreads / 32, all);
+      __syncthreads();
+      if (lo > all) return kTooShort;
+      if (hi > all) return kUnsure;
+    }
+  }
   if (n <= kCount) {
     const int each = sharers<kThreads>(n), first = tid / each;
     u64 mine[kRank];
@@ -131,21 +156,7 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
   }
   u64 total;
   u64 before = block_scan<kThreads>(part, sh.warp, (n + 32 * per - 1) / (32 * per), total);
-  u64 lo = ~0ull, hi = ~0ull;  // top-p keeps a token while the sum before it is below
-  if (top_p < 1.f) {
-    if (sum > 0.f) {
-      // the total in the weights' unit: 2^(max K - top + 62)
-      const Df mk = st.pw.recentre ? df(0.f) : df(st.M) * Df{st.pw.kh, st.pw.kl};
-      const float whole = rintf(mk.h), frac = (mk.h - whole) + mk.l;
-      const float P = top_p * sum * pow2_df(frac, Pow2Row{1.f, 0.f, 0.f, false}, sh.table).h;
-      const int e = static_cast<int>(whole) - st.top + 62;
-      lo = scaled_up(P * (1.f - kSumError), e);
-      hi = scaled_up(P * (1.f + kSumError), e) + 1;
-      if (hi > total && !complete) lo = 0;  // the list may not reach the border
-    } else {
-      lo = hi = top_p_target(total, top_p);
-    }
-  }
+  if (top_p < 1.f && k > 0) lo = hi = top_p_target(total, top_p);
   int c_lo = 0, c_hi = 0;
   for (int i = i0; i < i1; ++i) {
     const bool min_ok = static_cast<uint32_t>(sh.key[i] >> 32) >= kmin;
@@ -163,12 +174,12 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
   }
   __syncthreads();
   const int m = sh.count_lo;
-  if (m != sh.count_hi) return false;
+  if (m != sh.count_hi) return kUnsure;
   // the draw, by id
   if (m <= kCount) {
     // what the kept tokens of lower ids weigh
     const int each = sharers<kThreads>(m), first = tid / each;
-    if ((tid - lane) / each >= m) return true;  // a warp without tokens
+    if ((tid - lane) / each >= m) return kDone;  // a warp without tokens
     int id[kRank];
     u64 kept = 0, below[kRank];
 #pragma unroll
@@ -195,7 +206,7 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
       if (i < m && (tid & (each - 1)) == 0 && below[q] <= target && target < below[q] + sh.w[i])
         write_row(a, st, sh.table, row, id[q], key_value(static_cast<uint32_t>(sh.key[i] >> 32)), kept, m);
     }
-    return true;
+    return kDone;
   }
   // sorted once more, by id: the low word on top descends as the id ascends
   int n2 = 2 * kCount;
@@ -219,7 +230,51 @@ __device__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>
                 key_value(static_cast<uint32_t>(x)), total, m);
     before += w;
   }
-  return true;
+  return kDone;
+}
+
+// Sum of the integer weights of the whole row, by the whole CTA.
+template <int kDtype, int kThreads>
+__device__ __noinline__ u64 exact_total(const Row<kDtype>& r, const RowState& state,
+                                        Shared<kThreads>& sh) {
+  using E = Elem<kDtype>;
+  const RowState st = state;
+  const Pow2Pair k = {f2(st.pw.kh, st.pw.kh), f2(st.pw.kl, st.pw.kl),
+                      static_cast<uint32_t>(st.top) + (__float_as_uint(kPow2Magic) >> 8)};
+  const int nvec = r.nvec(), w0 = r.w0(), w1 = r.w1();
+  const uint4* const vec = r.vec();
+  u64 sum = 0;
+  for (int j0 = threadIdx.x; j0 < nvec; j0 += kUnroll * kThreads) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      const int j = j0 + n * kThreads;
+      x[n] = j >= w0 && j < w1 ? __ldg(vec + j) : j < nvec ? r.load_edge(j) : neg_inf_vec<kDtype>();
+    }
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      float v[E::kVec];
+      E::unpack(x[n], v);
+      if (st.pw.recentre) {
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) sum += weight(v[i], st, sh.table);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E::kVec; i += 2) {
+          u64 a, b;
+          pow2_shifted(f2(fmaxf(v[i], st.zlow), fmaxf(v[i + 1], st.zlow)), k, sh.table, a, b);
+          sum += a + b;
+        }
+      }
+    }
+  }
+  sum = warp_sum(sum);
+  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0;
+  for (int i = 0; i < kThreads / 32; ++i) sum += sh.warp[i];
+  __syncthreads();
+  return sum;
 }
 
 template <int kDtype, int kThreads>
@@ -241,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     return;
   }
   if (tid == 0) sh.items = sh.n = 0;
-  if (tid < 256) sh.table[tid] = __ldg(&g_pow2_table.t[tid]);
+  for (int i = tid; i < 256; i += kThreads) sh.table[i] = __ldg(&g_pow2_table.t[i]);
   RowState st;
   set_temperature(st, set.tau);
 
@@ -252,35 +307,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const int block = (steps + kMaxima / kThreads * kUnroll - 1) / (kMaxima / kThreads * kUnroll) * kUnroll;
   const int blocks = (steps + block - 1) / block;
   float tmax = -INFINITY, run = -INFINITY;
-  // The sum is relative to the thread's running maximum.  A term's argument carries two roundings
-  // of 2^-24 and the remainder of K, 2^-25 (together below 4.1e-6 of the term for 40 octaves;
-  // terms further down are below 2^-40 of the largest), its exponential 2^-22; the partial sums
-  // of a few hundred terms and up to 25 changes of the reference 2^-24 and 2^-22 each, the joining of
-  // the threads' sums 2^-22, the product in decide() 2^-21: together below kSumError = 1.5e-5.
-  F2 acc = f2(0.f, 0.f), acc2 = acc;
+  // The sum is relative to a reference of the thread that follows its largest logit, 8 octaves late,
+  // and is taken in three levels (a group of kUnroll vectors, a block, the row).  Its error, 2^-24 a
+  // rounding:
+  //  - a term's argument has two roundings and the remainder of K: 2.5 x 2^-24 |x| ln2.  The mass of
+  //    V <= 2^19 tokens lies within 19 octaves of the largest: below 2.0e-6;
+  //  - its exponential 2^-22; at most 5 changes of the reference in 40 octaves 2^-22 each: 1.5e-6;
+  //  - at most 8 + 1 + 8 + 40 additions in a thread and 10 among them: 4.0e-6;
+  //  - the joining of the threads' sums and what decide() multiplies it with: 1.0e-6.
+  // Together below kSumError = 1.5e-5.
+  F2 acc = f2(0.f, 0.f), whole = acc;
   const F2 kk = f2(st.pw.kh, st.pw.kh);
+  const float late = 8.f / st.pw.kh;
   const uint4* const vec = r.vec() + tid;
   const int w0 = r.w0(), w1 = r.w1(), full = w1 / kThreads;  // steps that all threads have whole
   uint4 x[kUnroll];
-  auto add_vec = [&](const uint4& u, F2 ref) {
-    float v[E::kVec];
-    E::unpack(u, v);
-#pragma unroll
-    for (int q = 0; q < E::kVec; q += 4) {
-      acc = add2(acc, ex2x2(mul2(add2(f2(v[q], v[q + 1]), ref), kk)));
-      acc2 = add2(acc2, ex2x2(mul2(add2(f2(v[q + 2], v[q + 3]), ref), kk)));
-    }
-  };
-  auto raise = [&](float most) {
-    if (most > run) {
-      const float f = ex2_approx((run - most) * st.pw.kh);
-      acc = mul2(acc, f2(f, f));
-      acc2 = mul2(acc2, f2(f, f));
-      run = most;
-    }
-    const float from = run == -INFINITY ? 0.f : -run;
-    return f2(from, from);
-  };
   for (int b = 0; b < blocks; ++b) {
     float bmax = -INFINITY;
     const int end = min(steps, (b + 1) * block);
@@ -302,11 +343,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       const float most = max_of<kDtype>(m);
       bmax = max_nan(bmax, most);
       if (need_sum) {
-        const F2 ref = raise(most);
+        if (most > run + late || run == -INFINITY) {
+          const float f = run == -INFINITY ? 0.f : ex2_approx((run - most) * st.pw.kh);
+          acc = mul2(acc, f2(f, f));
+          whole = mul2(whole, f2(f, f));
+          run = most;
+        }
+        const float from = run == -INFINITY ? 0.f : -run;
+        const F2 ref = f2(from, from);
+        F2 part = f2(0.f, 0.f), part2 = part;
 #pragma unroll
-        for (int n = 0; n < kUnroll; ++n) add_vec(x[n], ref);
+        for (int n = 0; n < kUnroll; ++n) {
+          float v[E::kVec];
+          E::unpack(x[n], v);
+#pragma unroll
+          for (int q = 0; q < E::kVec; q += 4) {
+            part = add2(part, ex2x2(mul2(add2(f2(v[q], v[q + 1]), ref), kk)));
+            part2 = add2(part2, ex2x2(mul2(add2(f2(v[q + 2], v[q + 3]), ref), kk)));
+          }
+        }
+        acc = add2(acc, add2(part, part2));
       }
     }
+    whole = add2(whole, acc);
+    acc = f2(0.f, 0.f);
     sh.top[b * kThreads + tid] = bmax;
     tmax = max_nan(tmax, bmax);
   }
@@ -338,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   st.M = M;
   float sum = 0.f;
   if (need_sum) {
-    const float2 t = unpack2(add2(acc, acc2));
+    const float2 t = unpack2(whole);
     sum = run == -INFINITY ? 0.f : (t.x + t.y) * ex2_approx((run - M) * st.pw.kh);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -363,7 +423,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     if (before == set.k - 1) sh.bound = mine;
     __syncthreads();
     bound = max(bound, sh.bound);
-  } else if (list_k) {
+  } else if (list_k || need_sum) {
+    // For top-p: the tokens below this hold less than 1 - p of the mass, were there V of them.  That
+    // can be thousands; as much of the list as is sure to fit serves most rows, and where it ends
+    // before the border does decide() says so.
+    if (need_sum) {
+      const float share = (1.f - set.top_p) * sum * (1.f - 0x1p-10f) / static_cast<float>(a.V);
+      if (share > 0.f)
+        bound = max(key_of(M + (__log2f(share) - 0x1p-10f) / st.pw.kh), kmin);
+    }
+    const uint32_t want = need_sum ? kCount * 3 / 4 : static_cast<uint32_t>(set.k);
     // in 256 bins from the largest logit down, over as much as the threads' maxima span, 64 octaves
     // or units at most; a logit further down is in the last bin, which bounds nothing
     for (int i = tid; i < kBins; i += kThreads) sh.group[i] = 0;
@@ -390,25 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         if (lane >= o) at += up;
       }
       at -= part;
-      const uint32_t k = static_cast<uint32_t>(set.k);
       if (lane == 0) sh.bound = kNegInfKey + 1;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int bin = lane * 8 + i;
         // every maximum of the bins up to this one is above its lower end
-        if (at < k && k <= at + count[i] && bin < 255)
+        if (at < want && want <= at + count[i] && bin < 255)
           sh.bound = max(key_of(M - (static_cast<float>(bin) + 1.01f) * per_bin), kNegInfKey + 1);
         at += count[i];
       }
     }
     __syncthreads();
     bound = max(bound, sh.bound);
-  } else if (need_sum) {
-    // the tokens below this hold less than 1 - p of the mass, were there V of them
-    const float share = (1.f - set.top_p) * sum * (1.f - 0x1p-10f) / static_cast<float>(a.V);
-    if (share > 0.f)
-      bound = max(key_of(M + (__log2f(share) - 0x1p-10f) / st.pw.kh), kmin);
   }
   bool done = bound > kNegInfKey + 1 || list_min;
   bound = max(bound, kNegInfKey + 1);
@@ -465,8 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const int n = sh.n;
     done = n <= kCap;
     if (done) {
-      done = decide<kThreads>(a, st, sh, row, set.u, n, set.k, set.top_p, kmin, bound == kmin,
-                              need_sum ? sum : 0.f);
+      Decided d = decide<kThreads>(a, st, sh, row, set.u, n, set.k, set.top_p, kmin, bound == kmin,
+                                   need_sum ? sum : 0.f, 0);
+      if (d == kUnsure) {
+        // the border is within the fp32 sum's error: the row once more, for its integer weights
+        __syncthreads();
+        const u64 exact = exact_total<kDtype, kThreads>(r, st, sh);
+        d = decide<kThreads>(a, st, sh, row, set.u, n, 0, set.top_p, kmin, bound == kmin, 0.f, exact);
+      }
+      done = d == kDone;
     }
   }
   if (!done && tid == 0) leave_undecided(a, row);

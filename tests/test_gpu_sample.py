@@ -249,3 +249,97 @@ def test_row_results_do_not_depend_on_the_batch(tim):
         for i in (0, 17, 39):
             one = tim.sample(z[i:i + 1], u[i:i + 1], **kw)
             assert all(torch.equal(a[i:i + 1], b) for a, b in zip(whole, one))
+
+
+# A row has 1024, 512, 256 or 128 threads as there are more rows than once, twice or four times the
+# SMs (152); the rows of a batch are compared where they are few and by sample where they are many.
+MANY = [dict(top_k=50, top_p=0.95, temperature=0.7), dict(top_k=200, top_p=0.9), dict(top_k=900, top_p=0.9),
+        dict(top_p=0.9, temperature=0.5), dict(top_p=0.99), dict(min_p=0.1), dict(top_p=0.8, min_p=0.2),
+        dict()]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,V", [(152, 9001), (153, 9001), (305, 6007), (609, 6007), (1300, 257)])
+def test_many_rows(tim, dtype, T, V):
+    import torch
+    base = _logits(24, V, dtype, 1000 + T, scale=2.5)
+    u = np.random.default_rng(T).random(24).astype(np.float32)
+    at = torch.arange(T, device="cuda") % 24
+    z, ut = base[at].contiguous(), torch.from_numpy(u).cuda()[at]
+    for kw in MANY:
+        # 24 rows against the oracle; as a batch the same rows over and over, at every place
+        want = _check(tim, base, u, **kw)
+        got = tim.sample(z, ut, **kw)
+        for g, w in zip(got, want):
+            assert torch.equal(g, torch.from_numpy(w).cuda()[at]), kw
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [12, 200, 400, 700])
+@pytest.mark.parametrize("rank", [60, 300, 2500])
+def test_top_p_on_a_border(tim, dtype, T, rank):
+    """top-p is the float32 next to the mass of a row's first `rank` tokens: between border and p
+    lie some 2^-26 of the mass, within what a float32 sum leaves open and far outside MARGIN."""
+    import torch
+    n = 12
+    base = _logits(n, 6007, dtype, 77, scale=2.0)
+    u = np.random.default_rng(78).random(n).astype(np.float32)
+    zh = base.double().cpu().numpy()
+    p = np.empty(n, np.float32)
+    for i in range(n):
+        e = np.sort(np.exp(zh[i] - zh[i].max()))[::-1]
+        p[i] = e[:rank].sum() / e.sum()
+    at = torch.arange(T, device="cuda") % n
+    want = _check(tim, base, u, top_p=torch.from_numpy(p).cuda(), least=n - 3)
+    got = tim.sample(base[at].contiguous(), torch.from_numpy(u).cuda()[at],
+                     top_p=torch.from_numpy(p).cuda()[at])
+    for g, w in zip(got, want):
+        assert torch.equal(g, torch.from_numpy(w).cuda()[at])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_largest_vocabulary(tim, dtype):
+    import torch
+    V = 393216
+    z = _logits(3, V, dtype, 21)
+    u = np.random.default_rng(22).random(3).astype(np.float32)
+    for kw in (dict(), dict(top_p=0.9), dict(top_p=0.99), dict(top_k=50, top_p=0.9),
+               dict(top_k=200000, top_p=0.9), dict(min_p=0.02)):
+        _check(tim, z, u, **kw)
+    with pytest.raises(tim.TimError, match="TIM_ERR_SHAPE"):
+        tim.sample(torch.zeros(1, V + 1, device="cuda"), torch.zeros(1, device="cuda"))
+
+
+def test_one_workspace_for_calls_of_all_sizes_in_turn(tim):
+    """Nothing of a call is left in the workspace: calls of other sizes and settings in turn with
+    one workspace, scoring's included, give what they give with their own."""
+    import torch
+    ws = tim.Workspace(1024)
+    for T, V, kw in ((700, 5003, dict(top_p=0.97)), (3, 151936, dict(top_p=0.99)), (200, 999, dict()),
+                     (40, 50257, dict(top_k=2000, top_p=0.9)), (1, 1, dict(top_k=1)),
+                     (700, 5003, dict(top_p=0.97))):
+        z = _logits(T, V, "bf16", T + V)
+        u = torch.rand(T, device="cuda")
+        a = tim.sample(z, u, workspace=ws, **kw)
+        b = tim.sample(z, u, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_calls_at_once(tim):
+    """On two streams, each with its own workspace."""
+    import torch
+    z = _logits(300, 50257, "bf16", 31)
+    u = torch.rand(300, device="cuda")
+    cases = [dict(top_p=0.97), dict(top_k=3000, top_p=0.9)]
+    want = [tim.sample(z, u, **kw) for kw in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [tim.Workspace(1024) for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, kw in enumerate(cases):
+            got[i].append(tim.sample(z, u, workspace=spaces[i], stream=streams[i], check=False, **kw))
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        spaces[i].check()
+        assert all(torch.equal(x, y) for g in got[i] for x, y in zip(g, w))
