@@ -419,27 +419,6 @@ __device__ __forceinline__ unsigned long long pow2_fixed(float z, const Pow2Row&
   return T + static_cast<unsigned long long>(static_cast<long long>(static_cast<int>(T >> 32)) *
                                              __float2int_rn(p));
 }
-// Two at once without recentring, as right shifts of `top` - n.
-struct Pow2Pair {
-  F2 kh, kl;
-  uint32_t top;  // top + (bits of kPow2Magic >> 8)
-};
-__device__ __forceinline__ void pow2_shifted(F2 z, const Pow2Pair& k, const unsigned long long* table,
-                                             unsigned long long& w0, unsigned long long& w1) {
-  const F2 magic = f2(kPow2Magic, kPow2Magic);
-  const F2 t = fma2(z, k.kh, magic);
-  const F2 g = fma2(z, k.kl, fma2(z, k.kh, fma2(t, f2(-1.f, -1.f), magic)));
-  const F2 p = mul2(g, fma2(g, fma2(g, f2(238388336.0f, 238388336.0f), f2(1031764992.0f, 1031764992.0f)),
-                            f2(2977044472.0f, 2977044472.0f)));
-  const float2 tt = unpack2(t), pp = unpack2(p);
-  const uint32_t b0 = __float_as_uint(tt.x), b1 = __float_as_uint(tt.y);
-  const unsigned long long T0 = table[b0 & 255u], T1 = table[b1 & 255u];
-  const long long q0 = static_cast<long long>(static_cast<int>(T0 >> 32)) * __float2int_rn(pp.x);
-  const long long q1 = static_cast<long long>(static_cast<int>(T1 >> 32)) * __float2int_rn(pp.y);
-  w0 = (T0 + static_cast<unsigned long long>(q0)) >> (k.top - (b0 >> 8));
-  w1 = (T1 + static_cast<unsigned long long>(q1)) >> (k.top - (b1 >> 8));
-}
-
 // The table, one copy a translation unit.
 static __device__ const Pow2Table g_pow2_table = make_pow2_table();
 

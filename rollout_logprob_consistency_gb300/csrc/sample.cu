@@ -13,53 +13,60 @@
 // summed as a 64-bit integer, at a scale that puts the row's total between 2^50 and 2^60: the
 // sums are exact in that scale and do not depend on the order or the split.
 //
-// This kernel decides the rows that few tokens decide, one CTA a row, reading it once: while
-// it streams, every thread notes the largest logits of blocks of its vectors (and, for
-// top-p alone, a running sum in fp32).  They bound the tokens that can be kept:
+// A row has one CTA, which reads it from memory once: while it streams, every thread notes the
+// largest logits of blocks of its vectors (and, for top-p alone, a running sum in fp32).  They bound
+// the tokens that can be kept:
 //  - the k-th largest of the threads' (or groups of threads') maxima is met by every top-k
 //    logit, they being k different logits;
 //  - for top-p the logit below which V tokens together would hold less than 1 - p;
 //  - min-p's own bound.
 // Only the blocks whose maximum meets the bound are read again (from L2); their tokens above it
 // are sorted and decided with integer weights.  Top-p alone needs the row's total: the fp32 sum
-// with its error bound decides unless the border lies within that error.  Rows that this does not
-// decide, and unfiltered ones, are marked for the kernel of sample_wide.cu.
-#include "sample.cuh"
+// with its error bound decides unless the border lies within that error.  A row that this does not
+// decide is read again as often as it takes (sample_deep.cuh).  Few unfiltered rows are a cluster's
+// each (sample_plain.cu).
+#include "sample_deep.cuh"
 
 namespace tim {
 
 using namespace sampling;
 
-cudaError_t launch_sample_wide(const SampleArgs& args, int dtype, int64_t T, bool plain,
-                               cudaStream_t stream, int num_sms);
+cudaError_t launch_sample_plain(const SampleArgs& args, int dtype, int64_t T, cudaStream_t stream);
 
 namespace {
 
-constexpr int kCap = 1024;     // tokens of the list
-constexpr int kListK = 256;    // largest top-k that the list serves
+constexpr int kCap = 2048;     // tokens of the list
+constexpr int kListK = 1024;   // largest top-k that the list serves
 constexpr int kBins = 256;
 constexpr int kCount = 512;    // orders by counting up to here
 constexpr int kUnroll = 4;     // vectors of a thread in flight
 constexpr int kMaxima = 5120;  // of blocks of the row, kept while it streams
+constexpr int kPlainRows = 100;  // unfiltered rows up to here are a cluster's each
 constexpr float kSumError = 0x1p-16f;  // of the fp32 sum, see its place
+
+// Blocks to be read again; eight CTAs of 128 threads have to fit an SM.
+template <int kThreads>
+constexpr int kItems = kThreads > 128 ? 2048 : 1024;
 
 template <int kThreads>
 struct Shared {
-  u64 table[256];
+  Tables table;
   union {
     float top[kMaxima];  // of block b of thread t: top[b kThreads + t]
     struct {
       u64 key[kCap];  // key << 32 | ~id: larger comes first
-      u64 w[kCap];
+      u64 w[kCount];  // of the first tokens
     };
+    DeepShared deep;
   };
+  DeepScratch scratch;
   uint32_t group[kThreads > kBins ? kThreads : kBins];
-  uint16_t item[kCap];  // blocks to be read again: the places of their maxima
-  u64 warp[kThreads / 32];
+  uint16_t item[kItems<kThreads>];  // blocks to be read again: the places of their maxima
+  u64 warp[32], total[kThreads / 32];
   uint32_t warpu[kThreads / 32];
   float warpf[kThreads / 32];
   uint32_t bound;
-  int items, n, count_lo, count_hi;
+  int items, n, count_lo, count_hi, hopeless;
 };
 
 // f 2^e as a whole number, e at least 24 - (exponent of f)
@@ -78,31 +85,26 @@ __device__ __forceinline__ int sharers(int n) {
 }
 
 // The row's token from the list of n tokens in sh.key, by the whole CTA; `complete`: the list
-// holds all that min-p keeps.  For top-p without top-k, `sum` > 0 is the row's fp32 total in units
-// of 2^(max K), and `exact` > 0 its integer one.
+// holds all that min-p keeps.  For top-p of the whole row, `sum` > 0 is the row's fp32 total in units
+// of 2^(max K).  False: the list ends before the border, or the border lies within the total's error.
 //
 // Up to kCount tokens the orders are found by counting: a token's comparisons are shared by as many
 // threads as there are, with no barrier between them; above it the squares cost more than a sort.
-enum Decided { kDone = 0, kUnsure, kTooShort };  // unsure: the fp32 total does not do
 template <int kThreads>
-__device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThreads>& sh, int64_t row,
-                       float u, int n, int k, float top_p, uint32_t kmin, bool complete,
-                       float sum, u64 exact) {
+__device__ __forceinline__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>& sh,
+                                       int64_t row, float u, int n, int k, float top_p,
+                                       uint32_t kmin, bool complete, float sum) {
   constexpr int kRank = kCount > kThreads ? kCount / kThreads : 1;
   const int tid = threadIdx.x, lane = tid & 31;
   u64 lo = ~0ull, hi = ~0ull;  // top-p keeps a token while the sum before it is below
-  if (sum > 0.f || exact > 0) {
-    if (exact > 0) {
-      lo = hi = top_p_target(exact, top_p);
-    } else {
-      // the total in the weights' unit: 2^(max K - top + 62)
-      const Df mk = st.pw.recentre ? df(0.f) : df(st.M) * Df{st.pw.kh, st.pw.kl};
-      const float whole = rintf(mk.h), frac = (mk.h - whole) + mk.l;
-      const float P = top_p * sum * pow2_df(frac, Pow2Row{1.f, 0.f, 0.f, false}, sh.table).h;
-      const int e = static_cast<int>(whole) - st.top + 62;
-      lo = scaled_up(P * (1.f - kSumError), e);
-      hi = scaled_up(P * (1.f + kSumError), e) + 1;
-    }
+  if (sum > 0.f) {
+    // the total in the weights' unit: 2^(max K - top + 62)
+    const Df mk = st.pw.recentre ? df(0.f) : df(st.M) * Df{st.pw.kh, st.pw.kl};
+    const float whole = rintf(mk.h), frac = (mk.h - whole) + mk.l;
+    const float P = top_p * sum * pow2_df(frac, Pow2Row{1.f, 0.f, 0.f, false}, sh.table.fine).h;
+    const int e = static_cast<int>(whole) - st.top + 62;
+    lo = scaled_up(P * (1.f - kSumError), e);
+    hi = scaled_up(P * (1.f + kSumError), e) + 1;
     if (!complete) {  // whether the list reaches the border, before any order is looked for
       u64 listed = 0;
       for (int i = tid; i < n; i += kThreads)
@@ -110,8 +112,7 @@ __device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThrea
       u64 all;
       block_scan<kThreads>(listed, sh.warp, kThreads / 32, all);
       __syncthreads();
-      if (lo > all) return kTooShort;
-      if (hi > all) return kUnsure;
+      if (hi > all) return false;
     }
   }
   if (n <= kCount) {
@@ -151,7 +152,7 @@ __device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThrea
   u64 part = 0;
   for (int i = i0; i < i1; ++i) {
     const u64 w = weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
-    sh.w[i] = w;
+    if (i < kCount) sh.w[i] = w;
     part += w;
   }
   u64 total;
@@ -162,7 +163,8 @@ __device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThrea
     const bool min_ok = static_cast<uint32_t>(sh.key[i] >> 32) >= kmin;
     c_lo += before < lo && min_ok ? 1 : 0;
     c_hi += before < hi && min_ok ? 1 : 0;
-    before += sh.w[i];
+    before += i < kCount ? sh.w[i]
+                         : weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
   }
   if ((tid - lane) * per < n) {  // this warp has tokens
     c_lo = __reduce_add_sync(0xFFFFFFFFu, c_lo);
@@ -174,12 +176,12 @@ __device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThrea
   }
   __syncthreads();
   const int m = sh.count_lo;
-  if (m != sh.count_hi) return kUnsure;
+  if (m != sh.count_hi) return false;
   // the draw, by id
   if (m <= kCount) {
     // what the kept tokens of lower ids weigh
     const int each = sharers<kThreads>(m), first = tid / each;
-    if ((tid - lane) / each >= m) return kDone;  // a warp without tokens
+    if ((tid - lane) / each >= m) return true;  // a warp without tokens
     int id[kRank];
     u64 kept = 0, below[kRank];
 #pragma unroll
@@ -206,7 +208,7 @@ __device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThrea
       if (i < m && (tid & (each - 1)) == 0 && below[q] <= target && target < below[q] + sh.w[i])
         write_row(a, st, sh.table, row, id[q], key_value(static_cast<uint32_t>(sh.key[i] >> 32)), kept, m);
     }
-    return kDone;
+    return true;
   }
   // sorted once more, by id: the low word on top descends as the id ascends
   int n2 = 2 * kCount;
@@ -230,51 +232,7 @@ __device__ Decided decide(const SampleArgs& a, const RowState& st, Shared<kThrea
                 key_value(static_cast<uint32_t>(x)), total, m);
     before += w;
   }
-  return kDone;
-}
-
-// Sum of the integer weights of the whole row, by the whole CTA.
-template <int kDtype, int kThreads>
-__device__ __noinline__ u64 exact_total(const Row<kDtype>& r, const RowState& state,
-                                        Shared<kThreads>& sh) {
-  using E = Elem<kDtype>;
-  const RowState st = state;
-  const Pow2Pair k = {f2(st.pw.kh, st.pw.kh), f2(st.pw.kl, st.pw.kl),
-                      static_cast<uint32_t>(st.top) + (__float_as_uint(kPow2Magic) >> 8)};
-  const int nvec = r.nvec(), w0 = r.w0(), w1 = r.w1();
-  const uint4* const vec = r.vec();
-  u64 sum = 0;
-  for (int j0 = threadIdx.x; j0 < nvec; j0 += kUnroll * kThreads) {
-    uint4 x[kUnroll];
-#pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const int j = j0 + n * kThreads;
-      x[n] = j >= w0 && j < w1 ? __ldg(vec + j) : j < nvec ? r.load_edge(j) : neg_inf_vec<kDtype>();
-    }
-#pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      float v[E::kVec];
-      E::unpack(x[n], v);
-      if (st.pw.recentre) {
-#pragma unroll
-        for (int i = 0; i < E::kVec; ++i) sum += weight(v[i], st, sh.table);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E::kVec; i += 2) {
-          u64 a, b;
-          pow2_shifted(f2(fmaxf(v[i], st.zlow), fmaxf(v[i + 1], st.zlow)), k, sh.table, a, b);
-          sum += a + b;
-        }
-      }
-    }
-  }
-  sum = warp_sum(sum);
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = 0;
-  for (int i = 0; i < kThreads / 32; ++i) sum += sh.warp[i];
-  __syncthreads();
-  return sum;
+  return true;
 }
 
 template <int kDtype, int kThreads>
@@ -286,17 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
-  pdl_launch_dependents();  // the wide kernel's CTAs may come as these go; it waits for all of them
   const Settings set = settings_of(a, row);
   const bool list_k = set.k > 0 && set.k <= kListK;
   const bool need_sum = set.k == 0 && set.top_p < 1.f;
   const bool list_min = set.min_p > 0.f && set.top_p >= 1.f;
-  if (set.bad == 0 && !list_k && !need_sum && !list_min) {
-    if (tid == 0) leave_undecided(a, row);
-    return;
-  }
-  if (tid == 0) sh.items = sh.n = 0;
-  for (int i = tid; i < 256; i += kThreads) sh.table[i] = __ldg(&g_pow2_table.t[i]);
+  if (tid == 0) sh.items = sh.n = sh.hopeless = 0;
+  load_tables(sh.table, tid, kThreads);
   RowState st;
   set_temperature(st, set.tau);
 
@@ -437,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     // or units at most; a logit further down is in the last bin, which bounds nothing
     for (int i = tid; i < kBins; i += kThreads) sh.group[i] = 0;
     uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, mykey > kNegInfKey ? mykey : 0xFFFFFFFFu);
-    if (lane == 0) sh.warpu[warp] = lo;
+    if (lane == 0) sh.warp[warp] = lo;  // warpu may still be read
     __syncthreads();
-    lo = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? sh.warpu[lane] : 0xFFFFFFFFu);
+    lo = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? static_cast<uint32_t>(sh.warp[lane]) : 0xFFFFFFFFu);
     const float range = fminf(M - key_value(lo), fmaxf(64.f, 64.f / st.pw.kh));
     const float per_bin = range * (1.f / 254.f), inv = per_bin > 0.f ? 1.f / per_bin : 0.f;
     for (int b = 0; b < blocks; ++b) {
@@ -461,19 +414,35 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       at -= part;
       if (lane == 0) sh.bound = kNegInfKey + 1;
       __syncwarp();
+      int last = -1;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int bin = lane * 8 + i;
         // every maximum of the bins up to this one is above its lower end
-        if (at < want && want <= at + count[i] && bin < 255)
+        if (at < want && want <= at + count[i] && bin < 255) {
           sh.bound = max(key_of(M - (static_cast<float>(bin) + 1.01f) * per_bin), kNegInfKey + 1);
+          last = bin;
+        }
         at += count[i];
+      }
+      if (need_sum) {
+        // a nucleus far beyond the list needs none: what the maxima hold, at most, and half as much more
+        last = __reduce_max_sync(0xFFFFFFFFu, last);
+        float held = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (lane * 8 + i <= last)
+            held += static_cast<float>(count[i]) * ex2_approx(static_cast<float>(-(lane * 8 + i)) * per_bin * st.pw.kh);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) held += __shfl_xor_sync(0xFFFFFFFFu, held, o);
+        if (lane == 0) sh.hopeless = sh.bound > bound && held * 1.5f < set.top_p * sum ? 1 : 0;
       }
     }
     __syncthreads();
     bound = max(bound, sh.bound);
   }
-  bool done = bound > kNegInfKey + 1 || list_min;
+  const bool whole_row = bound <= kNegInfKey + 1;  // all that is not -inf
+  bool done = (list_k || need_sum || list_min) && (!whole_row || list_min || a.V <= kCap) && sh.hopeless == 0;
   bound = max(bound, kNegInfKey + 1);
   if (done) {
     // the blocks to be read again
@@ -485,11 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       int at = 0;
       if (lane == 0) at = atomicAdd(&sh.items, __popc(who));
       at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1u));
-      if (again && at < kCap) sh.item[at] = static_cast<uint16_t>(b * kThreads + tid);
+      if (again && at < kItems<kThreads>) sh.item[at] = static_cast<uint16_t>(b * kThreads + tid);
     }
     __syncthreads();
-    const int items = sh.items <= kCap ? sh.items : 0;  // a block has a token at least
-    if (tid == 0 && sh.items > kCap) sh.n = kCap + 1;
+    const int items = sh.items <= kItems<kThreads> ? sh.items : 0;
+    if (tid == 0 && sh.items > kItems<kThreads>) sh.n = kCap + 1;
     // all their vectors at once, kUnroll of a thread in flight; the scale meanwhile
     const int vecs = items * block;
     for (int i0 = tid; i0 < vecs; i0 += kUnroll * kThreads) {
@@ -528,18 +497,45 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const int n = sh.n;
     done = n <= kCap;
     if (done) {
-      Decided d = decide<kThreads>(a, st, sh, row, set.u, n, set.k, set.top_p, kmin, bound == kmin,
-                                   need_sum ? sum : 0.f, 0);
-      if (d == kUnsure) {
-        // the border is within the fp32 sum's error: the row once more, for its integer weights
-        __syncthreads();
-        const u64 exact = exact_total<kDtype, kThreads>(r, st, sh);
-        d = decide<kThreads>(a, st, sh, row, set.u, n, 0, set.top_p, kmin, bound == kmin, 0.f, exact);
-      }
-      done = d == kDone;
+      // with all tokens in the list, top-p's total is the list's
+      const bool by_sum = need_sum && !whole_row;
+      done = decide<kThreads>(a, st, sh, row, set.u, n, need_sum && whole_row ? n : set.k, set.top_p, kmin,
+                              bound == kmin, by_sum ? sum : 0.f);
     }
   }
-  if (!done && tid == 0) leave_undecided(a, row);
+  if (done) return;
+
+  // ---- all of the row again
+  Deep<kDtype, kThreads> deep{a, sh.deep, sh.scratch, sh.table, sh.warp, sh.total, sh.warpu, r, st, tid, warp, lane};
+  // the scale: a bound of the sum of all, near enough
+  float most = sum;
+  if (!need_sum) {
+    most = 0.f;
+    if (!list_k && !list_min) {  // each block is at most so many times its maximum
+      for (int b = 0; b < blocks; ++b) most += ex2_approx((sh.top[b * kThreads + tid] - M) * st.pw.kh);
+      most *= static_cast<float>(block * E::kVec);
+    } else {  // the maxima are overwritten
+      deep.each(tid, nvec, kThreads, [&](const uint4& y, int) {
+        float v[E::kVec];
+        E::unpack(y, v);
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e) most += ex2_approx((v[e] - M) * st.pw.kh);
+      });
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(0xFFFFFFFFu, most, o);
+    if (lane == 0) sh.warpf[warp] = most;
+    __syncthreads();
+    most = lane < kWarps ? sh.warpf[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(0xFFFFFFFFu, most, o);
+  }
+  most = fmaxf(most, 1.f) * 1.001f;
+  set_scale(deep.st, most);
+  if (!list_k && !need_sum && !list_min && set.k == 0)
+    deep.plain(row, set.u);
+  else
+    deep.filtered(row, set.u, set.k, set.top_p, kmin, most);
 }
 
 template <int kDtype>
@@ -567,18 +563,15 @@ cudaError_t launch_sample(const void* logits, int dtype, int64_t ld, int64_t T, 
   const SampleArgs a = {logits, ld, V, uniform, p.temperature, p.top_k, p.top_p, p.min_p,
                         p.row_temperature, p.row_top_k, p.row_top_p, p.row_min_p, ids, logprob,
                         lse, kept, status};
-  // every row unfiltered: nothing for the list
+  // Every row unfiltered, and few of them: a cluster a row.
   const bool plain = p.row_temperature == nullptr && p.temperature != 0.f &&
                      p.row_top_k == nullptr && (p.top_k <= 0 || p.top_k >= V) &&
                      p.row_top_p == nullptr && p.top_p >= 1.f && p.row_min_p == nullptr &&
                      p.min_p == 0.f;
-  if (!plain) {
-    const cudaError_t e = dtype == TIM_F32    ? launch_list<TIM_F32>(a, T, stream, num_sms)
-                          : dtype == TIM_BF16 ? launch_list<TIM_BF16>(a, T, stream, num_sms)
-                                              : launch_list<TIM_F16>(a, T, stream, num_sms);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_sample_wide(a, dtype, T, plain, stream, num_sms);
+  if (plain && T <= kPlainRows) return launch_sample_plain(a, dtype, T, stream);
+  return dtype == TIM_F32    ? launch_list<TIM_F32>(a, T, stream, num_sms)
+         : dtype == TIM_BF16 ? launch_list<TIM_BF16>(a, T, stream, num_sms)
+                             : launch_list<TIM_F16>(a, T, stream, num_sms);
 }
 
 }  // namespace tim

@@ -31,15 +31,6 @@ struct SampleArgs {
   int* status;
 };
 
-// A row that the list could not decide is the wide kernel's: its out_kept is kUndecided less the
-// number of such rows before it, in no particular order, so that they can be shared out evenly.
-// The rows are counted in the workspace, beside the status word; the wide kernel clears the count.
-constexpr int kUndecided = -1;
-constexpr int kCountWord = 16;
-__device__ __forceinline__ void leave_undecided(const SampleArgs& a, int64_t row) {
-  a.kept[row] = kUndecided - (atomicAdd(a.status + kCountWord, 1) & 0x3FFFFFFF);
-}
-
 // Monotone map of float bits to unsigned (larger float -> larger key; -0 and +0 are one).
 __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t f = __float_as_uint(z + 0.f);
@@ -152,22 +143,55 @@ struct RowState {
   Pow2Row pw;
   Df inv_tau;
   float M;      // largest logit
-  int top;      // a weight w 2^(n - 62) of pow2_fixed is w >> (top - n)
+  int top;      // a weight w 2^(n - 62) is taken as w >> (top - n)
   float zlow;   // logits below have weight 0 and are raised to this one
   uint32_t kc;  // kept: key > kc, or key == kc and id <= idc
   int idc;
 };
 
-__device__ __forceinline__ u64 weight(float z, const RowState& s, const u64* table) {
-  int n;
-  if (s.pw.recentre) {
-    // logits so far apart that a float's step can be many octaves
-    if (!((z - s.pw.c) * s.pw.kh > static_cast<float>(s.top) - 62.5f)) return 0;
-  } else {
-    z = fmaxf(z, s.zlow);
+// The weights.  As pow2_fixed, with what a sum over a row wants: a table of 32 bits (a quarter of
+// the bank conflicts of one of 64), and p from a multiply-add with a number whose last place is 1, so
+// that its bits are 2^31 p and a constant.  2^(j/256) and 1 + p, both at scale 2^31, are each off by
+// 2^-32 and a little, their product at scale 2^62 by less than 2^-30.6.
+constexpr float kUnitMagic = 12582912.f;  // 1.5 * 2^23
+struct Tables {
+  u64 fine[256];  // pow2_fixed's
+  uint32_t t[256];
+};
+__device__ __forceinline__ void load_tables(Tables& tables, int tid, int threads) {
+  for (int i = tid; i < 256; i += threads) {
+    const u64 x = __ldg(&g_pow2_table.t[i]);
+    tables.fine[i] = x;
+    tables.t[i] = static_cast<uint32_t>((x + (1ull << 30)) >> 31);
   }
-  const u64 w = pow2_fixed(z, s.pw, table, n);
-  return w >> min(s.top - n, 63);
+}
+__device__ __forceinline__ u64 weight_of(float t, float g, const uint32_t* table) {
+  const float p = fmaf(g, fmaf(g, fmaf(g, 119194168.0f, 515882496.0f), 1488522236.0f), kUnitMagic);
+  const uint32_t q = __float_as_uint(p) + (0x80000000u - __float_as_uint(kUnitMagic));
+  return static_cast<u64>(table[__float_as_uint(t) & 255u]) * q;
+}
+// Without recentring; `shift` is top + (bits of kPow2Magic >> 8).  Any logit will do: below 2^15 the
+// sum t has a smaller exponent or a sign, its bits then give a shift above 63, and the shift
+// instruction makes that 0.
+__device__ __forceinline__ u64 weight_at(float z, float kh, float kl, uint32_t shift, const uint32_t* table) {
+  const float t = fmaf(z, kh, kPow2Magic);
+  const float g = fmaf(z, kl, fmaf(z, kh, kPow2Magic - t));
+  u64 w = weight_of(t, g, table);
+  asm("shr.u64 %0, %0, %1;" : "+l"(w) : "r"(shift - (__float_as_uint(t) >> 8)));
+  return w;
+}
+__device__ __forceinline__ uint32_t weight_shift(const RowState& s) {
+  return static_cast<uint32_t>(s.top) + (__float_as_uint(kPow2Magic) >> 8);
+}
+__device__ __forceinline__ u64 weight(float z, const RowState& s, const Tables& tables) {
+  if (!s.pw.recentre) return weight_at(z, s.pw.kh, s.pw.kl, weight_shift(s), tables.t);
+  // logits so far apart that a float's step can be many octaves; z - c = d + e exactly
+  if (!((z - s.pw.c) * s.pw.kh > static_cast<float>(s.top) - 62.5f)) return 0;
+  const float d = z - s.pw.c, b = d - z, e = (z - (d - b)) + (-s.pw.c - b);
+  const float t = fmaf(d, s.pw.kh, kPow2Magic);
+  const float g = fmaf(e, s.pw.kh, fmaf(d, s.pw.kl, fmaf(d, s.pw.kh, kPow2Magic - t)));
+  const int n = (__float_as_int(t) - __float_as_int(kPow2Magic)) >> 8;
+  return weight_of(t, g, tables.t) >> min(s.top - n, 63);
 }
 __device__ __forceinline__ bool keeps(uint32_t key, int id, const RowState& s) {
   return key > s.kc || (key == s.kc && id <= s.idc);
@@ -280,15 +304,15 @@ __device__ __forceinline__ void write_bad(const SampleArgs& a, int64_t row, int 
 
 // total: kept weights' sum; x: logit of the token; n: tokens kept; by one thread
 __device__ __forceinline__ void write_row(const SampleArgs& a, const RowState& st,
-                                              const u64* table, int64_t row, int id, float x,
-                                              u64 total, int n) {
+                                          const Tables& tables, int64_t row, int id, float x,
+                                          u64 total, int n) {
   // ln total as a pair: the leading 48 bits, and the scale
   const int lz = __clzll(static_cast<long long>(total));
   const u64 t = total << lz;
   const Df f = renorm(static_cast<float>(static_cast<uint32_t>(t >> 40)) * 0x1p-24f,
                       static_cast<float>(static_cast<uint32_t>(t >> 16) & 0xFFFFFFu) * 0x1p-48f);
   const float e = static_cast<float>(64 - lz + st.top - 62);
-  const Df ln = log_df(f, table) + Df{kLn2Hi, kLn2Lo} * df(e);
+  const Df ln = log_df(f, tables.fine) + Df{kLn2Hi, kLn2Lo} * df(e);
   const float base = st.pw.recentre ? st.pw.c : 0.f;
   const Df lse = ln + df(base) * st.inv_tau;
   a.ids[row] = id;
