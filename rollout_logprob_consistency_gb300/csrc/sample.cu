@@ -41,7 +41,6 @@ constexpr int kBins = 256;
 constexpr int kCount = 512;    // orders by counting up to here
 constexpr int kUnroll = 4;     // vectors of a thread in flight
 constexpr int kMaxima = 5120;  // of blocks of the row, kept while it streams
-constexpr int kPlainRows = 100;  // unfiltered rows up to here are a cluster's each
 constexpr float kSumError = 0x1p-16f;  // of the fp32 sum, see its place
 
 // Blocks to be read again; eight CTAs of 128 threads have to fit an SM.
@@ -252,6 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   load_tables(sh.table, tid, kThreads);
   RowState st;
   set_temperature(st, set.tau);
+  if (set.k == 0 && !need_sum && !list_min) {
+    __syncthreads();
+    Deep<kDtype, kThreads> deep{a, sh.deep, sh.scratch, sh.table, sh.warp, sh.total, sh.warpu, r, st, tid, warp, lane};
+    deep.plain(row, set.u, set.bad);
+    return;
+  }
 
   // ---- one pass: the largest logit of each of the thread's blocks, and the fp32 sum
   const int nvec = r.nvec();
@@ -508,34 +513,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   // ---- all of the row again
   Deep<kDtype, kThreads> deep{a, sh.deep, sh.scratch, sh.table, sh.warp, sh.total, sh.warpu, r, st, tid, warp, lane};
   // the scale: a bound of the sum of all, near enough
-  float most = sum;
-  if (!need_sum) {
+  float most = sum * 1.001f;
+  if (list_k || list_min) {  // the maxima are overwritten
+    most = deep.bound();
+  } else if (!need_sum) {  // each block is at most so many times its maximum
     most = 0.f;
-    if (!list_k && !list_min) {  // each block is at most so many times its maximum
-      for (int b = 0; b < blocks; ++b) most += ex2_approx((sh.top[b * kThreads + tid] - M) * st.pw.kh);
-      most *= static_cast<float>(block * E::kVec);
-    } else {  // the maxima are overwritten
-      deep.each(tid, nvec, kThreads, [&](const uint4& y, int) {
-        float v[E::kVec];
-        E::unpack(y, v);
-#pragma unroll
-        for (int e = 0; e < E::kVec; ++e) most += ex2_approx((v[e] - M) * st.pw.kh);
-      });
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(0xFFFFFFFFu, most, o);
-    if (lane == 0) sh.warpf[warp] = most;
-    __syncthreads();
-    most = lane < kWarps ? sh.warpf[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(0xFFFFFFFFu, most, o);
+    for (int b = 0; b < blocks; ++b) most += ex2_approx((sh.top[b * kThreads + tid] - M) * st.pw.kh);
+    most = deep.total_of(most * static_cast<float>(block * E::kVec));
   }
-  most = fmaxf(most, 1.f) * 1.001f;
   set_scale(deep.st, most);
-  if (!list_k && !need_sum && !list_min && set.k == 0)
-    deep.plain(row, set.u);
-  else
-    deep.filtered(row, set.u, set.k, set.top_p, kmin, most);
+  deep.filtered(row, set.u, set.k, set.top_p, kmin, most);
 }
 
 template <int kDtype>
@@ -563,12 +550,13 @@ cudaError_t launch_sample(const void* logits, int dtype, int64_t ld, int64_t T, 
   const SampleArgs a = {logits, ld, V, uniform, p.temperature, p.top_k, p.top_p, p.min_p,
                         p.row_temperature, p.row_top_k, p.row_top_p, p.row_min_p, ids, logprob,
                         lse, kept, status};
-  // Every row unfiltered, and few of them: a cluster a row.
+  // Every row unfiltered, and few of them: a cluster a row.  151936 logits in bf16: 16 rows 16 us (a CTA
+  // each 29), 38 rows 21 (31), 76 rows 31 (31), 152 rows 45 (33); in fp32 38 rows 27 (31), 76 rows 41 (33).
   const bool plain = p.row_temperature == nullptr && p.temperature != 0.f &&
                      p.row_top_k == nullptr && (p.top_k <= 0 || p.top_k >= V) &&
                      p.row_top_p == nullptr && p.top_p >= 1.f && p.row_min_p == nullptr &&
                      p.min_p == 0.f;
-  if (plain && T <= kPlainRows) return launch_sample_plain(a, dtype, T, stream);
+  if (plain && 3 * T <= num_sms) return launch_sample_plain(a, dtype, T, stream);
   return dtype == TIM_F32    ? launch_list<TIM_F32>(a, T, stream, num_sms)
          : dtype == TIM_BF16 ? launch_list<TIM_BF16>(a, T, stream, num_sms)
                              : launch_list<TIM_F16>(a, T, stream, num_sms);

@@ -114,6 +114,17 @@ __device__ __forceinline__ float max_of(const uint4& u) {
   return m;
 }
 
+// The smallest, of none that is NaN.
+template <int kDtype>
+__device__ __forceinline__ float min_of(const uint4& u) {
+  float v[Elem<kDtype>::kVec];
+  Elem<kDtype>::unpack(u, v);
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < Elem<kDtype>::kVec; ++i) m = fminf(m, v[i]);
+  return m;
+}
+
 // A row's settings; k = 0, top_p >= 1 and min_p = 0 where a filter is off.
 struct Settings {
   float u, tau, top_p, min_p;
@@ -144,16 +155,19 @@ struct RowState {
   Df inv_tau;
   float M;      // largest logit
   int top;      // a weight w 2^(n - 62) is taken as w >> (top - n)
-  float zlow;   // logits below have weight 0 and are raised to this one
   uint32_t kc;  // kept: key > kc, or key == kc and id <= idc
   int idc;
 };
 
-// The weights.  As pow2_fixed, with what a sum over a row wants: a table of 32 bits (a quarter of
-// the bank conflicts of one of 64), and p from a multiply-add with a number whose last place is 1, so
-// that its bits are 2^31 p and a constant.  2^(j/256) and 1 + p, both at scale 2^31, are each off by
-// 2^-32 and a little, their product at scale 2^62 by less than 2^-30.6.
-constexpr float kUnitMagic = 12582912.f;  // 1.5 * 2^23
+// The weights.  2^x = 2^n T[j] (1 + p) as in pow2_fixed, laid out for sums over a row, which the integer
+// pipe bounds:
+//  - n is the whole number next to x, not below it, from one fp32 multiply-add whose last place is 1
+//    (its factor 1 - 2^-24 makes every half go down); T[j] = 2^(j/256) for j <= 128 and 2^(j/256 - 1)
+//    above.  32 bits of it, a quarter of the bank conflicts of 64;
+//  - p from a multiply-add whose last place is 1 as well, so that its bits are 2^31 p and a constant.
+// T and 1 + p at scale 2^31 are each off by 2^-31.5 and 2^-32 and a little: the product, at scale
+// 2^62, by less than 2^-30.5.
+constexpr float kUnitMagic = 12582912.f;  // 1.5 * 2^23: a sum's last place is 1
 struct Tables {
   u64 fine[256];  // pow2_fixed's
   uint32_t t[256];
@@ -161,37 +175,39 @@ struct Tables {
 __device__ __forceinline__ void load_tables(Tables& tables, int tid, int threads) {
   for (int i = tid; i < 256; i += threads) {
     const u64 x = __ldg(&g_pow2_table.t[i]);
+    const int down = i <= 128 ? 31 : 32;
     tables.fine[i] = x;
-    tables.t[i] = static_cast<uint32_t>((x + (1ull << 30)) >> 31);
+    tables.t[i] = static_cast<uint32_t>((x + (1ull << (down - 1))) >> down);
   }
 }
-__device__ __forceinline__ u64 weight_of(float t, float g, const uint32_t* table) {
-  const float p = fmaf(g, fmaf(g, fmaf(g, 119194168.0f, 515882496.0f), 1488522236.0f), kUnitMagic);
-  const uint32_t q = __float_as_uint(p) + (0x80000000u - __float_as_uint(kUnitMagic));
-  return static_cast<u64>(table[__float_as_uint(t) & 255u]) * q;
+// A row's scale as weight_of takes it: a weight w 2^(n - 62) becomes w >> (top - n).
+__device__ __forceinline__ uint32_t shift_of(int top) {
+  return static_cast<uint32_t>(top) + __float_as_uint(kUnitMagic) + static_cast<uint32_t>(kPow2Magic);
 }
-// Without recentring; `shift` is top + (bits of kPow2Magic >> 8).  Any logit will do: below 2^15 the
-// sum t has a smaller exponent or a sign, its bits then give a shift above 63, and the shift
-// instruction makes that 0.
-__device__ __forceinline__ u64 weight_at(float z, float kh, float kl, uint32_t shift, const uint32_t* table) {
-  const float t = fmaf(z, kh, kPow2Magic);
-  const float g = fmaf(z, kl, fmaf(z, kh, kPow2Magic - t));
-  u64 w = weight_of(t, g, table);
-  asm("shr.u64 %0, %0, %1;" : "+l"(w) : "r"(shift - (__float_as_uint(t) >> 8)));
+// t = x + kPow2Magic rounded to 1/256, g = x less that multiple of 1/256.  Any x below 2^14 will do:
+// what is far below the scale gives a shift above 63, or a number without meaning that is as large,
+// and the shift instruction makes that 0.
+__device__ __forceinline__ u64 weight_of(float t, float g, uint32_t shift, const uint32_t* table) {
+  const float p = fmaf(g, fmaf(g, fmaf(g, 119194168.0f, 515882496.0f), 1488522236.0f), kUnitMagic);
+  const float n = fmaf(t, 1.f - 0x1p-24f, kUnitMagic);
+  const uint32_t q = __float_as_uint(p) + (0x80000000u - __float_as_uint(kUnitMagic));
+  u64 w = static_cast<u64>(table[__float_as_uint(t) & 255u]) * q;
+  asm("shr.u64 %0, %0, %1;" : "+l"(w) : "r"(shift - __float_as_uint(n)));
   return w;
 }
-__device__ __forceinline__ uint32_t weight_shift(const RowState& s) {
-  return static_cast<uint32_t>(s.top) + (__float_as_uint(kPow2Magic) >> 8);
+// Without recentring.
+__device__ __forceinline__ u64 weight_at(float z, float kh, float kl, uint32_t shift, const uint32_t* table) {
+  const float t = fmaf(z, kh, kPow2Magic);
+  return weight_of(t, fmaf(z, kl, fmaf(z, kh, kPow2Magic - t)), shift, table);
 }
 __device__ __forceinline__ u64 weight(float z, const RowState& s, const Tables& tables) {
-  if (!s.pw.recentre) return weight_at(z, s.pw.kh, s.pw.kl, weight_shift(s), tables.t);
+  if (!s.pw.recentre) return weight_at(z, s.pw.kh, s.pw.kl, shift_of(s.top), tables.t);
   // logits so far apart that a float's step can be many octaves; z - c = d + e exactly
-  if (!((z - s.pw.c) * s.pw.kh > static_cast<float>(s.top) - 62.5f)) return 0;
+  if (!((z - s.pw.c) * s.pw.kh > static_cast<float>(s.top) - 64.f)) return 0;
   const float d = z - s.pw.c, b = d - z, e = (z - (d - b)) + (-s.pw.c - b);
   const float t = fmaf(d, s.pw.kh, kPow2Magic);
   const float g = fmaf(e, s.pw.kh, fmaf(d, s.pw.kl, fmaf(d, s.pw.kh, kPow2Magic - t)));
-  const int n = (__float_as_int(t) - __float_as_int(kPow2Magic)) >> 8;
-  return weight_of(t, g, tables.t) >> min(s.top - n, 63);
+  return weight_of(t, g, shift_of(s.top), tables.t);
 }
 __device__ __forceinline__ bool keeps(uint32_t key, int id, const RowState& s) {
   return key > s.kc || (key == s.kc && id <= s.idc);
@@ -213,8 +229,6 @@ __device__ __forceinline__ void set_scale(RowState& st, float most) {
   st.pw.c = st.pw.recentre ? st.M : 0.f;
   const int N = st.pw.recentre ? 0 : static_cast<int>(ceilf(mk.h));
   st.top = N + 3 + ilogbf(most);
-  // top - n <= 63 for all logits from here up
-  st.zlow = (static_cast<float>(st.top) - 62.5f) / st.pw.kh;
 }
 
 // Sum over the threads before this one of the CTA, and over all; `warps` of them have any.

@@ -20,13 +20,13 @@ namespace tim {
 namespace sampling {
 
 constexpr int kDeepBins = 256;
-constexpr int kBins = 2048;     // of 1/64 octave, the last one for all below
+constexpr int kBins = 2048;     // of 1/64 octave
 constexpr int kDeepCap = 2048;  // tokens of the border's bins
 constexpr int kSteps = 128;     // 32-vector steps of a 32nd of the row, of 98305 vectors at most: 97
 
 struct DeepShared {
   union {
-    uint32_t bin[kBins];
+    uint32_t bin[kBins + 32];
     u64 list[kDeepCap];  // key << 32 | ~id
     struct {
       uint32_t count[2][kDeepBins], lo[2][kDeepBins], hi[2][kDeepBins];
@@ -36,6 +36,7 @@ struct DeepShared {
 };
 struct DeepScratch {
   uint32_t part_lo[32], part_hi[32];
+  int part_e[32];
   int bin_lo, bin_hi, found;
   uint32_t list_n, digit, in;
   u64 acc, border;
@@ -107,7 +108,8 @@ struct Deep {
     return warp_sum(warp64[lane]);
   }
   // The token at which the running sum first exceeds `target` (below the row's sum), in every
-  // thread; after row_sum(f), by the whole CTA.  one(z, id) is a token's number.
+  // thread; after row_sum(f), by the whole CTA.  one(z, id) is a token's number.  The parts' sums may
+  // be more than their tokens' by a rounding; a part with a sum has a token with one.
   template <class F, class G>
   __device__ __forceinline__ int locate(u64 target, F&& f, G&& one) {
     const u64 of = warp64[lane], to_here = warp_scan(of);
@@ -127,6 +129,9 @@ struct Deep {
       if (lane == 0) sh.step[(j - j0) >> 5] = sum;
     });
     __syncthreads();
+    u64 there = 0;
+    for (int i = lane; i < steps; i += 32) there += sh.step[i];
+    target = min(target, warp_sum(there) - 1);
     int i = 0;
     for (;; i += 32) {
       const u64 x = i + lane < steps ? sh.step[i + lane] : 0, at = warp_scan(x);
@@ -167,6 +172,30 @@ struct Deep {
     const uint32_t old = atomicAdd(lo, wl);
     const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
     if (wh != 0) atomicAdd(hi, wh);
+  }
+
+  // An upper bound, near enough, of the sum of all weights relative to the largest, in every thread.
+  __device__ __forceinline__ float bound() const {
+    float most = 0.f;
+    each(tid, r.nvec(), kThreads, [&](const uint4& x, int) {
+      float v[kVec];
+      E::unpack(x, v);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) most += ex2_approx((v[i] - st.M) * st.pw.kh);
+    });
+    return total_of(most);
+  }
+  __device__ __forceinline__ float total_of(float most) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(0xFFFFFFFFu, most, o);
+    __syncthreads();
+    if (lane == 0) warp32[warp] = __float_as_uint(most);
+    __syncthreads();
+    most = lane < kWarps ? __uint_as_float(warp32[lane]) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(0xFFFFFFFFu, most, o);
+    __syncthreads();
+    return fmaxf(most, 1.f) * 1.001f;
   }
 
   // ---- the border by digits.  Among the tokens that the state keeps: the last one before which
@@ -285,7 +314,7 @@ struct Deep {
   // False: not found this way (the state is as before).
   template <bool kMass>
   __device__ __forceinline__ bool narrow(int k, float p, float most, uint32_t& kept) {
-    const uint32_t shift = weight_shift(st);
+    const uint32_t shift = shift_of(st.top);
     const float zc = key_value(st.kc), M = st.M;
     const bool whole = st.kc == kNegInfKey;  // nothing is dropped yet
     const int nvec = r.nvec();
@@ -310,7 +339,7 @@ struct Deep {
         const float d = M - v[i];
         const int b = __float_as_int(fmaf(d, per, kUnitMagic)) - __float_as_int(kUnitMagic);
         const uint32_t m = kMass ? __float2uint_rn(ex2_approx(fmaf(-d, st.pw.kh, scale))) : 1u;
-        atomicAdd(&sh.bin[min(b, kBins - 1)], m);
+        atomicAdd(&sh.bin[b < kBins ? b : kBins + lane], m);  // all that is far below: not to one word
       }
     });
     __syncthreads();
@@ -346,7 +375,7 @@ struct Deep {
     }
     __syncthreads();
     const int lo = sc.bin_lo, hi = sc.bin_hi;
-    if (lo > hi || hi >= kBins - 1) return false;
+    if (lo > hi || hi >= kBins) return false;
     // a bin holds (M - z) per from half below it to half above
     const float z_hi = M - (static_cast<float>(lo) - 0.51f) / per;
     const float z_lo = M - (static_cast<float>(hi) + 0.51f) / per;
@@ -498,71 +527,156 @@ struct Deep {
       summed = false;
     }
     const float zc = key_value(st.kc);
-    const uint32_t shift = weight_shift(st);
-    // what a vector keeps; slots that are not the row's hold -inf
-    auto kept = [&](const float(&x)[kVec], int id0) {
-      float v[kVec];
-      uint32_t here = 0;
-      if (st.pw.recentre) {
+    auto finish = [&](auto&& kept) {
+      u64 total;
+      uint32_t all = n;
+      if (summed) {
+        total = warp_sum(warp64[lane]);
+      } else {
+        n = 0;
+        total = row_sum(kept);
+        all = count_all(n);
+      }
+      draw(row, u, total, all, kept, one);
+    };
+    if (st.pw.recentre) {
+      finish([&](const float(&v)[kVec], int id0) {
         u64 t = 0;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kVec; ++i) {
-          const u64 w = one(x[i], id0 + i);
-          n += keeps(key_of(x[i]), id0 + i, st) && in_row(id0 + i) ? 1 : 0;
-          t += w;
+          n += keeps(key_of(v[i]), id0 + i, st) && in_row(id0 + i) ? 1 : 0;
+          t += one(v[i], id0 + i);
         }
         return t;
-      }
-      if (st.idc == INT32_MAX) {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) here += x[i] >= zc ? 1 : 0;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) here += x[i] > zc || (x[i] == zc && id0 + i <= st.idc) ? 1 : 0;
-      }
-      if (here == 0) return static_cast<u64>(0);
-      n += here;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = x[i];
-      drop(v, id0, zc);
-      return weights_of(v, shift);
-    };
-    u64 total;
-    uint32_t all = n;
-    if (summed) {
-      total = warp_sum(warp64[lane]);
+      });
     } else {
-      n = 0;
-      total = row_sum(kept);
-      all = count_all(n);
+      const uint32_t shift = shift_of(st.top);
+      // what a vector keeps; slots that are not the row's hold -inf
+      finish([&](const float(&x)[kVec], int id0) {
+        float v[kVec];
+        uint32_t here = 0;
+        if (st.idc == INT32_MAX) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) here += x[i] >= zc ? 1 : 0;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) here += x[i] > zc || (x[i] == zc && id0 + i <= st.idc) ? 1 : 0;
+        }
+        if (here == 0) return static_cast<u64>(0);
+        n += here;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = x[i];
+        drop(v, id0, zc);
+        return weights_of(v, shift);
+      });
     }
-    draw(row, u, total, all, kept, one);
   }
 
-  // ---- the unfiltered row: all tokens but those of -inf are kept
-  __device__ __forceinline__ void plain(int64_t row, float u) {
+  // ---- the unfiltered row: all tokens but those of -inf are kept.  One pass from memory: a lane sums
+  // at a scale of its own, 2^(51 - e) with e at or above its largest x = z K, shifted right where e
+  // grows; at most 2^11.6 tokens of a lane, so below 2^63.  A part's sum is that of its lanes' at
+  // 2^(46 - e) for the largest e, below 2^63 again, and off by 2^-40 of the row's at most.
+  __device__ __forceinline__ void plain(int64_t row, float u, int bad) {
+    const int w0 = r.w0(), w1 = r.w1(), nvec = r.nvec();
+    const uint4* const vec = r.vec();
+    float tmax = -INFINITY;
     uint32_t n = 0;
-    auto one = [&](float z, int) { return weight(z, st, table); };
-    const uint32_t shift = weight_shift(st);
-    auto all = [&](const float(&v)[kVec], int) {
-      float low = v[0];
+    int e = INT32_MIN / 4;
+    for (int q = warp; q < kParts; q += kWarps) {
+      const int end = min(nvec, (q + 1) * part());
+      u64 sum = 0;
+      for (int j0 = q * part() + lane; j0 < end; j0 += kInFlight * 32) {
+        uint4 x[kInFlight];
 #pragma unroll
-      for (int i = 1; i < kVec; ++i) low = fminf(low, v[i]);
-      if (low > -INFINITY) {
-        n += kVec;
-      } else {
+        for (int i = 0; i < kInFlight; ++i) {
+          const int j = j0 + i * 32;
+          if (j >= w0 && j < min(w1, end))
+            x[i] = __ldg(vec + j);
+          else
+            x[i] = j < end ? r.load_edge(j) : neg_inf_vec<kDtype>();
+        }
+        uint4 high = x[0], low = x[0];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) n += v[i] > -INFINITY ? 1 : 0;
+        for (int i = 1; i < kInFlight; ++i) {
+          high = max_vec<kDtype>(high, x[i]);
+          low = min_vec<kDtype>(low, x[i]);
+        }
+        const float most = max_of<kDtype>(high);
+        tmax = max_nan(tmax, most);
+        const int ceil_x = min(__float2int_ru(fmaf(most, st.pw.kh, 0.01f)), 1 << 20);
+        if (ceil_x > e) {
+          sum = ceil_x - e < 64 ? sum >> (ceil_x - e) : 0;
+          e = ceil_x;
+        }
+        const uint32_t shift = shift_of(e + 11);
+        const bool all = min_of<kDtype>(low) > -INFINITY;
+        if (all) n += kInFlight * kVec;
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+          float v[kVec];
+          E::unpack(x[i], v);
+          sum += weights_of(v, shift);
+          if (!all) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) n += v[c] > -INFINITY ? 1 : 0;
+          }
+        }
       }
-      if (!st.pw.recentre) return weights_of(v, shift);
-      u64 t = 0;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) t += one(v[i], 0);
-      return t;
-    };
-    const u64 total = row_sum(all);
-    const uint32_t count = count_all(n);
-    draw(row, u, total, count, all, one);
+      const int high = __reduce_max_sync(0xFFFFFFFFu, e);
+      sum = warp_sum((sum >> 5) >> min(high - e, 63));
+      if (lane == 0) {
+        warp64[q] = sum;
+        sc.part_e[q] = high;
+      }
+    }
+    uint32_t key = !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
+    key = __reduce_max_sync(0xFFFFFFFFu, key);
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0) {
+      warp32[warp] = key;
+      total64[warp] = n;
+    }
+    __syncthreads();
+    key = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? warp32[lane] : 0u);
+    n = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? static_cast<uint32_t>(total64[lane]) : 0u);
+    if (bad == 0 && (key == 0xFFFFFFFFu || key <= kNegInfKey)) bad = TIM_ERR_NONFINITE;
+    if (bad != 0) {
+      if (tid == 0) write_bad(a, row, bad);
+      return;
+    }
+    st.M = key_value(key);
+    auto one = [&](float z, int) { return weight(z, st, table); };
+    if (!(fabsf(st.M * st.pw.kh) < 8000.f)) {
+      // beyond what weight_at splits: again, relative to the largest
+      set_scale(st, bound());
+      auto all = [&](const float(&v)[kVec], int) {
+        u64 t = 0;
+#pragma unroll 1
+        for (int i = 0; i < kVec; ++i) t += one(v[i], 0);
+        return t;
+      };
+      const u64 total = row_sum(all);
+      draw(row, u, total, n, all, one);
+      return;
+    }
+    // the row's scale: its total at 2^58 or 2^59
+    const int part_e = sc.part_e[lane], high = __reduce_max_sync(0xFFFFFFFFu, part_e);
+    const u64 mine = warp64[lane];
+    const u64 about = warp_sum((mine >> 5) >> min(high - part_e, 63));  // at 2^(41 - high)
+    st.pw.recentre = false;
+    st.pw.c = 0.f;
+    st.top = high - 41 + 63 - __clzll(static_cast<long long>(about)) + 4;
+    // The parts at that scale, 2^(62 - top).  One that has less than 2^14 units, 2^-44 of the row, might
+    // have no token of a whole one (2^13.6 tokens a part at most) and is left out.
+    const int d = 16 + part_e - st.top;
+    u64 scaled = d >= 0 ? mine << min(d, 63) : mine >> min(-d, 63);
+    if (scaled < 16384) scaled = 0;
+    __syncthreads();
+    if (warp == 0) warp64[lane] = scaled;
+    const uint32_t shift = shift_of(st.top);
+    const u64 total = warp_sum(scaled);
+    __syncthreads();
+    draw(row, u, total, n, [&](const float(&v)[kVec], int) { return weights_of(v, shift); }, one);
   }
 };
 

@@ -202,7 +202,7 @@ struct Sampler {
         return t;
       }, one);
     } else {
-      const uint32_t shift = weight_shift(st);
+      const uint32_t shift = shift_of(st.top);
       draw(row, u, n, [&](const float(&v)[kVec], int) { return weights_of(v, shift);
       }, one);
     }
