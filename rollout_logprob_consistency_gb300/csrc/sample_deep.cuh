@@ -579,7 +579,8 @@ struct Deep {
   __device__ __forceinline__ void plain(int64_t row, float u, int bad) {
     const int w0 = r.w0(), w1 = r.w1(), nvec = r.nvec();
     const uint4* const vec = r.vec();
-    float tmax = -INFINITY;
+    uint4 high = neg_inf_vec<kDtype>(), low = high;  // of all the lane's vectors so far
+    bool first = true;
     uint32_t n = 0;
     int e = INT32_MIN / 4;
     for (int q = warp; q < kParts; q += kWarps) {
@@ -593,42 +594,55 @@ struct Deep {
           if (j >= w0 && j < min(w1, end))
             x[i] = __ldg(vec + j);
           else
-            x[i] = j < end ? r.load_edge(j) : neg_inf_vec<kDtype>();
+            x[i] = j < end ? r.load_edge(j) : j0 >= w0 && j0 < w1 ? x[0] : neg_inf_vec<kDtype>();
         }
-        uint4 high = x[0], low = x[0];
+        if (first) low = x[0];
+        first = false;
+        const uint4 was = high;
 #pragma unroll
-        for (int i = 1; i < kInFlight; ++i) {
+        for (int i = 0; i < kInFlight; ++i) {
           high = max_vec<kDtype>(high, x[i]);
           low = min_vec<kDtype>(low, x[i]);
         }
-        const float most = max_of<kDtype>(high);
-        tmax = max_nan(tmax, most);
-        const int ceil_x = min(__float2int_ru(fmaf(most, st.pw.kh, 0.01f)), 1 << 20);
-        if (ceil_x > e) {
-          sum = ceil_x - e < 64 ? sum >> (ceil_x - e) : 0;
-          e = ceil_x;
+        if (((high.x ^ was.x) | (high.y ^ was.y) | (high.z ^ was.z) | (high.w ^ was.w)) != 0) {
+          const int ceil_x = min(__float2int_ru(fmaf(max_of<kDtype>(high), st.pw.kh, 0.01f)), 1 << 20);
+          if (ceil_x > e) {
+            sum = ceil_x - e < 64 ? sum >> (ceil_x - e) : 0;
+            e = ceil_x;
+          }
         }
         const uint32_t shift = shift_of(e + 11);
-        const bool all = min_of<kDtype>(low) > -INFINITY;
-        if (all) n += kInFlight * kVec;
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
           float v[kVec];
           E::unpack(x[i], v);
-          sum += weights_of(v, shift);
-          if (!all) {
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) n += v[c] > -INFINITY ? 1 : 0;
-          }
+          const u64 w = weights_of(v, shift);
+          if (j0 + i * 32 < end) sum += w;
         }
       }
-      const int high = __reduce_max_sync(0xFFFFFFFFu, e);
-      sum = warp_sum((sum >> 5) >> min(high - e, 63));
+      const int most_e = __reduce_max_sync(0xFFFFFFFFu, e);
+      sum = warp_sum((sum >> 5) >> min(most_e - e, 63));
       if (lane == 0) {
         warp64[q] = sum;
-        sc.part_e[q] = high;
+        sc.part_e[q] = most_e;
       }
     }
+    // the tokens above -inf: a lane that has met none of it has its vectors' slots
+    for (int q = warp; q < kParts; q += kWarps) {
+      const int j0 = q * part() + lane, end = min(nvec, (q + 1) * part());
+      if (j0 >= end) continue;
+      if (min_of<kDtype>(low) > -INFINITY) {
+        n += static_cast<uint32_t>((end - j0 + 31) / 32) * kVec;
+      } else {
+        each(j0, end, 32, [&](const uint4& x, int) {
+          float v[kVec];
+          E::unpack(x, v);
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) n += v[c] > -INFINITY ? 1 : 0;
+        });
+      }
+    }
+    const float tmax = max_of<kDtype>(high);
     uint32_t key = !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
     key = __reduce_max_sync(0xFFFFFFFFu, key);
     n = __reduce_add_sync(0xFFFFFFFFu, n);
@@ -660,12 +674,12 @@ struct Deep {
       return;
     }
     // the row's scale: its total at 2^58 or 2^59
-    const int part_e = sc.part_e[lane], high = __reduce_max_sync(0xFFFFFFFFu, part_e);
+    const int part_e = sc.part_e[lane], most_e = __reduce_max_sync(0xFFFFFFFFu, part_e);
     const u64 mine = warp64[lane];
-    const u64 about = warp_sum((mine >> 5) >> min(high - part_e, 63));  // at 2^(41 - high)
+    const u64 about = warp_sum((mine >> 5) >> min(most_e - part_e, 63));  // at 2^(41 - most_e)
     st.pw.recentre = false;
     st.pw.c = 0.f;
-    st.top = high - 41 + 63 - __clzll(static_cast<long long>(about)) + 4;
+    st.top = most_e - 41 + 63 - __clzll(static_cast<long long>(about)) + 4;
     // The parts at that scale, 2^(62 - top).  One that has less than 2^14 units, 2^-44 of the row, might
     // have no token of a whole one (2^13.6 tokens a part at most) and is left out.
     const int d = 16 + part_e - st.top;
