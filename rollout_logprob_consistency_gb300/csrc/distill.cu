@@ -57,22 +57,16 @@ enum Saved { kMax = 0, kInvSum, kLogSum, kRest, kHead, kLive };
 
 __device__ __forceinline__ bool in_head(int id, float lp) { return id >= 0 && lp != -INFINITY; }
 
-// Vector j of the row, to the same elements of `out`; one store where the two addresses agree
-// modulo 16 bytes and the vector is whole.
-template <int kDtype>
-__device__ __forceinline__ void store_vector(typename Elem<kDtype>::raw* out, const Row<kDtype>& r,
-                                             int j, bool same,
-                                             const float (&v)[Elem<kDtype>::kVec]) {
-  using E = Elem<kDtype>;
-  if (same && r.whole(j)) {
-    *reinterpret_cast<uint4*>(out - r.shift + static_cast<int64_t>(j) * E::kVec) = E::pack(v);
-    return;
-  }
+// The 16 bytes from byte `at` (below 16) on of the 32 in lo, hi.
+__device__ __forceinline__ uint4 bytes_from(const uint4& lo, const uint4& hi, int at) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-  for (int i = 0; i < E::kVec; ++i) {
-    const int e = j * E::kVec + i - r.shift;
-    if (e >= 0 && e < r.V) out[e] = E::narrow(v[i]);
-  }
+  for (int i = 0; i < 6; ++i) w[i] = (at & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (at & 4) ? w[i + 1] : w[i];
+  const int bits = (at & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 
 struct HeadSums {
@@ -94,54 +88,74 @@ __device__ __forceinline__ void gradient_vector(float (&v)[kVec], F2 ref, F2 k, 
   }
 }
 
-// The gradient of a slice's tokens, c 2^((z - M) log2e / tau), or zeros without a read.
+// The gradient of a slice's tokens, c 2^((z - M) log2e / tau), or zeros without a read.  The slice is of
+// the output's vectors, o; where the input's lie at other addresses modulo 16 bytes, one is put together
+// from two (1122 fp16 rows of 151936 at a stride of 43 more: 458 us with a store an element, see below).
 constexpr int kGradUnroll = 4;  // vectors of a thread in flight
 template <int kDtype, int kThreads>
 __device__ __forceinline__ void gradient_slice(const DistillArgs& a, const Row<kDtype>& r,
-                                               const Slice& s, typename Elem<kDtype>::raw* out,
-                                               float M, float c, bool zero) {
+                                               const Row<kDtype>& o, const Slice& s,
+                                               typename Elem<kDtype>::raw* out, float M, float c,
+                                               bool zero) {
   using E = Elem<kDtype>;
-  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
-  // the vectors that are one load and one store each
-  int j0 = 0, j1 = 0;
-  if (same && s.n > 0) {
-    j0 = r.whole(s.j0) ? 0 : 1;
-    j1 = max(j0, r.whole(s.j0 + s.n - 1) ? s.n : s.n - 1);
-  }
+  if (s.n <= 0) return;
+  // the vectors that are one store each
+  const int j0 = s.j0 + (o.whole(s.j0) ? 0 : 1);
+  const int j1 = max(j0, s.j0 + s.n - (o.whole(s.j0 + s.n - 1) ? 0 : 1));
   const F2 ref = f2(-M, -M), kk = f2(a.kh, a.kh), cc = f2(c, c);
-  const int64_t at = static_cast<int64_t>(s.j0) * E::kVec - r.shift;
-  const uint4* from = reinterpret_cast<const uint4*>(r.p + at);
-  uint4* to = reinterpret_cast<uint4*>(out + at);
+  const int delta = r.shift - o.shift;  // an element's slot in the input less that in the output
+  const uint4* const from = r.vec();
+  uint4* const to = reinterpret_cast<uint4*>(out - o.shift);
+  auto put = [&](int j, const uint4& u) {
+    float v[E::kVec];
+    E::unpack(u, v);
+    gradient_vector(v, ref, kk, cc);
+    __stcs(to + j, E::pack(v));
+  };
   if (zero) {
     for (int j = j0 + threadIdx.x; j < j1; j += kThreads) to[j] = make_uint4(0, 0, 0, 0);
-  } else {
+  } else if (delta == 0) {
     for (int j = j0 + threadIdx.x; j < j1; j += kGradUnroll * kThreads) {
       uint4 u[kGradUnroll];
 #pragma unroll
       for (int n = 0; n < kGradUnroll; ++n)
         if (j + n * kThreads < j1) u[n] = __ldcs(from + j + n * kThreads);
 #pragma unroll
-      for (int n = 0; n < kGradUnroll; ++n) {
-        if (j + n * kThreads < j1) {
-          float v[E::kVec];
-          E::unpack(u[n], v);
-          gradient_vector(v, ref, kk, cc);
-          __stcs(to + j + n * kThreads, E::pack(v));
+      for (int n = 0; n < kGradUnroll; ++n)
+        if (j + n * kThreads < j1) put(j + n * kThreads, u[n]);
+    }
+  } else {
+    const int back = delta < 0 ? 1 : 0, at = (delta + back * E::kVec) * static_cast<int>(sizeof(typename Elem<kDtype>::raw));
+    const int w0 = r.w0(), w1 = r.w1();
+    constexpr int kPairs = kGradUnroll / 2;
+    for (int j = j0 + threadIdx.x; j < j1; j += kPairs * kThreads) {
+      uint4 u[kPairs][2];
+#pragma unroll
+      for (int n = 0; n < kPairs; ++n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = j + n * kThreads - back + h;
+          if (j + n * kThreads < j1) u[n][h] = i >= w0 && i < w1 ? __ldg(from + i) : r.load_edge(i);
         }
+      }
+#pragma unroll
+      for (int n = 0; n < kPairs; ++n)
+        if (j + n * kThreads < j1) put(j + n * kThreads, bytes_from(u[n][0], u[n][1], at));
+    }
+  }
+  // the row's ends, which may be partly others': a thread an element
+  if (static_cast<int>(threadIdx.x) < 2 * E::kVec) {
+    const bool first = static_cast<int>(threadIdx.x) < E::kVec;
+    if (first ? j0 > s.j0 : j1 < s.j0 + s.n) {
+      const int j = first ? s.j0 : s.j0 + s.n - 1;
+      const int e = j * E::kVec + static_cast<int>(threadIdx.x) % E::kVec - o.shift;
+      if (e >= 0 && e < a.V) {
+        float v[2] = {zero ? 0.f : r.at(e), 0.f};
+        if (!zero) gradient_vector(v, ref, kk, cc);
+        out[e] = E::narrow(v[0]);
       }
     }
   }
-  // the others: the row's ends, or all where the output lies otherwise
-  auto edge = [&](int j) {
-    float v[E::kVec] = {};
-    if (!zero) {
-      E::unpack(r.load(s.j0 + j), v);
-      gradient_vector(v, ref, kk, cc);
-    }
-    store_vector<kDtype>(out, r, s.j0 + j, same, v);
-  };
-  if (static_cast<int>(threadIdx.x) < j0) edge(threadIdx.x);
-  for (int j = j1 + threadIdx.x; j < s.n; j += kThreads) edge(j);
 }
 
 // One entry's gradient with respect to s, M the row's maximum.
@@ -305,10 +319,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
       }
     }
     if constexpr (kGrad) {
-      const Row<kDtype> o(out, 0, 0, a.V);  // the output's own vectors
-      const float zeros[E::kVec] = {};
-      for (int j = tid; j < o.nvec(); j += kThreads)
-        store_vector<kDtype>(out, o, j, true, zeros);
+      const Row<kDtype> o(out, 0, 0, a.V);
+      gradient_slice<kDtype, kThreads>(a, r, o, Slice{0, o.nvec()}, out, 0.f, 0.f, true);
     }
     return;
   }
@@ -474,7 +486,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
   if constexpr (kGrad) {
     const float w = __ldg(a.grad + row), g = w * a.inv_h;
     const RowConstants t = s_terms;
-    gradient_slice<kDtype, kThreads>(a, r, Slice{0, nvec}, out, s_M, t.c_rest * t.inv * g, w == 0.f);
+    const Row<kDtype> o(out, 0, 0, a.V);
+    gradient_slice<kDtype, kThreads>(a, r, o, Slice{0, o.nvec()}, out, s_M, t.c_rest * t.inv * g, w == 0.f);
     if (w == 0.f) return;
     __syncthreads();  // the head's tokens are written again, after the whole row
     M = s_M;
@@ -492,21 +505,22 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   using raw = typename E::raw;
   const int64_t row = blockIdx.x / a.parts;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
-  const Slice s = slice_of(r.nvec(), blockIdx.x % a.parts, a.parts);
   raw* out = static_cast<raw*>(a.dlogits) + row * a.ldd;
+  const Row<kDtype> o(out, 0, 0, a.V);
+  const Slice s = slice_of(o.nvec(), blockIdx.x % a.parts, a.parts);
   const float* saved = a.saved + row * TIM_DISTILL_SAVED;
   const float w = __ldg(a.grad + row), live = saved[kLive], g = w * a.inv_h;
   const bool zero = live == 0.f || w == 0.f;
   const float M = saved[kMax], inv = saved[kInvSum];
   // NaN for a row the forward refused
-  gradient_slice<kDtype, kBackThreads>(a, r, s, out, M, live * saved[kRest] * inv * g, zero);
+  gradient_slice<kDtype, kBackThreads>(a, r, o, s, out, M, live * saved[kRest] * inv * g, zero);
   if (zero || live != live) return;
   __syncthreads();
   const float logS = saved[kLogSum];
   for (int k = threadIdx.x; k < a.K; k += kBackThreads) {
     const int id = __ldg(a.ids + row * a.K + k);
     const float lq = __ldg(a.lp + row * a.K + k);
-    const int slot = id + r.shift - s.j0 * E::kVec;
+    const int slot = id + o.shift - s.j0 * E::kVec;
     if (!in_head(id, lq) || id >= a.V || slot < 0 || slot >= s.n * E::kVec) continue;
     out[id] = E::narrow(head_gradient(a, r.at(id), lq, M, logS, inv, saved[kHead]) * g);
   }

@@ -172,6 +172,29 @@ def test_rows_at_any_address(tim, dtype, offset, pad, oo, op):
         assert bool((buf[:, :oo] == 5).all()) and bool((buf[:, oo + V:] == 5).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("offset,pad,oo,op", [(0, 1, 0, 0), (5, 2, 2, 1), (1, 2, 6, 1), (3, 4, 0, 7)])
+def test_wide_rows_between_other_addresses(tim, dtype, offset, pad, oo, op):
+    """Rows of several slices, each at another distance modulo 16 bytes from its gradient's."""
+    import torch
+    T, V = 9, 50021
+    z, ids, lp, w = _inputs(T, V, 40, dtype, 4, pad=pad, offset=offset)
+    ids[2] = -1
+    w[5] = 0.0
+    ref = _reference(z, ids, lp, w, 1.2, "reverse", True)
+    loss, lse, saved = tim.distill(z, ids, lp, 1.2, kind="reverse", tail=True)
+    _assert_loss(loss, lse, ref)
+    for fused in (False, True):
+        buf = torch.full((T, oo + V + op), 5.0, dtype=z.dtype, device="cuda")
+        out = buf[:, oo:oo + V]
+        if fused:
+            tim.distill_grad(z, ids, lp, w, 1.2, kind="reverse", tail=True, out_dlogits=out)
+        else:
+            tim.distill_backward(z, ids, lp, saved, w, 1.2, kind="reverse", out_dlogits=out)
+        _assert_grad(out, ref, fused)
+        assert bool((buf[:, :oo] == 5).all()) and bool((buf[:, oo + V:] == 5).all())
+
+
 @pytest.mark.parametrize("kind,tail", MODES)
 def test_masks_and_empty_rows(tim, kind, tail):
     """Entries that are none, rows without entries (whose logits are not read), masked logits."""

@@ -1,13 +1,13 @@
 """tim.sample on the GPU against the fp64 oracle.
 
 Tokens and kept counts have to be the oracle's wherever no border of a decision lies within
-MARGIN of the mass it is compared with.  The bar: every weight is good to 2^-32 relative, the
-sums are integers near 2^60 with a floor of at most one unit a token (V 2^-60 < 2^-41), so two
-sides of a border are each good to 2^-31: 4 x 2^-31 < 2e-9.  A row within that margin is not
-compared (none of the seeded rows here is).
-logprob and lse are computed in fp64 from such sums and rounded once to fp32: half a step of the
-value, plus 2^-31 for the sum, plus half a step of the float32 row maximum's product (fp64, below
-2^-40): tol = 2^-24 |x| + 2^-29.
+MARGIN of the mass it is compared with.  The bar: every weight is good to 2^-30.5 relative, the
+sums are integers of at least 2^50 with a floor of at most one unit a token (V 2^-50 < 2^-31.4),
+so two sides of a border are each good to 2^-29.9: 2 x 2^-29.9 < 2e-9.  A row within that margin
+is not compared.
+logprob and lse are computed as pairs of floats from such sums and rounded once to fp32: half a
+step of the value, plus 2^-29.9 for the sum, plus the pairs' roundings (below 2^-40):
+tol = 2^-24 |x| + 2^-29.
 """
 import math
 
