@@ -582,8 +582,8 @@ tim_status tim_logprob_noalloc(const void *hidden, const void *gamma, const void
  * logits is [T, V], row stride ld >= V elements (ld <= 2^31), any element-aligned
  * address, of one of the types below; 1 <= T <= 2^31 - 1, 1 <= V <=
  * TIM_LOGITS_MAX_V.  -inf is a token that cannot occur.  A row's results do not
- * depend on T or on the other rows; the float results of the same row at another
- * address modulo 16 bytes may differ in their last bits.
+ * depend on the other rows; the float results of the same row in a batch of another
+ * size or at another address modulo 16 bytes may differ in their last bits.
  * The workspace of these calls holds the status word alone: 1024 bytes, zero-
  * initialised once, and one workspace serves any number of calls at any sizes,
  * on one stream at a time.
@@ -609,9 +609,10 @@ typedef enum tim_dtype { TIM_F32 = 0, TIM_BF16 = 1, TIM_F16 = 2 } tim_dtype;
  *                   kept).
  * temperature = 0 is the greedy choice: the first token of the order, logprob 0,
  * out_lse_kept its logit, one token kept.
- * Sums are held in 64-bit integers of weights exact to 2^-33, so a token differs
- * from exact arithmetic's only if a border lies within about 1e-11 of the row's
- * mass.
+ * Sums are held in 64-bit integers of weights good to 2^-30.5, so a token or a count
+ * differs from exact arithmetic's, or between two batches that hold the row, only if a
+ * border lies within 2e-9 of the row's mass; the float results may then and
+ * otherwise differ in their last bit.
  *
  * params  host memory, read during the call.  row_* are device arrays [T] that
  *         take the place of the scalar beside them, or NULL.  temperature is 0 or

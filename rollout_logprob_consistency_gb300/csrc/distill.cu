@@ -90,7 +90,8 @@ __device__ __forceinline__ void gradient_vector(float (&v)[kVec], F2 ref, F2 k, 
 
 // The gradient of a slice's tokens, c 2^((z - M) log2e / tau), or zeros without a read.  The slice is of
 // the output's vectors, o; where the input's lie at other addresses modulo 16 bytes, one is put together
-// from two (1122 fp16 rows of 151936 at a stride of 43 more: 458 us with a store an element, see below).
+// from two (1122 fp16 rows of 151936 at a stride of 43 more: 458 us with a store an element,
+// 199 so).
 constexpr int kGradUnroll = 4;  // vectors of a thread in flight
 template <int kDtype, int kThreads>
 __device__ __forceinline__ void gradient_slice(const DistillArgs& a, const Row<kDtype>& r,

@@ -9,7 +9,7 @@
 //
 // A token drawn, or the last one that top-p keeps, is decided by sums of up to hundreds of
 // thousands of exponentials against a border: rounding them to 32 bits would move the
-// border past tokens.  Every weight that decides is therefore taken to 2^-33 (pow2_fixed) and
+// border past tokens.  Every weight that decides is therefore taken to 2^-30.5 (weight_of) and
 // summed as a 64-bit integer, at a scale that puts the row's total between 2^50 and 2^60: the
 // sums are exact in that scale and do not depend on the order or the split.
 //
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kCap = 2048;     // tokens of the list
 constexpr int kListK = 1024;   // largest top-k that the list serves
-constexpr int kBins = 256;
+constexpr int kMaximaBins = 256;
 constexpr int kCount = 512;    // orders by counting up to here
 constexpr int kUnroll = 4;     // vectors of a thread in flight
 constexpr int kMaxima = 5120;  // of blocks of the row, kept while it streams
@@ -59,7 +59,7 @@ struct Shared {
     DeepShared deep;
   };
   DeepScratch scratch;
-  uint32_t group[kThreads > kBins ? kThreads : kBins];
+  uint32_t group[kThreads > kMaximaBins ? kThreads : kMaximaBins];
   uint16_t item[kItems<kThreads>];  // blocks to be read again: the places of their maxima
   u64 warp[32], total[kThreads / 32];
   uint32_t warpu[kThreads / 32];
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const uint32_t want = need_sum ? kCount * 3 / 4 : static_cast<uint32_t>(set.k);
     // in 256 bins from the largest logit down, over as much as the threads' maxima span, 64 octaves
     // or units at most; a logit further down is in the last bin, which bounds nothing
-    for (int i = tid; i < kBins; i += kThreads) sh.group[i] = 0;
+    for (int i = tid; i < kMaximaBins; i += kThreads) sh.group[i] = 0;
     uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, mykey > kNegInfKey ? mykey : 0xFFFFFFFFu);
     if (lane == 0) sh.warp[warp] = lo;  // warpu may still be read
     __syncthreads();

@@ -1,8 +1,7 @@
 // Few unfiltered rows: a cluster of CTAs holds a row in shared memory, a slice each, and finds the
-// token by running sums of integer weights.
-//
-// One CTA reads a row of 151936 bf16 logits in 7 us and weighs it in 11; eight of them do both in 4,
-// and add two exchanges.  Many rows are better off with a CTA each (sample.cu).
+// token by running sums of integer weights.  One row of 151936 logits takes 14 us, most of it the
+// launch and the two exchanges; a CTA alone takes 29 for 8 such rows (sample.cu, which says from
+// where on that is the better way).
 //
 // A thread's largest logit gives the scale: the sum over the threads of (largest weight x
 // elements) bounds the row's total, and is at most that many times too large.
@@ -24,7 +23,7 @@ struct PlainArgs : SampleArgs {
 template <int kThreads>
 struct Shared {
   Tables table;
-  u64 xch[2][kMaxCluster][2];
+  u64 xch[kMaxCluster][2];  // every CTA's sum and count
   // of every warp of every CTA: largest key, and the threads' largest weights relative to it
   uint32_t gkey[kMaxCluster * kThreads / 32];
   float gsum[kMaxCluster * kThreads / 32];
@@ -46,20 +45,8 @@ struct Sampler {
   const uint4* slice;
   Row<kDtype> r;
   Slice s;
-  int rank, tid, warp, lane, phase;
+  int rank, tid, warp, lane;
   RowState st;
-
-  // ---- among the CTAs of the row: every CTA's two numbers to every CTA
-  __device__ __forceinline__ void exchange(u64 x, u64 y) {  // called by all; warp 0's values
-    if (warp == 0 && lane < a.cluster) {
-      cluster_store(cluster_addr(&sh.xch[phase & 1][rank][0], lane), x);
-      cluster_store(cluster_addr(&sh.xch[phase & 1][rank][1], lane), y);
-    }
-    cluster_arrive();
-    cluster_wait();
-    ++phase;
-  }
-  __device__ __forceinline__ u64 got(int rank_, int i) const { return sh.xch[(phase - 1) & 1][rank_][i]; }
 
   // id of slot i of the slice's vector j
   __device__ __forceinline__ int id_of(int j, int i) const { return (s.j0 + j) * kVec + i - r.shift; }
@@ -68,8 +55,7 @@ struct Sampler {
   __device__ __forceinline__ int part_steps() const { return (s.n + kThreads - 1) / kThreads; }
   __device__ __forceinline__ int part_start(int w) const { return w * part_steps() * 32; }
 
-  // The sum of f(z, id) over the slice; sh.warp[] gets the parts' sums.  f(v, id0, ends) is the sum
-  // of a vector.
+  // The sum of f(v, id0) over the slice's vectors; sh.warp[] gets the parts' sums.
   template <class F>
   __device__ __forceinline__ u64 slice_sum(F&& f) {
     const int j0 = part_start(warp), j1 = min(s.n, j0 + part_steps() * 32);
@@ -137,18 +123,6 @@ struct Sampler {
     for (int i = 0; i < kVec; ++i) t += weight_at(v[i], st.pw.kh, st.pw.kl, shift, sh.table.t);
     return t;
   }
-  // Sum and count of the whole row from every CTA's.
-  __device__ __forceinline__ u64 total_of(u64 mine, u64 n, u64& all) {
-    exchange(mine, n);
-    u64 t = 0;
-    all = 0;
-    for (int c = 0; c < a.cluster; ++c) {
-      t += got(c, 0);
-      all += got(c, 1);
-    }
-    return t;
-  }
-
   // The draw, f and one being the kept tokens' weights; f counts them in n.
   template <class F, class G>
   __device__ __forceinline__ void draw(int64_t row, float u, uint32_t& n, F&& f, G&& one) {
@@ -158,11 +132,19 @@ struct Sampler {
     __syncthreads();
     uint32_t cta_n = 0;
     for (int i = 0; i < kWarps; ++i) cta_n += sh.warpu[i];
-    u64 all;
-    const u64 total = total_of(mine, cta_n, all);
+    if (warp == 0 && lane < a.cluster) {  // to every CTA of the row
+      cluster_store(cluster_addr(&sh.xch[rank][0], lane), mine);
+      cluster_store(cluster_addr(&sh.xch[rank][1], lane), cta_n);
+    }
+    cluster_arrive();
+    cluster_wait();
+    u64 total = 0, all = 0, before = 0;
+    for (int c = 0; c < a.cluster; ++c) {
+      if (c < rank) before += sh.xch[c][0];
+      total += sh.xch[c][0];
+      all += sh.xch[c][1];
+    }
     const u64 target = draw_target(total, u);
-    u64 before = 0;
-    for (int c = 0; c < rank; ++c) before += got(c, 0);
     if (before <= target && target < before + mine) {  // one CTA of the row
       const int id = locate(target - before, f, one);
       if (tid == 0) write_row(a, st, sh.table, row, id, r.at(id), total, static_cast<int>(all));
@@ -203,8 +185,7 @@ struct Sampler {
       }, one);
     } else {
       const uint32_t shift = shift_of(st.top);
-      draw(row, u, n, [&](const float(&v)[kVec], int) { return weights_of(v, shift);
-      }, one);
+      draw(row, u, n, [&](const float(&v)[kVec], int) { return weights_of(v, shift); }, one);
     }
   }
 };
@@ -232,13 +213,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   load_tables(sh.table, tid, kThreads);
   const Settings set = settings_of(a, row);
   int bad = set.bad;
-  Sampler<kDtype, kThreads> S{a, sh, slice_mem, r, s, rank, tid, warp, lane, 0, {}};
+  Sampler<kDtype, kThreads> S{a, sh, slice_mem, r, s, rank, tid, warp, lane, {}};
   RowState& st = S.st;
   set_temperature(st, set.tau);
   const int never = 0;
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
-  if (!mbar_wait(&sh.bar, 0, &never)) set_status(a.status, TIM_ERR_TIMEOUT);
+  const bool late = !mbar_wait(&sh.bar, 0, &never);  // then the row is refused, by all its CTAs
+  if (late) set_status(a.status, TIM_ERR_TIMEOUT);
 
   // ---- the largest logit of each thread; of each warp, to every CTA of the row
   float tmax = -INFINITY;
@@ -248,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
     for (int j = tid + kThreads; j < s.n; j += kThreads) m = max_vec<kDtype>(m, slice_mem[j]);
     tmax = max_of<kDtype>(m);
   }
-  const uint32_t mykey = !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
+  const uint32_t mykey = late || !(tmax < INFINITY) ? 0xFFFFFFFFu : key_of(tmax);
   const uint32_t wkey = __reduce_max_sync(0xFFFFFFFFu, mykey);
   float sum = 0.f;
   if (wkey > kNegInfKey && wkey != 0xFFFFFFFFu) {
@@ -287,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2)
   }
   cluster_arrive();  // no CTA leaves while another may still write to it
   cluster_wait();
+  if (late) mbar_wait(&sh.bar, 0, &never);  // nor with its copy on the way
 }
 
 template <int kDtype, int kThreads>

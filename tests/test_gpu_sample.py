@@ -343,3 +343,47 @@ def test_two_calls_at_once(tim):
     for i, w in enumerate(want):
         spaces[i].check()
         assert all(torch.equal(x, y) for g in got[i] for x, y in zip(g, w))
+
+
+def _shapes(V, dtype, seed):
+    """Rows of many shapes: flat, steep, rising and falling along the row, one token or one stretch
+    far above the rest, logits that lie octaves apart, a few values alone, mostly masked."""
+    import torch
+    g = np.random.default_rng(seed)
+    z = g.normal(size=(12, V)) * 2.0
+    z[0] *= 0.05
+    z[1] = np.sort(z[1]) * 6
+    z[2] = -np.sort(-z[2]) * 6
+    z[3, V // 3] += 40
+    z[4, V // 2:V // 2 + 50] += 25
+    z[5] *= 900
+    z[6] = 5000 + z[6] * 2
+    z[7] = -9000 + z[7] * 3
+    z[8] = g.integers(-2, 3, size=V)
+    z[9] = np.where(g.random(V) < 0.6, 1.0, z[9])
+    z[10, g.random(V) < 0.9] = -np.inf
+    z[11] -= np.linspace(0, 60, V)
+    return torch.from_numpy(z.astype(np.float32)).cuda().to(_dtype(dtype))
+
+
+DEEP = [dict(), dict(temperature=0.05), dict(temperature=40.0), dict(top_p=0.6), dict(top_p=0.999),
+        dict(top_p=0.97, temperature=3.0), dict(top_p=0.9, min_p=0.3), dict(top_k=1500),
+        dict(top_k=3000, top_p=0.8), dict(top_k=2500, top_p=0.9, min_p=0.05), dict(min_p=0.001)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [12, 60, 200, 400, 700])
+def test_rows_beyond_the_list(tim, dtype, T):
+    import torch
+    base = _shapes(5003, dtype, 50)
+    u = np.random.default_rng(51).random(12).astype(np.float32)
+    at = torch.arange(T, device="cuda") % 12
+    z, ut = base[at].contiguous(), torch.from_numpy(u).cuda()[at]
+    for kw in DEEP:
+        want = _check(tim, base, u, **kw)
+        got = tim.sample(z, ut, **kw)
+        for i in (0, 3):
+            assert torch.equal(got[i], torch.from_numpy(want[i]).cuda()[at]), kw
+        for i in (1, 2):  # equal but for the last bit, see the header
+            w = torch.from_numpy(want[i]).cuda()[at]
+            assert bool(((got[i] - w).abs() <= 2.0 ** -23 * w.abs() + 2.0 ** -29).all()), kw
