@@ -23,6 +23,7 @@ Modules
 ``oracle.diag``     extended per-sequence diagnostics: |delta| quantiles,
                     probability MAE, top-1 flips, sequence TIS, K1/K3 sums,
                     ratio error, MIS weights, mean w^2.
+``oracle.logits_ops`` sampling and top-logit distillation of a row of logits.
 
 Every function cites the page passage it follows.  Pins that tie this oracle to
 something other than itself live in ``tests/test_oracle_pins.py`` and

@@ -449,6 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const bool whole_row = bound <= kNegInfKey + 1;  // all that is not -inf
   bool done = (list_k || need_sum || list_min) && (!whole_row || list_min || a.V <= kCap) && sh.hopeless == 0;
   bound = max(bound, kNegInfKey + 1);
+  // each block is at most so many times its maximum: a bound of the sum of all, for the scale
+  float held = 0.f;
+  if (!need_sum && !list_k) {
+    for (int b = 0; b < blocks; ++b) held += ex2_approx((sh.top[b * kThreads + tid] - M) * st.pw.kh);
+    held *= static_cast<float>(block * E::kVec);
+  }
   if (done) {
     // the blocks to be read again
     const float least = key_value(bound);
@@ -512,15 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 
   // ---- all of the row again
   Deep<kDtype, kThreads> deep{a, sh.deep, sh.scratch, sh.table, sh.warp, sh.total, sh.warpu, r, st, tid, warp, lane};
-  // the scale: a bound of the sum of all, near enough
-  float most = sum * 1.001f;
-  if (list_k || list_min) {  // the maxima are overwritten
-    most = deep.bound();
-  } else if (!need_sum) {  // each block is at most so many times its maximum
-    most = 0.f;
-    for (int b = 0; b < blocks; ++b) most += ex2_approx((sh.top[b * kThreads + tid] - M) * st.pw.kh);
-    most = deep.total_of(most * static_cast<float>(block * E::kVec));
-  }
+  // the scale: a bound of the sum of all, near enough; top-k's maxima are overwritten
+  const float most = need_sum ? sum * 1.001f : list_k ? deep.bound() : deep.total_of(held);
   set_scale(deep.st, most);
   deep.filtered(row, set.u, set.k, set.top_p, kmin, most);
 }
