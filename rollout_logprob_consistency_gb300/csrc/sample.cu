@@ -38,10 +38,15 @@ namespace {
 constexpr int kCap = 2048;     // tokens of the list
 constexpr int kListK = 1024;   // largest top-k that the list serves
 constexpr int kMaximaBins = 256;
-constexpr int kCount = 512;    // orders by counting up to here
+constexpr uint32_t kWant = 384;  // maxima that a top-p list is to hold
 constexpr int kUnroll = 4;     // vectors of a thread in flight
 constexpr int kMaxima = 5120;  // of blocks of the row, kept while it streams
 constexpr float kSumError = 0x1p-16f;  // of the fp32 sum, see its place
+
+// Orders are found by counting up to here, a token a thread at most (rows of a list of 200 take 33 us so
+// against 39 with a sort, 1024 rows of 65 in CTAs of 128 threads 82 against 86 with four a thread).
+template <int kThreads>
+constexpr int kCount = kThreads > 256 ? kThreads / 2 : 128;
 
 // Blocks to be read again; eight CTAs of 128 threads have to fit an SM.
 template <int kThreads>
@@ -54,7 +59,7 @@ struct Shared {
     float top[kMaxima];  // of block b of thread t: top[b kThreads + t]
     struct {
       u64 key[kCap];  // key << 32 | ~id: larger comes first
-      u64 w[kCount];  // of the first tokens
+      u64 w[kCount<kThreads>];  // of the first tokens
     };
     DeepShared deep;
   };
@@ -87,13 +92,13 @@ __device__ __forceinline__ int sharers(int n) {
 // holds all that min-p keeps.  For top-p of the whole row, `sum` > 0 is the row's fp32 total in units
 // of 2^(max K).  False: the list ends before the border, or the border lies within the total's error.
 //
-// Up to kCount tokens the orders are found by counting: a token's comparisons are shared by as many
-// threads as there are, with no barrier between them; above it the squares cost more than a sort.
+// Few tokens' orders are found by counting: a token's comparisons are shared by as many threads as
+// there are, with no barrier between them; for more of them the squares cost more than a sort.
 template <int kThreads>
 __device__ __forceinline__ bool decide(const SampleArgs& a, const RowState& st, Shared<kThreads>& sh,
                                        int64_t row, float u, int n, int k, float top_p,
                                        uint32_t kmin, bool complete, float sum) {
-  constexpr int kRank = kCount > kThreads ? kCount / kThreads : 1;
+  constexpr int kCounted = kCount<kThreads>;
   const int tid = threadIdx.x, lane = tid & 31;
   u64 lo = ~0ull, hi = ~0ull;  // top-p keeps a token while the sum before it is below
   if (sum > 0.f) {
@@ -114,30 +119,21 @@ __device__ __forceinline__ bool decide(const SampleArgs& a, const RowState& st, 
       if (hi > all) return false;
     }
   }
-  if (n <= kCount) {
-    const int each = sharers<kThreads>(n), first = tid / each;
-    u64 mine[kRank];
-    int at[kRank];
-#pragma unroll
-    for (int q = 0; q < kRank; ++q) {
-      const int i = first + q * kThreads;
-      mine[q] = i < n ? sh.key[i] : 0;
-      at[q] = 0;
-    }
+  if (k == 0 && top_p >= 1.f) {
+    // min-p alone: all of the list is kept, in any order
+  } else if (n <= kCounted) {
+    const int each = sharers<kThreads>(n), i = tid / each;
+    const u64 mine = i < n ? sh.key[i] : 0;
+    int at = 0;
     if ((tid - lane) / each < n) {
-      for (int j = tid & (each - 1); j < n; j += each) {
-        const u64 x = sh.key[j];
-#pragma unroll
-        for (int q = 0; q < kRank; ++q) at[q] += x > mine[q] ? 1 : 0;
-      }
+#pragma unroll 4
+      for (int j = tid & (each - 1); j < n; j += each) at += sh.key[j] > mine ? 1 : 0;
     }
-    for (int o = 1; o < each; o <<= 1) at[0] += __shfl_xor_sync(0xFFFFFFFFu, at[0], o);
+    for (int o = 1; o < each; o <<= 1) at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kRank; ++q)
-      if (first + q * kThreads < n && (tid & (each - 1)) == 0) sh.key[at[q]] = mine[q];
+    if (i < n && (tid & (each - 1)) == 0) sh.key[at] = mine;
   } else {
-    int n2 = 2 * kCount;
+    int n2 = 64;
     while (n2 < n) n2 <<= 1;
     for (int i = n + tid; i < n2; i += kThreads) sh.key[i] = 0;
     __syncthreads();
@@ -151,7 +147,7 @@ __device__ __forceinline__ bool decide(const SampleArgs& a, const RowState& st, 
   u64 part = 0;
   for (int i = i0; i < i1; ++i) {
     const u64 w = weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
-    if (i < kCount) sh.w[i] = w;
+    if (i < kCounted) sh.w[i] = w;
     part += w;
   }
   u64 total;
@@ -162,8 +158,8 @@ __device__ __forceinline__ bool decide(const SampleArgs& a, const RowState& st, 
     const bool min_ok = static_cast<uint32_t>(sh.key[i] >> 32) >= kmin;
     c_lo += before < lo && min_ok ? 1 : 0;
     c_hi += before < hi && min_ok ? 1 : 0;
-    before += i < kCount ? sh.w[i]
-                         : weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
+    before += i < kCounted ? sh.w[i]
+                           : weight(key_value(static_cast<uint32_t>(sh.key[i] >> 32)), st, sh.table);
   }
   if ((tid - lane) * per < n) {  // this warp has tokens
     c_lo = __reduce_add_sync(0xFFFFFFFFu, c_lo);
@@ -177,40 +173,29 @@ __device__ __forceinline__ bool decide(const SampleArgs& a, const RowState& st, 
   const int m = sh.count_lo;
   if (m != sh.count_hi) return false;
   // the draw, by id
-  if (m <= kCount) {
+  if (m <= kCounted) {
     // what the kept tokens of lower ids weigh
-    const int each = sharers<kThreads>(m), first = tid / each;
+    const int each = sharers<kThreads>(m), i = tid / each;
     if ((tid - lane) / each >= m) return true;  // a warp without tokens
-    int id[kRank];
-    u64 kept = 0, below[kRank];
-#pragma unroll
-    for (int q = 0; q < kRank; ++q) {
-      const int i = first + q * kThreads;
-      id[q] = i < m ? static_cast<int>(~static_cast<uint32_t>(sh.key[i])) : -1;
-      below[q] = 0;
-    }
+    const int id = i < m ? static_cast<int>(~static_cast<uint32_t>(sh.key[i])) : -1;
+    u64 kept = 0, below = 0;
+#pragma unroll 4
     for (int j = tid & (each - 1); j < m; j += each) {
       const u64 w = sh.w[j];
-      const int other = static_cast<int>(~static_cast<uint32_t>(sh.key[j]));
       kept += w;
-#pragma unroll
-      for (int q = 0; q < kRank; ++q) below[q] += other < id[q] ? w : 0;
+      below += static_cast<int>(~static_cast<uint32_t>(sh.key[j])) < id ? w : 0;
     }
     for (int o = 1; o < each; o <<= 1) {
       kept += __shfl_xor_sync(0xFFFFFFFFu, kept, o);
-      below[0] += __shfl_xor_sync(0xFFFFFFFFu, below[0], o);
+      below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
     }
     const u64 target = draw_target(kept, u);
-#pragma unroll
-    for (int q = 0; q < kRank; ++q) {
-      const int i = first + q * kThreads;
-      if (i < m && (tid & (each - 1)) == 0 && below[q] <= target && target < below[q] + sh.w[i])
-        write_row(a, st, sh.table, row, id[q], key_value(static_cast<uint32_t>(sh.key[i] >> 32)), kept, m);
-    }
+    if (i < m && (tid & (each - 1)) == 0 && below <= target && target < below + sh.w[i])
+      write_row(a, st, sh.table, row, id, key_value(static_cast<uint32_t>(sh.key[i] >> 32)), kept, m);
     return true;
   }
   // sorted once more, by id: the low word on top descends as the id ascends
-  int n2 = 2 * kCount;
+  int n2 = 64;
   while (n2 < m) n2 <<= 1;
   for (int i = tid; i < n2; i += kThreads) {
     const u64 x = sh.key[i];
@@ -390,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       if (share > 0.f)
         bound = max(key_of(M + (__log2f(share) - 0x1p-10f) / st.pw.kh), kmin);
     }
-    const uint32_t want = need_sum ? kCount * 3 / 4 : static_cast<uint32_t>(set.k);
+    const uint32_t want = need_sum ? kWant : static_cast<uint32_t>(set.k);
     // in 256 bins from the largest logit down, over as much as the threads' maxima span, 64 octaves
     // or units at most; a logit further down is in the last bin, which bounds nothing
     for (int i = tid; i < kMaximaBins; i += kThreads) sh.group[i] = 0;
