@@ -126,7 +126,8 @@ __device__ __forceinline__ void gradient_slice(const DistillArgs& a, const Row<k
         if (j + n * kThreads < j1) put(j + n * kThreads, u[n]);
     }
   } else {
-    const int back = delta < 0 ? 1 : 0, at = (delta + back * E::kVec) * static_cast<int>(sizeof(typename Elem<kDtype>::raw));
+    const int back = delta < 0 ? 1 : 0;
+    const int at = (delta + back * E::kVec) * static_cast<int>(sizeof(typename E::raw));
     const int w0 = r.w0(), w1 = r.w1();
     constexpr int kPairs = kGradUnroll / 2;
     for (int j = j0 + threadIdx.x; j < j1; j += kPairs * kThreads) {
@@ -260,6 +261,11 @@ __device__ __forceinline__ void merge(float& m, float& sum, float m2, float s2, 
 // Loss of a row by one CTA that streams it, and with kGrad the gradient in a second pass, which
 // finds the row in L2: a CTA's fixed work is spread over a whole row, and a row's bits cannot
 // depend on the batch.
+//
+// Bound by memory.  2048 rows of 151936 bf16 logits, K = 64: the loss 115 us, 5.4 TB/s (512 threads and
+// two CTAs an SM 136, 128 and eight 121; a cluster of eight CTAs a row with its slice in shared memory
+// 205); with the gradient, a quarter of the rows masked, 234 us for 1.09 GB, 4.7 TB/s (256 and four 249,
+// one of 1024 238, the cluster 260; plain stores and cached second reads 255).
 template <bool kGrad>
 constexpr int kRowThreads = kGrad ? 512 : 256;
 constexpr int kRowUnroll = 4;  // vectors of a thread in flight, and as many being summed
@@ -488,7 +494,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
     const float w = __ldg(a.grad + row), g = w * a.inv_h;
     const RowConstants t = s_terms;
     const Row<kDtype> o(out, 0, 0, a.V);
-    gradient_slice<kDtype, kThreads>(a, r, o, Slice{0, o.nvec()}, out, s_M, t.c_rest * t.inv * g, w == 0.f);
+    gradient_slice<kDtype, kThreads>(a, r, o, Slice{0, o.nvec()}, out, s_M, t.c_rest * t.inv * g,
+                                     w == 0.f);
     if (w == 0.f) return;
     __syncthreads();  // the head's tokens are written again, after the whole row
     M = s_M;
@@ -499,7 +506,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
 }
 
 // The gradient alone, from what the forward saved: a CTA a slice of a row, reading and writing
-// it once; the head's tokens are written again after the slice.
+// it once; the head's tokens are written again after the slice.  Bound by memory: 512 rows of
+// 151936 bf16 logits 52 us, 6.0 TB/s read and written.
 template <int kDtype>
 __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const DistillArgs a) {
   using E = Elem<kDtype>;

@@ -25,6 +25,10 @@
 // with its error bound decides unless the border lies within that error.  A row that this does not
 // decide is read again as often as it takes (sample_deep.cuh).  Few unfiltered rows are a cluster's
 // each (sample_plain.cu).
+//
+// Many rows are bound by memory: 1024 rows of 151936 bf16 logits with top-k 50 and top-p 0.95 take 82 us,
+// 3.8 TB/s; in a CTA's 90 us of life 62 are the stream, 4 the bound, 15 the second look in a loaded
+// memory system, 5 the decision.  One row takes 13 us: 3.5 the stream, the rest that chain.
 #include "sample_deep.cuh"
 
 namespace tim {
@@ -238,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   set_temperature(st, set.tau);
   if (set.k == 0 && !need_sum && !list_min) {
     __syncthreads();
-    Deep<kDtype, kThreads> deep{a, sh.deep, sh.scratch, sh.table, sh.warp, sh.total, sh.warpu, r, st, tid, warp, lane};
+    Deep<kDtype, kThreads> deep{a,        sh.deep, sh.scratch, sh.table, sh.warp, sh.total,
+                                sh.warpu, r,       st,         tid,      warp,    lane};
     deep.plain(row, set.u, set.bad);
     return;
   }
@@ -247,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const int nvec = r.nvec();
   const int steps = (nvec + kThreads - 1) / kThreads;  // vectors of a thread
   // steps of a block: whole groups of kUnroll, as few as there is room for their maxima
-  const int block = (steps + kMaxima / kThreads * kUnroll - 1) / (kMaxima / kThreads * kUnroll) * kUnroll;
+  constexpr int kGroups = kMaxima / kThreads * kUnroll;
+  const int block = (steps + kGroups - 1) / kGroups * kUnroll;
   const int blocks = (steps + block - 1) / block;
   float tmax = -INFINITY, run = -INFINITY;
   // The sum is relative to a reference of the thread that follows its largest logit, 8 octaves late,
@@ -277,7 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 #pragma unroll
         for (int n = 0; n < kUnroll; ++n) {
           const int j = tid + (i + n) * kThreads;
-          x[n] = j < w0 || j >= w1 ? (j < nvec ? r.load_edge(j) : neg_inf_vec<kDtype>()) : __ldg(p + n * kThreads);
+          x[n] = j >= w0 && j < w1 ? __ldg(p + n * kThreads)
+                 : j < nvec        ? r.load_edge(j)
+                                   : neg_inf_vec<kDtype>();
         }
       }
       uint4 m = x[0];
@@ -382,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, mykey > kNegInfKey ? mykey : 0xFFFFFFFFu);
     if (lane == 0) sh.warp[warp] = lo;  // warpu may still be read
     __syncthreads();
-    lo = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? static_cast<uint32_t>(sh.warp[lane]) : 0xFFFFFFFFu);
+    lo = __reduce_min_sync(0xFFFFFFFFu,
+                           lane < kWarps ? static_cast<uint32_t>(sh.warp[lane]) : 0xFFFFFFFFu);
     const float range = fminf(M - key_value(lo), fmaxf(64.f, 64.f / st.pw.kh));
     const float per_bin = range * (1.f / 254.f), inv = per_bin > 0.f ? 1.f / per_bin : 0.f;
     for (int b = 0; b < blocks; ++b) {
@@ -422,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (lane * 8 + i <= last)
-            held += static_cast<float>(count[i]) * ex2_approx(static_cast<float>(-(lane * 8 + i)) * per_bin * st.pw.kh);
+            held += static_cast<float>(count[i]) *
+                    ex2_approx(static_cast<float>(-(lane * 8 + i)) * per_bin * st.pw.kh);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) held += __shfl_xor_sync(0xFFFFFFFFu, held, o);
         if (lane == 0) sh.hopeless = sh.bound > bound && held * 1.5f < set.top_p * sum ? 1 : 0;
@@ -432,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     bound = max(bound, sh.bound);
   }
   const bool whole_row = bound <= kNegInfKey + 1;  // all that is not -inf
-  bool done = (list_k || need_sum || list_min) && (!whole_row || list_min || a.V <= kCap) && sh.hopeless == 0;
+  bool done = (list_k || need_sum || list_min) && (!whole_row || list_min || a.V <= kCap) &&
+              sh.hopeless == 0;
   bound = max(bound, kNegInfKey + 1);
   // each block is at most so many times its maximum: a bound of the sum of all, for the scale
   float held = 0.f;
@@ -495,14 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     if (done) {
       // with all tokens in the list, top-p's total is the list's
       const bool by_sum = need_sum && !whole_row;
-      done = decide<kThreads>(a, st, sh, row, set.u, n, need_sum && whole_row ? n : set.k, set.top_p, kmin,
-                              bound == kmin, by_sum ? sum : 0.f);
+      done = decide<kThreads>(a, st, sh, row, set.u, n, need_sum && whole_row ? n : set.k,
+                              set.top_p, kmin, bound == kmin, by_sum ? sum : 0.f);
     }
   }
   if (done) return;
 
   // ---- all of the row again
-  Deep<kDtype, kThreads> deep{a, sh.deep, sh.scratch, sh.table, sh.warp, sh.total, sh.warpu, r, st, tid, warp, lane};
+  Deep<kDtype, kThreads> deep{a,        sh.deep, sh.scratch, sh.table, sh.warp, sh.total,
+                              sh.warpu, r,       st,         tid,      warp,    lane};
   // the scale: a bound of the sum of all, near enough; top-k's maxima are overwritten
   const float most = need_sum ? sum * 1.001f : list_k ? deep.bound() : deep.total_of(held);
   set_scale(deep.st, most);

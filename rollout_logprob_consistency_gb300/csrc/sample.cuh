@@ -196,7 +196,8 @@ __device__ __forceinline__ u64 weight_of(float t, float g, uint32_t shift, const
   return w;
 }
 // Without recentring.
-__device__ __forceinline__ u64 weight_at(float z, float kh, float kl, uint32_t shift, const uint32_t* table) {
+__device__ __forceinline__ u64 weight_at(float z, float kh, float kl, uint32_t shift,
+                                         const uint32_t* table) {
   const float t = fmaf(z, kh, kPow2Magic);
   return weight_of(t, fmaf(z, kl, fmaf(z, kh, kPow2Magic - t)), shift, table);
 }

@@ -276,7 +276,8 @@ template <int kDtype, int kThreads>
 cudaError_t launch_rows(PlainArgs a, int64_t T, const RowPlan& p, cudaStream_t stream) {
   auto* kernel = sample_plain_kernel<kDtype, kThreads>;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(kernel, plan_row(TIM_LOGITS_MAX_V, sizeof(typename Elem<kDtype>::raw)).slice_bytes, allowed);
+  const RowPlan largest = plan_row(TIM_LOGITS_MAX_V, sizeof(typename Elem<kDtype>::raw));
+  const cudaError_t e = allow_smem(kernel, largest.slice_bytes, allowed);
   if (e != cudaSuccess) return e;
   a.cluster = p.cluster;
   return launch_clusters(kernel, T, p.cluster, kThreads, p.slice_bytes, stream, a);
