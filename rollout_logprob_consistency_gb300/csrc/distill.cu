@@ -29,6 +29,10 @@ namespace {
 constexpr int kBackThreads = 256;
 constexpr int kMaxWarps = 16;
 constexpr float kTailFloor = 0x1p-20f;  // a teacher's tail up to this is rounding
+// A warp's sum outside the head, relative to the head's largest, is taken again from here on: relative to
+// its own largest, so that a row's sum, its reciprocal and their products stay far from fp32's ends, and
+// arguments of 2^x where they are precise.
+constexpr float kRestFar = 0x1p40f;
 constexpr float kTailLeast = 0x1p-100f;  // below this share of the mass the student has no tail
 
 struct DistillArgs {
@@ -222,7 +226,7 @@ __device__ __forceinline__ RowLoss row_loss(const DistillArgs& a, float M, float
   const Df qr = df(1.f) - Q;
   // lane 0: S, lane 1: rest, lane 2: q_r
   const Df x = lane == 0 ? S : lane == 1 ? df(rest) : qr;
-  const bool fine = x.h >= 0x1p-126f && x.h < INFINITY;
+  const bool fine = x.h >= 0x1p-126f && x.h < 0x1p127f;  // what log_df takes
   const Df log_x = fine ? log_df(x) : df(__int_as_float(0x7FC00000));
   const Df logS = bcast(log_x), inv = reciprocal(S);
   const Df pr = df(rest) * inv;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
   __shared__ float redm[kMaxWarps], reds[kMaxWarps], s_hmax[kMaxWarps];
   __shared__ RowConstants s_terms;
   __shared__ float s_M;
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_far;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
 
   const int id0 = tid < a.K ? __ldg(ids + tid) : -1;
   const float lq0 = tid < a.K ? __ldg(lp + tid) : 0.f;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_far = 0;
   for (int i = tid; i < (nvec + 15) / 16; i += kThreads) marks_mem[i] = make_uint4(0, 0, 0, 0);
   auto usable = [&](int id, float lq) { return in_head(id, lq) && id < a.V && lq <= 1.f; };
   const float z0 = usable(id0, lq0) ? r.at(id0) : 0.f;
@@ -423,8 +427,10 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
     }
   };
   publish();
-  // an infinite sum, or a head without mass to refer to: again, with a running maximum
-  if (__syncthreads_or(!(sum < INFINITY) || hmax == -INFINITY)) {
+  if (lane == 0 && !(sum < kRestFar)) s_far = 1;
+  __syncthreads();
+  // far above the head, or a head without mass to refer to: again, with a running maximum
+  if (s_far != 0 || hmax == -INFINITY) {
     m = -INFINITY;
     sum = 0.f;
     for (int j = tid; j < nvec; j += kThreads) {

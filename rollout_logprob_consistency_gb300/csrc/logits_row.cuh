@@ -427,10 +427,10 @@ __device__ __forceinline__ Df exp_df(float x, const unsigned long long* table = 
   return pow2_df(x, Pow2Row{kLog2eHi, kLog2eLo, 0.f, false}, table);
 }
 
-// ln a for a positive finite a: l = ln of the leading bits in fp32, then
+// ln a for 2^-126 <= a < 2^127: l = ln of the leading bits in fp32, then
 // ln a = l + ln(a e^-l) with the small second term from its series.
 __device__ __forceinline__ Df log_df(Df a, const unsigned long long* table = g_pow2_table.t) {
-  const int e = static_cast<int>(__float_as_uint(a.h) >> 23) - 127;  // subnormals are not met
+  const int e = static_cast<int>(__float_as_uint(a.h) >> 23) - 127;
   const float s = __int_as_float((127 - e) << 23);
   const Df f = {a.h * s, a.l * s};
   const float l = __logf(f.h);
