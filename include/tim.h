@@ -649,7 +649,8 @@ tim_status tim_sample(const void *logits, int32_t dtype, int64_t ld, int64_t T, 
  * none; the others form H.  Q = sum_H q_k, P = sum_H p_k.  With tail = 1 the tokens
  * outside H are one more bucket, p_r = 1 - P (summed directly) and q_r = 1 - Q; it
  * is left out where q_r <= 2^-20 (the rounding of the teacher's own numbers) or
- * where no token outside H has any mass.
+ * where no token outside H has any mass: each lies 1074 octaves or more below the row's
+ * largest weight, which is the range of a double (-inf, the lowest value of a type).
  *   TIM_DISTILL_FORWARD_KL  loss = sum_H q_k (ln q_k - ln p_k) [+ q_r (ln q_r - ln p_r)]
  *   TIM_DISTILL_REVERSE_KL  loss = sum_H p_k (ln p_k - ln q_k) [+ p_r (ln p_r - ln q_r)]
  *   out_lse[t] = ln sum_v exp(s_v)

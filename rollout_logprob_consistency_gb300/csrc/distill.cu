@@ -33,7 +33,10 @@ constexpr float kTailFloor = 0x1p-20f;  // a teacher's tail up to this is roundi
 // its own largest, so that a row's sum, its reciprocal and their products stay far from fp32's ends, and
 // arguments of 2^x where they are precise.
 constexpr float kRestFar = 0x1p40f;
-constexpr float kTailLeast = 0x1p-100f;  // below this share of the mass the student has no tail
+// The same where the tail counts and no warp's sum reaches this: p_r may be anything down to
+// kTailOctaves below the row's largest weight, the least that 64 bits hold.
+constexpr float kRestNear = 0x1p-40f;
+constexpr float kTailOctaves = 1074.f;
 
 struct DistillArgs {
   const void* logits;
@@ -57,7 +60,7 @@ struct DistillArgs {
 };
 
 // What the backward needs of a row, as saved by the forward.
-enum Saved { kMax = 0, kInvSum, kLogSum, kRest, kHead, kLive };
+enum Saved { kMax = 0, kInvSum, kLogSum, kRest, kHead, kLive, kRef };
 
 __device__ __forceinline__ bool in_head(int id, float lp) { return id >= 0 && lp != -INFINITY; }
 
@@ -92,7 +95,7 @@ __device__ __forceinline__ void gradient_vector(float (&v)[kVec], F2 ref, F2 k, 
   }
 }
 
-// The gradient of a slice's tokens, c 2^((z - M) log2e / tau), or zeros without a read.  The slice is of
+// The gradient of a slice's tokens, c 2^((z - zref) log2e / tau), or zeros without a read.  The slice is of
 // the output's vectors, o; where the input's lie at other addresses modulo 16 bytes, one is put together
 // from two (1122 fp16 rows of 151936 at a stride of 43 more: 458 us with a store an element,
 // 199 so).
@@ -100,14 +103,14 @@ constexpr int kGradUnroll = 4;  // vectors of a thread in flight
 template <int kDtype, int kThreads>
 __device__ __forceinline__ void gradient_slice(const DistillArgs& a, const Row<kDtype>& r,
                                                const Row<kDtype>& o, const Slice& s,
-                                               typename Elem<kDtype>::raw* out, float M, float c,
-                                               bool zero) {
+                                               typename Elem<kDtype>::raw* out, float zref,
+                                               float c, bool zero) {
   using E = Elem<kDtype>;
   if (s.n <= 0) return;
   // the vectors that are one store each
   const int j0 = s.j0 + (o.whole(s.j0) ? 0 : 1);
   const int j1 = max(j0, s.j0 + s.n - (o.whole(s.j0 + s.n - 1) ? 0 : 1));
-  const F2 ref = f2(-M, -M), kk = f2(a.kh, a.kh), cc = f2(c, c);
+  const F2 ref = f2(-zref, -zref), kk = f2(a.kh, a.kh), cc = f2(c, c);
   const int delta = r.shift - o.shift;  // an element's slot in the input less that in the output
   const uint4* const from = r.vec();
   uint4* const to = reinterpret_cast<uint4*>(out - o.shift);
@@ -177,34 +180,39 @@ __device__ __forceinline__ Df bcast(Df v, int lane = 0) {
 }
 
 // The row's constants in fp32, from which its gradients follow (good to about 2^-22), from the
-// sum `rest` of the weights outside the head relative to M and the head's sums relative to hmax.
+// sum `rest` of the weights outside the head relative to ref, the head's sums relative to hmax, and the
+// row's largest M.  Outside the head the gradient is c_rest inv 2^((z - ref) log2e / tau): where the
+// rest is far below, its tokens' shares of it, which carry q_r, need no number as small as p_r.
 struct RowConstants {
   float inv, logS;  // of the sum relative to M: reciprocal and logarithm
   float c_rest, c_head;
+  bool tail;
 };
 __device__ __forceinline__ RowConstants row_constants(const DistillArgs& a, float M, float hmax,
-                                                      float rest, const HeadSums& h) {
+                                                      float ref, float rest, const HeadSums& h) {
   const bool near = hmax == M || hmax == -INFINITY;
   const float x = near ? 0.f : (hmax - M) * a.kh, shift = x * kLn2Hi;
   const float f = ex2_approx(x);
-  const float P0 = h.e.h * f, S = rest + P0, Q = h.q.h;
+  const float down = ref == M ? 0.f : (ref - M) * a.kh;  // octaves, <= 0
+  const float r = ex2_approx(down), rest_M = rest * r;
+  const float P0 = h.e.h * f, S = rest_M + P0, Q = h.q.h;
   RowConstants t;
   t.inv = 1.f / S;
   t.logS = logf(S);
-  const float P = P0 * t.inv, pr = rest * t.inv;
+  const float P = P0 * t.inv, pr = rest * t.inv;  // p_r is pr r
   const float qr = (df(1.f) - h.q).h;
-  const bool tail = a.tail != 0 && qr > kTailFloor && pr > kTailLeast;
+  t.tail = a.tail != 0 && qr > kTailFloor && rest > 0.f && down > -kTailOctaves;
   if (a.kind == TIM_DISTILL_FORWARD_KL) {
-    t.c_rest = tail ? Q - qr * (P0 / rest) : Q;
-    t.c_head = tail ? Q + qr : Q;
+    t.c_rest = t.tail ? Q * r - qr * (P0 / rest) : Q * r;
+    t.c_head = t.tail ? Q + qr : Q;
   } else {
     float B = (P0 != 0.f ? h.ex.h * f * t.inv - P * (t.logS - shift) : P0) + P;
     t.c_rest = 0.f;
-    if (tail) {
-      t.c_rest = logf(pr / qr) + 1.f;
-      B += pr * t.c_rest;
+    if (t.tail) {
+      t.c_rest = logf(pr / qr) + down * kLn2Hi + 1.f;
+      B += pr * r * t.c_rest;
     }
-    t.c_rest -= B;
+    t.c_rest = (t.c_rest - B) * r;
     t.c_head = 1.f - B;
   }
   return t;
@@ -216,28 +224,31 @@ __device__ __forceinline__ RowConstants row_constants(const DistillArgs& a, floa
 struct RowLoss {
   float loss, lse;
 };
-__device__ __forceinline__ RowLoss row_loss(const DistillArgs& a, float M, float hmax, float rest,
-                                            const HeadSums& h) {
+__device__ __forceinline__ RowLoss row_loss(const DistillArgs& a, float M, float hmax, float ref,
+                                            float rest, const HeadSums& h, bool tail) {
   const int lane = threadIdx.x & 31;
   const bool none = hmax == -INFINITY;  // no token of the head has any mass: all its terms are 0
   const Df shift = none ? df(0.f) : scaled(hmax, M, a);  // <= 0
   const Df f = none || hmax == M ? df(1.f) : pow2_df(hmax, Pow2Row{a.kh, a.kl, M, true});
-  const Df P0 = h.e * f, Q = h.q, S = df(rest) + P0;
+  // what is far below the largest counts in S with fp32's relative precision, and no more is seen of it
+  const Df down = ref == M ? df(0.f) : scaled(ref, M, a);  // <= 0
+  const float rest_M = ref == M ? rest : rest * ex2_approx((ref - M) * a.kh);
+  const Df P0 = h.e * f, Q = h.q, S = df(rest_M) + P0;
   const Df qr = df(1.f) - Q;
   // lane 0: S, lane 1: rest, lane 2: q_r
   const Df x = lane == 0 ? S : lane == 1 ? df(rest) : qr;
   const bool fine = x.h >= 0x1p-126f && x.h < 0x1p127f;  // what log_df takes
   const Df log_x = fine ? log_df(x) : df(__int_as_float(0x7FC00000));
   const Df logS = bcast(log_x), inv = reciprocal(S);
-  const Df pr = df(rest) * inv;
+  const Df pr = df(rest_M) * inv;
   const Df up = logS - shift;                                 // ln p_k = x_k - up
-  const Df ar = bcast(log_x, 1) - logS - bcast(log_x, 2);     // ln p_r - ln q_r
+  const Df ar = bcast(log_x, 1) + down - logS - bcast(log_x, 2);  // ln p_r - ln q_r
   Df L;
   if (a.kind == TIM_DISTILL_FORWARD_KL)
     L = h.qx + Q * up;
   else
     L = P0.h != 0.f ? ((h.ex * f) - P0 * up) * inv : P0;
-  if (a.tail != 0 && qr.h > kTailFloor && pr.h > kTailLeast)
+  if (tail)
     L = a.kind == TIM_DISTILL_FORWARD_KL ? L - qr * ar : L + pr * ar;
   return {L.h, (df(M) * Df{a.inv_h, a.inv_l} + logS).h};
 }
@@ -283,8 +294,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
   __shared__ HeadSums red[kMaxWarps];
   __shared__ float redm[kMaxWarps], reds[kMaxWarps], s_hmax[kMaxWarps];
   __shared__ RowConstants s_terms;
-  __shared__ float s_M;
-  __shared__ int s_bad, s_far;
+  __shared__ float s_M, s_ref;
+  __shared__ int s_bad, s_far, s_near;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;
   const Row<kDtype> r(a.logits, row, a.ld, a.V);
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
 
   const int id0 = tid < a.K ? __ldg(ids + tid) : -1;
   const float lq0 = tid < a.K ? __ldg(lp + tid) : 0.f;
-  if (tid == 0) s_bad = s_far = 0;
+  if (tid == 0) s_bad = s_far = s_near = 0;
   for (int i = tid; i < (nvec + 15) / 16; i += kThreads) marks_mem[i] = make_uint4(0, 0, 0, 0);
   auto usable = [&](int id, float lq) { return in_head(id, lq) && id < a.V && lq <= 1.f; };
   const float z0 = usable(id0, lq0) ? r.at(id0) : 0.f;
@@ -428,9 +439,16 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
   };
   publish();
   if (lane == 0 && !(sum < kRestFar)) s_far = 1;
+  if (lane == 0 && sum >= kRestNear) s_near = 1;
   __syncthreads();
-  // far above the head, or a head without mass to refer to: again, with a running maximum
-  if (s_far != 0 || hmax == -INFINITY) {
+  bool again = s_far != 0 || hmax == -INFINITY;
+  if (a.tail != 0 && s_near == 0) {
+    Df Q = df(0.f);
+    for (int i = 0; i < head_warps; ++i) Q = Q + red[i].q;
+    again |= (df(1.f) - Q).h > kTailFloor * 0.5f;
+  }
+  // far above the head, far below it, or a head without mass to refer to: again, with a running maximum
+  if (again) {
     m = -INFINITY;
     sum = 0.f;
     for (int j = tid; j < nvec; j += kThreads) {
@@ -453,6 +471,7 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
   const float nan = __int_as_float(0x7FC00000);
   HeadSums hs = {};
   float M = 0.f;
+  bool tail = false;
   if (warp == 0) {
     m = lane < warps ? redm[lane] : -INFINITY;
     sum = lane < warps ? reds[lane] : 0.f;
@@ -465,12 +484,14 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
     if (head_warps > 1) hs = warp_sum(hs, 8);
     hs = HeadSums{bcast(hs.e), bcast(hs.q), bcast(hs.qx), bcast(hs.ex)};
     M = fmaxf(hmax, m);
-    if (m != -INFINITY) sum *= ex2_approx((m - M) * k2);
+    if (m == -INFINITY) m = M;  // nothing outside
+    RowConstants c = row_constants(a, M, hmax, m, sum, hs);
+    tail = c.tail;
     if (lane == 0) {
-      RowConstants c = row_constants(a, M, hmax, sum, hs);
       if (s_bad != 0) c.c_rest = c.c_head = nan;
       s_terms = c;
       s_M = M;
+      s_ref = m;
       if constexpr (!kGrad) {
         float* saved = a.saved + row * TIM_DISTILL_SAVED;
         saved[kMax] = M;
@@ -479,14 +500,15 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
         saved[kRest] = c.c_rest;
         saved[kHead] = c.c_head;
         saved[kLive] = s_bad != 0 ? nan : 1.f;
-        saved[kLive + 1] = saved[kLive + 2] = 0.f;
+        saved[kRef] = m;
+        saved[kRef + 1] = 0.f;
       }
     }
     __syncwarp();
   }
   if (kGrad) __syncthreads();
   if (warp == 0) {  // nothing waits for the loss
-    const RowLoss v = row_loss(a, M, hmax, sum, hs);
+    const RowLoss v = row_loss(a, M, hmax, m, sum, hs, tail);
     if (lane == 0) {
       if (s_bad != 0)
         set_status(a.status, s_bad);
@@ -500,8 +522,8 @@ __global__ void __launch_bounds__(kRowThreads<kGrad>, kGrad ? 2 : 4)
     const float w = __ldg(a.grad + row), g = w * a.inv_h;
     const RowConstants t = s_terms;
     const Row<kDtype> o(out, 0, 0, a.V);
-    gradient_slice<kDtype, kThreads>(a, r, o, Slice{0, o.nvec()}, out, s_M, t.c_rest * t.inv * g,
-                                     w == 0.f);
+    gradient_slice<kDtype, kThreads>(a, r, o, Slice{0, o.nvec()}, out, s_ref,
+                                     t.c_rest * t.inv * g, w == 0.f);
     if (w == 0.f) return;
     __syncthreads();  // the head's tokens are written again, after the whole row
     M = s_M;
@@ -528,7 +550,8 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   const bool zero = live == 0.f || w == 0.f;
   const float M = saved[kMax], inv = saved[kInvSum];
   // NaN for a row the forward refused
-  gradient_slice<kDtype, kBackThreads>(a, r, o, s, out, M, live * saved[kRest] * inv * g, zero);
+  gradient_slice<kDtype, kBackThreads>(a, r, o, s, out, saved[kRef], live * saved[kRest] * inv * g,
+                                       zero);
   if (zero || live != live) return;
   __syncthreads();
   const float logS = saved[kLogSum];

@@ -128,3 +128,60 @@ def test_outside_far_above_the_head(tim, dtype, tau, weight, layout, kind, tail)
     """A finite row has a finite loss and a gradient of full precision, whatever the sum outside the
     head is relative to the head's largest."""
     _check(tim, *_apart(ABOVE, layout, dtype, tau, weight), tau, kind, tail)
+
+
+BELOW = [-x * math.log(2) for x in (20, 39, 41, 53, 60, 90, 99, 101, 104, 115, 120, 125, 127, 140, 160,
+                                    300, 700, 1000)]
+
+
+@pytest.mark.parametrize("kind,tail", MODES)
+@pytest.mark.parametrize("layout", ["one", "all"])
+@pytest.mark.parametrize("dtype,tau", [("f32", 1.0), ("f32", 0.1), ("f32", 1e-3), ("bf16", 1.0), ("f16", 1.0)])
+def test_outside_far_below_the_head(tim, dtype, tau, layout, kind, tail):  # noqa: F811
+    """The rest keeps its bucket, loss and gradient, as long as it has any mass."""
+    _check(tim, *_apart(BELOW, layout, dtype, tau, 1.0), tau, kind, tail)
+
+
+def test_rest_of_one_token_by_hand(tim):  # noqa: F811
+    """p_r = e^-72, q = (0.9, 0.1): L = 0.9 ln 0.9 + 0.1 (ln 0.1 + 72), gradient 0.1 and -0.1."""
+    import torch
+    z = torch.full((1, 300), -400.0, device="cuda")
+    z[0, 7], z[0, 250] = 20.0, -52.0
+    ids = torch.tensor([[7]], dtype=torch.int32, device="cuda")
+    lp = torch.tensor([[0.9]], device="cuda").log()
+    one = torch.ones(1, device="cuda")
+    loss, grad = tim.distill_grad(z, ids, lp, one, tail=True)
+    assert float(loss) == pytest.approx(0.9 * math.log(0.9) + 0.1 * (math.log(0.1) + 72), rel=1e-6)
+    want = torch.zeros(300)
+    want[7], want[250] = 0.1, -0.1
+    assert float((grad[0].cpu() - want).abs().max()) <= 1e-6
+
+
+def test_rest_without_mass(tim):  # noqa: F811
+    """-inf, the type's lowest value, and whatever is more than 1074 octaves down: no bucket."""
+    import torch
+    z, ids, lp, w = _apart([-60.0] * 4, "all", "f32", 1.0, 1.0)
+    out = torch.ones_like(z, dtype=torch.bool).scatter_(1, ids.long(), False)
+    for i, low in enumerate((-math.inf, torch.finfo(torch.float32).min, -800.0, -750.0)):
+        z[i, out[i]] = low
+    for kind in ("forward", "reverse"):
+        a = tim.distill_grad(z, ids, lp, w, kind=kind, tail=True)
+        b = tim.distill_grad(z, ids, lp, w, kind=kind, tail=False)
+        assert torch.equal(a[0][:3], b[0][:3]) and torch.equal(a[1][:3], b[1][:3])
+        assert bool(a[0].isfinite().all()) and bool(a[1].isfinite().all())
+
+
+@pytest.mark.parametrize("kind,tail", MODES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [1e-6, 1e-4, 0.05, 0.3, 1.0, 40.0, 1e6])
+def test_every_temperature_in_every_call(tim, tau, dtype, kind, tail):  # noqa: F811
+    import torch
+    g = np.random.default_rng(23)
+    T, V, K = 6, 2003, 16
+    z = torch.from_numpy((g.normal(size=(T, V)) * 2).astype(np.float32)).cuda().to(_dtype(dtype))
+    ids = torch.from_numpy(np.stack([g.permutation(V)[:K] for _ in range(T)]).astype(np.int32)).cuda()
+    z[T // 2:].scatter_(1, ids[T // 2:].long(), z[T // 2:].gather(1, ids[T // 2:].long()) + 9)
+    t = g.normal(size=(T, K)) * 2
+    lp = torch.from_numpy((t - np.log(np.exp(t).sum(1, keepdims=True)) - 0.1).astype(np.float32)).cuda()
+    w = torch.from_numpy(g.normal(size=T).astype(np.float32)).cuda()
+    _check(tim, z, ids, lp, w, tau, kind, tail)
