@@ -730,7 +730,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, o
     if isinstance(top_k, torch.Tensor):
         p.row_top_k = _vector(top_k, i32, T, dev, "top_k")
     else:
-        p.top_k = int(top_k)
+        p.top_k = min(max(int(top_k), 0), 2 ** 31 - 1)  # ctypes would keep the low 32 bits
     if isinstance(top_p, torch.Tensor):
         p.row_top_p = _vector(top_p, f32, T, dev, "top_p")
     else:
