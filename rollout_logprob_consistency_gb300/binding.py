@@ -698,12 +698,23 @@ def _run(dev, stream, call):
     call allocates belongs to the stream that uses it."""
     torch = _torch()
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be on {dev}")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream or None)
     if torch.cuda.current_device() == dev.index:
         return call(torch._C._cuda_getCurrentRawStream(dev.index) or None)
     with torch.cuda.device(dev):
         return call(torch._C._cuda_getCurrentRawStream(dev.index) or None)
+
+
+def _status_workspace(workspace, dev, stream):
+    """The caller's workspace, on ``dev``, or one of this call's own."""
+    if workspace is None:
+        return Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+    if workspace.buf.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    return workspace
 
 
 def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, out=None,
@@ -748,7 +759,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, o
         if o is None:  # views of one allocation would take the host longer than four
             o = (torch.empty(T, dtype=i32, device=dev), torch.empty(T, dtype=f32, device=dev),
                  torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=i32, device=dev))
-        ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        ws = _status_workspace(workspace, dev, stream)
         _check(lib().tim_sample(logits.data_ptr(), code, ld, T, V, u, _c.byref(p), o[0].data_ptr(),
                                 o[1].data_ptr(), o[2].data_ptr(), o[3].data_ptr(), ws.ptr,
                                 ws.nbytes, sp), "tim_sample")
@@ -799,7 +810,7 @@ def distill(logits, teacher_ids, teacher_logprob, temperature: float = 1.0, *,
         if o is None:
             o = (torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev),
                  torch.empty(T, DISTILL_SAVED, dtype=f32, device=dev))
-        ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        ws = _status_workspace(workspace, dev, stream)
         _check(lib().tim_distill(logits.data_ptr(), code, ld, T, V, teacher_ids.data_ptr(),
                                  teacher_logprob.data_ptr(), K, temperature, kd, int(bool(tail)),
                                  o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), ws.ptr,
@@ -864,7 +875,7 @@ def distill_grad(logits, teacher_ids, teacher_logprob, grad_loss, temperature: f
         if o is None:
             o = torch.empty(T, V, dtype=logits.dtype, device=dev)
         loss = torch.empty(T, dtype=torch.float32, device=dev)
-        ws = workspace or Workspace(LOGITS_WORKSPACE_BYTES, dev, stream)
+        ws = _status_workspace(workspace, dev, stream)
         _check(lib().tim_distill_grad(logits.data_ptr(), code, ld, T, V, teacher_ids.data_ptr(),
                                       teacher_logprob.data_ptr(), K, temperature, kd,
                                       int(bool(tail)), g, loss.data_ptr(), o.data_ptr(), ldd,
