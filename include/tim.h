@@ -662,7 +662,9 @@ tim_status tim_sample(const void *logits, int32_t dtype, int64_t ld, int64_t T, 
  * out_saved for the same arguments.
  *
  * tim_distill_grad: out_loss of tim_distill and out_dlogits of tim_distill_backward in
- * one call, for weights grad_loss that are known beforehand: logits is read once.
+ * one call, for weights grad_loss that are known beforehand.  A row's second reading follows
+ * its first and comes from L2 as far as the rows in flight, two an SM, fit there: most of it
+ * with 16-bit logits, little with wide fp32 rows.
  *
  * teacher_ids  int32 [T, K]; teacher_logprob float32 [T, K]; 1 <= K <=
  *              TIM_DISTILL_MAX_K.  temperature in [1e-6, 1e6].

@@ -862,8 +862,8 @@ def distill_grad(logits, teacher_ids, teacher_logprob, grad_loss, temperature: f
                  kind: str = "forward", tail: bool = False, out_dlogits=None,
                  workspace: Optional[Workspace] = None, stream=None, check: bool = True):
     """The loss of ``distill`` and the gradient of ``distill_backward`` for row weights
-    ``grad_loss`` float32 [T] that are known beforehand (tim_distill_grad): ``logits`` is read
-    once.  Returns (loss f32 [T], dlogits)."""
+    ``grad_loss`` float32 [T] that are known beforehand (tim_distill_grad): a row's second reading
+    follows its first and comes from L2 as far as it is still there.  Returns (loss f32 [T], dlogits)."""
     torch = _torch()
     T, V, code, ld, K, kd = _distill_args(logits, teacher_ids, teacher_logprob, kind)
     dev = logits.device

@@ -369,8 +369,6 @@ constexpr Pow2Table make_pow2_table() {
   return T;
 }
 
-constexpr int kPow2Bits = 8;
-
 // What a row's logits are raised with: 2^((z - c) K), where c is subtracted only if `recentre`.
 struct Pow2Row {
   float kh, kl;  // K = log2(e) / temperature

@@ -10,8 +10,9 @@
 // A token drawn, or the last one that top-p keeps, is decided by sums of up to hundreds of
 // thousands of exponentials against a border: rounding them to 32 bits would move the
 // border past tokens.  Every weight that decides is therefore taken to 2^-30.5 (weight_of) and
-// summed as a 64-bit integer, at a scale that puts the row's total between 2^50 and 2^60: the
-// sums are exact in that scale and do not depend on the order or the split.
+// summed as a 64-bit integer, at a scale that puts the total between 2^50 and 2^60 (a list's, of 2048
+// tokens at most, between 2^47 and 2^60): the sums are exact in that scale and do not depend on the
+// order or the split, and what a token loses below one unit is 2^-31 of the total for all together.
 //
 // A row has one CTA, which reads it from memory once: while it streams, every thread notes the
 // largest logits of blocks of its vectors (and, for top-p alone, a running sum in fp32).  They bound

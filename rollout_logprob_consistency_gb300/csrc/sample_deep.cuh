@@ -338,8 +338,9 @@ struct Deep {
       sc.all = 1;
     }
     __syncthreads();
-    // ---- the bins.  Masses at a scale at which they sum to less than 2^32, rounded: V / 2 units of
-    // 2^-31 of the total, or 1e-4, are the largest error.
+    // ---- the bins.  Masses at a scale at which they sum to 2^30 up to 2^32, each rounded to a whole unit:
+    // V / 2 of them, 7e-5 of the sum at V = 151936 and within the 2^-13 below up to V = 262144.  Where the
+    // error is larger the list may not hold the border, which shows, and digits find it.
     const float per = 64.f * st.pw.kh, scale = static_cast<float>(30 - ilogbf(most));
     each(tid, nvec, kThreads, [&](const uint4& x, int j) {
       float v[kVec];
