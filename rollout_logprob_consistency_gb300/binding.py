@@ -921,7 +921,9 @@ def distill_loss(logits, teacher_ids, teacher_logprob, temperature: float = 1.0,
                  workspace: Optional[Workspace] = None, check: bool = True):
     """Differentiable per-row distillation loss f32 [T] (gradient with respect to ``logits``
     alone, once): ``distill`` forward, ``distill_backward`` backward.  Runs on the current
-    stream."""
+    stream.  To capture a step into a graph call ``distill`` and ``distill_backward``, or
+    ``distill_grad``, themselves: autograd's backward must not be captured while an eager
+    graph of the same leaf lives."""
     global _DISTILL
     if _DISTILL is None:
         _DISTILL = _distill_function()
