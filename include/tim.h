@@ -699,6 +699,40 @@ tim_status tim_distill_backward(const void *logits, int32_t dtype, int64_t ld, i
                                 void *out_dlogits, int64_t ldd, tim_stream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Embedding lookup, and its gradient.
+ *
+ *   out[t, i]    = scale table[ids[t], i]               (fp32 product, rounded once)
+ *   dtable[v, i] = scale sum_{t: ids[t] = v} dy[t, i]   (fp32 sums in a fixed order)
+ * ids[t] = -1 is no token: a row of zeros, and no gradient.  With a table tied to the
+ * LM head, accumulate = 1 adds to the out_dW of tim_logprob_backward, the other half of
+ * that matrix's gradient; rows that no token names are then not touched, with 0 they
+ * are zeroed.  The same call gives the same bits; a row's last bits may depend on the
+ * other tokens (on where the sorted batch is cut).
+ *
+ * table        [V, d] of dtype, row stride ld >= d;  out [T, d] of dtype, row stride ldo;
+ *              must not meet table.
+ * dy           [T, d] of dtype, row stride ldy;  out_dtable [V, d] contiguous, of
+ *              out_dtype (TIM_F32 or dtype); must not meet dy.  In 16 bits a row is rounded
+ *              once a call; with more than 131072 tokens, once every so many.
+ * T >= 1 (up to 2^31 - 1), 1 <= V <= 2^31 - 256, 1 <= d <= 65536, strides up to 2^31;
+ * scale finite.  Any element-aligned address; rows of whole 16-byte vectors are faster.
+ * workspace    tim_embed: 1024 bytes; tim_embed_backward: tim_embed_backward_workspace_size
+ *              bytes, which serve smaller T and tim_embed too; zero-initialised once.
+ * Errors as tim_sample.  Via tim_status_sync: TIM_ERR_TOKEN_RANGE (an id below -1 or from V
+ *   up: NaN in its row of out, no part in dtable).
+ * ------------------------------------------------------------------------ */
+tim_status tim_embed(const void *table, int32_t dtype, int64_t ld, const int32_t *ids, int64_t T,
+                     int32_t V, int32_t d, float scale, void *out, int64_t ldo, void *workspace,
+                     size_t workspace_bytes, tim_stream_t stream);
+
+size_t tim_embed_backward_workspace_size(int64_t T, int32_t V, int32_t d);
+
+tim_status tim_embed_backward(const void *dy, int32_t dtype, int64_t ldy, const int32_t *ids,
+                              int64_t T, int32_t V, int32_t d, float scale, void *out_dtable,
+                              int32_t out_dtype, int32_t accumulate, void *workspace,
+                              size_t workspace_bytes, tim_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Self-test of the bounded waits (the pages have no counterpart: it exercises
  * this library's own failure detection).  Every mbarrier wait in the LM-head
  * kernel gives up after a time limit, records TIM_ERR_TIMEOUT in the status

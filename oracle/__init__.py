@@ -24,6 +24,8 @@ Modules
                     probability MAE, top-1 flips, sequence TIS, K1/K3 sums,
                     ratio error, MIS weights, mean w^2.
 ``oracle.logits_ops`` sampling and top-logit distillation of a row of logits.
+``oracle.ends``     verification of drafted tokens, embedding lookup and gradient,
+                    residual update with the norms around a block.
 
 Every function cites the page passage it follows.  Pins that tie this oracle to
 something other than itself live in ``tests/test_oracle_pins.py`` and
@@ -47,3 +49,4 @@ from .diag import (  # noqa: F401
     QUANTILES, oracle_diag, oracle_diag_lenient, quantile_linear,
 )
 from .logits_ops import distill_row, sample_row  # noqa: E402,F401
+from . import ends  # noqa: E402,F401

@@ -12,4 +12,5 @@ from .binding import (  # noqa: F401
     processed_logprob, quantize_fp8_rows, logprob_fp8, split_tf32, logprob_fp32,
     logprob_backward, selftest_wait_timeout, rmsnorm_backward, linear_logprob,
     logprob_noalloc, sample, distill, distill_backward, distill_grad, distill_loss,
+    embed, embed_backward, embed_backward_workspace_size, embedding,
 )

@@ -125,6 +125,14 @@ _SIGNATURES.update({
                                         _vp, _vp, _vp, _i64, _vp]),
 })
 
+_SIGNATURES.update({
+    "tim_embed": (_c.c_int, [_vp, _i32, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _sz,
+                             _vp]),
+    "tim_embed_backward_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "tim_embed_backward": (_c.c_int, [_vp, _i32, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _i32, _i32,
+                                      _vp, _sz, _vp]),
+})
+
 _lib = None
 
 
@@ -929,6 +937,145 @@ def distill_loss(logits, teacher_ids, teacher_logprob, temperature: float = 1.0,
         _DISTILL = _distill_function()
     return _DISTILL.apply(logits, teacher_ids, teacher_logprob, temperature, kind, tail,
                           workspace, check)
+
+
+# ----------------------------------------------------------------------------- a model's two ends
+
+def _sized_workspace(workspace, dev, stream, size):
+    """The caller's workspace, on ``dev``, or one of this call's own."""
+    if workspace is None:
+        return Workspace(size(), dev, stream)
+    if workspace.buf.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    return workspace
+
+
+def _matrix(t, T, d, code, dev, name):
+    """Row stride of a [T, d] tensor of the type with that code on ``dev``."""
+    rows, cols, c, ld = _logits_args(t, name)
+    if (rows, cols) != (T, d):
+        raise ValueError(f"{name} must be [{T}, {d}], got {list(t.shape)}")
+    if c != code:
+        raise TypeError(f"{name} must be of the type of the other matrices, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return ld
+
+
+def embed(table, ids, scale: float = 1.0, *, out=None, workspace: Optional[Workspace] = None,
+          stream=None, check: bool = True):
+    """out[t] = scale table[ids[t]] (tim_embed) for ``table`` [V, d] (float32, bfloat16 or float16
+    CUDA tensor, rows contiguous, any row stride) and ``ids`` int32 [T]; -1 is no token, a row of
+    zeros.  Returns [T, d] in the table's type, or ``out``."""
+    torch = _torch()
+    V, d, code, ld = _logits_args(table, "table")
+    dev = table.device
+    _need(ids, torch.int32, "ids", 1)
+    T = ids.shape[0]
+    i = _vector(ids, torch.int32, T, dev, "ids")
+    ldo = d if out is None else _matrix(out, T, d, code, dev, "out")
+
+    def call(sp):
+        o = out
+        if o is None:
+            o = torch.empty(T, d, dtype=table.dtype, device=dev)
+        ws = _status_workspace(workspace, dev, stream)
+        _check(lib().tim_embed(table.data_ptr(), code, ld, i, T, V, d, scale, o.data_ptr(), ldo,
+                               ws.ptr, ws.nbytes, sp), "tim_embed")
+        if check:
+            ws.check("tim_embed", stream)
+        return o
+
+    return _run(dev, stream, call)
+
+
+def embed_backward_workspace_size(T: int, V: int, d: int) -> int:
+    """Bytes of the workspace of ``embed_backward``; it serves ``embed`` too."""
+    return int(lib().tim_embed_backward_workspace_size(int(T), int(V), int(d)))
+
+
+def embed_backward(dy, ids, V: int, scale: float = 1.0, *, dtype=None, out_dtable=None,
+                   accumulate: bool = False, workspace: Optional[Workspace] = None, stream=None,
+                   check: bool = True):
+    """Gradient of ``embed`` with respect to its table (tim_embed_backward): dtable[v] = scale
+    times the sum of the rows of ``dy`` [T, d] whose id is v, [V, d] in float32, or in ``dtype`` =
+    dy's.  ``out_dtable`` (contiguous) is written; with ``accumulate`` it is added to, as the ``dW``
+    of ``logprob_backward`` where table and LM head are one matrix."""
+    torch = _torch()
+    T, d, code, ld = _logits_args(dy, "dy")
+    dev = dy.device
+    i = _vector(ids, torch.int32, T, dev, "ids")
+    V = int(V)
+    if dtype is None:
+        dtype = torch.float32 if out_dtable is None else out_dtable.dtype
+    if dtype not in (torch.float32, dy.dtype):
+        raise TypeError(f"the gradient must be float32 or {dy.dtype}, got {dtype}")
+    if out_dtable is not None:
+        _need(out_dtable, dtype, "out_dtable", 2)
+        if tuple(out_dtable.shape) != (V, d) or out_dtable.device != dev:
+            raise ValueError(f"out_dtable must be [{V}, {d}] on {dev}")
+    elif accumulate:
+        raise ValueError("accumulate needs out_dtable")
+
+    def call(sp):
+        o = out_dtable
+        if o is None:
+            o = torch.empty(V, d, dtype=dtype, device=dev)
+        ws = _sized_workspace(workspace, dev, stream, lambda: embed_backward_workspace_size(T, V, d))
+        _check(lib().tim_embed_backward(dy.data_ptr(), code, ld, i, T, V, d, scale, o.data_ptr(),
+                                        _DTYPE_CODES[dtype], int(bool(accumulate)), ws.ptr,
+                                        ws.nbytes, sp), "tim_embed_backward")
+        if check:
+            ws.check("tim_embed_backward", stream)
+        return o
+
+    return _run(dev, stream, call)
+
+
+def _rows(t):
+    """A gradient as the library takes it."""
+    if t is not None and (t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < t.shape[1]):
+        t = t.contiguous()
+    return t
+
+
+def _embedding_function():
+    torch = _torch()
+
+    class Embedding(torch.autograd.Function):
+        """tim_embed with the gradient of tim_embed_backward, in the table's type."""
+
+        @staticmethod
+        def forward(ctx, table, ids, scale, workspace, check):
+            ctx.save_for_backward(ids)
+            ctx.V, ctx.scale, ctx.workspace, ctx.check = table.shape[0], scale, workspace, check
+            return embed(table, ids, scale, workspace=workspace, check=check)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy):
+            ids, = ctx.saved_tensors
+            grad = embed_backward(_rows(dy), ids, ctx.V, ctx.scale, dtype=dy.dtype,
+                                  workspace=ctx.workspace, check=ctx.check)
+            return grad, None, None, None, None
+
+    return Embedding
+
+
+_EMBEDDING = None
+
+
+def embedding(table, ids, scale: float = 1.0, *, workspace: Optional[Workspace] = None,
+              check: bool = True):
+    """Differentiable ``embed`` (gradient with respect to ``table``, once, in its type).
+    ``workspace``: of ``embed_backward_workspace_size`` bytes, for both directions.  Runs on the
+    current stream.  To capture a step into a graph call ``embed`` and ``embed_backward``
+    themselves: autograd's backward must not be captured while an eager graph of the same leaf
+    lives."""
+    global _EMBEDDING
+    if _EMBEDDING is None:
+        _EMBEDDING = _embedding_function()
+    return _EMBEDDING.apply(table, ids, scale, workspace, check)
 
 
 # ----------------------------------------------------------------------------- vocab-parallel

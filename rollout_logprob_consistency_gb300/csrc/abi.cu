@@ -98,6 +98,13 @@ cudaError_t launch_distill_backward(const void* logits, int dtype, int64_t ld, i
                                     const int32_t* ids, const float* lp, int K, float temperature,
                                     int kind, const float* saved, const float* grad, void* dlogits,
                                     int64_t ldd, cudaStream_t stream);
+cudaError_t launch_embed(const void* table, int dtype, int64_t ld, const int32_t* ids, int64_t T,
+                         int V, int d, float scale, void* out, int64_t ldo, int* status,
+                         cudaStream_t stream);
+size_t embed_backward_bytes(int64_t T, int d);
+cudaError_t launch_embed_backward(const void* dy, int dtype, int64_t ld, const int32_t* ids,
+                                  int64_t T, int V, int d, float scale, void* out, int out_dtype,
+                                  int accumulate, void* ws, cudaStream_t stream);
 
 namespace {
 
@@ -262,6 +269,32 @@ bool matrices_meet(const void* a, int64_t lda, const void* b, int64_t ldb, int32
   const uintptr_t a1 = a0 + static_cast<uintptr_t>((T - 1) * lda + V) * es;
   const uintptr_t b1 = b0 + static_cast<uintptr_t>((T - 1) * ldb + V) * es;
   return a0 < b1 && b0 < a1;
+}
+
+// Bytes from a matrix's first element to behind its last.
+size_t extent(int64_t ld, int64_t rows, int32_t d, int32_t dtype) {
+  return (static_cast<size_t>(rows - 1) * static_cast<size_t>(ld) + static_cast<size_t>(d)) *
+         dtype_bytes(dtype);
+}
+bool meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a_bytes != 0 && b_bytes != 0 && a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+}
+
+// A matrix of rows of d elements with row stride ld.
+tim_status check_matrix(const void* p, int32_t dtype, int64_t ld, int32_t d) {
+  const size_t es = dtype_bytes(dtype);
+  if (p == nullptr || es == 0 || !aligned(p, es)) return TIM_ERR_INVALID_ARG;
+  if (ld < d || ld > (static_cast<int64_t>(1) << 31)) return TIM_ERR_SHAPE;
+  return TIM_OK;
+}
+
+bool embed_shape(int64_t T, int32_t V, int32_t d) {
+  return T >= 1 && T <= INT32_MAX && V >= 1 && V <= INT32_MAX - 256 && d >= 1 && d <= 65536;
+}
+tim_status check_embed(int64_t T, int32_t V, int32_t d, float scale, const int32_t* ids) {
+  if (ids == nullptr || !aligned(ids, 4) || !std::isfinite(scale)) return TIM_ERR_INVALID_ARG;
+  return embed_shape(T, V, d) ? TIM_OK : TIM_ERR_SHAPE;
 }
 
 tim_status check_distill(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
@@ -921,6 +954,49 @@ tim_status tim_distill_backward(const void* logits, int32_t dtype, int64_t ld, i
   return from_cuda(launch_distill_backward(logits, dtype, ld, T, V, teacher_ids, teacher_logprob,
                                            K, temperature, kind, saved, grad_loss, out_dlogits,
                                            ldd, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tim_status tim_embed(const void* table, int32_t dtype, int64_t ld, const int32_t* ids, int64_t T,
+                     int32_t V, int32_t d, float scale, void* out, int64_t ldo, void* workspace,
+                     size_t workspace_bytes, tim_stream_t stream) {
+  tim_status s = check_embed(T, V, d, scale, ids);
+  if (s != TIM_OK) return s;
+  if ((s = check_matrix(table, dtype, ld, d)) != TIM_OK) return s;
+  if ((s = check_matrix(out, dtype, ldo, d)) != TIM_OK) return s;
+  if (meet(table, extent(ld, V, d, dtype), out, extent(ldo, T, d, dtype)) ||
+      meet(ids, static_cast<size_t>(T) * 4, out, extent(ldo, T, d, dtype)))
+    return TIM_ERR_INVALID_ARG;
+  if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  return from_cuda(launch_embed(table, dtype, ld, ids, T, V, d, scale, out, ldo,
+                                static_cast<int*>(workspace),
+                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tim_embed_backward_workspace_size(int64_t T, int32_t V, int32_t d) {
+  return embed_shape(T, V, d) ? embed_backward_bytes(T, d) : 0;
+}
+
+tim_status tim_embed_backward(const void* dy, int32_t dtype, int64_t ldy, const int32_t* ids,
+                              int64_t T, int32_t V, int32_t d, float scale, void* out_dtable,
+                              int32_t out_dtype, int32_t accumulate, void* workspace,
+                              size_t workspace_bytes, tim_stream_t stream) {
+  tim_status s = check_embed(T, V, d, scale, ids);
+  if (s != TIM_OK) return s;
+  if ((s = check_matrix(dy, dtype, ldy, d)) != TIM_OK) return s;
+  if ((s = check_matrix(out_dtable, out_dtype, d, d)) != TIM_OK) return s;
+  if (out_dtype != TIM_F32 && out_dtype != dtype) return TIM_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return TIM_ERR_INVALID_ARG;
+  const size_t table = extent(d, V, d, out_dtype);
+  if (meet(dy, extent(ldy, T, d, dtype), out_dtable, table) ||
+      meet(ids, static_cast<size_t>(T) * 4, out_dtable, table))
+    return TIM_ERR_INVALID_ARG;
+  if ((s = check_workspace(workspace, workspace_bytes, embed_backward_bytes(T, d))) != TIM_OK)
+    return s;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  return from_cuda(launch_embed_backward(dy, dtype, ldy, ids, T, V, d, scale, out_dtable, out_dtype,
+                                         accumulate, workspace,
+                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,393 @@
+// Embedding lookup with a scale, and its gradient by sorted tokens.
+//
+//   out[t] = scale table[ids[t]]                      (fp32 product, one rounding)
+//   dtable[v] (+)= scale sum_{t: ids[t] = v} dy[t]    (fp32 sums in a fixed order, one rounding)
+//
+// The lookup is memory's: distinct rows read, T rows written.
+//
+// The gradient is a sum over equal tokens, so the tokens are sorted first (embed_sort.cuh's one
+// launch: the order of equal ids is their order in the batch), and the sorted list is cut into
+// pieces of a fixed number of rows.  A piece's CTA walks its rows with a column vector a thread and
+// an fp32 running sum, writes the tokens that lie wholly within, and leaves the sums of the first and
+// the last where they go on beyond it; a second launch joins those in order.  No atomics: the same
+// call gives the same bits.  Rows of the table that no token names are zeroed by CTAs of the same
+// launch, which look the row up in the sorted list; with `accumulate` they are not touched.
+#include "embed_sort.cuh"
+#include "logits_row.cuh"
+
+namespace tim {
+namespace {
+
+// ---- the lookup
+
+constexpr int kLookupThreads = 128;
+constexpr int kLookupVecs = 4;  // of a thread, in flight together
+
+struct LookupArgs {
+  const void* table;
+  int64_t ld;
+  const int32_t* ids;
+  int V, d;
+  float scale;
+  void* out;
+  int64_t ldo;
+  int* status;
+};
+
+// kWide: rows of whole 16-byte vectors at both sides; else an element a load.
+template <int kDtype, bool kWide>
+__global__ void __launch_bounds__(kLookupThreads) embed_kernel(const LookupArgs a) {
+  using E = Elem<kDtype>;
+  using raw = typename E::raw;
+  constexpr int kOf = kWide ? E::kVec : 1;
+  const int64_t row = blockIdx.x;
+  const int id = __ldg(a.ids + row);
+  const bool bad = id < -1 || id >= a.V;
+  if (bad && threadIdx.x == 0 && blockIdx.y == 0) set_status(a.status, TIM_ERR_TOKEN_RANGE);
+  raw* const out = static_cast<raw*>(a.out) + row * a.ldo;
+  const raw* const from = static_cast<const raw*>(a.table) + (id >= 0 && !bad ? id : 0) * a.ld;
+  const int n = a.d / kOf;  // whole where kWide
+  for (int c0 = blockIdx.y * kLookupThreads * kLookupVecs + threadIdx.x; c0 < n;
+       c0 += gridDim.y * kLookupThreads * kLookupVecs) {
+    if (bad || id < 0) {
+      const raw fill = E::narrow(bad ? __int_as_float(0x7FC00000) : 0.f);
+#pragma unroll
+      for (int k = 0; k < kLookupVecs; ++k) {
+        const int c = c0 + k * kLookupThreads;
+        if (c < n)
+          for (int i = 0; i < kOf; ++i) out[c * kOf + i] = fill;
+      }
+      continue;
+    }
+    if constexpr (kWide) {
+      uint4 x[kLookupVecs];
+#pragma unroll
+      for (int k = 0; k < kLookupVecs; ++k) {
+        const int c = c0 + k * kLookupThreads;
+        if (c < n) x[k] = __ldg(reinterpret_cast<const uint4*>(from) + c);
+      }
+#pragma unroll
+      for (int k = 0; k < kLookupVecs; ++k) {
+        const int c = c0 + k * kLookupThreads;
+        if (c >= n) continue;
+        float v[E::kVec];
+        E::unpack(x[k], v);
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) v[i] *= a.scale;
+        reinterpret_cast<uint4*>(out)[c] = E::pack(v);
+      }
+    } else {
+      raw x[kLookupVecs];
+#pragma unroll
+      for (int k = 0; k < kLookupVecs; ++k) {
+        const int c = c0 + k * kLookupThreads;
+        if (c < n) x[k] = from[c];
+      }
+#pragma unroll
+      for (int k = 0; k < kLookupVecs; ++k) {
+        const int c = c0 + k * kLookupThreads;
+        if (c < n) out[c] = E::narrow(E::widen(x[k]) * a.scale);
+      }
+    }
+  }
+}
+
+bool wide(const void* p, int64_t ld, int d, int es) {
+  return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * es) |
+           static_cast<uintptr_t>(static_cast<int64_t>(d) * es)) & 15u) == 0;
+}
+
+template <int kDtype>
+cudaError_t launch_lookup(const LookupArgs& a, int64_t T, cudaStream_t stream) {
+  constexpr int es = sizeof(typename Elem<kDtype>::raw);
+  const bool w = wide(a.table, a.ld, a.d, es) && wide(a.out, a.ldo, a.d, es);
+  const int n = w ? a.d / Elem<kDtype>::kVec : a.d;
+  const int per = kLookupThreads * kLookupVecs;
+  const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(std::min((n + per - 1) / per, 64)));
+  if (w)
+    embed_kernel<kDtype, true><<<grid, kLookupThreads, 0, stream>>>(a);
+  else
+    embed_kernel<kDtype, false><<<grid, kLookupThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// ---- the gradient
+
+constexpr int kGradThreads = 256;
+constexpr int kZeroRows = 32;  // table rows of a CTA that zeroes
+constexpr int kRows = 8;       // rows in flight
+constexpr int kMaxPiece = 64;
+
+struct GradArgs {
+  const void* dy;
+  int64_t ld;
+  const uint32_t* id;   // sorted; V: none
+  const uint32_t* row;  // the rows in that order
+  int T, V, d, piece, pieces, slices;
+  float scale;
+  void* out;
+  int accumulate;
+  float* partial;  // [pieces][2][d]: of a piece's first and last token
+};
+
+template <int kDtype, int kVec>
+__device__ __forceinline__ void load_cols(const typename Elem<kDtype>::raw* p, float (&v)[kVec]) {
+  if constexpr (kVec == 1)
+    v[0] = Elem<kDtype>::widen(__ldg(p));
+  else
+    Elem<kDtype>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+// kVec columns of the table's gradient, of type kOut.
+template <int kOut, int kVec>
+__device__ __forceinline__ void store_cols(typename Elem<kOut>::raw* p, const float (&acc)[kVec],
+                                           float scale, int accumulate) {
+  using E = Elem<kOut>;
+  if constexpr (kVec == 1) {
+    p[0] = E::narrow(accumulate ? fmaf(acc[0], scale, E::widen(p[0])) : acc[0] * scale);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kVec; q += E::kVec) {
+      uint4* const at = reinterpret_cast<uint4*>(p + q);
+      float v[E::kVec];
+      if (accumulate) {
+        E::unpack(*at, v);
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) v[i] = fmaf(acc[q + i], scale, v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) v[i] = acc[q + i] * scale;
+      }
+      *at = E::pack(v);
+    }
+  }
+}
+
+// Whether table row v has a token: looked up in the sorted list.
+__device__ __forceinline__ bool named(const GradArgs& a, uint32_t v) {
+  int lo = 0, hi = a.T;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.id + mid) < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo < a.T && __ldg(a.id + lo) == v;
+}
+
+template <int kDtype, int kOut, int kVec>
+__global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const GradArgs a) {
+  using raw = typename Elem<kDtype>::raw;
+  using raw_out = typename Elem<kOut>::raw;
+  __shared__ uint32_t ids[kMaxPiece + 2], rows[kMaxPiece];
+  __shared__ uint32_t mask;
+  const int tid = threadIdx.x, n = a.d / kVec;
+  const uint32_t none = static_cast<uint32_t>(a.V);
+  const int work = a.pieces * a.slices;
+  if (static_cast<int>(blockIdx.x) >= work) {
+    // ---- rows without a token
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x - work) * kZeroRows;
+    if (tid < 32) {
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, v0 + tid < a.V &&
+                                                        !named(a, static_cast<uint32_t>(v0) + tid));
+      if (tid == 0) mask = m;
+    }
+    __syncthreads();
+    const float zero[kVec] = {};
+    for (uint32_t m = mask; m != 0; m &= m - 1) {
+      raw_out* const out = static_cast<raw_out*>(a.out) + (v0 + __ffs(m) - 1) * a.d;
+      for (int c = tid; c < n; c += kGradThreads) store_cols<kOut, kVec>(out + c * kVec, zero, 0.f, 0);
+    }
+    return;
+  }
+  // ---- a piece of the sorted list, a slice of the columns
+  const int p = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kGradThreads + tid;
+  const int i0 = p * a.piece, len = min(a.piece, a.T - i0);
+  for (int i = tid; i < len + 2; i += kGradThreads) {
+    const int at = i0 - 1 + i;
+    ids[i] = at >= 0 && at < a.T ? __ldg(a.id + at) : 0xFFFFFFFFu;  // no token's
+    if (i < len) rows[i] = __ldg(a.row + i0 + i);
+  }
+  __syncthreads();
+  if (c >= n) return;
+  const raw* const dy = static_cast<const raw*>(a.dy) + c * kVec;
+  float acc[kVec] = {};
+  uint32_t cur = ids[1];
+  bool first = true;
+  auto flush = [&](bool last) {
+    if (cur >= none) return;
+    const bool from_before = first && ids[0] == cur, goes_on = last && ids[len + 1] == cur;
+    if (from_before || goes_on) {
+      float* const to =
+          a.partial + (static_cast<int64_t>(p) * 2 + (from_before ? 0 : 1)) * a.d + c * kVec;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) to[i] = acc[i];
+    } else {
+      store_cols<kOut, kVec>(static_cast<raw_out*>(a.out) + static_cast<int64_t>(cur) * a.d + c * kVec,
+                             acc, a.scale, a.accumulate);
+    }
+  };
+  for (int r0 = 0; r0 < len; r0 += kRows) {
+    if (ids[1 + r0] >= none) {  // only such follow
+      flush(false);
+      return;
+    }
+    float v[kRows][kVec];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (r0 + k < len && ids[1 + r0 + k] < none)
+        load_cols<kDtype, kVec>(dy + static_cast<int64_t>(rows[r0 + k]) * a.ld, v[k]);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (r0 + k >= len) break;
+      const uint32_t id = ids[1 + r0 + k];
+      if (id != cur) {
+        flush(false);
+        cur = id;
+        first = false;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+      }
+      if (id >= none) return;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += v[k][i];
+    }
+  }
+  flush(true);
+}
+
+// The tokens whose rows lie in several pieces: the CTA of the piece where one begins adds its parts.
+template <int kOut, int kVec>
+__global__ void __launch_bounds__(kGradThreads) embed_join_kernel(const GradArgs a) {
+  using raw_out = typename Elem<kOut>::raw;
+  const int p = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kGradThreads + threadIdx.x;
+  const int i0 = p * a.piece, i1 = i0 + a.piece;  // all but the last piece are whole
+  if (i1 >= a.T) return;
+  const uint32_t id = __ldg(a.id + i1 - 1);
+  if (id >= static_cast<uint32_t>(a.V) || __ldg(a.id + i1) != id) return;
+  if (i0 > 0 && __ldg(a.id + i0 - 1) == id) return;  // begins before this piece
+  if (c >= a.d / kVec) return;
+  float acc[kVec];
+  const float* const part = a.partial + c * kVec;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = part[(static_cast<int64_t>(p) * 2 + 1) * a.d + i];
+  for (int q = p + 1; q < a.pieces; q += kRows) {
+    float v[kRows][kVec];
+    bool in[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      in[k] = q + k < a.pieces && __ldg(a.id + static_cast<int64_t>(q + k) * a.piece) == id;
+      if (in[k]) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[k][i] = part[static_cast<int64_t>(q + k) * 2 * a.d + i];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (!in[k]) break;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += v[k][i];
+    }
+    if (!in[kRows - 1]) break;
+  }
+  store_cols<kOut, kVec>(static_cast<raw_out*>(a.out) + static_cast<int64_t>(id) * a.d + c * kVec, acc,
+                         a.scale, a.accumulate);
+}
+
+template <int kDtype, int kOut, int kVec>
+cudaError_t launch_grad(const GradArgs& args, cudaStream_t stream) {
+  GradArgs a = args;
+  a.slices = (a.d / kVec + kGradThreads - 1) / kGradThreads;
+  const int64_t zero = a.accumulate ? 0 : (static_cast<int64_t>(a.V) + kZeroRows - 1) / kZeroRows;
+  const int64_t work = static_cast<int64_t>(a.pieces) * a.slices;
+  if (work + zero > INT32_MAX) return cudaErrorInvalidValue;
+  embed_grad_kernel<kDtype, kOut, kVec>
+      <<<static_cast<unsigned>(work + zero), kGradThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.pieces == 1) return e;
+  embed_join_kernel<kOut, kVec><<<static_cast<unsigned>(work), kGradThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+template <int kDtype>
+cudaError_t launch_grad_type(const GradArgs& a, int out_dtype, cudaStream_t stream) {
+  constexpr int es = sizeof(typename Elem<kDtype>::raw), kVec = Elem<kDtype>::kVec;
+  const int eo = out_dtype == TIM_F32 ? 4 : 2;
+  const bool w = wide(a.dy, a.ld, a.d, es) && wide(a.out, a.d, a.d, eo);
+  if (out_dtype == TIM_F32)
+    return w ? launch_grad<kDtype, TIM_F32, kVec>(a, stream)
+             : launch_grad<kDtype, TIM_F32, 1>(a, stream);
+  if constexpr (kDtype != TIM_F32) {
+    if (out_dtype == kDtype)
+      return w ? launch_grad<kDtype, kDtype, kVec>(a, stream)
+               : launch_grad<kDtype, kDtype, 1>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// Rows of a piece.
+int piece_rows(int64_t T) { return T <= 8192 ? 16 : kMaxPiece; }
+
+struct EmbedWs {
+  size_t id_off, row_off, partial_off, total;
+};
+EmbedWs embed_ws(int64_t T, int d) {
+  const int64_t n = std::min<int64_t>(T, kSortRows);
+  EmbedWs w;
+  w.id_off = 1024;
+  w.row_off = align_up(w.id_off + static_cast<size_t>(n) * 4, 1024);
+  w.partial_off = align_up(w.row_off + static_cast<size_t>(n) * 4, 1024);
+  // fewer tokens than n can have more pieces (a last batch, a smaller call with this workspace)
+  const size_t small = static_cast<size_t>((std::min<int64_t>(n, 8192) + 15) / 16);
+  const size_t large = static_cast<size_t>((n + kMaxPiece - 1) / kMaxPiece);
+  w.total = align_up(w.partial_off + std::max(small, large) * 2 * static_cast<size_t>(d) * 4, 1024);
+  return w;
+}
+
+}  // namespace
+
+cudaError_t launch_embed(const void* table, int dtype, int64_t ld, const int32_t* ids, int64_t T,
+                         int V, int d, float scale, void* out, int64_t ldo, int* status,
+                         cudaStream_t stream) {
+  const LookupArgs a = {table, ld, ids, V, d, scale, out, ldo, status};
+  return dtype == TIM_F32    ? launch_lookup<TIM_F32>(a, T, stream)
+         : dtype == TIM_BF16 ? launch_lookup<TIM_BF16>(a, T, stream)
+                             : launch_lookup<TIM_F16>(a, T, stream);
+}
+
+size_t embed_backward_bytes(int64_t T, int d) { return embed_ws(T, d).total; }
+
+cudaError_t launch_embed_backward(const void* dy, int dtype, int64_t ld, const int32_t* ids, int64_t T,
+                                  int V, int d, float scale, void* out, int out_dtype, int accumulate,
+                                  void* ws, cudaStream_t stream) {
+  const EmbedWs w = embed_ws(T, d);
+  uint8_t* const b = static_cast<uint8_t*>(ws);
+  const int es = dtype == TIM_F32 ? 4 : 2;
+  // The sort takes kSortRows tokens at a time; more of them are added batch by batch.
+  for (int64_t t0 = 0; t0 < T; t0 += kSortRows) {
+    uint32_t* const id = reinterpret_cast<uint32_t*>(b + w.id_off);
+    uint32_t* const row = reinterpret_cast<uint32_t*>(b + w.row_off);
+    GradArgs a = {};
+    a.T = static_cast<int>(std::min<int64_t>(T - t0, kSortRows));
+    a.dy = static_cast<const uint8_t*>(dy) + t0 * ld * es;
+    a.ld = ld;
+    a.id = id;
+    a.row = row;
+    a.V = V;
+    a.d = d;
+    a.piece = piece_rows(a.T);
+    a.pieces = (a.T + a.piece - 1) / a.piece;
+    a.scale = scale;
+    a.out = out;
+    a.accumulate = accumulate || t0 > 0;
+    a.partial = reinterpret_cast<float*>(b + w.partial_off);
+    cudaError_t e = launch_embed_sort(ids + t0, a.T, V, id, row, static_cast<int*>(ws), stream);
+    if (e != cudaSuccess) return e;
+    e = dtype == TIM_F32    ? launch_grad_type<TIM_F32>(a, out_dtype, stream)
+        : dtype == TIM_BF16 ? launch_grad_type<TIM_BF16>(a, out_dtype, stream)
+                            : launch_grad_type<TIM_F16>(a, out_dtype, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace tim

@@ -1,0 +1,168 @@
+// The tokens of a batch in the order of their ids, equal ids in the order of their rows: a radix sort in one
+// launch, by a cluster of CTAs that keep all of it in their shared memory.
+//
+// A pass orders by 9 bits of the id, lowest first.  Every warp has 32 kItems tokens that follow one
+// another in the list and counts its digits, equal ones of a step ranked by lane; the counts of a
+// digit's earlier warps, then of its earlier CTAs (whose totals are exchanged), then of all lower
+// digits give each token its place, and it is stored there, in whichever CTA that is.  V = 151936
+// takes two passes, three cluster barriers.
+#pragma once
+
+#include <algorithm>
+
+#include "logits_row.cuh"
+
+namespace tim {
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+constexpr int kSortItems = 16;  // of a thread, at most
+constexpr int kSortRows = kSortCluster * kSortThreads * kSortItems;
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
+
+struct SortArgs {
+  const int32_t* ids;
+  int T, V, passes;
+  uint32_t* out_id;  // V: no token
+  uint32_t* out_row;
+  int* status;
+};
+
+template <int kItems>
+struct SortShared {
+  uint64_t item[kSortThreads * kItems];  // id << 32 | row
+  uint32_t total[kSortCluster][kDigits];
+  uint32_t base[kDigits];
+  uint32_t warp[kDigits / 32];
+  uint16_t count[kSortWarps][kDigits];
+};
+
+template <int kItems>
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortArgs a) {
+  extern __shared__ uint4 sort_mem[];
+  SortShared<kItems>& sh = *reinterpret_cast<SortShared<kItems>*>(sort_mem);
+  constexpr int kOfCta = kSortThreads * kItems;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank(), size = gridDim.x;  // one cluster
+  const uint32_t first = warp * 32 * kItems + lane;        // of the CTA's tokens
+  uint32_t id[kItems], row[kItems], place[kItems];
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    row[k] = rank * kOfCta + first + k * 32;
+    id[k] = static_cast<uint32_t>(a.V);  // none, and beyond the end: last, in order
+    if (row[k] < static_cast<uint32_t>(a.T)) {
+      const int t = __ldg(a.ids + row[k]);
+      bad |= t < -1 || t >= a.V;
+      if (t >= 0 && t < a.V) id[k] = static_cast<uint32_t>(t);
+    }
+  }
+  if (bad) set_status(a.status, TIM_ERR_TOKEN_RANGE);
+  cluster_arrive();
+  cluster_wait();  // every CTA of the cluster runs
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * kDigitBits;
+    if (pass > 0) {
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const uint64_t x = sh.item[first + k * 32];
+        id[k] = static_cast<uint32_t>(x >> 32);
+        row[k] = static_cast<uint32_t>(x);
+      }
+    }
+    uint16_t* const mine = sh.count[warp];
+    for (int i = lane; i < kDigits / 2; i += 32) reinterpret_cast<uint32_t*>(mine)[i] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const uint32_t digit = (id[k] >> shift) & (kDigits - 1);
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
+      const uint32_t before = mine[digit];
+      place[k] = before + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if ((same >> lane) == 1u) mine[digit] = static_cast<uint16_t>(before + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    if (tid < kDigits) {  // over the warps
+      uint32_t n = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t x = sh.count[w][tid];
+        sh.count[w][tid] = static_cast<uint16_t>(n);
+        n += x;
+      }
+      for (uint32_t c = 0; c < size; ++c) cluster_store32(cluster_addr(&sh.total[rank][tid], c), n);
+    }
+    cluster_arrive();
+    cluster_wait();
+    uint32_t before = 0, all = 0, at = 0;
+    if (tid < kDigits) {
+      for (uint32_t c = 0; c < size; ++c) {
+        const uint32_t n = sh.total[c][tid];
+        if (c < rank) before += n;
+        all += n;
+      }
+      at = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        if (lane >= o) at += up;
+      }
+      if (lane == 31) sh.warp[warp] = at;
+    }
+    __syncthreads();
+    if (tid < kDigits) {
+      for (int w = 0; w < warp; ++w) before += sh.warp[w];
+      sh.base[tid] = before + at - all;
+    }
+    __syncthreads();
+    const bool last = pass + 1 == a.passes;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const uint32_t digit = (id[k] >> shift) & (kDigits - 1);
+      const uint32_t to = sh.base[digit] + mine[digit] + place[k];
+      if (last) {
+        if (to < static_cast<uint32_t>(a.T)) {
+          a.out_id[to] = id[k];
+          a.out_row[to] = row[k];
+        }
+      } else {
+        cluster_store(cluster_addr(&sh.item[to % kOfCta], to / kOfCta),
+                      static_cast<uint64_t>(id[k]) << 32 | row[k]);
+      }
+    }
+    if (!last) {
+      cluster_arrive();
+      cluster_wait();
+    }
+  }
+}
+
+template <int kItems>
+cudaError_t launch_sort(const SortArgs& a, int cluster, cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(embed_sort_kernel<kItems>, sizeof(SortShared<kItems>), allowed);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(embed_sort_kernel<kItems>, 1, cluster, kSortThreads,
+                         sizeof(SortShared<kItems>), stream, a);
+}
+
+// The ids of T <= kSortRows tokens in order, and their rows; ids that are none, or out of range
+// (noted in the status word), as V at the end.
+cudaError_t launch_embed_sort(const int32_t* ids, int T, int V, uint32_t* out_id, uint32_t* out_row,
+                              int* status, cudaStream_t stream) {
+  int bits = 1;
+  while (bits < 32 && (static_cast<uint32_t>(V) >> bits) != 0) ++bits;
+  const SortArgs a = {ids, T, V, (bits + kDigitBits - 1) / kDigitBits, out_id, out_row, status};
+  int cluster = 1;
+  while (cluster < kSortCluster && cluster * kSortThreads * 4 < T) cluster *= 2;
+  return cluster * kSortThreads * 4 >= T ? launch_sort<4>(a, cluster, stream)
+                                         : launch_sort<kSortItems>(a, cluster, stream);
+}
+
+}  // namespace
+}  // namespace tim
