@@ -733,6 +733,80 @@ tim_status tim_embed_backward(const void *dy, int32_t dtype, int64_t ldy, const 
                               size_t workspace_bytes, tim_stream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * The residual update after a block, with the norms before and after it.
+ *
+ * With h the residual stream, x the block's output, per row:
+ *   n  = x / sqrt(mean_i x_i^2 + eps) gamma_post     (gamma_post NULL: n = x)
+ *   h' = h + scale g n                               (rounded to dtype: out_h)
+ *   y  = h' / sqrt(mean_i h'_i^2 + eps) gamma        (gamma NULL: no out_y)
+ * The gate g is none (1), one number a row (TIM_GATE_TOKEN, [T], stride ld_gate), a
+ * channel (TIM_GATE_CHANNEL, [d]) or an element (TIM_GATE_ELEMENT, [T, d]).  h' is the
+ * hidden state that tim_logprob takes, y the next block's input.  Sums are fp32, in an
+ * order that depends on d and on whether rows lie on 16-byte boundaries: a row's bits do
+ * not depend on the batch.  Infinite and NaN values go through to their row's results; the
+ * mean of the squares has to lie within fp32's range.
+ *
+ * tim_residual_norm_backward: from the gradients dh of out_h and dy of out_y (either may be
+ * NULL: zeros), with h = out_h and the rounding of h' passed straight through,
+ * r = 1/sqrt(mean + eps):
+ *   H           = dh + r2 gamma dy - h r2^3/d sum_i(gamma_i dy_i h_i)
+ *   dresidual   = H;   dgamma = sum_t dy h r2
+ *   dn          = scale g H;   dgate = scale n H, summed over what a gate is shared by
+ *   dblock      = r1 gamma_post dn - x r1^3/d sum_i(gamma_post_i dn_i x_i)   (or dn)
+ *   dgamma_post = sum_t dn x r1
+ * dgamma, dgamma_post and the channel gate's gradient are fp32 [d], the token gate's fp32
+ * [T], the element gate's of dtype; accumulate = 1 adds to the first three.  They are
+ * summed over rows in a fixed order (for a given batch and GPU).  Where a sum over a row is
+ * not finite, neither are the sums over rows.
+ *
+ * b           host memory, read during the call: what both directions take.
+ * Matrices are [T, d] of b->dtype with a row stride ld >= d (up to 2^31), at any element-
+ * aligned address (whole 16-byte vectors are faster); gammas [d] of dtype.
+ * 1 <= T <= 2^31 - 1, 1 <= d <= TIM_RESIDUAL_MAX_D; scale finite, eps finite and >= 0.
+ * h is read with dy alone (and may be NULL without).
+ * Outputs must not meet inputs or one another, but out_h may be residual itself and
+ * out_y the block's output (same address and stride).
+ * workspace   of the backward: tim_residual_norm_backward_workspace_size(T, d) bytes, which
+ *             serve smaller T too.
+ * Errors: TIM_ERR_INVALID_ARG, TIM_ERR_SHAPE, TIM_ERR_WORKSPACE,
+ *   TIM_ERR_UNSUPPORTED_DEVICE, TIM_ERR_CUDA (immediate).
+ * ------------------------------------------------------------------------ */
+#define TIM_RESIDUAL_MAX_D 16384
+#define TIM_GATE_NONE 0
+#define TIM_GATE_TOKEN 1
+#define TIM_GATE_CHANNEL 2
+#define TIM_GATE_ELEMENT 3
+
+typedef struct tim_block {
+  int64_t T;
+  int32_t d;
+  int32_t dtype;
+  const void *block;
+  int64_t ld_block;
+  const void *gamma_post; /* or NULL */
+  const void *gate;       /* NULL with TIM_GATE_NONE */
+  int64_t ld_gate;        /* of TIM_GATE_TOKEN and TIM_GATE_ELEMENT */
+  int32_t gate_kind;
+  float scale;
+  const void *gamma; /* or NULL */
+  float eps;
+  int32_t reserved;
+} tim_block;
+
+tim_status tim_residual_norm(const tim_block *b, const void *residual, int64_t ld_residual,
+                             void *out_h, int64_t ld_h, void *out_y, int64_t ld_y,
+                             tim_stream_t stream);
+
+size_t tim_residual_norm_backward_workspace_size(int64_t T, int32_t d);
+
+tim_status tim_residual_norm_backward(const tim_block *b, const void *h, int64_t ld_h,
+                                      const void *dh, int64_t ld_dh, const void *dy, int64_t ld_dy,
+                                      void *out_dresidual, int64_t ld_dresidual, void *out_dblock,
+                                      int64_t ld_dblock, float *out_dgamma, float *out_dgamma_post,
+                                      void *out_dgate, int64_t ld_dgate, int32_t accumulate,
+                                      void *workspace, size_t workspace_bytes, tim_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Self-test of the bounded waits (the pages have no counterpart: it exercises
  * this library's own failure detection).  Every mbarrier wait in the LM-head
  * kernel gives up after a time limit, records TIM_ERR_TIMEOUT in the status

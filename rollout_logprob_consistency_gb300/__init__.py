@@ -13,4 +13,5 @@ from .binding import (  # noqa: F401
     logprob_backward, selftest_wait_timeout, rmsnorm_backward, linear_logprob,
     logprob_noalloc, sample, distill, distill_backward, distill_grad, distill_loss,
     embed, embed_backward, embed_backward_workspace_size, embedding,
+    residual_norm, residual_norm_backward, residual_norm_backward_workspace_size, block_residual,
 )

@@ -125,12 +125,23 @@ _SIGNATURES.update({
                                         _vp, _vp, _vp, _i64, _vp]),
 })
 
+class _Block(_c.Structure):
+    _fields_ = [("T", _i64), ("d", _i32), ("dtype", _i32), ("block", _vp), ("ld_block", _i64),
+                ("gamma_post", _vp), ("gate", _vp), ("ld_gate", _i64), ("gate_kind", _i32),
+                ("scale", _f32), ("gamma", _vp), ("eps", _f32), ("reserved", _i32)]
+
+
 _SIGNATURES.update({
     "tim_embed": (_c.c_int, [_vp, _i32, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _sz,
                              _vp]),
     "tim_embed_backward_workspace_size": (_sz, [_i64, _i32, _i32]),
     "tim_embed_backward": (_c.c_int, [_vp, _i32, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _i32, _i32,
                                       _vp, _sz, _vp]),
+    "tim_residual_norm": (_c.c_int, [_c.POINTER(_Block), _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "tim_residual_norm_backward_workspace_size": (_sz, [_i64, _i32]),
+    "tim_residual_norm_backward": (_c.c_int, [_c.POINTER(_Block), _vp, _i64, _vp, _i64, _vp, _i64,
+                                              _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _vp,
+                                              _sz, _vp]),
 })
 
 _lib = None
@@ -1076,6 +1087,184 @@ def embedding(table, ids, scale: float = 1.0, *, workspace: Optional[Workspace] 
     if _EMBEDDING is None:
         _EMBEDDING = _embedding_function()
     return _EMBEDDING.apply(table, ids, scale, workspace, check)
+
+
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ELEMENT = range(4)
+
+
+def _block_args(block, gamma, gamma_post, gate, scale, eps):
+    torch = _torch()
+    T, d, code, ld = _logits_args(block, "block")
+    dev, dtype = block.device, block.dtype
+    b = _Block(T, d, code, block.data_ptr(), ld, None, None, 0, GATE_NONE, scale, None, eps, 0)
+    if gamma is not None:
+        b.gamma = _vector(gamma, dtype, d, dev, "gamma")
+    if gamma_post is not None:
+        b.gamma_post = _vector(gamma_post, dtype, d, dev, "gamma_post")
+    if gate is None:
+        return b, T, d, code, dev
+    if not isinstance(gate, torch.Tensor) or gate.dtype != dtype or gate.device != dev:
+        raise TypeError(f"gate must be a {dtype} tensor on {dev}")
+    b.gate = gate.data_ptr()
+    if gate.dim() == 1:
+        b.gate_kind = GATE_CHANNEL
+        _vector(gate, dtype, d, dev, "gate")
+    elif tuple(gate.shape) == (T, 1):
+        b.gate_kind = GATE_TOKEN
+        b.ld_gate = gate.stride(0) if T > 1 else 1
+        if b.ld_gate < 1:
+            raise ValueError("gate must have a number of its own for each row")
+    else:
+        b.gate_kind = GATE_ELEMENT
+        b.ld_gate = _matrix(gate, T, d, code, dev, "gate")
+    return b, T, d, code, dev
+
+
+def residual_norm(residual, block, gamma, eps: float, *, gamma_post=None, gate=None,
+                  scale: float = 1.0, out=None, stream=None):
+    """The residual update after a block with the norms around it (tim_residual_norm):
+
+        n = block / rms(block) gamma_post   (block itself without gamma_post)
+        h = residual + scale gate n         y = h / rms(h) gamma
+
+    for [T, d] CUDA tensors of one type (float32, bfloat16 or float16, rows contiguous, any row
+    strides), gammas [d] or None, ``gate`` None, [d] (a number a channel), [T, 1] (a row) or [T, d].
+    Returns (h, y), y None without ``gamma``.  ``out`` = (h, y) to write; h may be ``residual`` and
+    y ``block`` themselves."""
+    torch = _torch()
+    b, T, d, code, dev = _block_args(block, gamma, gamma_post, gate, scale, eps)
+    ldr = _matrix(residual, T, d, code, dev, "residual")
+    ldh = ldy = d
+    if out is not None:
+        ldh = _matrix(out[0], T, d, code, dev, "out h")
+        if gamma is not None:
+            ldy = _matrix(out[1], T, d, code, dev, "out y")
+
+    def call(sp):
+        if out is not None:
+            h, y = out[0], out[1] if gamma is not None else None
+        else:
+            h = torch.empty(T, d, dtype=block.dtype, device=dev)
+            y = torch.empty(T, d, dtype=block.dtype, device=dev) if gamma is not None else None
+        _check(lib().tim_residual_norm(_c.byref(b), residual.data_ptr(), ldr, h.data_ptr(), ldh,
+                                       None if y is None else y.data_ptr(), ldy, sp),
+               "tim_residual_norm")
+        return h, y
+
+    return _run(dev, stream, call)
+
+
+def residual_norm_backward_workspace_size(T: int, d: int) -> int:
+    """Bytes of the workspace of ``residual_norm_backward``."""
+    return int(lib().tim_residual_norm_backward_workspace_size(int(T), int(d)))
+
+
+def residual_norm_backward(h, block, dh, dy, gamma, eps: float, *, gamma_post=None, gate=None,
+                           scale: float = 1.0, out=None, accumulate: bool = False,
+                           workspace: Optional[Workspace] = None, stream=None):
+    """Gradients of ``residual_norm`` (tim_residual_norm_backward) from ``dh`` and ``dy`` of its
+    results, [T, d] in their type, either of which may be None (zeros); ``h`` is its first result
+    (needed with ``dy`` alone).  Returns (dresidual, dblock, dgamma f32 [d], dgamma_post f32 [d],
+    dgate), None where there is no such argument; dgate is float32 [d] or [T, 1], or of the gate's
+    type [T, d].  ``out`` = the five tensors to write (None where there is none); with
+    ``accumulate`` the sums over rows, [d], are added to it."""
+    torch = _torch()
+    f32 = torch.float32
+    b, T, d, code, dev = _block_args(block, gamma, gamma_post, gate, scale, eps)
+    if dy is not None and gamma is None:
+        raise ValueError("dy without gamma")
+    ldh = _matrix(h, T, d, code, dev, "h") if dy is not None else d
+    ldy = _matrix(dy, T, d, code, dev, "dy") if dy is not None else d
+    ldd = _matrix(dh, T, d, code, dev, "dh") if dh is not None else d
+    ldr = ldb = ldg = d
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None:
+        ldr = _matrix(out[0], T, d, code, dev, "out dresidual")
+        ldb = _matrix(out[1], T, d, code, dev, "out dblock")
+        for t, given, name in ((out[2], gamma, "dgamma"), (out[3], gamma_post, "dgamma_post")):
+            if given is not None:
+                _vector(t, f32, d, dev, "out " + name)
+        if b.gate_kind == GATE_ELEMENT:
+            ldg = _matrix(out[4], T, d, code, dev, "out dgate")
+        elif b.gate_kind != GATE_NONE:
+            _need(out[4], f32, "out dgate")
+            if out[4].shape != gate.shape or out[4].device != dev:
+                raise ValueError(f"out dgate must be {list(gate.shape)} on {dev}")
+
+    def call(sp):
+        o = out
+        if o is None:
+            dgate = None
+            if b.gate_kind != GATE_NONE:
+                dgate = torch.empty(gate.shape, device=dev,
+                                    dtype=gate.dtype if b.gate_kind == GATE_ELEMENT else f32)
+            o = (torch.empty(T, d, dtype=block.dtype, device=dev),
+                 torch.empty(T, d, dtype=block.dtype, device=dev),
+                 None if gamma is None else torch.empty(d, dtype=f32, device=dev),
+                 None if gamma_post is None else torch.empty(d, dtype=f32, device=dev), dgate)
+        ws = _sized_workspace(workspace, dev, stream,
+                              lambda: residual_norm_backward_workspace_size(T, d))
+
+        def at(t, given=True):
+            return t.data_ptr() if given and t is not None else None
+
+        _check(lib().tim_residual_norm_backward(
+            _c.byref(b), at(h, dy is not None), ldh, at(dh), ldd, at(dy), ldy, o[0].data_ptr(), ldr,
+            o[1].data_ptr(), ldb, at(o[2], gamma is not None), at(o[3], gamma_post is not None),
+            at(o[4], gate is not None), ldg, int(bool(accumulate)), ws.ptr, ws.nbytes, sp),
+            "tim_residual_norm_backward")
+        return o
+
+    return _run(dev, stream, call)
+
+
+def _block_residual_function():
+    torch = _torch()
+
+    class BlockResidual(torch.autograd.Function):
+        """tim_residual_norm with the gradients of tim_residual_norm_backward, in their types."""
+
+        @staticmethod
+        def forward(ctx, residual, block, gamma, gamma_post, gate, eps, scale, workspace):
+            h, y = residual_norm(residual, block, gamma, eps, gamma_post=gamma_post, gate=gate,
+                                 scale=scale)
+            ctx.save_for_backward(h, block, gamma, gamma_post, gate)
+            ctx.eps, ctx.scale, ctx.workspace = eps, scale, workspace
+            ctx.set_materialize_grads(False)
+            return h, y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dh, dy):
+            h, block, gamma, gamma_post, gate = ctx.saved_tensors
+            if dh is None and dy is None:
+                return (None,) * 8
+            grads = residual_norm_backward(h, block, _rows(dh), _rows(dy), gamma, ctx.eps,
+                                           gamma_post=gamma_post, gate=gate, scale=ctx.scale,
+                                           workspace=ctx.workspace)
+            return (*grads[:2], *(None if t is None else g.to(t.dtype)
+                                  for g, t in zip(grads[2:], (gamma, gamma_post, gate))),
+                    None, None, None)
+
+    return BlockResidual
+
+
+_BLOCK_RESIDUAL = None
+
+
+def block_residual(residual, block, gamma, eps: float, *, gamma_post=None, gate=None,
+                   scale: float = 1.0, workspace: Optional[Workspace] = None):
+    """Differentiable ``residual_norm`` (all gradients, once, in the types of their tensors):
+    returns (h, y), y None without ``gamma``.  ``workspace``: of
+    ``residual_norm_backward_workspace_size`` bytes, for the backward.  Runs on the current stream.
+    To capture a step into a graph call ``residual_norm`` and ``residual_norm_backward``
+    themselves: autograd's backward must not be captured while an eager graph of the same leaves
+    lives."""
+    global _BLOCK_RESIDUAL
+    if _BLOCK_RESIDUAL is None:
+        _BLOCK_RESIDUAL = _block_residual_function()
+    return _BLOCK_RESIDUAL.apply(residual, block, gamma, gamma_post, gate, eps, scale, workspace)
 
 
 # ----------------------------------------------------------------------------- vocab-parallel

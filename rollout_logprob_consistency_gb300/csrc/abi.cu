@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "residual_norm.cuh"
 #include "tim_common.cuh"
 
 namespace tim {
@@ -296,6 +297,44 @@ tim_status check_embed(int64_t T, int32_t V, int32_t d, float scale, const int32
   if (ids == nullptr || !aligned(ids, 4) || !std::isfinite(scale)) return TIM_ERR_INVALID_ARG;
   return embed_shape(T, V, d) ? TIM_OK : TIM_ERR_SHAPE;
 }
+
+tim_status check_block(const tim_block* b) {
+  if (b == nullptr) return TIM_ERR_INVALID_ARG;
+  if (b->T < 1 || b->T > INT32_MAX || b->d < 1 || b->d > TIM_RESIDUAL_MAX_D) return TIM_ERR_SHAPE;
+  const tim_status s = check_matrix(b->block, b->dtype, b->ld_block, b->d);
+  if (s != TIM_OK) return s;
+  const size_t es = dtype_bytes(b->dtype);
+  if (!aligned(b->gamma, es) || !aligned(b->gamma_post, es) || !aligned(b->gate, es))
+    return TIM_ERR_INVALID_ARG;
+  if (!std::isfinite(b->scale) || !(std::isfinite(b->eps) && b->eps >= 0.f))
+    return TIM_ERR_INVALID_ARG;
+  if (b->gate_kind < TIM_GATE_NONE || b->gate_kind > TIM_GATE_ELEMENT ||
+      (b->gate_kind == TIM_GATE_NONE) != (b->gate == nullptr))
+    return TIM_ERR_INVALID_ARG;
+  if (b->gate_kind == TIM_GATE_ELEMENT) return check_matrix(b->gate, b->dtype, b->ld_gate, b->d);
+  if (b->gate_kind == TIM_GATE_TOKEN) return check_matrix(b->gate, b->dtype, b->ld_gate, 1);
+  return TIM_OK;
+}
+
+// The memory of an operand.
+struct Span {
+  const void* p;
+  size_t bytes;
+  int64_t ld;
+};
+Span span(const tim_block* b, const void* p, int64_t ld) {
+  return Span{p, extent(ld, b->T, b->d, b->dtype), ld};
+}
+Span row_span(const tim_block* b, const void* p) {
+  return Span{p, p == nullptr ? 0 : static_cast<size_t>(b->d) * dtype_bytes(b->dtype), 0};
+}
+Span gate_span(const tim_block* b) {
+  if (b->gate_kind == TIM_GATE_ELEMENT) return span(b, b->gate, b->ld_gate);
+  if (b->gate_kind == TIM_GATE_TOKEN)
+    return Span{b->gate, extent(b->ld_gate, b->T, 1, b->dtype), b->ld_gate};
+  return row_span(b, b->gate);
+}
+bool meet(const Span& a, const Span& b) { return meet(a.p, a.bytes, b.p, b.bytes); }
 
 tim_status check_distill(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t V,
                          const int32_t* ids, const float* lp, int32_t K, float temperature,
@@ -997,6 +1036,117 @@ tim_status tim_embed_backward(const void* dy, int32_t dtype, int64_t ldy, const 
   return from_cuda(launch_embed_backward(dy, dtype, ldy, ids, T, V, d, scale, out_dtable, out_dtype,
                                          accumulate, workspace,
                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tim_status tim_residual_norm(const tim_block* b, const void* residual, int64_t ld_residual,
+                             void* out_h, int64_t ld_h, void* out_y, int64_t ld_y,
+                             tim_stream_t stream) {
+  tim_status s = check_block(b);
+  if (s != TIM_OK) return s;
+  if ((s = check_matrix(residual, b->dtype, ld_residual, b->d)) != TIM_OK) return s;
+  if ((s = check_matrix(out_h, b->dtype, ld_h, b->d)) != TIM_OK) return s;
+  if (b->gamma != nullptr && (s = check_matrix(out_y, b->dtype, ld_y, b->d)) != TIM_OK) return s;
+  Span in[5], out[2] = {};
+  in[0] = span(b, residual, ld_residual);
+  in[1] = span(b, b->block, b->ld_block);
+  in[2] = gate_span(b);
+  in[3] = row_span(b, b->gamma);
+  in[4] = row_span(b, b->gamma_post);
+  out[0] = span(b, out_h, ld_h);
+  if (b->gamma != nullptr) out[1] = span(b, out_y, ld_y);
+  for (int o = 0; o < 2; ++o)
+    for (int i = 0; i < 5; ++i)
+      if (meet(out[o], in[i]) && !(i == o && out[o].p == in[i].p && out[o].ld == in[i].ld))
+        return TIM_ERR_INVALID_ARG;
+  if (meet(out[0], out[1])) return TIM_ERR_INVALID_ARG;
+  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  NormArgs a = {};
+  a.b = *b;
+  a.residual = residual;
+  a.ld_residual = ld_residual;
+  a.out_h = out_h;
+  a.ld_h = ld_h;
+  a.out_y = b->gamma != nullptr ? out_y : nullptr;
+  a.ld_y = ld_y;
+  return from_cuda(launch_residual_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tim_residual_norm_backward_workspace_size(int64_t T, int32_t d) {
+  if (T < 1 || T > INT32_MAX || d < 1 || d > TIM_RESIDUAL_MAX_D) return 0;
+  return residual_norm_backward_bytes(T, d);
+}
+
+tim_status tim_residual_norm_backward(const tim_block* b, const void* h, int64_t ld_h,
+                                      const void* dh, int64_t ld_dh, const void* dy, int64_t ld_dy,
+                                      void* out_dresidual, int64_t ld_dresidual, void* out_dblock,
+                                      int64_t ld_dblock, float* out_dgamma, float* out_dgamma_post,
+                                      void* out_dgate, int64_t ld_dgate, int32_t accumulate,
+                                      void* workspace, size_t workspace_bytes, tim_stream_t stream) {
+  tim_status s = check_block(b);
+  if (s != TIM_OK) return s;
+  const bool pre = dy != nullptr;
+  if (pre && b->gamma == nullptr) return TIM_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return TIM_ERR_INVALID_ARG;
+  if (pre && (s = check_matrix(h, b->dtype, ld_h, b->d)) != TIM_OK) return s;
+  if (pre && (s = check_matrix(dy, b->dtype, ld_dy, b->d)) != TIM_OK) return s;
+  if (dh != nullptr && (s = check_matrix(dh, b->dtype, ld_dh, b->d)) != TIM_OK) return s;
+  if ((s = check_matrix(out_dresidual, b->dtype, ld_dresidual, b->d)) != TIM_OK) return s;
+  if ((s = check_matrix(out_dblock, b->dtype, ld_dblock, b->d)) != TIM_OK) return s;
+  if (b->gamma != nullptr && (out_dgamma == nullptr || !aligned(out_dgamma, 4)))
+    return TIM_ERR_INVALID_ARG;
+  if (b->gamma_post != nullptr && (out_dgamma_post == nullptr || !aligned(out_dgamma_post, 4)))
+    return TIM_ERR_INVALID_ARG;
+  Span in[7] = {}, out[5] = {};
+  if (pre) in[0] = span(b, h, ld_h);
+  if (pre) in[1] = span(b, dy, ld_dy);
+  if (dh != nullptr) in[2] = span(b, dh, ld_dh);
+  in[3] = span(b, b->block, b->ld_block);
+  in[4] = gate_span(b);
+  in[5] = row_span(b, b->gamma);
+  in[6] = row_span(b, b->gamma_post);
+  const size_t sums = static_cast<size_t>(b->d) * 4;
+  out[0] = span(b, out_dresidual, ld_dresidual);
+  out[1] = span(b, out_dblock, ld_dblock);
+  if (b->gamma != nullptr) out[2] = Span{out_dgamma, sums, 0};
+  if (b->gamma_post != nullptr) out[3] = Span{out_dgamma_post, sums, 0};
+  if (b->gate_kind == TIM_GATE_ELEMENT) {
+    if ((s = check_matrix(out_dgate, b->dtype, ld_dgate, b->d)) != TIM_OK) return s;
+    out[4] = span(b, out_dgate, ld_dgate);
+  } else if (b->gate_kind != TIM_GATE_NONE) {
+    if (out_dgate == nullptr || !aligned(out_dgate, 4)) return TIM_ERR_INVALID_ARG;
+    out[4] = Span{out_dgate, b->gate_kind == TIM_GATE_TOKEN ? static_cast<size_t>(b->T) * 4 : sums,
+                  0};
+  }
+  for (int o = 0; o < 5; ++o) {
+    for (int i = 0; i < 7; ++i)
+      if (meet(out[o], in[i])) return TIM_ERR_INVALID_ARG;
+    for (int i = 0; i < o; ++i)
+      if (meet(out[o], out[i])) return TIM_ERR_INVALID_ARG;
+  }
+  if ((s = check_workspace(workspace, workspace_bytes, residual_norm_backward_bytes(b->T, b->d))) !=
+      TIM_OK)
+    return s;
+  int sms = 0;
+  if ((s = check_device(&sms)) != TIM_OK) return s;
+  NormGradArgs a = {};
+  a.b = *b;
+  a.h = pre ? h : nullptr;
+  a.ld_h = ld_h;
+  a.dh = dh;
+  a.ld_dh = ld_dh;
+  a.dy = dy;
+  a.ld_dy = ld_dy;
+  a.out_dresidual = out_dresidual;
+  a.ld_dresidual = ld_dresidual;
+  a.out_dblock = out_dblock;
+  a.ld_dblock = ld_dblock;
+  a.out_dgamma = out_dgamma;
+  a.out_dgamma_post = out_dgamma_post;
+  a.out_dgate = out_dgate;
+  a.ld_dgate = ld_dgate;
+  a.accumulate = accumulate;
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 1024);
+  return from_cuda(launch_residual_norm_backward(a, reinterpret_cast<cudaStream_t>(stream), sms));
 }
 
 }  // extern "C"

@@ -1,0 +1,435 @@
+// The residual update after a block, with the norms before and after it, and its gradient.
+//
+//   n  = x / sqrt(mean x^2 + eps) gamma_post   (or x)          x: the block's output
+//   h' = h + scale g n                                          g: a gate a channel, a token, an element
+//   y  = h' / sqrt(mean h'^2 + eps) gamma                       the next block's input
+//
+// h' is rounded to its type before y is taken from it, so that y is what any later reader of the
+// stored h' computes (tim_logprob's final norm among them).
+//
+// Memory's: a row is read once into registers and its one or two sums are taken by the CTA that
+// holds it.  How a row is split over threads depends on d alone, so a row's bits do not depend on
+// the batch.
+#include "residual_norm.cuh"
+
+#include <algorithm>
+#include <type_traits>
+
+#include "logits_row.cuh"
+
+namespace tim {
+namespace {
+
+// A row's elements: thread t holds kVecs vectors of 16 bytes.  kWide: they are whole vectors of
+// memory, t, t + threads, ...; else (rows that do not start at 16-byte boundaries, or end between
+// them) the same registers are filled with single elements, neighbouring threads' next to one another.
+// What lies beyond the row reads as 0.
+template <int kDtype, bool kWide>
+struct Cols {
+  using E = Elem<kDtype>;
+  using raw = typename E::raw;
+  static constexpr int kVec = E::kVec;
+  static __device__ __forceinline__ int col(int k, int i) {
+    const int v = k * blockDim.x;
+    return kWide ? (v + threadIdx.x) * kVec + i : v * kVec + i * blockDim.x + threadIdx.x;
+  }
+  static __device__ __forceinline__ uint4 load(const void* p, int k, int d) {
+    const raw* const row = static_cast<const raw*>(p);
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kWide) {
+      if (col(k, 0) < d) u = *reinterpret_cast<const uint4*>(row + col(k, 0));
+    } else {
+      raw* const to = reinterpret_cast<raw*>(&u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (col(k, i) < d) to[i] = row[col(k, i)];
+    }
+    return u;
+  }
+  static __device__ __forceinline__ void store(void* p, int k, int d, const uint4& u) {
+    raw* const row = static_cast<raw*>(p);
+    if constexpr (kWide) {
+      if (col(k, 0) < d) *reinterpret_cast<uint4*>(row + col(k, 0)) = u;
+    } else {
+      const raw* const from = reinterpret_cast<const raw*>(&u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (col(k, i) < d) row[col(k, i)] = from[i];
+    }
+  }
+  static __device__ __forceinline__ const void* at(const void* p, int64_t offset) {
+    return static_cast<const raw*>(p) + offset;
+  }
+  static __device__ __forceinline__ void* at(void* p, int64_t offset) {
+    return static_cast<raw*>(p) + offset;
+  }
+};
+
+// The sums of kN numbers over the CTA, in a fixed order, in every thread.  Two calls in a row need
+// different scratch.
+template <int kN>
+__device__ __forceinline__ void block_sum(float (&v)[kN], float (*scratch)[kN]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], o);
+  if (lane == 0)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) scratch[warp][n] = v[n];
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    v[n] = lane < warps ? scratch[lane][n] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], o);
+  }
+}
+
+// Where row's gate begins: of a channel gate all rows'.
+template <class C>
+__device__ __forceinline__ const void* gate_of(const tim_block& b, int64_t row) {
+  return C::at(b.gate, b.gate_kind == TIM_GATE_CHANNEL ? 0 : row * b.ld_gate);
+}
+
+template <int kDtype, bool kWide, int kVecs, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1) residual_norm_kernel(const NormArgs a) {
+  using E = Elem<kDtype>;
+  using C = Cols<kDtype, kWide>;
+  constexpr int kVec = E::kVec;
+  __shared__ float scratch[2][32][1];
+  const tim_block& b = a.b;
+  const int64_t row = blockIdx.x;
+  const int d = b.d;
+  uint4 xs[kVecs], hs[kVecs];
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    xs[k] = C::load(C::at(b.block, row * b.ld_block), k, d);
+    hs[k] = C::load(C::at(a.residual, row * a.ld_residual), k, d);
+  }
+  float r1 = 1.f;
+  if (b.gamma_post != nullptr) {
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      float v[kVec];
+      E::unpack(xs[k], v);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) ss[0] = fmaf(v[i], v[i], ss[0]);
+    }
+    block_sum(ss, scratch[0]);
+    r1 = 1.f / sqrtf(ss[0] / static_cast<float>(d) + b.eps);
+  }
+  const void* const gate = gate_of<C>(b, row);
+  const float by_row = b.gate_kind == TIM_GATE_TOKEN
+                           ? E::widen(*static_cast<const typename E::raw*>(gate))
+                           : 1.f;
+  float ss[1] = {0.f};
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    float n[kVec], v[kVec], w[kVec];
+    E::unpack(xs[k], n);
+    E::unpack(hs[k], v);
+    if (b.gamma_post != nullptr) {
+      E::unpack(C::load(b.gamma_post, k, d), w);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) n[i] = n[i] * r1 * w[i];
+    }
+    if (b.gate_kind >= TIM_GATE_CHANNEL) {
+      E::unpack(C::load(gate, k, d), w);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) n[i] *= w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = fmaf(b.scale, n[i] * by_row, v[i]);
+    hs[k] = E::pack(v);
+    C::store(C::at(a.out_h, row * a.ld_h), k, d, hs[k]);
+    E::unpack(hs[k], v);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) ss[0] = fmaf(v[i], v[i], ss[0]);
+  }
+  if (b.gamma == nullptr) return;
+  block_sum(ss, scratch[1]);
+  const float r2 = 1.f / sqrtf(ss[0] / static_cast<float>(d) + b.eps);
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    float v[kVec], w[kVec];
+    E::unpack(hs[k], v);
+    E::unpack(C::load(b.gamma, k, d), w);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = (v[i] * r2) * w[i];
+    C::store(C::at(a.out_y, row * a.ld_y), k, d, E::pack(v));
+  }
+}
+
+// ---- the gradient.  With H the whole gradient of h':
+//   H      = dh' + r2 gamma dy - h' r2^3/d sum(gamma dy h')      dh = H
+//   dn     = scale g H,  dg = scale n H (summed over what a gate is shared by)
+//   dx     = r1 gamma_post dn - x r1^3/d sum(gamma_post dn x)   (or dn)
+//   dgamma = sum_t dy h' r2,  dgamma_post = sum_t dn x r1
+// Two sums a row, the second from the first; the sums over rows stay in registers, a thread's columns
+// over all rows of its CTA, and are left in the workspace for residual_fold_kernel.
+template <int kDtype, bool kWide, int kVecs, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1) residual_norm_backward_kernel(const NormGradArgs a) {
+  using E = Elem<kDtype>;
+  using C = Cols<kDtype, kWide>;
+  constexpr int kVec = E::kVec;
+  __shared__ float scratch1[32][3], scratch2[32][2];
+  const tim_block& b = a.b;
+  const int d = b.d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const bool pre = a.dy != nullptr, post = b.gamma_post != nullptr;
+  const bool by_channel = b.gate_kind == TIM_GATE_CHANNEL, by_element = b.gate_kind == TIM_GATE_ELEMENT;
+  const bool by_token = b.gate_kind == TIM_GATE_TOKEN;
+  float acc_pre[kVecs][kVec] = {}, acc_post[kVecs][kVec] = {}, acc_gate[kVecs][kVec] = {};
+  for (int64_t row = blockIdx.x; row < b.T; row += gridDim.x) {
+    const void* const gate = gate_of<C>(b, row);
+    uint4 hs[kVecs], xs[kVecs], ys[kVecs], ds[kVecs];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      xs[k] = C::load(C::at(b.block, row * b.ld_block), k, d);
+      if (pre) {
+        hs[k] = C::load(C::at(a.h, row * a.ld_h), k, d);
+        ys[k] = C::load(C::at(a.dy, row * a.ld_dy), k, d);
+      }
+      ds[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.dh != nullptr) ds[k] = C::load(C::at(a.dh, row * a.ld_dh), k, d);
+    }
+    float s1[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      float v[kVec], w[kVec], u[kVec];
+      if (pre) {
+        E::unpack(hs[k], v);
+        E::unpack(ys[k], u);
+        E::unpack(C::load(b.gamma, k, d), w);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          s1[0] = fmaf(v[i], v[i], s1[0]);
+          s1[1] = fmaf(w[i] * u[i], v[i], s1[1]);
+        }
+      }
+      if (post) {
+        E::unpack(xs[k], v);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) s1[2] = fmaf(v[i], v[i], s1[2]);
+      }
+    }
+    if (pre || post) block_sum(s1, scratch1);
+    const float r2 = pre ? 1.f / sqrtf(s1[0] * inv_d + b.eps) : 0.f;
+    const float c2 = pre ? r2 * r2 * r2 * inv_d * s1[1] : 0.f;
+    const float r1 = post ? 1.f / sqrtf(s1[2] * inv_d + b.eps) : 1.f;
+    const float by_row =
+        b.scale * (by_token ? E::widen(*static_cast<const typename E::raw*>(gate)) : 1.f);
+    float s2[2] = {0.f, 0.f};
+    float H[kVecs][kVec];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      float v[kVec], w[kVec], u[kVec];
+      E::unpack(ds[k], H[k]);
+      if (pre) {
+        E::unpack(hs[k], v);
+        E::unpack(ys[k], u);
+        E::unpack(C::load(b.gamma, k, d), w);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          H[k][i] += r2 * w[i] * u[i] - c2 * v[i];
+          acc_pre[k][i] = fmaf(u[i] * v[i], r2, acc_pre[k][i]);
+        }
+      }
+      C::store(C::at(a.out_dresidual, row * a.ld_dresidual), k, d, E::pack(H[k]));
+      // from here on u: the block's output, v: n before the gate, w: the post gamma
+      E::unpack(xs[k], u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = u[i];
+      if (post) {
+        E::unpack(C::load(b.gamma_post, k, d), w);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = u[i] * r1 * w[i];
+      }
+      if (by_channel) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc_gate[k][i] = fmaf(H[k][i] * v[i], b.scale, acc_gate[k][i]);
+      } else if (by_element) {
+        float g[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) g[i] = b.scale * H[k][i] * v[i];
+        C::store(C::at(a.out_dgate, row * a.ld_dgate), k, d, E::pack(g));
+      } else if (by_token) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) s2[1] = fmaf(H[k][i], v[i], s2[1]);
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) H[k][i] *= by_row;
+      if (by_channel || by_element) {
+        E::unpack(C::load(gate, k, d), v);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) H[k][i] *= v[i];
+      }
+      if (post) {  // H is dn now
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          acc_post[k][i] = fmaf(H[k][i] * u[i], r1, acc_post[k][i]);
+          H[k][i] *= w[i];
+          s2[0] = fmaf(H[k][i], u[i], s2[0]);
+        }
+      }
+    }
+    if (post || by_token) block_sum(s2, scratch2);
+    if (by_token && threadIdx.x == 0) static_cast<float*>(a.out_dgate)[row] = b.scale * s2[1];
+    const float c1 = post ? r1 * r1 * r1 * inv_d * s2[0] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (post) {
+        float u[kVec];
+        E::unpack(xs[k], u);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) H[k][i] = r1 * H[k][i] - c1 * u[i];
+      }
+      C::store(C::at(a.out_dblock, row * a.ld_dblock), k, d, E::pack(H[k]));
+    }
+    __syncthreads();  // the scratch is the next row's
+  }
+  float* const part = a.partial + static_cast<int64_t>(blockIdx.x) * 3 * d;
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int c = C::col(k, i);
+      if (c >= d) continue;
+      if (b.gamma != nullptr) part[c] = acc_pre[k][i];
+      if (post) part[d + c] = acc_post[k][i];
+      if (by_channel) part[2 * d + c] = acc_gate[k][i];
+    }
+}
+
+// out[c] (+)= sum over the CTAs of part[.][which][c], in order: a CTA has 32 columns of one kind, and
+// its warps share the parts of a column.
+constexpr int kFoldWarps = 8;
+struct FoldArgs {
+  const float* partial;
+  int parts, d, accumulate;
+  float* out[3];
+};
+__global__ void __launch_bounds__(32 * kFoldWarps) residual_fold_kernel(const FoldArgs a) {
+  __shared__ float sum[kFoldWarps][32];
+  float* const out = a.out[blockIdx.y];
+  if (out == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const int per = (a.parts + kFoldWarps - 1) / kFoldWarps;
+  float acc = 0.f;
+  if (c < a.d) {
+    const float* const p = a.partial + static_cast<int64_t>(blockIdx.y) * a.d + c;
+    const int i1 = min(a.parts, (warp + 1) * per);
+#pragma unroll 8
+    for (int i = warp * per; i < i1; ++i) acc += __ldg(p + static_cast<int64_t>(i) * 3 * a.d);
+  }
+  sum[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0 || c >= a.d) return;
+#pragma unroll
+  for (int w = 1; w < kFoldWarps; ++w) acc += sum[w][lane];
+  out[c] = a.accumulate ? out[c] + acc : acc;
+}
+
+bool wide(const void* p, int64_t ld, int es) {
+  return p == nullptr ||
+         ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * es)) & 15u) == 0;
+}
+int elem_bytes(int dtype) { return dtype == TIM_F32 ? 4 : 2; }
+// Whether the operands that both directions take have rows of whole vectors.
+bool wide(const tim_block& b) {
+  const int es = elem_bytes(b.dtype);
+  return b.d * es % 16 == 0 && wide(b.block, b.ld_block, es) && wide(b.gamma, 0, es) &&
+         wide(b.gamma_post, 0, es) && (b.gate_kind != TIM_GATE_CHANNEL || wide(b.gate, 0, es)) &&
+         (b.gate_kind != TIM_GATE_ELEMENT || wide(b.gate, b.ld_gate, es));
+}
+
+template <int kN>
+using Int = std::integral_constant<int, kN>;
+
+// f(vectors of a thread, threads a row), by the row's vectors alone.
+template <class F>
+cudaError_t with_split(int nvec, F&& f) {
+  if (nvec <= 64) return f(Int<1>(), Int<64>());
+  if (nvec <= 128) return f(Int<1>(), Int<128>());
+  if (nvec <= 256) return f(Int<1>(), Int<256>());
+  if (nvec <= 512) return f(Int<2>(), Int<256>());
+  if (nvec <= 1024) return f(Int<2>(), Int<512>());
+  if (nvec <= 2048) return f(Int<2>(), Int<1024>());
+  return f(Int<4>(), Int<1024>());
+}
+constexpr int kMaxParts = 1024;
+
+template <int kDtype, bool kWide>
+cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
+  const int nvec = (a.b.d + Elem<kDtype>::kVec - 1) / Elem<kDtype>::kVec;
+  return with_split(nvec, [&](auto vecs, auto threads) {
+    residual_norm_kernel<kDtype, kWide, vecs.value, threads.value>
+        <<<static_cast<unsigned>(a.b.T), threads.value, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+template <int kDtype, bool kWide>
+cudaError_t launch_backward(const NormGradArgs& a, cudaStream_t stream, int num_sms) {
+  const int nvec = (a.b.d + Elem<kDtype>::kVec - 1) / Elem<kDtype>::kVec;
+  FoldArgs f = {};
+  f.partial = a.partial;
+  f.d = a.b.d;
+  f.accumulate = a.accumulate;
+  if (a.b.gamma != nullptr) f.out[0] = a.out_dgamma;
+  if (a.b.gamma_post != nullptr) f.out[1] = a.out_dgamma_post;
+  if (a.b.gate_kind == TIM_GATE_CHANNEL) f.out[2] = static_cast<float*>(a.out_dgate);
+  const cudaError_t e = with_split(nvec, [&](auto vecs, auto threads) {
+    const int64_t resident = static_cast<int64_t>(num_sms) * std::max(1, 512 / threads.value);
+    f.parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.b.T, resident), kMaxParts));
+    residual_norm_backward_kernel<kDtype, kWide, vecs.value, threads.value>
+        <<<f.parts, threads.value, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+  if (e != cudaSuccess) return e;
+  if (f.out[0] == nullptr && f.out[1] == nullptr && f.out[2] == nullptr) return e;
+  residual_fold_kernel<<<dim3((a.b.d + 31) / 32, 3), 32 * kFoldWarps, 0, stream>>>(f);
+  return cudaGetLastError();
+}
+
+// f(type, whether rows are whole vectors)
+template <class F>
+cudaError_t by_type(int dtype, bool w, F&& f) {
+  using Yes = std::bool_constant<true>;
+  using No = std::bool_constant<false>;
+  if (dtype == TIM_F32) return w ? f(Int<TIM_F32>(), Yes()) : f(Int<TIM_F32>(), No());
+  if (dtype == TIM_BF16) return w ? f(Int<TIM_BF16>(), Yes()) : f(Int<TIM_BF16>(), No());
+  return w ? f(Int<TIM_F16>(), Yes()) : f(Int<TIM_F16>(), No());
+}
+
+}  // namespace
+
+cudaError_t launch_residual_norm(const NormArgs& a, cudaStream_t stream) {
+  const int es = elem_bytes(a.b.dtype);
+  const bool w = wide(a.b) && wide(a.residual, a.ld_residual, es) && wide(a.out_h, a.ld_h, es) &&
+                 wide(a.out_y, a.ld_y, es);
+  return by_type(a.b.dtype, w, [&](auto type, auto is_wide) {
+    return launch_forward<type.value, is_wide.value>(a, stream);
+  });
+}
+
+size_t residual_norm_backward_bytes(int64_t T, int d) {
+  return align_up(1024 + static_cast<size_t>(std::min<int64_t>(T, kMaxParts)) * 3 *
+                             static_cast<size_t>(d) * 4,
+                  1024);
+}
+
+cudaError_t launch_residual_norm_backward(const NormGradArgs& a, cudaStream_t stream, int num_sms) {
+  const int es = elem_bytes(a.b.dtype);
+  const bool w = wide(a.b) && wide(a.h, a.ld_h, es) && wide(a.dh, a.ld_dh, es) &&
+                 wide(a.dy, a.ld_dy, es) && wide(a.out_dresidual, a.ld_dresidual, es) &&
+                 wide(a.out_dblock, a.ld_dblock, es) &&
+                 (a.b.gate_kind != TIM_GATE_ELEMENT || wide(a.out_dgate, a.ld_dgate, es));
+  return by_type(a.b.dtype, w, [&](auto type, auto is_wide) {
+    return launch_backward<type.value, is_wide.value>(a, stream, num_sms);
+  });
+}
+
+}  // namespace tim
