@@ -699,6 +699,62 @@ tim_status tim_distill_backward(const void *logits, int32_t dtype, int64_t ld, i
                                 void *out_dlogits, int64_t ldd, tim_stream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Verification of drafted tokens.
+ *
+ * B sequences with up to N drafted tokens each; row (b, j) of the target's logits
+ * predicts position j, row (b, N) what follows the last draft.  p_j and q_j are the
+ * distributions that temperature, top-k, top-p and min-p leave of a target's and a
+ * drafter's row, as tim_sample defines them (temperature 0: all on the first token of
+ * the order).  Per sequence, with x_j = draft_ids[b, j], the first -1 of which ends the
+ * drafts:
+ *   x_j is accepted, j = 0, 1, ..., while  uniform[b, j] q_j(x_j) < p_j(x_j);
+ *   at the first that is not, the token y is the smallest v with
+ *     sum_{w <= v} r_w > uniform_draw[b] sum_w r_w,  r = max(p_j - q_j, 0)
+ *     (where r sums to less than 2^-28, what is left of two distributions that agree: with
+ *     p_j in its place);
+ *   where all drafts are accepted y is drawn the same way from the p of the row after the
+ *     last, which is tim_sample's token for that row and number.
+ *   out_ids[b]      the accepted tokens, y, and -1 up to N + 1 numbers;
+ *   out_logprob[b]  ln p_j of each (score A of tim_compare), 0 beyond y;
+ *   out_accepted[b] how many drafts were accepted.
+ * The tokens are distributed as p, whatever the drafter proposes.  Sums are held in
+ * 64-bit integers of p_v and q_v good to 2^-30.3 each, so a token differs from exact
+ * arithmetic's only if a border lies within 2^-28 of the mass of p, or
+ * uniform q(x) within 2^-29 of p(x) relative to it.
+ *
+ * target, draft  logits of dtype: row (b, j) begins at logits + b ld_seq + j ld_pos
+ *                elements, strides of 0 up to 2^40, any element-aligned address; draft may
+ *                be NULL: the drafter is certain, q_j(x_j) = 1 (tokens found by lookup).
+ *                Rows behind the end of a sequence's drafts are not read.
+ * V              1 .. TIM_LOGITS_MAX_V;  1 <= N <= TIM_VERIFY_MAX_DRAFTS;  B >= 1,
+ *                B (2 N + 1) <= 2^28 - 1.
+ * draft_ids      int32 [B, N];  uniform float32 [B, N];  uniform_draw float32 [B], both
+ *                in [0, 1).
+ * params         as of tim_sample with row_* [B], a setting a sequence; draft_params those
+ *                the drafter drew with, NULL: the same.
+ * out_*          int32 [B, N + 1], float32 [B, N + 1], int32 [B]; must not meet draft_ids.
+ * workspace      tim_verify_workspace_size(B, N) bytes, which serve smaller B and N and
+ *                the other operators on logits too; zero-initialised once.
+ * Errors: as tim_sample.  Via tim_status_sync: TIM_ERR_TOKEN_RANGE (an id below -1 or
+ *   from V up), TIM_ERR_INVALID_ARG (a uniform number or a setting out of range),
+ *   TIM_ERR_NONFINITE (a row read that has NaN, +inf or -inf alone).  A sequence that
+ *   reaches such a position gets ids -1, logprob NaN and 0 accepted, the others are as
+ *   always; the status word also names rows that no sequence reaches, since all rows up to
+ *   the end of the drafts are read.
+ * ------------------------------------------------------------------------ */
+#define TIM_VERIFY_MAX_DRAFTS 1024
+
+size_t tim_verify_workspace_size(int64_t B, int32_t N);
+
+tim_status tim_verify(const void *target, int64_t target_ld_seq, int64_t target_ld_pos,
+                      const void *draft, int64_t draft_ld_seq, int64_t draft_ld_pos, int32_t dtype,
+                      int64_t B, int32_t N, int32_t V, const int32_t *draft_ids,
+                      const float *uniform, const float *uniform_draw,
+                      const tim_sample_params *params, const tim_sample_params *draft_params,
+                      int32_t *out_ids, float *out_logprob, int32_t *out_accepted, void *workspace,
+                      size_t workspace_bytes, tim_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Embedding lookup, and its gradient.
  *
  *   out[t, i]    = scale table[ids[t], i]               (fp32 product, rounded once)

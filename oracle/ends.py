@@ -104,62 +104,69 @@ def residual_norm_backward(h, x, dh, dy, gamma, gamma_post, gate, scale: float, 
 
 # ----------------------------------------------------------------------------- verification
 
+NO_REST = 2.0 ** -28  # of max(p - q, 0), below which p is drawn from
+
+
 def processed(z, temperature: float, top_k: int, top_p: float, min_p: float):
-    """(p [V], the tokens in the filters' order that top-p looks at, how near the nearest border)."""
+    """(p [V], ln p [V], how near the nearest border of a filter lies)."""
     z = np.asarray(z, dtype=np.float64)
     V = z.shape[0]
-    p = np.zeros(V)
+    lp = np.full(V, -np.inf)
     order = np.lexsort((np.arange(V), -z))
     if temperature == 0.0:
-        p[order[0]] = 1.0
-        return p, math.inf
+        lp[order[0]] = 0.0
+        return np.exp(lp), lp, math.inf
     order = order[z[order] > -np.inf]
     if 0 < top_k < V:
         order = order[:top_k]
-    w = np.exp((z[order] - z[order[0]]) / temperature)
+    s = (z[order] - z[order[0]]) / temperature
+    w = np.exp(s)
     keep, margin = w >= min_p, math.inf
     if top_p < 1.0:
         before = np.concatenate(([0.0], np.cumsum(w)[:-1])) / np.sum(w)
         keep &= before < top_p
         margin = float(np.min(np.abs(before - top_p)))
-    p[order[keep]] = w[keep] / np.sum(w[keep])
-    return p, margin
+    lp[order[keep]] = s[keep] - math.log(np.sum(w[keep]))
+    return np.exp(lp), lp, margin
 
 
 def verify_sequence(target, draft, ids, uniform, uniform_draw: float, settings, draft_settings=None):
     """ids, logprob [N + 1], accepted, and ``margin``: how near the nearest border of a decision lies,
-    in units of the mass of p and q (of an acceptance: relative to p of the token)."""
+    in units of the mass of p (of an acceptance: relative to p of the token)."""
     N = len(ids)
     out, lps, margin = [], [], math.inf
     for j in range(N + 1):
-        p, m = processed(target[j], *settings)
+        p, lp, m = processed(target[j], *settings)
         margin = min(margin, m)
         x = int(ids[j]) if j < N else -1
         r = p
         if x >= 0:
             if draft is None:
-                q = np.zeros_like(p)
+                q, lq = np.zeros_like(p), 0.0
                 q[x] = 1.0
             else:
-                q, m = processed(draft[j], *(draft_settings or settings))
+                q, lq, m = processed(draft[j], *(draft_settings or settings))
+                lq = lq[x]
                 margin = min(margin, m)
-            if p[x] > 0 and uniform[j] > 0:
-                margin = min(margin, abs(uniform[j] * q[x] - p[x]) / p[x])
-            if uniform[j] * q[x] < p[x]:
+            # u q(x) < p(x), which both may lie below the range of a number
+            ln_uq = lq + (math.log(uniform[j]) if uniform[j] > 0 else -math.inf)
+            if lp[x] > -math.inf and ln_uq > -math.inf:
+                margin = min(margin, abs(ln_uq - lp[x]))
+            if ln_uq < lp[x]:
                 out.append(x)
-                lps.append(math.log(p[x]))
+                lps.append(float(lp[x]))
                 continue
             rest = np.maximum(p - q, 0.0)
-            if rest.sum() > 0:
+            margin = min(margin, abs(rest.sum() - NO_REST))
+            if rest.sum() >= NO_REST:
                 r = rest
         c = np.cumsum(r)
         at = int(np.searchsorted(c, uniform_draw * c[-1], side="right"))
         y = min(at, int(np.nonzero(r)[0][-1]))
         if uniform_draw > 0:
-            # the borders next to the draw; a sum that is far away is none
             margin = min(margin, float(np.min(np.abs(c - uniform_draw * c[-1]))))
         out.append(y)
-        lps.append(math.log(p[y]))
+        lps.append(float(lp[y]))
         break
     n = len(out) - 1
     pad = N + 1 - len(out)

@@ -132,6 +132,10 @@ class _Block(_c.Structure):
 
 
 _SIGNATURES.update({
+    "tim_verify_workspace_size": (_sz, [_i64, _i32]),
+    "tim_verify": (_c.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i32, _i32, _vp, _vp,
+                              _vp, _c.POINTER(_SampleParams), _c.POINTER(_SampleParams), _vp, _vp,
+                              _vp, _vp, _sz, _vp]),
     "tim_embed": (_c.c_int, [_vp, _i32, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _i64, _vp, _sz,
                              _vp]),
     "tim_embed_backward_workspace_size": (_sz, [_i64, _i32, _i32]),
@@ -677,8 +681,8 @@ DISTILL_KINDS = {"forward": 0, "reverse": 1}
 _DTYPE_CODES = {}
 
 
-def _logits_args(t, name):
-    """(T, V, dtype code, row stride) of a [T, V] CUDA tensor whose rows are contiguous."""
+def _type_code(t, name):
+    """The dtype code of a CUDA tensor."""
     torch = _torch()
     if not _DTYPE_CODES:
         _DTYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
@@ -689,6 +693,12 @@ def _logits_args(t, name):
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    return code
+
+
+def _logits_args(t, name):
+    """(T, V, dtype code, row stride) of a [T, V] CUDA tensor whose rows are contiguous."""
+    code = _type_code(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     T, V = t.shape
@@ -736,6 +746,30 @@ def _status_workspace(workspace, dev, stream):
     return workspace
 
 
+def _sample_params(temperature, top_k, top_p, min_p, n, dev):
+    """The settings as numbers, or as [n] tensors on ``dev``."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    p = _SampleParams(1.0, 0, 1.0, 0.0, None, None, None, None)
+    if isinstance(temperature, torch.Tensor):
+        p.row_temperature = _vector(temperature, f32, n, dev, "temperature")
+    else:
+        p.temperature = temperature
+    if isinstance(top_k, torch.Tensor):
+        p.row_top_k = _vector(top_k, i32, n, dev, "top_k")
+    else:
+        p.top_k = min(max(int(top_k), 0), 2 ** 31 - 1)  # ctypes would keep the low 32 bits
+    if isinstance(top_p, torch.Tensor):
+        p.row_top_p = _vector(top_p, f32, n, dev, "top_p")
+    else:
+        p.top_p = top_p
+    if isinstance(min_p, torch.Tensor):
+        p.row_min_p = _vector(min_p, f32, n, dev, "min_p")
+    else:
+        p.min_p = min_p
+    return p
+
+
 def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, out=None,
            workspace: Optional[Workspace] = None, stream=None, check: bool = True):
     """Draw one token a row from ``logits`` [T, V] (float32, bfloat16 or float16 CUDA tensor,
@@ -752,23 +786,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, o
     dev = logits.device
     f32, i32 = torch.float32, torch.int32
     u = _vector(uniform, f32, T, dev, "uniform")
-    p = _SampleParams(1.0, 0, 1.0, 0.0, None, None, None, None)
-    if isinstance(temperature, torch.Tensor):
-        p.row_temperature = _vector(temperature, f32, T, dev, "temperature")
-    else:
-        p.temperature = temperature
-    if isinstance(top_k, torch.Tensor):
-        p.row_top_k = _vector(top_k, i32, T, dev, "top_k")
-    else:
-        p.top_k = min(max(int(top_k), 0), 2 ** 31 - 1)  # ctypes would keep the low 32 bits
-    if isinstance(top_p, torch.Tensor):
-        p.row_top_p = _vector(top_p, f32, T, dev, "top_p")
-    else:
-        p.top_p = top_p
-    if isinstance(min_p, torch.Tensor):
-        p.row_min_p = _vector(min_p, f32, T, dev, "min_p")
-    else:
-        p.min_p = min_p
+    p = _sample_params(temperature, top_k, top_p, min_p, T, dev)
     if out is not None:
         for t, dtype, name in zip(out, (i32, f32, f32, i32), ("ids", "logprob", "lse_kept", "kept")):
             _vector(t, dtype, T, dev, "out " + name)
@@ -971,6 +989,83 @@ def _matrix(t, T, d, code, dev, name):
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
     return ld
+
+
+def verify_workspace_size(B: int, N: int) -> int:
+    """Bytes of the workspace of ``verify`` for B sequences of up to N drafts."""
+    return int(lib().tim_verify_workspace_size(int(B), int(N)))
+
+
+def _sequence_rows(t, B, n, V, dev, name):
+    """(dtype code, sequence stride, position stride) of a [B, n, V] tensor with contiguous rows."""
+    code = _type_code(t, name)
+    if tuple(t.shape) != (B, n, V):
+        raise ValueError(f"{name} must be [{B}, {n}, {V}], got {list(t.shape)}")
+    if V > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    return code, t.stride(0), t.stride(1)
+
+
+def verify(target, draft_ids, uniform, uniform_draw, draft=None, temperature=1.0, top_k=0,
+           top_p=1.0, min_p=0.0, *, draft_settings=None, out=None,
+           workspace: Optional[Workspace] = None, stream=None, check: bool = True):
+    """Accept or refuse drafted tokens against a target's logits (tim_verify), so that what comes
+    out is distributed as ``sample`` would draw from ``target``.
+
+    ``target`` [B, N + 1, V] and ``draft`` [B, N, V] are logits (float32, bfloat16 or float16 CUDA
+    tensors of one type, rows contiguous, any strides of the first two dimensions); without
+    ``draft`` the drafter is certain of its tokens.  ``draft_ids`` int32 [B, N], the first -1 of a
+    row ends its drafts; ``uniform`` float32 [B, N] and ``uniform_draw`` float32 [B] in [0, 1).
+    ``temperature``, ``top_k``, ``top_p``, ``min_p`` as in ``sample``, numbers or [B] tensors;
+    ``draft_settings`` = the same four of the drafter, the target's if not given.
+    Returns (ids i32 [B, N + 1]: the accepted tokens, one drawn, then -1; logprob f32 [B, N + 1]
+    under the target; accepted i32 [B]).  ``out`` = the three result tensors to write."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    _need(draft_ids, i32, "draft_ids", 2)
+    B, N = draft_ids.shape
+    dev = draft_ids.device
+    if not isinstance(target, torch.Tensor) or target.dim() != 3:
+        raise ValueError("target must be a [B, N + 1, V] tensor")
+    V = target.shape[2]
+    code, ts, tp = _sequence_rows(target, B, N + 1, V, dev, "target")
+    ds = dp = 0
+    if draft is not None:
+        dcode, ds, dp = _sequence_rows(draft, B, N, V, dev, "draft")
+        if dcode != code:
+            raise TypeError(f"draft must be {target.dtype}, got {draft.dtype}")
+    _need(uniform, f32, "uniform", 2)
+    if uniform.shape != draft_ids.shape or uniform.device != dev:
+        raise ValueError(f"uniform must be [{B}, {N}] on {dev}")
+    u = _vector(uniform_draw, f32, B, dev, "uniform_draw")
+    p = _sample_params(temperature, top_k, top_p, min_p, B, dev)
+    q = None if draft_settings is None else _c.byref(_sample_params(*draft_settings, B, dev))
+    if out is not None:
+        for t, dtype, shape, name in zip(out, (i32, f32, i32), ((B, N + 1), (B, N + 1), (B,)),
+                                         ("ids", "logprob", "accepted")):
+            _need(t, dtype, "out " + name)
+            if tuple(t.shape) != shape or t.device != dev:
+                raise ValueError(f"out {name} must be {list(shape)} on {dev}")
+
+    def call(sp):
+        o = out
+        if o is None:
+            o = (torch.empty(B, N + 1, dtype=i32, device=dev),
+                 torch.empty(B, N + 1, dtype=f32, device=dev),
+                 torch.empty(B, dtype=i32, device=dev))
+        ws = _sized_workspace(workspace, dev, stream, lambda: verify_workspace_size(B, N))
+        _check(lib().tim_verify(target.data_ptr(), ts, tp,
+                                None if draft is None else draft.data_ptr(), ds, dp, code, B, N, V,
+                                draft_ids.data_ptr(), uniform.data_ptr(), u, _c.byref(p), q,
+                                o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), ws.ptr, ws.nbytes,
+                                sp), "tim_verify")
+        if check:
+            ws.check("tim_verify", stream)
+        return o
+
+    return _run(dev, stream, call)
 
 
 def embed(table, ids, scale: float = 1.0, *, out=None, workspace: Optional[Workspace] = None,

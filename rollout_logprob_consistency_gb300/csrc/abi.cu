@@ -6,6 +6,7 @@
 
 #include "residual_norm.cuh"
 #include "tim_common.cuh"
+#include "verify.cuh"
 
 namespace tim {
 cudaError_t launch_rmsnorm_rows(const void* hidden, const void* gamma, int64_t T, int d, float eps,
@@ -280,6 +281,25 @@ size_t extent(int64_t ld, int64_t rows, int32_t d, int32_t dtype) {
 bool meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return a_bytes != 0 && b_bytes != 0 && a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+}
+
+// The settings of tim_sample that are numbers, and the addresses of the others.
+tim_status check_settings(const tim_sample_params& p) {
+  if (!aligned(p.row_temperature, 4) || !aligned(p.row_top_k, 4) || !aligned(p.row_top_p, 4) ||
+      !aligned(p.row_min_p, 4))
+    return TIM_ERR_INVALID_ARG;
+  if (p.row_temperature == nullptr && p.temperature != 0.f &&
+      !(p.temperature >= 1e-6f && p.temperature <= 1e6f))
+    return TIM_ERR_INVALID_ARG;
+  if (p.row_top_p == nullptr && !(p.top_p > 0.f)) return TIM_ERR_INVALID_ARG;
+  if (p.row_min_p == nullptr && !(p.min_p >= 0.f && p.min_p <= 1.f)) return TIM_ERR_INVALID_ARG;
+  return TIM_OK;
+}
+
+tim_status check_drafts(int64_t B, int32_t N) {
+  if (N < 1 || N > TIM_VERIFY_MAX_DRAFTS || B < 1 || B > ((1 << 28) - 1) / (2 * N + 1))
+    return TIM_ERR_SHAPE;
+  return TIM_OK;
 }
 
 // A matrix of rows of d elements with row stride ld.
@@ -921,14 +941,9 @@ tim_status tim_sample(const void* logits, int32_t dtype, int64_t ld, int64_t T, 
     return TIM_ERR_INVALID_ARG;
   const tim_sample_params& p = *params;
   if (!aligned(uniform, 4) || !aligned(out_ids, 4) || !aligned(out_logprob, 4) ||
-      !aligned(out_lse_kept, 4) || !aligned(out_kept, 4) || !aligned(p.row_temperature, 4) ||
-      !aligned(p.row_top_k, 4) || !aligned(p.row_top_p, 4) || !aligned(p.row_min_p, 4))
+      !aligned(out_lse_kept, 4) || !aligned(out_kept, 4))
     return TIM_ERR_INVALID_ARG;
-  if (p.row_temperature == nullptr && p.temperature != 0.f &&
-      !(p.temperature >= 1e-6f && p.temperature <= 1e6f))
-    return TIM_ERR_INVALID_ARG;
-  if (p.row_top_p == nullptr && !(p.top_p > 0.f)) return TIM_ERR_INVALID_ARG;
-  if (p.row_min_p == nullptr && !(p.min_p >= 0.f && p.min_p <= 1.f)) return TIM_ERR_INVALID_ARG;
+  if ((s = check_settings(p)) != TIM_OK) return s;
   if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;
@@ -993,6 +1008,50 @@ tim_status tim_distill_backward(const void* logits, int32_t dtype, int64_t ld, i
   return from_cuda(launch_distill_backward(logits, dtype, ld, T, V, teacher_ids, teacher_logprob,
                                            K, temperature, kind, saved, grad_loss, out_dlogits,
                                            ldd, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tim_verify_workspace_size(int64_t B, int32_t N) {
+  return check_drafts(B, N) == TIM_OK ? verify_bytes(B, N) : 0;
+}
+
+tim_status tim_verify(const void* target, int64_t target_ld_seq, int64_t target_ld_pos,
+                      const void* draft, int64_t draft_ld_seq, int64_t draft_ld_pos, int32_t dtype,
+                      int64_t B, int32_t N, int32_t V, const int32_t* draft_ids,
+                      const float* uniform, const float* uniform_draw,
+                      const tim_sample_params* params, const tim_sample_params* draft_params,
+                      int32_t* out_ids, float* out_logprob, int32_t* out_accepted, void* workspace,
+                      size_t workspace_bytes, tim_stream_t stream) {
+  const size_t es = dtype_bytes(dtype);
+  if (target == nullptr || es == 0 || !aligned(target, es) || !aligned(draft, es) ||
+      draft_ids == nullptr || uniform == nullptr || uniform_draw == nullptr || params == nullptr ||
+      out_ids == nullptr || out_logprob == nullptr || out_accepted == nullptr)
+    return TIM_ERR_INVALID_ARG;
+  if (!aligned(draft_ids, 4) || !aligned(uniform, 4) || !aligned(uniform_draw, 4) ||
+      !aligned(out_ids, 4) || !aligned(out_logprob, 4) || !aligned(out_accepted, 4))
+    return TIM_ERR_INVALID_ARG;
+  tim_status s = check_drafts(B, N);
+  if (s != TIM_OK) return s;
+  if (V < 1 || V > TIM_LOGITS_MAX_V) return TIM_ERR_SHAPE;
+  const int64_t far = static_cast<int64_t>(1) << 40;
+  if (target_ld_seq < 0 || target_ld_seq > far || target_ld_pos < 0 || target_ld_pos > far ||
+      draft_ld_seq < 0 || draft_ld_seq > far || draft_ld_pos < 0 || draft_ld_pos > far)
+    return TIM_ERR_SHAPE;
+  if ((s = check_settings(*params)) != TIM_OK) return s;
+  if (draft_params != nullptr && (s = check_settings(*draft_params)) != TIM_OK) return s;
+  const size_t ids = static_cast<size_t>(B) * static_cast<size_t>(N) * 4;
+  const size_t all = ids + static_cast<size_t>(B) * 4;
+  if (meet(draft_ids, ids, out_ids, all) || meet(draft_ids, ids, out_logprob, all) ||
+      meet(draft_ids, ids, out_accepted, static_cast<size_t>(B) * 4))
+    return TIM_ERR_INVALID_ARG;
+  if ((s = check_workspace(workspace, workspace_bytes, verify_bytes(B, N))) != TIM_OK) return s;
+  int sms = 0;
+  if ((s = check_device(&sms)) != TIM_OK) return s;
+  return from_cuda(launch_verify(VerifyMatrix{target, target_ld_seq, target_ld_pos},
+                                 VerifyMatrix{draft, draft_ld_seq, draft_ld_pos}, dtype, B, N, V,
+                                 draft_ids, uniform, uniform_draw, *params,
+                                 draft_params != nullptr ? *draft_params : *params, out_ids,
+                                 out_logprob, out_accepted, workspace,
+                                 reinterpret_cast<cudaStream_t>(stream), sms));
 }
 
 tim_status tim_embed(const void* table, int32_t dtype, int64_t ld, const int32_t* ids, int64_t T,

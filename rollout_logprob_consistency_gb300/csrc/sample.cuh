@@ -12,6 +12,7 @@ namespace sampling {
 using u64 = unsigned long long;
 
 struct SampleArgs {
+  static constexpr bool kBorder = false;  // whether write_row uses a row's border
   const void* logits;
   int64_t ld;
   int V;
@@ -148,6 +149,12 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row
   if (t.k <= 0 || t.k >= a.V) t.k = 0;
   return t;
 }
+
+template <int kDtype>
+__device__ __forceinline__ Row<kDtype> row_of(const SampleArgs& a, int64_t row) {
+  return Row<kDtype>(a.logits, row, a.ld, a.V);
+}
+__device__ __forceinline__ bool wanted(const SampleArgs&, int64_t) { return true; }
 
 // What a row's weights are taken with.
 struct RowState {
@@ -317,17 +324,24 @@ __device__ __forceinline__ void write_bad(const SampleArgs& a, int64_t row, int 
   a.kept[row] = 0;
 }
 
-// total: kept weights' sum; x: logit of the token; n: tokens kept; by one thread
-__device__ __forceinline__ void write_row(const SampleArgs& a, const RowState& st,
-                                          const Tables& tables, int64_t row, int id, float x,
-                                          u64 total, int n) {
-  // ln total as a pair: the leading 48 bits, and the scale
+// ln of a sum of weights as a pair: the leading 48 bits, and the scale
+__device__ __forceinline__ Df log_total(u64 total, int top, const Tables& tables) {
   const int lz = __clzll(static_cast<long long>(total));
   const u64 t = total << lz;
   const Df f = renorm(static_cast<float>(static_cast<uint32_t>(t >> 40)) * 0x1p-24f,
                       static_cast<float>(static_cast<uint32_t>(t >> 16) & 0xFFFFFFu) * 0x1p-48f);
-  const float e = static_cast<float>(64 - lz + st.top - 62);
-  const Df ln = log_df(f, tables.fine) + Df{kLn2Hi, kLn2Lo} * df(e);
+  const float e = static_cast<float>(64 - lz + top - 62);
+  return log_df(f, tables.fine) + Df{kLn2Hi, kLn2Lo} * df(e);
+}
+
+// The border of a row without filters: key << 32 | ~id of the last token above -inf.
+constexpr u64 kAllKept = static_cast<u64>(kNegInfKey + 1) << 32;
+
+// total: kept weights' sum; x: logit of the token; n: tokens kept; by one thread
+__device__ __forceinline__ void write_row(const SampleArgs& a, const RowState& st,
+                                          const Tables& tables, int64_t row, int id, float x,
+                                          u64 total, int n, u64) {
+  const Df ln = log_total(total, st.top, tables);
   const float base = st.pw.recentre ? st.pw.c : 0.f;
   const Df lse = ln + df(base) * st.inv_tau;
   a.ids[row] = id;

@@ -47,7 +47,7 @@ struct DeepScratch {
   int all;
 };
 
-template <int kDtype, int kThreads>
+template <int kDtype, int kThreads, class Args>
 struct Deep {
   using E = Elem<kDtype>;
   static constexpr int kVec = E::kVec;
@@ -58,7 +58,7 @@ struct Deep {
   static constexpr int kStream = 4;
   static constexpr int kParts = 32;    // of the row, for its running sums
 
-  const SampleArgs& a;
+  const Args& a;
   DeepShared& sh;
   DeepScratch& sc;
   const Tables& table;
@@ -502,9 +502,10 @@ struct Deep {
 
   // The draw, f and one being the kept tokens' weights, of `n` tokens; after row_sum(f).
   template <class F, class G>
-  __device__ __forceinline__ void draw(int64_t row, float u, u64 total, uint32_t n, F&& f, G&& one) {
+  __device__ __forceinline__ void draw(int64_t row, float u, u64 total, uint32_t n, u64 border, F&& f,
+                                       G&& one) {
     const int id = locate(draw_target(total, u), f, one);
-    if (tid == 0) write_row(a, st, table, row, id, r.at(id), total, static_cast<int>(n));
+    if (tid == 0) write_row(a, st, table, row, id, r.at(id), total, static_cast<int>(n), border);
   }
   // Sum of a count over the CTA's threads.
   __device__ __forceinline__ uint32_t count_all(uint32_t n) {
@@ -553,7 +554,9 @@ struct Deep {
         total = row_sum(kept);
         all = count_all(n);
       }
-      draw(row, u, total, all, kept, one);
+      draw(row, u, total, all,
+           (static_cast<u64>(st.kc) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(st.idc)), kept,
+           one);
     };
     if (st.pw.recentre) {
       finish([&](const float(&v)[kVec], int id0) {
@@ -686,7 +689,7 @@ struct Deep {
         return t;
       };
       const u64 total = row_sum(all);
-      draw(row, u, total, n, all, one);
+      draw(row, u, total, n, kAllKept, all, one);
       return;
     }
     // the row's scale: its total at 2^58 or 2^59
@@ -706,7 +709,8 @@ struct Deep {
     const uint32_t shift = shift_of(st.top);
     const u64 total = warp_sum(scaled);
     __syncthreads();
-    draw(row, u, total, n, [&](const float(&v)[kVec], int) { return weights_of(v, shift); }, one);
+    draw(row, u, total, n, kAllKept,
+         [&](const float(&v)[kVec], int) { return weights_of(v, shift); }, one);
   }
 };
 

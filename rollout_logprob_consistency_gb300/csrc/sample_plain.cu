@@ -147,7 +147,7 @@ struct Sampler {
     const u64 target = draw_target(total, u);
     if (before <= target && target < before + mine) {  // one CTA of the row
       const int id = locate(target - before, f, one);
-      if (tid == 0) write_row(a, st, sh.table, row, id, r.at(id), total, static_cast<int>(all));
+      if (tid == 0) write_row(a, st, sh.table, row, id, r.at(id), total, static_cast<int>(all), kAllKept);
     }
   }
 
