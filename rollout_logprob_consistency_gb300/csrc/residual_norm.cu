@@ -167,13 +167,74 @@ __global__ void __launch_bounds__(kThreads, 1) residual_norm_kernel(const NormAr
 //   dn     = scale g H,  dg = scale n H (summed over what a gate is shared by)
 //   dx     = r1 gamma_post dn - x r1^3/d sum(gamma_post dn x)   (or dn)
 //   dgamma = sum_t dy h' r2,  dgamma_post = sum_t dn x r1
-// Two sums a row, the second from the first; the sums over rows stay in registers, a thread's columns
-// over all rows of its CTA, and are left in the workspace for residual_fold_kernel.
-template <int kDtype, bool kWide, int kVecs, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1) residual_norm_backward_kernel(const NormGradArgs a) {
+// Two sums a row, the second from the first.  A CTA takes every gridDim-th row; the sums over its rows
+// stay in registers, a thread's columns, and are left in the workspace for residual_fold_kernel.
+//
+// kStages: the rows that are on their way to shared memory while one is worked on, copied by the
+// threads that will read them, so that they wait for their own copies alone.  0: rows are read where
+// they lie, each time they are needed.
+
+// Where a row's four operands come from.
+template <int kDtype, bool kWide, int kVecs, int kThreads, int kStages>
+struct RowSource {
+  using C = Cols<kDtype, kWide>;
+  const NormGradArgs& a;
+  uint4* mem;
+  const void* at[4];  // block, h, dy, dh; null: zeros
+
+  __device__ __forceinline__ void point(int64_t row) {
+    at[0] = C::at(a.b.block, row * a.b.ld_block);
+    at[1] = a.h != nullptr ? C::at(a.h, row * a.ld_h) : nullptr;
+    at[2] = a.dy != nullptr ? C::at(a.dy, row * a.ld_dy) : nullptr;
+    at[3] = a.dh != nullptr ? C::at(a.dh, row * a.ld_dh) : nullptr;
+  }
+  __device__ __forceinline__ uint4* slot(int stage, int t, int k) const {
+    return mem + ((stage * 4 + t) * kVecs + k) * kThreads + threadIdx.x;
+  }
+  // Zeros where no copy will write.
+  __device__ __forceinline__ void clear() {
+    point(0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k)
+        if (at[t] == nullptr || C::col(k, 0) >= a.b.d)
+          for (int s = 0; s < kStages; ++s) *slot(s, t, k) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // Starts the copies of a row, if there is one; a group for the wait either way.
+  __device__ __forceinline__ void start(int64_t row, int stage) {
+    if (row < a.b.T) {
+      point(row);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+          if (at[t] != nullptr && C::col(k, 0) < a.b.d)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, t, k))),
+                         "l"(C::at(at[t], C::col(k, 0)))
+                         : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  }
+  __device__ __forceinline__ uint4 get(int stage, int t, int k) const {
+    if constexpr (kStages == 0) {
+      return at[t] != nullptr ? C::load(at[t], k, a.b.d) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      return *slot(stage, t, k);
+    }
+  }
+};
+
+template <int kDtype, bool kWide, int kVecs, int kThreads, int kStages>
+__global__ void __launch_bounds__(kThreads, kThreads <= 512 && kVecs == 1 ? 1024 / kThreads : 1)
+    residual_norm_backward_kernel(const NormGradArgs a) {
   using E = Elem<kDtype>;
   using C = Cols<kDtype, kWide>;
-  constexpr int kVec = E::kVec;
+  constexpr int kVec = E::kVec, kHalf = kVec / 2;
+  extern __shared__ uint4 ring[];
   __shared__ float scratch1[32][3], scratch2[32][2];
   const tim_block& b = a.b;
   const int d = b.d;
@@ -181,131 +242,177 @@ __global__ void __launch_bounds__(kThreads, 1) residual_norm_backward_kernel(con
   const bool pre = a.dy != nullptr, post = b.gamma_post != nullptr;
   const bool by_channel = b.gate_kind == TIM_GATE_CHANNEL, by_element = b.gate_kind == TIM_GATE_ELEMENT;
   const bool by_token = b.gate_kind == TIM_GATE_TOKEN;
-  float acc_pre[kVecs][kVec] = {}, acc_post[kVecs][kVec] = {}, acc_gate[kVecs][kVec] = {};
-  for (int64_t row = blockIdx.x; row < b.T; row += gridDim.x) {
-    const void* const gate = gate_of<C>(b, row);
-    uint4 hs[kVecs], xs[kVecs], ys[kVecs], ds[kVecs];
+  RowSource<kDtype, kWide, kVecs, kThreads, kStages> src{a, ring, {}};
+  if constexpr (kStages > 0) {
+    src.clear();
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      xs[k] = C::load(C::at(b.block, row * b.ld_block), k, d);
-      if (pre) {
-        hs[k] = C::load(C::at(a.h, row * a.ld_h), k, d);
-        ys[k] = C::load(C::at(a.dy, row * a.ld_dy), k, d);
-      }
-      ds[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.dh != nullptr) ds[k] = C::load(C::at(a.dh, row * a.ld_dh), k, d);
+    for (int s = 0; s < kStages; ++s)
+      src.start(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  }
+  auto load2 = [](const uint4& u, F2 (&v)[kHalf]) {
+    float f[kVec];
+    E::unpack(u, f);
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+  };
+  auto pack2 = [](const F2 (&v)[kHalf]) {
+    float f[kVec];
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const float2 t = unpack2(v[i]);
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
     }
-    float s1[3] = {0.f, 0.f, 0.f};
+    return E::pack(f);
+  };
+  F2 acc_pre[kVecs][kHalf], acc_post[kVecs][kHalf], acc_gate[kVecs][kHalf];
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k)
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) acc_pre[k][i] = acc_post[k][i] = acc_gate[k][i] = f2(0.f, 0.f);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < b.T; row += gridDim.x) {
+    if constexpr (kStages > 0)
+      src.wait();
+    else
+      src.point(row);
+    F2 t1[3] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      float v[kVec], w[kVec], u[kVec];
+      F2 v[kHalf], w[kHalf], u[kHalf];
       if (pre) {
-        E::unpack(hs[k], v);
-        E::unpack(ys[k], u);
-        E::unpack(C::load(b.gamma, k, d), w);
+        load2(src.get(stage, 1, k), v);
+        load2(src.get(stage, 2, k), u);
+        load2(C::load(b.gamma, k, d), w);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          s1[0] = fmaf(v[i], v[i], s1[0]);
-          s1[1] = fmaf(w[i] * u[i], v[i], s1[1]);
+        for (int i = 0; i < kHalf; ++i) {
+          t1[0] = fma2(v[i], v[i], t1[0]);
+          t1[1] = fma2(mul2(w[i], u[i]), v[i], t1[1]);
         }
       }
       if (post) {
-        E::unpack(xs[k], v);
+        load2(src.get(stage, 0, k), v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) s1[2] = fmaf(v[i], v[i], s1[2]);
+        for (int i = 0; i < kHalf; ++i) t1[2] = fma2(v[i], v[i], t1[2]);
       }
+    }
+    float s1[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const float2 t = unpack2(t1[i]);
+      s1[i] = t.x + t.y;
     }
     if (pre || post) block_sum(s1, scratch1);
     const float r2 = pre ? 1.f / sqrtf(s1[0] * inv_d + b.eps) : 0.f;
     const float c2 = pre ? r2 * r2 * r2 * inv_d * s1[1] : 0.f;
     const float r1 = post ? 1.f / sqrtf(s1[2] * inv_d + b.eps) : 1.f;
+    const void* const gate = gate_of<C>(b, row);
     const float by_row =
         b.scale * (by_token ? E::widen(*static_cast<const typename E::raw*>(gate)) : 1.f);
-    float s2[2] = {0.f, 0.f};
-    float H[kVecs][kVec];
+    const F2 r2s = f2(r2, r2), c2s = f2(-c2, -c2), r1s = f2(r1, r1), by_rows = f2(by_row, by_row);
+    F2 t2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+    F2 H[kVecs][kHalf];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      float v[kVec], w[kVec], u[kVec];
-      E::unpack(ds[k], H[k]);
+      F2 v[kHalf], w[kHalf], u[kHalf];
+      load2(src.get(stage, 3, k), H[k]);
       if (pre) {
-        E::unpack(hs[k], v);
-        E::unpack(ys[k], u);
-        E::unpack(C::load(b.gamma, k, d), w);
+        load2(src.get(stage, 1, k), v);
+        load2(src.get(stage, 2, k), u);
+        load2(C::load(b.gamma, k, d), w);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          H[k][i] += r2 * w[i] * u[i] - c2 * v[i];
-          acc_pre[k][i] = fmaf(u[i] * v[i], r2, acc_pre[k][i]);
+        for (int i = 0; i < kHalf; ++i) {
+          H[k][i] = fma2(mul2(r2s, w[i]), u[i], fma2(c2s, v[i], H[k][i]));
+          acc_pre[k][i] = fma2(mul2(u[i], v[i]), r2s, acc_pre[k][i]);
         }
       }
-      C::store(C::at(a.out_dresidual, row * a.ld_dresidual), k, d, E::pack(H[k]));
+      C::store(C::at(a.out_dresidual, row * a.ld_dresidual), k, d, pack2(H[k]));
       // from here on u: the block's output, v: n before the gate, w: the post gamma
-      E::unpack(xs[k], u);
+      load2(src.get(stage, 0, k), u);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = u[i];
+      for (int i = 0; i < kHalf; ++i) v[i] = u[i];
       if (post) {
-        E::unpack(C::load(b.gamma_post, k, d), w);
+        load2(C::load(b.gamma_post, k, d), w);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = u[i] * r1 * w[i];
+        for (int i = 0; i < kHalf; ++i) v[i] = mul2(mul2(u[i], r1s), w[i]);
       }
       if (by_channel) {
+        const F2 s = f2(b.scale, b.scale);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc_gate[k][i] = fmaf(H[k][i] * v[i], b.scale, acc_gate[k][i]);
+        for (int i = 0; i < kHalf; ++i) acc_gate[k][i] = fma2(mul2(H[k][i], v[i]), s, acc_gate[k][i]);
       } else if (by_element) {
-        float g[kVec];
+        const F2 s = f2(b.scale, b.scale);
+        F2 g[kHalf];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) g[i] = b.scale * H[k][i] * v[i];
-        C::store(C::at(a.out_dgate, row * a.ld_dgate), k, d, E::pack(g));
+        for (int i = 0; i < kHalf; ++i) g[i] = mul2(mul2(s, H[k][i]), v[i]);
+        C::store(C::at(a.out_dgate, row * a.ld_dgate), k, d, pack2(g));
       } else if (by_token) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) s2[1] = fmaf(H[k][i], v[i], s2[1]);
+        for (int i = 0; i < kHalf; ++i) t2[1] = fma2(H[k][i], v[i], t2[1]);
       }
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) H[k][i] *= by_row;
+      for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(H[k][i], by_rows);
       if (by_channel || by_element) {
-        E::unpack(C::load(gate, k, d), v);
+        load2(C::load(gate, k, d), v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) H[k][i] *= v[i];
+        for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(H[k][i], v[i]);
       }
       if (post) {  // H is dn now
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          acc_post[k][i] = fmaf(H[k][i] * u[i], r1, acc_post[k][i]);
-          H[k][i] *= w[i];
-          s2[0] = fmaf(H[k][i], u[i], s2[0]);
+        for (int i = 0; i < kHalf; ++i) {
+          acc_post[k][i] = fma2(mul2(H[k][i], u[i]), r1s, acc_post[k][i]);
+          H[k][i] = mul2(H[k][i], w[i]);
+          t2[0] = fma2(H[k][i], u[i], t2[0]);
         }
       }
+    }
+    float s2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 t = unpack2(t2[i]);
+      s2[i] = t.x + t.y;
     }
     if (post || by_token) block_sum(s2, scratch2);
     if (by_token && threadIdx.x == 0) static_cast<float*>(a.out_dgate)[row] = b.scale * s2[1];
     const float c1 = post ? r1 * r1 * r1 * inv_d * s2[0] : 0.f;
+    const F2 c1s = f2(-c1, -c1);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (post) {
-        float u[kVec];
-        E::unpack(xs[k], u);
+        F2 u[kHalf];
+        load2(src.get(stage, 0, k), u);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) H[k][i] = r1 * H[k][i] - c1 * u[i];
+        for (int i = 0; i < kHalf; ++i) H[k][i] = fma2(r1s, H[k][i], mul2(c1s, u[i]));
       }
-      C::store(C::at(a.out_dblock, row * a.ld_dblock), k, d, E::pack(H[k]));
+      C::store(C::at(a.out_dblock, row * a.ld_dblock), k, d, pack2(H[k]));
     }
-    __syncthreads();  // the scratch is the next row's
+    if constexpr (kStages > 0) {
+      src.start(row + static_cast<int64_t>(kStages) * gridDim.x, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    // with two sums a row each one's barrier parts the other's scratch from the next row's; with one:
+    if ((pre || post) != (post || by_token)) __syncthreads();
   }
   float* const part = a.partial + static_cast<int64_t>(blockIdx.x) * 3 * d;
-#pragma unroll
-  for (int k = 0; k < kVecs; ++k)
+  auto leave = [&](int which, int k, const F2 (&v)[kHalf]) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int c = C::col(k, i);
-      if (c >= d) continue;
-      if (b.gamma != nullptr) part[c] = acc_pre[k][i];
-      if (post) part[d + c] = acc_post[k][i];
-      if (by_channel) part[2 * d + c] = acc_gate[k][i];
+      const float2 t = unpack2(v[i / 2]);
+      if (c < d) part[which * d + c] = i % 2 == 0 ? t.x : t.y;
     }
+  };
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    if (b.gamma != nullptr) leave(0, k, acc_pre[k]);
+    if (post) leave(1, k, acc_post[k]);
+    if (by_channel) leave(2, k, acc_gate[k]);
+  }
 }
 
 // out[c] (+)= sum over the CTAs of part[.][which][c], in order: a CTA has 32 columns of one kind, and
 // its warps share the parts of a column.
-constexpr int kFoldWarps = 8;
+constexpr int kFoldWarps = 32;
 struct FoldArgs {
   const float* partial;
   int parts, d, accumulate;
@@ -359,6 +466,17 @@ cudaError_t with_split(int nvec, F&& f) {
   if (nvec <= 2048) return f(Int<2>(), Int<1024>());
   return f(Int<4>(), Int<1024>());
 }
+// The same for the gradient, whose threads hold three sums a column.
+template <class F>
+cudaError_t with_backward_split(int nvec, F&& f) {
+  if (nvec <= 64) return f(Int<1>(), Int<64>());
+  if (nvec <= 128) return f(Int<1>(), Int<128>());
+  if (nvec <= 256) return f(Int<1>(), Int<256>());
+  if (nvec <= 512) return f(Int<1>(), Int<512>());
+  if (nvec <= 1024) return f(Int<2>(), Int<512>());
+  if (nvec <= 2048) return f(Int<2>(), Int<1024>());
+  return f(Int<4>(), Int<1024>());
+}
 constexpr int kMaxParts = 1024;
 
 template <int kDtype, bool kWide>
@@ -371,6 +489,10 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   });
 }
 
+// Rows of a CTA in shared memory; 0 beyond what an SM has.
+template <int kVecs, int kThreads>
+constexpr int kRowsAhead = kVecs * kThreads <= 512 ? 3 : kVecs * kThreads <= 1024 ? 2 : 0;
+
 template <int kDtype, bool kWide>
 cudaError_t launch_backward(const NormGradArgs& a, cudaStream_t stream, int num_sms) {
   const int nvec = (a.b.d + Elem<kDtype>::kVec - 1) / Elem<kDtype>::kVec;
@@ -381,11 +503,19 @@ cudaError_t launch_backward(const NormGradArgs& a, cudaStream_t stream, int num_
   if (a.b.gamma != nullptr) f.out[0] = a.out_dgamma;
   if (a.b.gamma_post != nullptr) f.out[1] = a.out_dgamma_post;
   if (a.b.gate_kind == TIM_GATE_CHANNEL) f.out[2] = static_cast<float*>(a.out_dgate);
-  const cudaError_t e = with_split(nvec, [&](auto vecs, auto threads) {
-    const int64_t resident = static_cast<int64_t>(num_sms) * std::max(1, 512 / threads.value);
+  const cudaError_t e = with_backward_split(nvec, [&](auto vecs, auto threads) {
+    constexpr int kVecs = vecs.value, kThreads = threads.value;
+    constexpr int kStages = kWide ? kRowsAhead<kVecs, kThreads> : 0;
+    constexpr size_t smem = static_cast<size_t>(kStages) * 4 * kVecs * kThreads * 16;
+    auto* const kernel = residual_norm_backward_kernel<kDtype, kWide, kVecs, kThreads, kStages>;
+    static std::atomic<uint64_t> allowed{0};
+    if (smem > 0) {
+      const cudaError_t err = allow_smem(kernel, smem, allowed);
+      if (err != cudaSuccess) return err;
+    }
+    const int64_t resident = static_cast<int64_t>(num_sms) * (kVecs == 1 ? std::min(1024 / kThreads, 6) : 1);
     f.parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.b.T, resident), kMaxParts));
-    residual_norm_backward_kernel<kDtype, kWide, vecs.value, threads.value>
-        <<<f.parts, threads.value, 0, stream>>>(a);
+    kernel<<<f.parts, kThreads, smem, stream>>>(a);
     return cudaGetLastError();
   });
   if (e != cudaSuccess) return e;
