@@ -188,8 +188,15 @@ __global__ void __launch_bounds__(kThreads, 1) residual_norm_kernel(const NormAr
 //   dn     = scale g H,  dg = scale n H (summed over what a gate is shared by)
 //   dx     = r1 gamma_post dn - x r1^3/d sum(gamma_post dn x)   (or dn)
 //   dgamma = sum_t dy h' r2,  dgamma_post = sum_t dn x r1
-// Two sums a row, the second from the first.  A CTA takes every gridDim-th row; the sums over its rows
-// stay in registers, a thread's columns, and are left in the workspace for residual_fold_kernel.
+// Two sums a row, the second from the first: with t = H gamma_post x all that is left are
+//   q = sum t (of a gate a channel or an element: sum g t),
+//   dx = scale g r1 (gamma_post H - x r1^2/d q),   dg = scale r1 t   (a token's: scale r1 q).
+// A CTA takes every gridDim-th row; the sums over its rows stay in registers, a thread's columns, and are
+// left in the workspace for residual_fold_kernel.
+//
+// 16384 rows of 4096 bf16 with both norms and a gate a token take 158 us, 5.1 TB/s, and the fold 4.5: the
+// instructions bound it (half the issue slots, 16 warps an SM), most of them the unpacking of 16-bit
+// numbers.
 //
 // kStages: the rows that are on their way to shared memory while one is worked on, copied by the
 // threads that will read them, so that they wait for their own copies alone.  0: rows are read where
@@ -237,6 +244,21 @@ struct RowSource {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  // The gammas and a channel gate, which every row needs.
+  __device__ __forceinline__ uint4* shared_slot(int n, int k) const {
+    return mem + ((kStages * 4 + n) * kVecs + k) * kThreads + threadIdx.x;
+  }
+  __device__ __forceinline__ void keep(int n, const void* p) const {
+    if (p == nullptr) return;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) *shared_slot(n, k) = C::load(p, k, a.b.d);
+  }
+  __device__ __forceinline__ uint4 kept(int n, const void* p, int k) const {
+    if constexpr (kStages == 0)
+      return C::load(p, k, a.b.d);
+    else
+      return *shared_slot(n, k);
+  }
   __device__ __forceinline__ void wait() const {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
   }
@@ -249,23 +271,31 @@ struct RowSource {
   }
 };
 
-template <int kDtype, bool kWide, int kVecs, int kThreads, int kStages>
-__global__ void __launch_bounds__(kThreads, kThreads * kVecs <= 512 ? 1024 / (kThreads * kVecs) : 1)
+// CTAs of an SM, at most six: those of 64 threads would leave many parts to the fold.
+template <int kVecs, int kThreads>
+constexpr int kResident = kVecs * kThreads > 512 ? 1 : std::min(1024 / (kThreads * kVecs), 6);
+
+template <int kDtype, bool kWide, int kVecs, int kThreads, int kStages, bool kChannel>
+__global__ void __launch_bounds__(kThreads, kResident<kVecs, kThreads>)
     residual_norm_backward_kernel(const NormGradArgs a) {
   using E = Elem<kDtype>;
   using C = Cols<kDtype, kWide>;
   constexpr int kVec = E::kVec, kHalf = kVec / 2;
   extern __shared__ uint4 ring[];
-  __shared__ float scratch1[3][32], scratch2[2][32];
+  __shared__ float scratch1[3][32], scratch2[1][32];
   const tim_block& b = a.b;
   const int d = b.d;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool pre = a.dy != nullptr, post = b.gamma_post != nullptr;
-  const bool by_channel = b.gate_kind == TIM_GATE_CHANNEL, by_element = b.gate_kind == TIM_GATE_ELEMENT;
-  const bool by_token = b.gate_kind == TIM_GATE_TOKEN;
+  constexpr bool by_channel = kChannel;
+  const bool by_element = !kChannel && b.gate_kind == TIM_GATE_ELEMENT;
+  const bool by_token = !kChannel && b.gate_kind == TIM_GATE_TOKEN;
   RowSource<kDtype, kWide, kVecs, kThreads, kStages> src{a, ring, {}};
   if constexpr (kStages > 0) {
     src.clear();
+    src.keep(0, b.gamma);
+    src.keep(1, b.gamma_post);
+    if (by_channel) src.keep(2, b.gate);
 #pragma unroll
     for (int s = 0; s < kStages; ++s)
       src.start(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
@@ -291,24 +321,32 @@ __global__ void __launch_bounds__(kThreads, kThreads * kVecs <= 512 ? 1024 / (kT
   for (int k = 0; k < kVecs; ++k)
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) acc_pre[k][i] = acc_post[k][i] = acc_gate[k][i] = f2(0.f, 0.f);
+  // a token's gate is asked for a row ahead
+  auto gate_at = [&](int64_t row) {
+    return row < b.T ? E::widen(*static_cast<const typename E::raw*>(gate_of<C>(b, row))) : 0.f;
+  };
+  float row_gate = by_token ? gate_at(blockIdx.x) : 1.f;
   int stage = 0;
   for (int64_t row = blockIdx.x; row < b.T; row += gridDim.x) {
     if constexpr (kStages > 0)
       src.wait();
     else
       src.point(row);
+    // H holds gamma dy until its sums are known
     F2 t1[3] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+    F2 H[kVecs][kHalf];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      F2 v[kHalf], w[kHalf], u[kHalf];
+      F2 v[kHalf], w[kHalf];
       if (pre) {
         load2(src.get(stage, 1, k), v);
-        load2(src.get(stage, 2, k), u);
-        load2(C::load(b.gamma, k, d), w);
+        load2(src.get(stage, 2, k), H[k]);
+        load2(src.kept(0, b.gamma, k), w);
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) {
+          H[k][i] = mul2(H[k][i], w[i]);
           t1[0] = fma2(v[i], v[i], t1[0]);
-          t1[1] = fma2(mul2(w[i], u[i]), v[i], t1[1]);
+          t1[1] = fma2(H[k][i], v[i], t1[1]);
         }
       }
       if (post) {
@@ -327,75 +365,63 @@ __global__ void __launch_bounds__(kThreads, kThreads * kVecs <= 512 ? 1024 / (kT
     const float r2 = pre ? rsqrtf(s1[0] * inv_d + b.eps) : 0.f;
     const float c2 = pre ? r2 * r2 * r2 * inv_d * s1[1] : 0.f;
     const float r1 = post ? rsqrtf(s1[2] * inv_d + b.eps) : 1.f;
-    const void* const gate = gate_of<C>(b, row);
-    const float by_row =
-        b.scale * (by_token ? E::widen(*static_cast<const typename E::raw*>(gate)) : 1.f);
-    const F2 r2s = f2(r2, r2), c2s = f2(-c2, -c2), r1s = f2(r1, r1), by_rows = f2(by_row, by_row);
-    F2 t2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-    F2 H[kVecs][kHalf];
+    const float by_row = b.scale * row_gate;  // all of the gate that is not an element's own
+    if (by_token) row_gate = gate_at(row + gridDim.x);
+    const F2 r2s = f2(r2, r2), c2s = f2(-c2, -c2), by_r1 = f2(by_row * r1, by_row * r1);
+    F2 tq = f2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       F2 v[kHalf], w[kHalf], u[kHalf];
-      load2(src.get(stage, 3, k), H[k]);
+      load2(src.get(stage, 3, k), w);
       if (pre) {
         load2(src.get(stage, 1, k), v);
         load2(src.get(stage, 2, k), u);
-        load2(C::load(b.gamma, k, d), w);
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) {
-          H[k][i] = fma2(mul2(r2s, w[i]), u[i], fma2(c2s, v[i], H[k][i]));
+          H[k][i] = fma2(r2s, H[k][i], fma2(c2s, v[i], w[i]));
           acc_pre[k][i] = fma2(mul2(u[i], v[i]), r2s, acc_pre[k][i]);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) H[k][i] = w[i];
       }
       C::store(C::at(a.out_dresidual, row * a.ld_dresidual), k, d, pack2(H[k]));
-      // from here on u: the block's output, v: n before the gate, w: the post gamma
       load2(src.get(stage, 0, k), u);
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) v[i] = u[i];
-      if (post) {
-        load2(C::load(b.gamma_post, k, d), w);
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) v[i] = mul2(mul2(u[i], r1s), w[i]);
-      }
-      if (by_channel) {
-        const F2 s = f2(b.scale, b.scale);
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) acc_gate[k][i] = fma2(mul2(H[k][i], v[i]), s, acc_gate[k][i]);
-      } else if (by_element) {
-        const F2 s = f2(b.scale, b.scale);
-        F2 g[kHalf];
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) g[i] = mul2(mul2(s, H[k][i]), v[i]);
-        C::store(C::at(a.out_dgate, row * a.ld_dgate), k, d, pack2(g));
-      } else if (by_token) {
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) t2[1] = fma2(H[k][i], v[i], t2[1]);
-      }
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(H[k][i], by_rows);
+      if (post) load2(src.kept(1, b.gamma_post, k), w);
       if (by_channel || by_element) {
-        load2(C::load(gate, k, d), v);
+        F2 t[kHalf];
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) t[i] = mul2(post ? mul2(H[k][i], w[i]) : H[k][i], u[i]);
+        if (by_channel) {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) acc_gate[k][i] = fma2(t[i], by_r1, acc_gate[k][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) t[i] = mul2(t[i], by_r1);
+          C::store(C::at(a.out_dgate, row * a.ld_dgate), k, d, pack2(t));
+        }
+        load2(by_channel ? src.kept(2, b.gate, k) : C::load(gate_of<C>(b, row), k, d), v);
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(H[k][i], v[i]);
       }
-      if (post) {  // H is dn now
+      if (post) {
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) {
-          acc_post[k][i] = fma2(mul2(H[k][i], u[i]), r1s, acc_post[k][i]);
+          const F2 t = mul2(H[k][i], u[i]);
+          acc_post[k][i] = fma2(t, by_r1, acc_post[k][i]);
+          tq = fma2(t, w[i], tq);
           H[k][i] = mul2(H[k][i], w[i]);
-          t2[0] = fma2(H[k][i], u[i], t2[0]);
         }
+      } else if (by_token) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) tq = fma2(H[k][i], u[i], tq);
       }
     }
-    float s2[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 t = unpack2(t2[i]);
-      s2[i] = t.x + t.y;
-    }
-    if (post || by_token) block_sum(s2, scratch2);
-    if (by_token && threadIdx.x == 0) static_cast<float*>(a.out_dgate)[row] = b.scale * s2[1];
-    const float c1 = post ? r1 * r1 * r1 * inv_d * s2[0] : 0.f;
+    const float2 tqs = unpack2(tq);
+    float q[1] = {tqs.x + tqs.y};
+    if (post || by_token) block_sum(q, scratch2);
+    if (by_token && threadIdx.x == 0) static_cast<float*>(a.out_dgate)[row] = b.scale * r1 * q[0];
+    const float c1 = post ? by_row * r1 * r1 * r1 * inv_d * q[0] : 0.f;
     const F2 c1s = f2(-c1, -c1);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
@@ -403,7 +429,10 @@ __global__ void __launch_bounds__(kThreads, kThreads * kVecs <= 512 ? 1024 / (kT
         F2 u[kHalf];
         load2(src.get(stage, 0, k), u);
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) H[k][i] = fma2(r1s, H[k][i], mul2(c1s, u[i]));
+        for (int i = 0; i < kHalf; ++i) H[k][i] = fma2(by_r1, H[k][i], mul2(c1s, u[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(by_r1, H[k][i]);
       }
       C::store(C::at(a.out_dblock, row * a.ld_dblock), k, d, pack2(H[k]));
     }
@@ -476,43 +505,36 @@ bool wide(const tim_block& b) {
 template <int kN>
 using Int = std::integral_constant<int, kN>;
 
-// f(vectors of a thread, threads a row), by the row's vectors alone.
-template <class F>
+// f(vectors of a thread, threads a row), by the row's vectors alone.  Two vectors from 512 on: the gradient
+// of rows of 4096 bf16 took 158 us so, 168 with one vector and twice the threads, 239 with four.
+template <int kDtype, class F>
 cudaError_t with_split(int nvec, F&& f) {
   if (nvec <= 64) return f(Int<1>(), Int<64>());
   if (nvec <= 128) return f(Int<1>(), Int<128>());
   if (nvec <= 256) return f(Int<1>(), Int<256>());
   if (nvec <= 512) return f(Int<2>(), Int<256>());
   if (nvec <= 1024) return f(Int<2>(), Int<512>());
-  if (nvec <= 2048) return f(Int<2>(), Int<1024>());
-  return f(Int<4>(), Int<1024>());
-}
-// The same for the gradient, whose threads hold three sums a column.
-template <class F>
-cudaError_t with_backward_split(int nvec, F&& f) {
-  if (nvec <= 64) return f(Int<1>(), Int<64>());
-  if (nvec <= 128) return f(Int<1>(), Int<128>());
-  if (nvec <= 256) return f(Int<1>(), Int<256>());
-  if (nvec <= 512) return f(Int<2>(), Int<256>());
-  if (nvec <= 1024) return f(Int<2>(), Int<512>());
-  if (nvec <= 2048) return f(Int<2>(), Int<1024>());
-  return f(Int<4>(), Int<1024>());
+  if constexpr (kDtype == TIM_F32) {
+    if (nvec > 2048) return f(Int<4>(), Int<1024>());
+  }
+  return f(Int<2>(), Int<1024>());
 }
 constexpr int kMaxParts = 1024;
 
 template <int kDtype, bool kWide>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   const int nvec = (a.b.d + Elem<kDtype>::kVec - 1) / Elem<kDtype>::kVec;
-  return with_split(nvec, [&](auto vecs, auto threads) {
+  return with_split<kDtype>(nvec, [&](auto vecs, auto threads) {
     residual_norm_kernel<kDtype, kWide, vecs.value, threads.value>
         <<<static_cast<unsigned>(a.b.T), threads.value, 0, stream>>>(a);
     return cudaGetLastError();
   });
 }
 
-// Rows of a CTA in shared memory; 0 beyond what an SM has.
+// Rows of a CTA in shared memory, beside what every row needs: two, so that two CTAs of 256 threads share
+// an SM (three rows leave room for one: 277 us instead of 171); none where an SM's memory would not do.
 template <int kVecs, int kThreads>
-constexpr int kRowsAhead = kVecs * kThreads <= 512 ? 3 : kVecs * kThreads <= 1024 ? 2 : 0;
+constexpr int kRowsAhead = kVecs * kThreads <= 1024 ? 2 : 0;
 
 template <int kDtype, bool kWide>
 cudaError_t launch_backward(const NormGradArgs& a, cudaStream_t stream, int num_sms) {
@@ -524,20 +546,26 @@ cudaError_t launch_backward(const NormGradArgs& a, cudaStream_t stream, int num_
   if (a.b.gamma != nullptr) f.out[0] = a.out_dgamma;
   if (a.b.gamma_post != nullptr) f.out[1] = a.out_dgamma_post;
   if (a.b.gate_kind == TIM_GATE_CHANNEL) f.out[2] = static_cast<float*>(a.out_dgate);
-  const cudaError_t e = with_backward_split(nvec, [&](auto vecs, auto threads) {
+  const cudaError_t e = with_split<kDtype>(nvec, [&](auto vecs, auto threads) {
     constexpr int kVecs = vecs.value, kThreads = threads.value;
     constexpr int kStages = kWide ? kRowsAhead<kVecs, kThreads> : 0;
-    constexpr size_t smem = static_cast<size_t>(kStages) * 4 * kVecs * kThreads * 16;
-    auto* const kernel = residual_norm_backward_kernel<kDtype, kWide, kVecs, kThreads, kStages>;
-    static std::atomic<uint64_t> allowed{0};
-    if (smem > 0) {
-      const cudaError_t err = allow_smem(kernel, smem, allowed);
-      if (err != cudaSuccess) return err;
-    }
-    const int64_t resident = static_cast<int64_t>(num_sms) * std::min(std::max(1024 / (kThreads * kVecs), 1), 6);
-    f.parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.b.T, resident), kMaxParts));
-    kernel<<<f.parts, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    constexpr size_t smem =
+        kStages == 0 ? 0 : static_cast<size_t>(kStages * 4 + 3) * kVecs * kThreads * 16;
+    auto launch = [&](auto channel) {
+      auto* const kernel =
+          residual_norm_backward_kernel<kDtype, kWide, kVecs, kThreads, kStages, channel.value>;
+      static std::atomic<uint64_t> allowed{0};
+      if (smem > 0) {
+        const cudaError_t err = allow_smem(kernel, smem, allowed);
+        if (err != cudaSuccess) return err;
+      }
+      const int64_t resident = static_cast<int64_t>(num_sms) * kResident<kVecs, kThreads>;
+      f.parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.b.T, resident), kMaxParts));
+      kernel<<<f.parts, kThreads, smem, stream>>>(a);
+      return cudaGetLastError();
+    };
+    return a.b.gate_kind == TIM_GATE_CHANNEL ? launch(std::bool_constant<true>())
+                                             : launch(std::bool_constant<false>());
   });
   if (e != cudaSuccess) return e;
   if (f.out[0] == nullptr && f.out[1] == nullptr && f.out[2] == nullptr) return e;
