@@ -106,7 +106,7 @@ cudaError_t launch_embed(const void* table, int dtype, int64_t ld, const int32_t
 size_t embed_backward_bytes(int64_t T, int d);
 cudaError_t launch_embed_backward(const void* dy, int dtype, int64_t ld, const int32_t* ids,
                                   int64_t T, int V, int d, float scale, void* out, int out_dtype,
-                                  int accumulate, void* ws, cudaStream_t stream);
+                                  int accumulate, void* ws, cudaStream_t stream, int num_sms);
 
 namespace {
 
@@ -1091,10 +1091,11 @@ tim_status tim_embed_backward(const void* dy, int32_t dtype, int64_t ldy, const 
     return TIM_ERR_INVALID_ARG;
   if ((s = check_workspace(workspace, workspace_bytes, embed_backward_bytes(T, d))) != TIM_OK)
     return s;
-  if ((s = check_device(nullptr)) != TIM_OK) return s;
+  int sms = 0;
+  if ((s = check_device(&sms)) != TIM_OK) return s;
   return from_cuda(launch_embed_backward(dy, dtype, ldy, ids, T, V, d, scale, out_dtable, out_dtype,
                                          accumulate, workspace,
-                                         reinterpret_cast<cudaStream_t>(stream)));
+                                         reinterpret_cast<cudaStream_t>(stream), sms));
 }
 
 tim_status tim_residual_norm(const tim_block* b, const void* residual, int64_t ld_residual,

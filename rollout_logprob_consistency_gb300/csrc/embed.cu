@@ -10,9 +10,11 @@
 // pieces of a fixed number of rows.  A piece's CTA walks its rows with a column vector a thread and
 // an fp32 running sum, writes the tokens that lie wholly within, and leaves the sums of the first and
 // the last where they go on beyond it; a second launch joins those in order.  No atomics: the same
-// call gives the same bits.  Rows of the table that no token names are zeroed by CTAs of the same
-// launch, which look the row up in the sorted list; with `accumulate` they are not touched.
+// call gives the same bits.  The table's gradient is zeroed by the rest of the sort's launch, which
+// has eight SMs' work otherwise; with `accumulate` it is added to.
 #include "embed_sort.cuh"
+#include <type_traits>
+
 #include "logits_row.cuh"
 
 namespace tim {
@@ -114,7 +116,6 @@ cudaError_t launch_lookup(const LookupArgs& a, int64_t T, cudaStream_t stream) {
 // ---- the gradient
 
 constexpr int kGradThreads = 256;
-constexpr int kZeroRows = 32;  // table rows of a CTA that zeroes
 constexpr int kRows = 8;       // rows in flight
 constexpr int kMaxPiece = 64;
 
@@ -130,13 +131,25 @@ struct GradArgs {
   float* partial;  // [pieces][2][d]: of a piece's first and last token
 };
 
+// kVec columns of a row as they lie in memory.
 template <int kDtype, int kVec>
-__device__ __forceinline__ void load_cols(const typename Elem<kDtype>::raw* p, float (&v)[kVec]) {
-  if constexpr (kVec == 1)
-    v[0] = Elem<kDtype>::widen(__ldg(p));
-  else
-    Elem<kDtype>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), v);
-}
+struct Loaded {
+  using E = Elem<kDtype>;
+  std::conditional_t<kVec == 1, typename E::raw, uint4> x;
+  __device__ __forceinline__ void load(const typename E::raw* p) {
+    x = __ldg(reinterpret_cast<const decltype(x)*>(p));
+  }
+  __device__ __forceinline__ void add_to(float (&acc)[kVec]) const {
+    if constexpr (kVec == 1) {
+      acc[0] += E::widen(x);
+    } else {
+      float v[kVec];
+      E::unpack(x, v);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += v[i];
+    }
+  }
+};
 // kVec columns of the table's gradient, of type kOut.
 template <int kOut, int kVec>
 __device__ __forceinline__ void store_cols(typename Elem<kOut>::raw* p, const float (&acc)[kVec],
@@ -162,45 +175,14 @@ __device__ __forceinline__ void store_cols(typename Elem<kOut>::raw* p, const fl
   }
 }
 
-// Whether table row v has a token: looked up in the sorted list.
-__device__ __forceinline__ bool named(const GradArgs& a, uint32_t v) {
-  int lo = 0, hi = a.T;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.id + mid) < v)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  return lo < a.T && __ldg(a.id + lo) == v;
-}
-
 template <int kDtype, int kOut, int kVec>
-__global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 4) embed_grad_kernel(const GradArgs a) {
   using raw = typename Elem<kDtype>::raw;
   using raw_out = typename Elem<kOut>::raw;
   __shared__ uint32_t ids[kMaxPiece + 2], rows[kMaxPiece];
-  __shared__ uint32_t mask;
   const int tid = threadIdx.x, n = a.d / kVec;
   const uint32_t none = static_cast<uint32_t>(a.V);
-  const int work = a.pieces * a.slices;
-  if (static_cast<int>(blockIdx.x) >= work) {
-    // ---- rows without a token
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x - work) * kZeroRows;
-    if (tid < 32) {
-      const unsigned m = __ballot_sync(0xFFFFFFFFu, v0 + tid < a.V &&
-                                                        !named(a, static_cast<uint32_t>(v0) + tid));
-      if (tid == 0) mask = m;
-    }
-    __syncthreads();
-    const float zero[kVec] = {};
-    for (uint32_t m = mask; m != 0; m &= m - 1) {
-      raw_out* const out = static_cast<raw_out*>(a.out) + (v0 + __ffs(m) - 1) * a.d;
-      for (int c = tid; c < n; c += kGradThreads) store_cols<kOut, kVec>(out + c * kVec, zero, 0.f, 0);
-    }
-    return;
-  }
-  // ---- a piece of the sorted list, a slice of the columns
+  // a piece of the sorted list, a slice of the columns
   const int p = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kGradThreads + tid;
   const int i0 = p * a.piece, len = min(a.piece, a.T - i0);
   for (int i = tid; i < len + 2; i += kGradThreads) {
@@ -232,11 +214,11 @@ __global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const GradArgs
       flush(false);
       return;
     }
-    float v[kRows][kVec];
+    Loaded<kDtype, kVec> v[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
       if (r0 + k < len && ids[1 + r0 + k] < none)
-        load_cols<kDtype, kVec>(dy + static_cast<int64_t>(rows[r0 + k]) * a.ld, v[k]);
+        v[k].load(dy + static_cast<int64_t>(rows[r0 + k]) * a.ld);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (r0 + k >= len) break;
@@ -249,8 +231,7 @@ __global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const GradArgs
         for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
       }
       if (id >= none) return;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] += v[k][i];
+      v[k].add_to(acc);
     }
   }
   flush(true);
@@ -298,11 +279,9 @@ template <int kDtype, int kOut, int kVec>
 cudaError_t launch_grad(const GradArgs& args, cudaStream_t stream) {
   GradArgs a = args;
   a.slices = (a.d / kVec + kGradThreads - 1) / kGradThreads;
-  const int64_t zero = a.accumulate ? 0 : (static_cast<int64_t>(a.V) + kZeroRows - 1) / kZeroRows;
   const int64_t work = static_cast<int64_t>(a.pieces) * a.slices;
-  if (work + zero > INT32_MAX) return cudaErrorInvalidValue;
   embed_grad_kernel<kDtype, kOut, kVec>
-      <<<static_cast<unsigned>(work + zero), kGradThreads, 0, stream>>>(a);
+      <<<static_cast<unsigned>(work), kGradThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.pieces == 1) return e;
   embed_join_kernel<kOut, kVec><<<static_cast<unsigned>(work), kGradThreads, 0, stream>>>(a);
@@ -358,7 +337,7 @@ size_t embed_backward_bytes(int64_t T, int d) { return embed_ws(T, d).total; }
 
 cudaError_t launch_embed_backward(const void* dy, int dtype, int64_t ld, const int32_t* ids, int64_t T,
                                   int V, int d, float scale, void* out, int out_dtype, int accumulate,
-                                  void* ws, cudaStream_t stream) {
+                                  void* ws, cudaStream_t stream, int num_sms) {
   const EmbedWs w = embed_ws(T, d);
   uint8_t* const b = static_cast<uint8_t*>(ws);
   const int es = dtype == TIM_F32 ? 4 : 2;
@@ -378,9 +357,12 @@ cudaError_t launch_embed_backward(const void* dy, int dtype, int64_t ld, const i
     a.pieces = (a.T + a.piece - 1) / a.piece;
     a.scale = scale;
     a.out = out;
-    a.accumulate = accumulate || t0 > 0;
+    const bool zero = t0 == 0 && !accumulate;
+    a.accumulate = !zero;
     a.partial = reinterpret_cast<float*>(b + w.partial_off);
-    cudaError_t e = launch_embed_sort(ids + t0, a.T, V, id, row, static_cast<int*>(ws), stream);
+    cudaError_t e = launch_embed_sort(ids + t0, a.T, V, id, row, static_cast<int*>(ws), out,
+                                      zero ? static_cast<int64_t>(V) * d * (out_dtype == TIM_F32 ? 4 : 2) : 0,
+                                      num_sms, stream);
     if (e != cudaSuccess) return e;
     e = dtype == TIM_F32    ? launch_grad_type<TIM_F32>(a, out_dtype, stream)
         : dtype == TIM_BF16 ? launch_grad_type<TIM_BF16>(a, out_dtype, stream)

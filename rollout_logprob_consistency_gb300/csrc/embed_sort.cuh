@@ -1,5 +1,6 @@
 // The tokens of a batch in the order of their ids, equal ids in the order of their rows: a radix sort in one
-// launch, by a cluster of CTAs that keep all of it in their shared memory.
+// launch, by a cluster of CTAs that keep all of it in their shared memory.  The other clusters of
+// the launch, if there are any, zero the table's gradient meanwhile.
 //
 // A pass orders by 9 bits of the id, lowest first.  Every warp has 32 kItems tokens that follow one
 // another in the list and counts its digits, equal ones of a step ranked by lane; the counts of a
@@ -26,10 +27,32 @@ constexpr int kDigits = 1 << kDigitBits;
 struct SortArgs {
   const int32_t* ids;
   int T, V, passes;
+  uint32_t size;  // CTAs of the cluster
   uint32_t* out_id;  // V: no token
   uint32_t* out_row;
   int* status;
+  uint8_t* zero;  // zero_bytes of it become 0, by all clusters but the first
+  int64_t zero_bytes;
 };
+
+// Bytes [a, b) of the zeroed memory, by a CTA.
+__device__ __forceinline__ void zero_range(uint8_t* p, int64_t a, int64_t b) {
+  const int64_t whole = (b - a) / 16;
+  uint4* const v = reinterpret_cast<uint4*>(p + a);
+  for (int64_t i = threadIdx.x; i < whole; i += blockDim.x) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t rest = a + whole * 16 + threadIdx.x;
+  if (rest < b) p[rest] = 0;
+}
+// Element-aligned memory: its first bytes up to a 16-byte boundary, and what follows in equal shares.
+__device__ __forceinline__ void zero_share(uint8_t* p, int64_t bytes, int part, int parts) {
+  const int64_t head = min(bytes, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u));
+  if (part == 0 && static_cast<int64_t>(threadIdx.x) < head) p[threadIdx.x] = 0;
+  p += head;
+  bytes -= head;
+  constexpr int64_t kChunk = 65536;  // neighbouring CTAs write neighbouring chunks
+  for (int64_t a = part * kChunk; a < bytes; a += parts * kChunk)
+    zero_range(p, a, min(bytes, a + kChunk));
+}
 
 template <int kItems>
 struct SortShared {
@@ -41,12 +64,16 @@ struct SortShared {
 };
 
 template <int kItems>
-__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads, kItems <= 4 ? 2 : 1) embed_sort_kernel(const SortArgs a) {
   extern __shared__ uint4 sort_mem[];
   SortShared<kItems>& sh = *reinterpret_cast<SortShared<kItems>*>(sort_mem);
   constexpr int kOfCta = kSortThreads * kItems;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank(), size = gridDim.x;  // one cluster
+  const uint32_t rank = cluster_rank(), size = a.size;
+  if (blockIdx.x >= size) {
+    zero_share(a.zero, a.zero_bytes, blockIdx.x - size, gridDim.x - size);
+    return;
+  }
   const uint32_t first = warp * 32 * kItems + lane;        // of the CTA's tokens
   uint32_t id[kItems], row[kItems], place[kItems];
   bool bad = false;
@@ -143,25 +170,39 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
 }
 
 template <int kItems>
-cudaError_t launch_sort(const SortArgs& a, int cluster, cudaStream_t stream) {
+cudaError_t launch_sort(const SortArgs& a, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem(embed_sort_kernel<kItems>, sizeof(SortShared<kItems>), allowed);
   if (e != cudaSuccess) return e;
-  return launch_clusters(embed_sort_kernel<kItems>, 1, cluster, kSortThreads,
+  // as many CTAs as an SM's threads take twice over, or as there are chunks
+  const int64_t chunks = (a.zero_bytes + 65535) / 65536;
+  const int64_t others = std::min<int64_t>((chunks + a.size - 1) / a.size, 2 * num_sms / a.size);
+  return launch_clusters(embed_sort_kernel<kItems>, 1 + others, static_cast<int>(a.size), kSortThreads,
                          sizeof(SortShared<kItems>), stream, a);
 }
 
 // The ids of T <= kSortRows tokens in order, and their rows; ids that are none, or out of range
 // (noted in the status word), as V at the end.
 cudaError_t launch_embed_sort(const int32_t* ids, int T, int V, uint32_t* out_id, uint32_t* out_row,
-                              int* status, cudaStream_t stream) {
+                              int* status, void* zero, int64_t zero_bytes, int num_sms,
+                              cudaStream_t stream) {
   int bits = 1;
   while (bits < 32 && (static_cast<uint32_t>(V) >> bits) != 0) ++bits;
-  const SortArgs a = {ids, T, V, (bits + kDigitBits - 1) / kDigitBits, out_id, out_row, status};
-  int cluster = 1;
-  while (cluster < kSortCluster && cluster * kSortThreads * 4 < T) cluster *= 2;
-  return cluster * kSortThreads * 4 >= T ? launch_sort<4>(a, cluster, stream)
-                                         : launch_sort<kSortItems>(a, cluster, stream);
+  SortArgs a = {};
+  a.ids = ids;
+  a.T = T;
+  a.V = V;
+  a.passes = (bits + kDigitBits - 1) / kDigitBits;
+  a.size = 1;
+  while (a.size < kSortCluster && a.size * kSortThreads * 4 < static_cast<uint32_t>(T)) a.size *= 2;
+  a.out_id = out_id;
+  a.out_row = out_row;
+  a.status = status;
+  a.zero = static_cast<uint8_t*>(zero);
+  a.zero_bytes = zero_bytes;
+  return a.size * kSortThreads * 4 >= static_cast<uint32_t>(T)
+             ? launch_sort<4>(a, num_sms, stream)
+             : launch_sort<kSortItems>(a, num_sms, stream);
 }
 
 }  // namespace
