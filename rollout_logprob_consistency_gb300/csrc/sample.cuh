@@ -202,6 +202,29 @@ __device__ __forceinline__ u64 weight_of(float t, float g, uint32_t shift, const
   asm("shr.u64 %0, %0, %1;" : "+l"(w) : "r"(shift - __float_as_uint(n)));
   return w;
 }
+// Two of them, the fp32 part in packed operations: the same bits.  magic: kPow2Magic and whatever is to be
+// added to z K, a multiple of 1/256.
+struct PairScale {
+  F2 kh, kl, magic;
+};
+__device__ __forceinline__ PairScale pair_scale(float kh, float kl, float magic) {
+  return PairScale{f2(kh, kh), f2(kl, kl), f2(magic, magic)};
+}
+__device__ __forceinline__ void weights_of_two(float z0, float z1, const PairScale& s, uint32_t shift,
+                                               const uint32_t* table, u64& w0, u64& w1) {
+  const F2 z = f2(z0, z1), unit = f2(kUnitMagic, kUnitMagic);
+  const F2 t = fma2(z, s.kh, s.magic);
+  const F2 g = fma2(z, s.kl, fma2(z, s.kh, fma2(t, f2(-1.f, -1.f), s.magic)));
+  const F2 c2 = f2(515882496.0f, 515882496.0f), c1 = f2(1488522236.0f, 1488522236.0f);
+  const F2 p = fma2(g, fma2(g, fma2(g, f2(119194168.0f, 119194168.0f), c2), c1), unit);
+  const float2 n = unpack2(fma2(t, f2(1.f - 0x1p-24f, 1.f - 0x1p-24f), unit));
+  const float2 ts = unpack2(t), ps = unpack2(p);
+  const uint32_t one = 0x80000000u - __float_as_uint(kUnitMagic);
+  w0 = static_cast<u64>(table[__float_as_uint(ts.x) & 255u]) * (__float_as_uint(ps.x) + one);
+  w1 = static_cast<u64>(table[__float_as_uint(ts.y) & 255u]) * (__float_as_uint(ps.y) + one);
+  asm("shr.u64 %0, %0, %1;" : "+l"(w0) : "r"(shift - __float_as_uint(n.x)));
+  asm("shr.u64 %0, %0, %1;" : "+l"(w1) : "r"(shift - __float_as_uint(n.y)));
+}
 // Without recentring.
 __device__ __forceinline__ u64 weight_at(float z, float kh, float kl, uint32_t shift,
                                          const uint32_t* table) {

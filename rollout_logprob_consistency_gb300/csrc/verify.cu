@@ -17,6 +17,8 @@
 // row the border falls walks it once more.
 #include "verify.cuh"
 
+#include <type_traits>
+
 #include "sample_list.cuh"
 
 namespace tim {
@@ -131,9 +133,11 @@ __device__ __forceinline__ void write_row(const VerifyArgs& a, const RowState& s
 
 // ---- the second launch
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
+constexpr int kParts = kCluster * kWarps;  // of a row, one a warp
+constexpr int kAhead = 2;                  // vectors of a lane and matrix in flight
 
 __device__ __forceinline__ bool keeps(const VerifyRow& r, float z, int id) {
   return ((static_cast<u64>(key_of(z)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(id))) >=
@@ -151,18 +155,20 @@ __device__ __forceinline__ Df log_uniform(float u) {
 struct FinishShared {
   Tables fine;
   uint32_t table[2][256];
-  u64 part[kCluster * kWarps];  // of every warp of every CTA
+  u64 part[kParts];
   int n, refused, bad, found;
 };
 
 // A row of one matrix at the refused position: its kept tokens' probabilities at scale 2^60,
-// 2^((z - M) K - lse log2e).  The normaliser's multiple of 1/256 goes to the exponent (weight_of
-// takes any), the rest of it into a table of the row's own, so that what weight_of expands stays within 2^-9.
+// 2^((z - M) K - lse log2e).  What is added to z K, as a multiple of 1/256, goes to the exponent
+// (weights_of_two takes any), the rest of it into a table of the row's own, so that what is expanded
+// stays within 2^-9.  Where z K itself is too large to split, z - M is taken first.
 template <int kDtype>
 struct Dist {
   const typename Elem<kDtype>::raw* p;
   float zc, M, kh, kl, magic;  // kept: above zc, or zc with an id up to idc
   int idc;
+  bool all, recentre;  // all: whatever is above -inf is kept
   const uint32_t* table;
 
   __device__ __forceinline__ void set(const VerifyRow& r, const void* logits, float tau, uint32_t* to,
@@ -171,10 +177,14 @@ struct Dist {
     p = static_cast<const typename Elem<kDtype>::raw*>(logits);
     zc = key_value(static_cast<uint32_t>(r.border >> 32));
     idc = static_cast<int>(min(~static_cast<uint32_t>(r.border), 0x7FFFFFFFu));
+    all = r.border <= kAllKept;
     M = r.M;
     kh = K.h;
     kl = K.l;
-    const Df c = Df{kLog2eHi, kLog2eLo} * Df{-r.lse_h, -r.lse_l};
+    const Df mk = df(M) * K;
+    recentre = !(fabsf(mk.h) < 8192.f);
+    Df c = Df{kLog2eHi, kLog2eLo} * Df{-r.lse_h, -r.lse_l};
+    if (!recentre) c = c - mk;
     const float whole = rintf(c.h * 256.f) * (1.f / 256.f);
     magic = kPow2Magic + whole;
     table = to;
@@ -190,8 +200,11 @@ struct Dist {
       to[j] = static_cast<uint32_t>((t + (1ull << (down - 1))) >> down);
     }
   }
-  __device__ __forceinline__ u64 at(float z, int id) const {
-    if (!(z > zc || (z == zc && id <= idc))) return 0;
+  __device__ __forceinline__ float keep(float z, int id) const {
+    return z > zc || (z == zc && id <= idc) ? z : -INFINITY;
+  }
+  // of a logit far from 0
+  __device__ __forceinline__ u64 far(float z) const {
     // z - M = d + e exactly
     const float d = z - M, b = d - z, e = (z - (d - b)) + (-M - b);
     if (!(d * kh > -128.f)) return 0;
@@ -199,97 +212,135 @@ struct Dist {
     const float g = fmaf(e, kh, fmaf(d, kl, fmaf(d, kh, magic - t)));
     return weight_of(t, g, shift_of(2), table);
   }
+  // of the tokens id and id + 1
+  __device__ __forceinline__ void two(float z0, float z1, int id, u64& w0, u64& w1) const {
+    if (!all) {
+      z0 = keep(z0, id);
+      z1 = keep(z1, id + 1);
+    }
+    if (recentre) {
+      w0 = far(z0);
+      w1 = far(z1);
+    } else {
+      weights_of_two(z0, z1, pair_scale(kh, kl, magic), shift_of(2), table, w0, w1);
+    }
+  }
 };
 
 // kWide: both rows in 16-byte vectors, which begin `shift` tokens before them; else token by token.
 template <int kDtype, bool kWide>
 struct Residual {
   using E = Elem<kDtype>;
+  using raw = typename E::raw;
   static constexpr int kOf = kWide ? E::kVec : 1;  // tokens a lane looks at together
+  using Loaded = std::conditional_t<kWide, uint4, raw>;
   const Dist<kDtype>&p, &q;
   int V, shift, x;  // x: what the drafter is certain of, -1 with its logits
 
   __device__ __forceinline__ int groups() const { return (shift + V + kOf - 1) / kOf; }
-  // r of group j's tokens, and their sum
-  __device__ __forceinline__ u64 values(int j, u64 (&r)[kOf]) const {
+  __device__ __forceinline__ Loaded load(const raw* row, int j) const {
     const int id0 = j * kOf - shift;
-    u64 sum = 0;
-    float zp[kOf], zq[kOf];
     if constexpr (kWide) {
-      if (id0 >= 0 && id0 + kOf <= V) {
-        E::unpack(__ldg(reinterpret_cast<const uint4*>(p.p + id0)), zp);
-        if (x < 0) E::unpack(__ldg(reinterpret_cast<const uint4*>(q.p + id0)), zq);
-      } else {
+      if (id0 >= 0 && id0 + kOf <= V) return __ldg(reinterpret_cast<const uint4*>(row + id0));
+      float z[kOf];
 #pragma unroll
-        for (int i = 0; i < kOf; ++i) {
-          const bool in = id0 + i >= 0 && id0 + i < V;
-          zp[i] = in ? E::widen(p.p[id0 + i]) : -INFINITY;
-          zq[i] = in && x < 0 ? E::widen(q.p[id0 + i]) : -INFINITY;
-        }
-      }
+      for (int i = 0; i < kOf; ++i)
+        z[i] = id0 + i >= 0 && id0 + i < V ? E::widen(row[id0 + i]) : -INFINITY;
+      return E::pack(z);
     } else {
-      zp[0] = E::widen(__ldg(p.p + id0));
-      if (x < 0) zq[0] = E::widen(__ldg(q.p + id0));
+      return __ldg(row + id0);
+    }
+  }
+  // f(token, r of it) in order, of group j's tokens that have any; two at a time, so that few are held.
+  template <class F>
+  __device__ __forceinline__ void each(const Loaded& lp, const Loaded& lq, int j, F&& f) const {
+    constexpr int kHeld = kOf + kOf % 2;
+    const int id0 = j * kOf - shift;
+    float zp[kHeld], zq[kHeld];
+    if constexpr (kWide) {
+      E::unpack(lp, zp);
+      E::unpack(lq, zq);
+    } else {
+      zp[0] = E::widen(lp);
+      zq[0] = E::widen(lq);
+      zp[1] = zq[1] = -INFINITY;
     }
     bool any = false;
 #pragma unroll
     for (int i = 0; i < kOf; ++i) any |= zp[i] >= p.zc;
-    if (!any) {
+    if (!any) return;
 #pragma unroll
-      for (int i = 0; i < kOf; ++i) r[i] = 0;
-      return 0;
+    for (int i = 0; i < kHeld; i += 2) {
+      u64 a0, a1, b0, b1;
+      p.two(zp[i], zp[i + 1], id0 + i, a0, a1);
+      if (x < 0) {
+        q.two(zq[i], zq[i + 1], id0 + i, b0, b1);
+      } else {
+        b0 = id0 + i == x ? a0 : 0;
+        b1 = id0 + i + 1 == x ? a1 : 0;
+      }
+      f(id0 + i, a0 > b0 ? a0 - b0 : 0);
+      f(id0 + i + 1, a1 > b1 ? a1 - b1 : 0);
     }
-#pragma unroll
-    for (int i = 0; i < kOf; ++i) {
-      const int id = id0 + i;
-      const u64 a = p.at(zp[i], id);
-      const u64 b = x < 0 ? q.at(zq[i], id) : id == x ? a : 0;
-      r[i] = a > b ? a - b : 0;
-      sum += r[i];
-    }
-    return sum;
   }
 
   // The token, in every thread of the CTA that has it; -1 in the others, -2 where r sums to less than
   // 2^-28: p and q are good to 2^-30.3 each, so two that agree leave up to 2^-29.3.
   __device__ __forceinline__ int draw(FinishShared& sh, float u) const {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int part = (groups() + kCluster * kWarps * 32 - 1) / (kCluster * kWarps * 32) * 32;
+    const int part = (groups() + kParts * 32 - 1) / (kParts * 32) * 32;
     const int mine = static_cast<int>(cluster_rank()) * kWarps + warp;
     const int j0 = min(groups(), mine * part), j1 = min(groups(), j0 + part);
-    u64 sum = 0, r[kOf];
-    for (int j = j0 + lane; j < j1; j += 32) sum += values(j, r);
+    const raw* const other = x < 0 ? q.p : p.p;
+    u64 sum = 0;
+    for (int j = j0 + lane; j < j1; j += kAhead * 32) {
+      Loaded lp[kAhead], lq[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n)
+        if (j + n * 32 < j1) {
+          lp[n] = load(p.p, j + n * 32);
+          lq[n] = load(other, j + n * 32);
+        }
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n)
+        if (j + n * 32 < j1) each(lp[n], lq[n], j + n * 32, [&](int, u64 r) { sum += r; });
+    }
     sum = warp_sum(sum);
     if (lane < kCluster) cluster_store(cluster_addr(&sh.part[mine], lane), sum);
     if (tid == 0) sh.found = -1;
     cluster_arrive();
     cluster_wait();
-    static_assert(kCluster * kWarps == 64, "two parts a lane");
-    const u64 lo = warp_scan(sh.part[lane]);
-    const u64 hi = __shfl_sync(0xFFFFFFFFu, lo, 31) + warp_scan(sh.part[32 + lane]);
-    const u64 total = __shfl_sync(0xFFFFFFFFu, hi, 31);
+    u64 before = 0, total = 0;
+#pragma unroll
+    for (int i = lane; i < kParts; i += 32) {
+      total += sh.part[i];
+      before += i < mine ? sh.part[i] : 0;
+    }
+    total = warp_sum(total);
+    before = warp_sum(before);
     if (total < 1ull << 32) return -2;
     const u64 target = draw_target(total, u);
-    const int w = __popc(__ballot_sync(0xFFFFFFFFu, lo <= target)) +
-                  __popc(__ballot_sync(0xFFFFFFFFu, hi <= target));
-    if (w == mine) {  // this warp's part: once more, a step at a time
-      u64 at = __shfl_sync(0xFFFFFFFFu, w < 32 ? lo : hi, w & 31) - sh.part[w];
+    if (before <= target && target < before + sum) {  // this warp's part: once more, a step at a time
       for (int i = j0; i < j1; i += 32) {
         const int j = i + lane;
-        const u64 here = j < j1 ? values(j, r) : 0;
+        u64 here = 0;
+        Loaded lp, lq;
+        if (j < j1) {
+          lp = load(p.p, j);
+          lq = load(other, j);
+          each(lp, lq, j, [&](int, u64 r) { here += r; });
+        }
         const u64 to = warp_scan(here), all = __shfl_sync(0xFFFFFFFFu, to, 31);
-        if (target < at + all) {
-          u64 before = at + to - here;
-          if (j < j1) {
-#pragma unroll
-            for (int e = 0; e < kOf; ++e) {
-              if (before <= target && target < before + r[e]) sh.found = j * kOf - shift + e;
-              before += r[e];
-            }
-          }
+        if (target < before + all) {
+          u64 at = before + to - here;
+          if (at <= target && target < at + here)  // one lane
+            each(lp, lq, j, [&](int id, u64 r) {
+              if (at <= target && target < at + r) sh.found = id;
+              at += r;
+            });
           break;
         }
-        at += all;
+        before += all;
       }
     }
     __syncthreads();
@@ -359,7 +410,7 @@ __device__ __forceinline__ void decide_drafts(const VerifyArgs& a, int64_t b, co
 }
 
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads) verify_finish_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) verify_finish_kernel(const VerifyArgs a) {
   using E = Elem<kDtype>;
   using raw = typename E::raw;
   __shared__ FinishShared sh;
