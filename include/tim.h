@@ -737,10 +737,9 @@ tim_status tim_distill_backward(const void *logits, int32_t dtype, int64_t ld, i
  *                the other operators on logits too; zero-initialised once.
  * Errors: as tim_sample.  Via tim_status_sync: TIM_ERR_TOKEN_RANGE (an id below -1 or
  *   from V up), TIM_ERR_INVALID_ARG (a uniform number or a setting out of range),
- *   TIM_ERR_NONFINITE (a row read that has NaN, +inf or -inf alone).  A sequence that
- *   reaches such a position gets ids -1, logprob NaN and 0 accepted, the others are as
- *   always; the status word also names rows that no sequence reaches, since all rows up to
- *   the end of the drafts are read.
+ *   TIM_ERR_NONFINITE (a row that has NaN, +inf or -inf alone).  A sequence that reaches
+ *   such a position gets ids -1, logprob NaN and 0 accepted, the others are as always.
+ *   What lies behind a refused draft counts for nothing, whether it was read or not.
  * ------------------------------------------------------------------------ */
 #define TIM_VERIFY_MAX_DRAFTS 1024
 

@@ -8,15 +8,17 @@
 //   sum_{w <= v} r_w > u' sum r  (from p where r is next to nothing);  after the last draft, from p
 // so that what comes out is distributed as p, whatever q is.
 //
-// Two launches.  The first is the sampler's main kernel over all rows of both matrices at once: it
-// leaves each row's border (the last token kept), its normaliser and, for the target's, the token
-// that u' draws from p.  The second has a cluster of CTAs for each sequence: every CTA decides on the
-// drafts (a lane a position, few loads), and where one is refused its two rows are read again, mostly
-// from L2: p and q as 64-bit integers at scale 2^60, good to 2^-30.3 each, so that the sums of
-// max(p - q, 0) are exact in that scale and do not depend on the split; the warp in whose part of the
-// row the border falls walks it once more.
+// Two launches.  The first is the sampler's main kernel over the rows of both matrices, position by
+// position: it leaves each row's border (the last token kept), its normaliser and, for the target's,
+// the token that u' draws from p.  The CTA that is the second to finish a position's two rows decides
+// on its draft, and rows behind a refused draft that have not been begun by then are not read: nothing
+// of the result comes from them.  The second launch has a cluster of CTAs for each sequence.  Where a
+// draft is refused its two rows are read again, mostly from L2: p and q as 64-bit integers at scale
+// 2^60, good to 2^-30.3 each, so that the sums of max(p - q, 0) are exact in that scale and do not
+// depend on the split; the warp in whose part of the row the border falls walks it once more.
 #include "verify.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 #include "sample_list.cuh"
@@ -37,16 +39,25 @@ struct alignas(16) VerifyRow {
   int bad;
 };
 
+// What is decided of a draft: ln p of the token, and the code of a position that cannot be decided.
+struct Judged {
+  float logprob;
+  int code;
+};
+
 struct VerifyArgs {
   static constexpr bool kBorder = true;
   VerifyMatrix target, draft;
   int64_t B;
-  int N, V;
+  int N, V, dtype;
   const int32_t* ids;
   const float* uniform;
   const float* uniform_draw;
   tim_sample_params target_set, draft_set;
-  VerifyRow* rows;  // B (N + 1) of the target, B N of the draft
+  VerifyRow* rows;    // B (N + 1) of the target, B N of the draft
+  Judged* judged;     // B N
+  uint32_t* refused;  // B: the first position that ends a sequence, all ones at first
+  uint32_t* done;     // B N: finished rows of a position, less one at first
   int32_t* out_ids;
   float* out_logprob;
   int32_t* out_accepted;
@@ -56,21 +67,21 @@ __host__ __device__ __forceinline__ bool draft_given(const VerifyArgs& a) {
   return a.draft.logits != nullptr;
 }
 
-// A row of the first launch: the target's first, then the drafter's.
+// A row of the first launch: position by position, in each the sequences' target and draft.
 struct Where {
   int64_t b;
   int j;
   bool target;
 };
-__device__ __forceinline__ Where where(const VerifyArgs& a, int64_t row) {
-  const int64_t targets = a.B * (a.N + 1);
-  Where w;
-  w.target = row < targets;
-  const int of = w.target ? a.N + 1 : a.N;
-  if (!w.target) row -= targets;
-  w.b = row / of;
-  w.j = static_cast<int>(row - w.b * of);
-  return w;
+__device__ __forceinline__ Where where(const VerifyArgs& a, int64_t at) {
+  const uint32_t row = static_cast<uint32_t>(at);  // B (2 N + 1) < 2^28
+  const uint32_t of = static_cast<uint32_t>(draft_given(a) ? 2 * a.B : a.B), j = row / of;
+  const uint32_t i = row - j * of;
+  const bool pair = draft_given(a) && static_cast<int>(j) < a.N;
+  return Where{static_cast<int64_t>(pair ? i >> 1 : i), static_cast<int>(j), !pair || (i & 1) == 0};
+}
+__device__ __forceinline__ VerifyRow& state_of(const VerifyArgs& a, const Where& w) {
+  return a.rows[w.target ? w.b * (a.N + 1) + w.j : a.B * (a.N + 1) + w.b * a.N + w.j];
 }
 template <int kDtype>
 __device__ __forceinline__ Row<kDtype> row_of(const VerifyArgs& a, int64_t row) {
@@ -79,14 +90,19 @@ __device__ __forceinline__ Row<kDtype> row_of(const VerifyArgs& a, int64_t row) 
   const VerifyMatrix& m = w.target ? a.target : a.draft;
   return Row<kDtype>(static_cast<const raw*>(m.logits) + w.b * m.ld_seq + w.j * m.ld_pos, 0, 0, a.V);
 }
-// Rows behind the end of a sequence's drafts are not read: the target's at the end still is.
+// Rows behind the end of a sequence's drafts are not read (the target's at the end still is), nor those
+// behind a refused draft.
 __device__ __forceinline__ bool wanted(const VerifyArgs& a, int64_t row) {
   const Where w = where(a, row);
   const int32_t* const ids = a.ids + w.b * a.N;
   const int n = w.target ? w.j : w.j + 1;
   bool all = true;
   for (int i = threadIdx.x & 31; i < n; i += 32) all = all && __ldg(ids + i) >= 0;
-  return __all_sync(0xFFFFFFFFu, all);
+  // by one thread, for the CTA to go on or not as one
+  __shared__ bool on;
+  if (threadIdx.x == 0) on = __ldcg(a.refused + w.b) >= static_cast<uint32_t>(w.j);
+  __syncthreads();
+  return __all_sync(0xFFFFFFFFu, all) && on;
 }
 __device__ __forceinline__ bool in_range(float u) { return u >= 0.f && u < 1.f; }
 __device__ __forceinline__ Settings settings_of(const VerifyArgs& a, int64_t b, bool target) {
@@ -108,11 +124,79 @@ __device__ __forceinline__ Settings settings_of(const VerifyArgs& a, int64_t row
   const Where w = where(a, row);
   return settings_of(a, w.b, w.target);
 }
+
+__device__ __forceinline__ bool keeps(const VerifyRow& r, float z, int id) {
+  return ((static_cast<u64>(key_of(z)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(id))) >=
+         r.border;
+}
+// ln of the probability of a kept token of logit z
+__device__ __forceinline__ Df log_prob(const VerifyRow& r, float z, float tau) {
+  return (df(z) - df(r.M)) * reciprocal(df(tau)) - Df{r.lse_h, r.lse_l};
+}
+// ln u for 0 < u < 1
+__device__ __forceinline__ Df log_uniform(float u) {
+  return u < 0x1p-100f ? log_df(df(u * 0x1p100f)) - Df{kLn2Hi, kLn2Lo} * df(100.f) : log_df(df(u));
+}
+__device__ __forceinline__ VerifyRow read_row(const VerifyRow* p) {
+  static_assert(sizeof(VerifyRow) == 32, "two vectors");
+  uint4 v[2] = {__ldcg(reinterpret_cast<const uint4*>(p)), __ldcg(reinterpret_cast<const uint4*>(p) + 1)};
+  return *reinterpret_cast<const VerifyRow*>(v);
+}
+
+// A row of a position is finished: by the last of them, whether its draft is accepted.
+template <int kDtype>
+__device__ __noinline__ void judge(const VerifyArgs& a, int64_t b, int j) {
+  using E = Elem<kDtype>;
+  using raw = typename E::raw;
+  if (j >= a.N) return;
+  const int64_t at = b * a.N + j;
+  const int id = __ldg(a.ids + at);
+  if (id < 0) return;
+  __threadfence();
+  if (draft_given(a)) {
+    if (atomicAdd(a.done + at, 1u) == 0xFFFFFFFFu) return;
+    __threadfence();
+  }
+  const VerifyRow p = read_row(a.rows + b * (a.N + 1) + j);
+  const float u = __ldg(a.uniform + at);
+  Judged r = {0.f, p.bad};
+  if (id >= a.V) r.code = TIM_ERR_TOKEN_RANGE;
+  if (r.code == 0 && !in_range(u)) r.code = TIM_ERR_INVALID_ARG;
+  bool accepted = false;
+  if (r.code == 0) {
+    const float z = E::widen(
+        __ldg(static_cast<const raw*>(a.target.logits) + b * a.target.ld_seq + j * a.target.ld_pos + id));
+    const Df ln_p = log_prob(p, z, settings_of(a, b, true).tau);
+    Df ln_q = df(0.f);
+    bool certain = u == 0.f;  // whatever q is
+    if (draft_given(a)) {
+      const VerifyRow q = read_row(a.rows + a.B * (a.N + 1) + at);
+      const float zq = E::widen(
+          __ldg(static_cast<const raw*>(a.draft.logits) + b * a.draft.ld_seq + j * a.draft.ld_pos + id));
+      r.code = q.bad;
+      certain = certain || !keeps(q, zq, id);
+      ln_q = log_prob(q, zq, settings_of(a, b, false).tau);
+    }
+    // in logarithms: p and q may both lie below the range of a float
+    accepted = r.code == 0 && keeps(p, z, id) && (certain || (log_uniform(u) + ln_q - ln_p).h < 0.f);
+    r.logprob = ln_p.h;
+  }
+  a.judged[at] = r;
+  if (!accepted) atomicMin(a.refused + b, static_cast<uint32_t>(j));
+}
+
+__device__ __forceinline__ void leave(const VerifyArgs& a, int64_t row, const VerifyRow& r) {
+  const Where w = where(a, row);
+  state_of(a, w) = r;
+  a.dtype == TIM_F32    ? judge<TIM_F32>(a, w.b, w.j)
+  : a.dtype == TIM_BF16 ? judge<TIM_BF16>(a, w.b, w.j)
+                        : judge<TIM_F16>(a, w.b, w.j);
+}
+// What cannot be read ends its sequence, if that gets there: only then is it reported.
 __device__ __forceinline__ void write_bad(const VerifyArgs& a, int64_t row, int code) {
-  set_status(a.status, code);
   VerifyRow r = {};
   r.bad = code;
-  a.rows[row] = r;
+  leave(a, row, r);
 }
 __device__ __forceinline__ void write_row(const VerifyArgs& a, const RowState& st,
                                           const Tables& tables, int64_t row, int id, float x,
@@ -128,7 +212,7 @@ __device__ __forceinline__ void write_row(const VerifyArgs& a, const RowState& s
   r.logprob = n == 1 ? 0.f : ((df(x) - df(st.M)) * st.inv_tau - ln).h;
   r.id = id;
   r.bad = 0;
-  a.rows[row] = r;
+  leave(a, row, r);
 }
 
 // ---- the second launch
@@ -137,20 +221,6 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kParts = kCluster * kWarps;  // of a row, one a warp
-constexpr int kAhead = 2;                  // vectors of a lane and matrix in flight
-
-__device__ __forceinline__ bool keeps(const VerifyRow& r, float z, int id) {
-  return ((static_cast<u64>(key_of(z)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(id))) >=
-         r.border;
-}
-// ln of the probability of a kept token of logit z
-__device__ __forceinline__ Df log_prob(const VerifyRow& r, float z, float tau) {
-  return (df(z) - df(r.M)) * reciprocal(df(tau)) - Df{r.lse_h, r.lse_l};
-}
-// ln u for 0 < u < 1
-__device__ __forceinline__ Df log_uniform(float u) {
-  return u < 0x1p-100f ? log_df(df(u * 0x1p100f)) - Df{kLn2Hi, kLn2Lo} * df(100.f) : log_df(df(u));
-}
 
 struct FinishShared {
   Tables fine;
@@ -203,8 +273,8 @@ struct Dist {
   __device__ __forceinline__ float keep(float z, int id) const {
     return z > zc || (z == zc && id <= idc) ? z : -INFINITY;
   }
-  // of a logit far from 0
-  __device__ __forceinline__ u64 far(float z) const {
+  // of a logit far from 0; rare, and not worth its place between the others
+  __device__ __noinline__ u64 far(float z) const {
     // z - M = d + e exactly
     const float d = z - M, b = d - z, e = (z - (d - b)) + (-M - b);
     if (!(d * kh > -128.f)) return 0;
@@ -293,17 +363,21 @@ struct Residual {
     const int j0 = min(groups(), mine * part), j1 = min(groups(), j0 + part);
     const raw* const other = x < 0 ? q.p : p.p;
     u64 sum = 0;
-    for (int j = j0 + lane; j < j1; j += kAhead * 32) {
-      Loaded lp[kAhead], lq[kAhead];
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n)
-        if (j + n * 32 < j1) {
-          lp[n] = load(p.p, j + n * 32);
-          lq[n] = load(other, j + n * 32);
-        }
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n)
-        if (j + n * 32 < j1) each(lp[n], lq[n], j + n * 32, [&](int, u64 r) { sum += r; });
+    Loaded lp, lq;
+    int j = j0 + lane;
+    if (j < j1) {
+      lp = load(p.p, j);
+      lq = load(other, j);
+    }
+    while (j < j1) {  // the next vectors are on their way meanwhile
+      const int at = j;
+      const Loaded zp = lp, zq = lq;
+      j += 32;
+      if (j < j1) {
+        lp = load(p.p, j);
+        lq = load(other, j);
+      }
+      each(zp, zq, at, [&](int, u64 r) { sum += r; });
     }
     sum = warp_sum(sum);
     if (lane < kCluster) cluster_store(cluster_addr(&sh.part[mine], lane), sum);
@@ -322,22 +396,23 @@ struct Residual {
     const u64 target = draw_target(total, u);
     if (before <= target && target < before + sum) {  // this warp's part: once more, a step at a time
       for (int i = j0; i < j1; i += 32) {
-        const int j = i + lane;
-        u64 here = 0;
-        Loaded lp, lq;
+        u64 r[kOf + kOf % 2] = {}, here = 0;
+        j = i + lane;
         if (j < j1) {
-          lp = load(p.p, j);
-          lq = load(other, j);
-          each(lp, lq, j, [&](int, u64 r) { here += r; });
+          int n = 0;
+          each(load(p.p, j), load(other, j), j, [&](int, u64 x) {
+            r[n++] = x;
+            here += x;
+          });
         }
         const u64 to = warp_scan(here), all = __shfl_sync(0xFFFFFFFFu, to, 31);
         if (target < before + all) {
           u64 at = before + to - here;
-          if (at <= target && target < at + here)  // one lane
-            each(lp, lq, j, [&](int id, u64 r) {
-              if (at <= target && target < at + r) sh.found = id;
-              at += r;
-            });
+#pragma unroll
+          for (int n = 0; n < kOf; ++n) {
+            if (at <= target && target < at + r[n]) sh.found = j * kOf - shift + n;
+            at += r[n];
+          }
           break;
         }
         before += all;
@@ -348,63 +423,35 @@ struct Residual {
   }
 };
 
-// The drafts of a sequence, by one warp: a lane a position.  Writes what is accepted; sh.n of them, the
-// token that is refused there or -1, and the code of a position that cannot be decided.
-template <int kDtype>
-__device__ __forceinline__ void decide_drafts(const VerifyArgs& a, int64_t b, const VerifyRow* ps,
-                                              const VerifyRow* qs,
-                                              const typename Elem<kDtype>::raw* target,
-                                              const typename Elem<kDtype>::raw* draft, float tau,
-                                              float draft_tau, bool writes, FinishShared& sh) {
-  using E = Elem<kDtype>;
+// What came of a sequence's drafts, by one warp: writes those that were accepted; sh.n of them, the token
+// that was refused there or -1, and the code of a position that could not be decided.
+__device__ __forceinline__ void gather_drafts(const VerifyArgs& a, int64_t b, bool writes,
+                                              FinishShared& sh) {
   const int lane = threadIdx.x & 31;
   const int32_t* const ids = a.ids + b * a.N;
-  int n = 0;
-  for (int j0 = 0; j0 <= a.N; j0 += 32) {
-    const int j = j0 + lane;
-    const int id = j < a.N ? __ldg(ids + j) : -1;
-    // a row is there for every position up to the end of the drafts
-    const unsigned ends = __ballot_sync(0xFFFFFFFFu, id < 0);
-    const bool reached = j <= a.N && (ends & ((1u << lane) - 1u)) == 0;
-    int code = 0;
-    bool stop = true;
-    float lp = 0.f;
-    if (reached) {
-      const VerifyRow p = ps[j];
-      code = id < -1 || id >= a.V ? TIM_ERR_TOKEN_RANGE : p.bad;
-      if (id >= 0 && code == 0) {
-        const float u = __ldg(a.uniform + b * a.N + j);
-        const float z = E::widen(target[static_cast<int64_t>(j) * a.target.ld_pos + id]);
-        const Df ln_p = log_prob(p, z, tau);
-        Df ln_q = df(0.f);
-        bool certain = u == 0.f;  // whatever q is
-        if (!in_range(u)) code = TIM_ERR_INVALID_ARG;
-        if (draft_given(a)) {
-          const VerifyRow q = qs[j];
-          const float zq = E::widen(draft[static_cast<int64_t>(j) * a.draft.ld_pos + id]);
-          if (q.bad != 0) code = q.bad;
-          certain = certain || !keeps(q, zq, id);
-          ln_q = log_prob(q, zq, draft_tau);
-        }
-        // in logarithms: p and q may both lie below the range of a float
-        stop = !(keeps(p, z, id) && (certain || (log_uniform(u) + ln_q - ln_p).h < 0.f));
-        lp = ln_p.h;
-      }
+  int drafts = a.N;
+  for (int j0 = 0; j0 < a.N; j0 += 32) {
+    const unsigned ends = __ballot_sync(0xFFFFFFFFu, j0 + lane < a.N && __ldg(ids + j0 + lane) < 0);
+    if (ends != 0) {
+      drafts = j0 + __ffs(ends) - 1;
+      break;
     }
-    const unsigned stops = __ballot_sync(0xFFFFFFFFu, stop || code != 0);
-    const int k = stops != 0 ? __ffs(stops) - 1 : 32;  // accepted of these
-    if (writes && lane < k) {
-      a.out_ids[b * (a.N + 1) + j] = id;
-      a.out_logprob[b * (a.N + 1) + j] = lp;
+  }
+  const int n = static_cast<int>(min(a.refused[b], static_cast<uint32_t>(drafts)));
+  if (writes) {
+    for (int j = lane; j < n; j += 32) {
+      a.out_ids[b * (a.N + 1) + j] = __ldg(ids + j);
+      a.out_logprob[b * (a.N + 1) + j] = a.judged[b * a.N + j].logprob;
     }
-    n += k;
-    if (stops != 0) {
-      if (lane == k) {
-        sh.n = n;
-        sh.refused = id;
-        sh.bad = code;
-      }
-      return;
+  }
+  if (lane == 0) {
+    sh.n = n;
+    if (n < drafts) {
+      sh.refused = __ldg(ids + n);
+      sh.bad = a.judged[b * a.N + n].code;
+    } else {
+      sh.refused = -1;
+      sh.bad = n < a.N && __ldg(ids + n) < -1 ? TIM_ERR_TOKEN_RANGE : a.rows[b * (a.N + 1) + n].bad;
     }
   }
 }
@@ -423,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_finish_kernel(const Verify
   const raw* const draft = static_cast<const raw*>(a.draft.logits) + b * a.draft.ld_seq;
   const float tau = settings_of(a, b, true).tau, draft_tau = settings_of(a, b, false).tau;
   cluster_arrive();
-  if (tid < 32) decide_drafts<kDtype>(a, b, ps, qs, target, draft, tau, draft_tau, writes, sh);
+  if (tid < 32) gather_drafts(a, b, writes, sh);
   load_tables(sh.fine, tid, kThreads);
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
@@ -479,12 +526,14 @@ template <int kDtype>
 cudaError_t launch_type(const VerifyArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t rows = a.B * (a.N + 1) + (draft_given(a) ? a.B * a.N : 0);
   const unsigned g = static_cast<unsigned>(rows);
-  // threads a row as in sample.cu
-  if (rows <= num_sms)
+  // As few threads a row as let the rows of a position run at once (sample.cu has the same for all its
+  // rows): the next position's then come when something is known of this one's drafts.
+  const int64_t wave = std::min(rows, draft_given(a) ? 2 * a.B : a.B);
+  if (wave <= num_sms)
     sample_list_kernel<kDtype, 1024, VerifyArgs><<<g, 1024, 0, stream>>>(a);
-  else if (rows <= 2 * num_sms)
+  else if (wave <= 2 * num_sms)
     sample_list_kernel<kDtype, 512, VerifyArgs><<<g, 512, 0, stream>>>(a);
-  else if (rows <= 4 * num_sms)
+  else if (wave <= 4 * num_sms)
     sample_list_kernel<kDtype, 256, VerifyArgs><<<g, 256, 0, stream>>>(a);
   else
     sample_list_kernel<kDtype, 128, VerifyArgs><<<g, 128, 0, stream>>>(a);
@@ -493,12 +542,23 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t stream, int num_sms) {
   return launch_clusters(verify_finish_kernel<kDtype>, a.B, kCluster, kThreads, 0, stream, a);
 }
 
+struct VerifyWs {
+  size_t rows_off, judged_off, counts_off, counts, total;
+};
+VerifyWs verify_ws(int64_t B, int32_t N) {
+  const size_t b = static_cast<size_t>(B), n = static_cast<size_t>(N);
+  VerifyWs w;
+  w.rows_off = 1024;
+  w.judged_off = w.rows_off + b * (2 * n + 1) * sizeof(VerifyRow);
+  w.counts_off = w.judged_off + b * n * sizeof(Judged);
+  w.counts = b * (n + 1) * 4;
+  w.total = align_up(w.counts_off + w.counts, 1024);
+  return w;
+}
+
 }  // namespace
 
-size_t verify_bytes(int64_t B, int32_t N) {
-  return align_up(1024 + static_cast<size_t>(B) * (2 * static_cast<size_t>(N) + 1) * sizeof(VerifyRow),
-                  1024);
-}
+size_t verify_bytes(int64_t B, int32_t N) { return verify_ws(B, N).total; }
 
 cudaError_t launch_verify(const VerifyMatrix& target, const VerifyMatrix& draft, int dtype, int64_t B,
                           int N, int V, const int32_t* ids, const float* uniform,
@@ -516,11 +576,19 @@ cudaError_t launch_verify(const VerifyMatrix& target, const VerifyMatrix& draft,
   a.uniform_draw = uniform_draw;
   a.target_set = target_set;
   a.draft_set = draft_set;
-  a.rows = reinterpret_cast<VerifyRow*>(static_cast<uint8_t*>(ws) + 1024);
+  const VerifyWs w = verify_ws(B, N);
+  uint8_t* const mem = static_cast<uint8_t*>(ws);
+  a.dtype = dtype;
+  a.rows = reinterpret_cast<VerifyRow*>(mem + w.rows_off);
+  a.judged = reinterpret_cast<Judged*>(mem + w.judged_off);
+  a.refused = reinterpret_cast<uint32_t*>(mem + w.counts_off);
+  a.done = a.refused + B;
   a.out_ids = out_ids;
   a.out_logprob = out_logprob;
   a.out_accepted = out_accepted;
   a.status = static_cast<int*>(ws);
+  const cudaError_t e = cudaMemsetAsync(a.refused, 0xFF, w.counts, stream);
+  if (e != cudaSuccess) return e;
   return dtype == TIM_F32    ? launch_type<TIM_F32>(a, stream, num_sms)
          : dtype == TIM_BF16 ? launch_type<TIM_BF16>(a, stream, num_sms)
                              : launch_type<TIM_F16>(a, stream, num_sms);

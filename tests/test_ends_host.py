@@ -151,7 +151,7 @@ def _verify(tim, **kw):
     (dict(q=(1.0, 0, 1.0, -1.0)), ARG), (dict(rows=(P + 1, None, None, None)), ARG), (dict(out=None), ARG),
     (dict(lp=None), ARG), (dict(n=None), ARG), (dict(n=P + 2), ARG), (dict(out=FAR[2] + 44), ARG),
     (dict(lp=FAR[2] - 60), ARG), (dict(n=FAR[2]), ARG), (dict(ws=None), WORKSPACE), (dict(ws=P + 8), WORKSPACE),
-    (dict(nbytes=1024), WORKSPACE)])
+    (dict(nbytes=1024 + 4 * 7 * 32), WORKSPACE)])
 def test_verify_refusals(tim, kw, code):
     assert _verify(tim, **kw) == code
 
@@ -251,7 +251,7 @@ def test_residual_norm_backward_refusals(tim, kw, code):
 def test_workspace_sizes(tim):
     """None for what is refused; never less for a smaller call, so that a workspace serves those too."""
     assert tim.verify_workspace_size(0, 3) == 0 and tim.verify_workspace_size(4, 0) == 0
-    assert tim.verify_workspace_size(4, 3) >= 1024 + 4 * 7 * 32
+    assert tim.verify_workspace_size(4, 3) >= 1024 + 4 * 7 * 32 + 4 * 3 * 8 + 4 * 4 * 4
     assert tim.embed_backward_workspace_size(0, 10, 8) == 0 and tim.embed_backward_workspace_size(5, 10, 0) == 0
     sizes = [tim.embed_backward_workspace_size(T, 1000, 64) for T in
              (1, 2, 100, 8191, 8192, 8193, 32768, 32769, 131072, 131073, 1 << 20)]
