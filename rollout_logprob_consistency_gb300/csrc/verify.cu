@@ -10,9 +10,9 @@
 //
 // Two launches.  The first is the sampler's main kernel over the rows of both matrices, position by
 // position: it leaves each row's border (the last token kept), its normaliser and, for the target's,
-// the token that u' draws from p.  The CTA that is the second to finish a position's two rows decides
-// on its draft, and rows behind a refused draft that have not been begun by then are not read: nothing
-// of the result comes from them.  The second launch has a cluster of CTAs for each sequence.  Where a
+// the token that u' draws from p.  With more rows than SMs the CTA that is the second to finish a
+// position's two rows decides on its draft, and rows behind a refused draft that have not been begun by
+// then are not read: nothing of the result comes from them.  The second launch has a cluster of CTAs for each sequence.  Where a
 // draft is refused its two rows are read again, mostly from L2: p and q as 64-bit integers at scale
 // 2^60, good to 2^-30.3 each, so that the sums of max(p - q, 0) are exact in that scale and do not
 // depend on the split; the warp in whose part of the row the border falls walks it once more.
@@ -50,6 +50,8 @@ struct VerifyArgs {
   VerifyMatrix target, draft;
   int64_t B;
   int N, V, dtype;
+  int cluster;   // CTAs of a sequence in the second launch
+  bool in_rows;  // drafts are decided on as their rows are finished; else by the second launch
   const int32_t* ids;
   const float* uniform;
   const float* uniform_draw;
@@ -90,6 +92,9 @@ __device__ __forceinline__ Row<kDtype> row_of(const VerifyArgs& a, int64_t row) 
   const VerifyMatrix& m = w.target ? a.target : a.draft;
   return Row<kDtype>(static_cast<const raw*>(m.logits) + w.b * m.ld_seq + w.j * m.ld_pos, 0, 0, a.V);
 }
+__device__ __forceinline__ bool refused_before(const VerifyArgs& a, const Where& w) {
+  return __ldcg(a.refused + w.b) < static_cast<uint32_t>(w.j);
+}
 // Rows behind the end of a sequence's drafts are not read (the target's at the end still is), nor those
 // behind a refused draft.
 __device__ __forceinline__ bool wanted(const VerifyArgs& a, int64_t row) {
@@ -98,11 +103,9 @@ __device__ __forceinline__ bool wanted(const VerifyArgs& a, int64_t row) {
   const int n = w.target ? w.j : w.j + 1;
   bool all = true;
   for (int i = threadIdx.x & 31; i < n; i += 32) all = all && __ldg(ids + i) >= 0;
-  // by one thread, for the CTA to go on or not as one
-  __shared__ bool on;
-  if (threadIdx.x == 0) on = __ldcg(a.refused + w.b) >= static_cast<uint32_t>(w.j);
-  __syncthreads();
-  return __all_sync(0xFFFFFFFFu, all) && on;
+  all = __all_sync(0xFFFFFFFFu, all);
+  if (!a.in_rows) return all;
+  return __syncthreads_and(all && !refused_before(a, w)) != 0;
 }
 __device__ __forceinline__ bool in_range(float u) { return u >= 0.f && u < 1.f; }
 __device__ __forceinline__ Settings settings_of(const VerifyArgs& a, int64_t b, bool target) {
@@ -143,54 +146,61 @@ __device__ __forceinline__ VerifyRow read_row(const VerifyRow* p) {
   return *reinterpret_cast<const VerifyRow*>(v);
 }
 
-// A row of a position is finished: by the last of them, whether its draft is accepted.
+// Whether the draft of a position whose rows are finished is accepted.
 template <int kDtype>
-__device__ __noinline__ void judge(const VerifyArgs& a, int64_t b, int j) {
+__device__ __forceinline__ Judged judge(const VerifyArgs& a, int64_t b, int j, bool& accepted) {
   using E = Elem<kDtype>;
   using raw = typename E::raw;
-  if (j >= a.N) return;
   const int64_t at = b * a.N + j;
   const int id = __ldg(a.ids + at);
-  if (id < 0) return;
+  const VerifyRow p = read_row(a.rows + b * (a.N + 1) + j);
+  const float u = __ldg(a.uniform + at);
+  Judged r = {0.f, p.bad};
+  accepted = false;
+  if (id >= a.V) r.code = TIM_ERR_TOKEN_RANGE;
+  if (r.code == 0 && !in_range(u)) r.code = TIM_ERR_INVALID_ARG;
+  if (r.code != 0) return r;
+  const float z = E::widen(
+      __ldg(static_cast<const raw*>(a.target.logits) + b * a.target.ld_seq + j * a.target.ld_pos + id));
+  const Df ln_p = log_prob(p, z, settings_of(a, b, true).tau);
+  Df ln_q = df(0.f);
+  bool certain = u == 0.f;  // whatever q is
+  if (draft_given(a)) {
+    const VerifyRow q = read_row(a.rows + a.B * (a.N + 1) + at);
+    const float zq = E::widen(
+        __ldg(static_cast<const raw*>(a.draft.logits) + b * a.draft.ld_seq + j * a.draft.ld_pos + id));
+    r.code = q.bad;
+    certain = certain || !keeps(q, zq, id);
+    ln_q = log_prob(q, zq, settings_of(a, b, false).tau);
+  }
+  // in logarithms: p and q may both lie below the range of a float
+  accepted = r.code == 0 && keeps(p, z, id) && (certain || (log_uniform(u) + ln_q - ln_p).h < 0.f);
+  r.logprob = ln_p.h;
+  return r;
+}
+
+// A row of a position is finished: the last of them decides on its draft.
+template <int kDtype>
+__device__ __noinline__ void finished(const VerifyArgs& a, int64_t b, int j) {
+  const int64_t at = b * a.N + j;
+  if (j >= a.N || __ldg(a.ids + at) < 0) return;
   __threadfence();
   if (draft_given(a)) {
     if (atomicAdd(a.done + at, 1u) == 0xFFFFFFFFu) return;
     __threadfence();
   }
-  const VerifyRow p = read_row(a.rows + b * (a.N + 1) + j);
-  const float u = __ldg(a.uniform + at);
-  Judged r = {0.f, p.bad};
-  if (id >= a.V) r.code = TIM_ERR_TOKEN_RANGE;
-  if (r.code == 0 && !in_range(u)) r.code = TIM_ERR_INVALID_ARG;
-  bool accepted = false;
-  if (r.code == 0) {
-    const float z = E::widen(
-        __ldg(static_cast<const raw*>(a.target.logits) + b * a.target.ld_seq + j * a.target.ld_pos + id));
-    const Df ln_p = log_prob(p, z, settings_of(a, b, true).tau);
-    Df ln_q = df(0.f);
-    bool certain = u == 0.f;  // whatever q is
-    if (draft_given(a)) {
-      const VerifyRow q = read_row(a.rows + a.B * (a.N + 1) + at);
-      const float zq = E::widen(
-          __ldg(static_cast<const raw*>(a.draft.logits) + b * a.draft.ld_seq + j * a.draft.ld_pos + id));
-      r.code = q.bad;
-      certain = certain || !keeps(q, zq, id);
-      ln_q = log_prob(q, zq, settings_of(a, b, false).tau);
-    }
-    // in logarithms: p and q may both lie below the range of a float
-    accepted = r.code == 0 && keeps(p, z, id) && (certain || (log_uniform(u) + ln_q - ln_p).h < 0.f);
-    r.logprob = ln_p.h;
-  }
-  a.judged[at] = r;
+  bool accepted;
+  a.judged[at] = judge<kDtype>(a, b, j, accepted);
   if (!accepted) atomicMin(a.refused + b, static_cast<uint32_t>(j));
 }
 
 __device__ __forceinline__ void leave(const VerifyArgs& a, int64_t row, const VerifyRow& r) {
   const Where w = where(a, row);
   state_of(a, w) = r;
-  a.dtype == TIM_F32    ? judge<TIM_F32>(a, w.b, w.j)
-  : a.dtype == TIM_BF16 ? judge<TIM_BF16>(a, w.b, w.j)
-                        : judge<TIM_F16>(a, w.b, w.j);
+  if (!a.in_rows) return;
+  a.dtype == TIM_F32    ? finished<TIM_F32>(a, w.b, w.j)
+  : a.dtype == TIM_BF16 ? finished<TIM_BF16>(a, w.b, w.j)
+                        : finished<TIM_F16>(a, w.b, w.j);
 }
 // What cannot be read ends its sequence, if that gets there: only then is it reported.
 __device__ __forceinline__ void write_bad(const VerifyArgs& a, int64_t row, int code) {
@@ -219,14 +229,15 @@ __device__ __forceinline__ void write_row(const VerifyArgs& a, const RowState& s
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kParts = kCluster * kWarps;  // of a row, one a warp
+constexpr int kMaxCluster = 8;
 
 struct FinishShared {
   Tables fine;
   uint32_t table[2][256];
-  u64 part[kParts];
-  int n, refused, bad, found;
+  u64 part[kMaxCluster * kWarps];  // of every warp of every CTA
+  u64 step[kWarps];
+  u64 left;
+  int n, refused, bad, owner, found;
 };
 
 // A row of one matrix at the refused position: its kept tokens' probabilities at scale 2^60,
@@ -356,102 +367,137 @@ struct Residual {
 
   // The token, in every thread of the CTA that has it; -1 in the others, -2 where r sums to less than
   // 2^-28: p and q are good to 2^-30.3 each, so two that agree leave up to 2^-29.3.
-  __device__ __forceinline__ int draw(FinishShared& sh, float u) const {
+  //
+  // Sums over parts of the row, one a warp of the cluster, then over pieces of the part that the border falls
+  // into, one a warp of its CTA; a warp then walks its piece.
+  __device__ __forceinline__ int draw(FinishShared& sh, float u, int cluster) const {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int part = (groups() + kParts * 32 - 1) / (kParts * 32) * 32;
-    const int mine = static_cast<int>(cluster_rank()) * kWarps + warp;
-    const int j0 = min(groups(), mine * part), j1 = min(groups(), j0 + part);
+    const int rank = static_cast<int>(cluster_rank()), parts = cluster * kWarps;
+    const int part = (groups() + parts * 32 - 1) / (parts * 32) * 32;
     const raw* const other = x < 0 ? q.p : p.p;
-    u64 sum = 0;
-    Loaded lp, lq;
-    int j = j0 + lane;
-    if (j < j1) {
-      lp = load(p.p, j);
-      lq = load(other, j);
-    }
-    while (j < j1) {  // the next vectors are on their way meanwhile
-      const int at = j;
-      const Loaded zp = lp, zq = lq;
-      j += 32;
+    int j0 = min(groups(), (rank * kWarps + warp) * part), j1 = min(groups(), j0 + part);
+    if (tid == 0) sh.owner = sh.found = -1;
+#pragma unroll 1
+    for (int level = 0;; ++level) {
+      u64 sum = 0;
+      Loaded lp, lq;
+      int j = j0 + lane;
       if (j < j1) {
         lp = load(p.p, j);
         lq = load(other, j);
       }
-      each(zp, zq, at, [&](int, u64 r) { sum += r; });
-    }
-    sum = warp_sum(sum);
-    if (lane < kCluster) cluster_store(cluster_addr(&sh.part[mine], lane), sum);
-    if (tid == 0) sh.found = -1;
-    cluster_arrive();
-    cluster_wait();
-    u64 before = 0, total = 0;
-#pragma unroll
-    for (int i = lane; i < kParts; i += 32) {
-      total += sh.part[i];
-      before += i < mine ? sh.part[i] : 0;
-    }
-    total = warp_sum(total);
-    before = warp_sum(before);
-    if (total < 1ull << 32) return -2;
-    const u64 target = draw_target(total, u);
-    if (before <= target && target < before + sum) {  // this warp's part: once more, a step at a time
-      for (int i = j0; i < j1; i += 32) {
-        u64 r[kOf + kOf % 2] = {}, here = 0;
-        j = i + lane;
+      while (j < j1) {  // the next vectors are on their way meanwhile
+        const int at = j;
+        const Loaded zp = lp, zq = lq;
+        j += 32;
         if (j < j1) {
-          int n = 0;
-          each(load(p.p, j), load(other, j), j, [&](int, u64 x) {
-            r[n++] = x;
-            here += x;
-          });
+          lp = load(p.p, j);
+          lq = load(other, j);
         }
-        const u64 to = warp_scan(here), all = __shfl_sync(0xFFFFFFFFu, to, 31);
-        if (target < before + all) {
-          u64 at = before + to - here;
-#pragma unroll
-          for (int n = 0; n < kOf; ++n) {
-            if (at <= target && target < at + r[n]) sh.found = j * kOf - shift + n;
-            at += r[n];
-          }
-          break;
-        }
-        before += all;
+        each(zp, zq, at, [&](int, u64 r) { sum += r; });
       }
+      sum = warp_sum(sum);
+      if (level == 0) {
+        const int mine = rank * kWarps + warp;
+        if (lane < cluster) cluster_store(cluster_addr(&sh.part[mine], lane), sum);
+        cluster_arrive();
+        cluster_wait();
+        u64 before = 0, total = 0;
+        for (int i = lane; i < parts; i += 32) {
+          total += sh.part[i];
+          before += i < mine ? sh.part[i] : 0;
+        }
+        total = warp_sum(total);
+        before = warp_sum(before);
+        if (total < 1ull << 32) return -2;
+        const u64 target = draw_target(total, u);
+        if (before <= target && target < before + sum && lane == 0) {
+          sh.owner = warp;
+          sh.left = target - before;
+        }
+        __syncthreads();
+        if (sh.owner < 0) return -1;
+        const int o0 = min(groups(), (rank * kWarps + sh.owner) * part), o1 = min(groups(), o0 + part);
+        const int piece = (part / 32 + kWarps - 1) / kWarps * 32;
+        j0 = min(o1, o0 + warp * piece);
+        j1 = min(o1, j0 + piece);
+        continue;
+      }
+      if (lane == 0) sh.step[warp] = sum;
+      __syncthreads();
+      const u64 target = sh.left;
+      u64 before = 0;
+      for (int i = 0; i < warp; ++i) before += sh.step[i];
+      if (before <= target && target < before + sum) {
+        for (int i = j0; i < j1; i += 32) {
+          u64 r[kOf + kOf % 2] = {}, here = 0;
+          j = i + lane;
+          if (j < j1) {
+            int n = 0;
+            each(load(p.p, j), load(other, j), j, [&](int, u64 x) {
+              r[n++] = x;
+              here += x;
+            });
+          }
+          const u64 to = warp_scan(here), all = __shfl_sync(0xFFFFFFFFu, to, 31);
+          if (target < before + all) {
+            u64 at = before + to - here;
+#pragma unroll
+            for (int n = 0; n < kOf; ++n) {
+              if (at <= target && target < at + r[n]) sh.found = j * kOf - shift + n;
+              at += r[n];
+            }
+            break;
+          }
+          before += all;
+        }
+      }
+      __syncthreads();
+      return sh.found;
     }
-    __syncthreads();
-    return sh.found;
   }
 };
 
-// What came of a sequence's drafts, by one warp: writes those that were accepted; sh.n of them, the token
-// that was refused there or -1, and the code of a position that could not be decided.
+// What comes of a sequence's drafts, by one warp: writes those that are accepted; sh.n of them, the token
+// that is refused there or -1, and the code of a position that cannot be decided.
+template <int kDtype>
 __device__ __forceinline__ void gather_drafts(const VerifyArgs& a, int64_t b, bool writes,
                                               FinishShared& sh) {
   const int lane = threadIdx.x & 31;
   const int32_t* const ids = a.ids + b * a.N;
-  int drafts = a.N;
-  for (int j0 = 0; j0 < a.N; j0 += 32) {
-    const unsigned ends = __ballot_sync(0xFFFFFFFFu, j0 + lane < a.N && __ldg(ids + j0 + lane) < 0);
-    if (ends != 0) {
-      drafts = j0 + __ffs(ends) - 1;
-      break;
+  const uint32_t known = a.in_rows ? a.refused[b] : 0xFFFFFFFFu;
+  for (int j0 = 0; j0 <= a.N; j0 += 32) {
+    const int j = j0 + lane;
+    const int id = j < a.N ? __ldg(ids + j) : -1;
+    // up to the end of the drafts or the first that was refused
+    const unsigned ends = __ballot_sync(0xFFFFFFFFu, id < 0 || static_cast<uint32_t>(j) >= known);
+    const int end = ends != 0 ? __ffs(ends) - 1 : 32;
+    Judged r = {0.f, 0};
+    bool accepted = false;
+    if (lane < end && a.in_rows) {
+      r = a.judged[b * a.N + j];
+      accepted = true;
+    } else if (lane < end) {
+      r = judge<kDtype>(a, b, j, accepted);
+    } else if (lane == end) {
+      if (id >= 0)
+        r = a.judged[b * a.N + j];
+      else
+        r.code = id < -1 ? TIM_ERR_TOKEN_RANGE : a.rows[b * (a.N + 1) + j].bad;
     }
-  }
-  const int n = static_cast<int>(min(a.refused[b], static_cast<uint32_t>(drafts)));
-  if (writes) {
-    for (int j = lane; j < n; j += 32) {
-      a.out_ids[b * (a.N + 1) + j] = __ldg(ids + j);
-      a.out_logprob[b * (a.N + 1) + j] = a.judged[b * a.N + j].logprob;
+    const unsigned stops = __ballot_sync(0xFFFFFFFFu, !accepted);
+    const int n = stops != 0 ? __ffs(stops) - 1 : 32;  // accepted of these
+    if (writes && lane < n) {
+      a.out_ids[b * (a.N + 1) + j] = id;
+      a.out_logprob[b * (a.N + 1) + j] = r.logprob;
     }
-  }
-  if (lane == 0) {
-    sh.n = n;
-    if (n < drafts) {
-      sh.refused = __ldg(ids + n);
-      sh.bad = a.judged[b * a.N + n].code;
-    } else {
-      sh.refused = -1;
-      sh.bad = n < a.N && __ldg(ids + n) < -1 ? TIM_ERR_TOKEN_RANGE : a.rows[b * (a.N + 1) + n].bad;
+    if (stops != 0) {
+      if (lane == n) {
+        sh.n = j;
+        sh.refused = id;
+        sh.bad = r.code;
+      }
+      return;
     }
   }
 }
@@ -462,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_finish_kernel(const Verify
   using raw = typename E::raw;
   __shared__ FinishShared sh;
   const int tid = threadIdx.x;
-  const int64_t b = blockIdx.x / kCluster, out = b * (a.N + 1);
+  const int64_t b = blockIdx.x / a.cluster, out = b * (a.N + 1);
   const bool writes = cluster_rank() == 0;
   const VerifyRow* const ps = a.rows + b * (a.N + 1);
   const VerifyRow* const qs = a.rows + a.B * (a.N + 1) + b * a.N;
@@ -470,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_finish_kernel(const Verify
   const raw* const draft = static_cast<const raw*>(a.draft.logits) + b * a.draft.ld_seq;
   const float tau = settings_of(a, b, true).tau, draft_tau = settings_of(a, b, false).tau;
   cluster_arrive();
-  if (tid < 32) gather_drafts(a, b, writes, sh);
+  if (tid < 32) gather_drafts<kDtype>(a, b, writes, sh);
   load_tables(sh.fine, tid, kThreads);
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
@@ -507,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_finish_kernel(const Verify
     const int x = draft_given(a) ? -1 : refused;
     const uintptr_t at = reinterpret_cast<uintptr_t>(z);
     if (x >= 0 || ((at ^ reinterpret_cast<uintptr_t>(zq)) & 15u) == 0)
-      id = Residual<kDtype, true>{P, Q, a.V, static_cast<int>((at & 15u) / sizeof(raw)), x}.draw(sh, u);
+      id = Residual<kDtype, true>{P, Q, a.V, static_cast<int>((at & 15u) / sizeof(raw)), x}.draw(sh, u, a.cluster);
     else
-      id = Residual<kDtype, false>{P, Q, a.V, 0, x}.draw(sh, u);
+      id = Residual<kDtype, false>{P, Q, a.V, 0, x}.draw(sh, u, a.cluster);
   }
   if (tid != 0) return;
   if (id >= 0) {
@@ -528,7 +574,7 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t stream, int num_sms) {
   const unsigned g = static_cast<unsigned>(rows);
   // As few threads a row as let the rows of a position run at once (sample.cu has the same for all its
   // rows): the next position's then come when something is known of this one's drafts.
-  const int64_t wave = std::min(rows, draft_given(a) ? 2 * a.B : a.B);
+  const int64_t wave = a.in_rows ? (draft_given(a) ? 2 * a.B : a.B) : rows;
   if (wave <= num_sms)
     sample_list_kernel<kDtype, 1024, VerifyArgs><<<g, 1024, 0, stream>>>(a);
   else if (wave <= 2 * num_sms)
@@ -539,7 +585,7 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t stream, int num_sms) {
     sample_list_kernel<kDtype, 128, VerifyArgs><<<g, 128, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_clusters(verify_finish_kernel<kDtype>, a.B, kCluster, kThreads, 0, stream, a);
+  return launch_clusters(verify_finish_kernel<kDtype>, a.B, a.cluster, kThreads, 0, stream, a);
 }
 
 struct VerifyWs {
@@ -587,8 +633,16 @@ cudaError_t launch_verify(const VerifyMatrix& target, const VerifyMatrix& draft,
   a.out_logprob = out_logprob;
   a.out_accepted = out_accepted;
   a.status = static_cast<int*>(ws);
-  const cudaError_t e = cudaMemsetAsync(a.refused, 0xFF, w.counts, stream);
-  if (e != cudaSuccess) return e;
+  // Eight CTAs a sequence while they all run in two rounds; four beyond: what is done once a CTA (the
+  // drafts, the tables) then weighs less.  151936 bf16 tokens, most drafts refused somewhere: 48 sequences
+  // 25 us with eight, 33 with four; 128 sequences 65 and 55 (two: 62).
+  a.cluster = kMaxCluster * B <= 4 * num_sms ? kMaxCluster : kMaxCluster / 2;
+  // Rows that run all at once have nothing to gain from what the others say, and a chain less each.
+  a.in_rows = B * (N + 1) + (draft_given(a) ? B * N : 0) > num_sms;
+  if (a.in_rows) {
+    const cudaError_t e = cudaMemsetAsync(a.refused, 0xFF, w.counts, stream);
+    if (e != cudaSuccess) return e;
+  }
   return dtype == TIM_F32    ? launch_type<TIM_F32>(a, stream, num_sms)
          : dtype == TIM_BF16 ? launch_type<TIM_BF16>(a, stream, num_sms)
                              : launch_type<TIM_F16>(a, stream, num_sms);
