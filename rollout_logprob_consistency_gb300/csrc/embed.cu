@@ -12,6 +12,10 @@
 // the last where they go on beyond it; a second launch joins those in order.  No atomics: the same
 // call gives the same bits.  The table's gradient is zeroed by the rest of the sort's launch, which
 // has eight SMs' work otherwise; with `accumulate` it is added to.
+//
+// 32768 tokens of 4096 bf16 into 151936 rows take 200 to 219 us for sort and zeros (1.24 GB, 5.7 to 6.2
+// TB/s; the sort alone 18), 61 for the pieces and 9 for the joins.  Zeroing only the rows without a token, in
+// the launch of the pieces, took 302 + 18 + 11.
 #include "embed_sort.cuh"
 #include <type_traits>
 
@@ -22,6 +26,8 @@ namespace {
 
 // ---- the lookup
 
+// 32768 tokens of 4096 bf16 from 151936 rows take 63 us, 5.4 TB/s with every distinct row counted once; 8
+// vectors a thread, 64 or 256 threads and streaming stores take 62 to 66.
 constexpr int kLookupThreads = 128;
 constexpr int kLookupVecs = 4;  // of a thread, in flight together
 
@@ -244,9 +250,9 @@ __global__ void __launch_bounds__(kGradThreads) embed_join_kernel(const GradArgs
   const int p = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kGradThreads + threadIdx.x;
   const int i0 = p * a.piece, i1 = i0 + a.piece;  // all but the last piece are whole
   if (i1 >= a.T) return;
-  const uint32_t id = __ldg(a.id + i1 - 1);
-  if (id >= static_cast<uint32_t>(a.V) || __ldg(a.id + i1) != id) return;
-  if (i0 > 0 && __ldg(a.id + i0 - 1) == id) return;  // begins before this piece
+  const uint32_t id = __ldg(a.id + i1 - 1), next = __ldg(a.id + i1);
+  const uint32_t before = i0 > 0 ? __ldg(a.id + i0 - 1) : 0xFFFFFFFFu;
+  if (id >= static_cast<uint32_t>(a.V) || next != id || before == id) return;  // or begins earlier
   if (c >= a.d / kVec) return;
   float acc[kVec];
   const float* const part = a.partial + c * kVec;
@@ -303,7 +309,7 @@ cudaError_t launch_grad_type(const GradArgs& a, int out_dtype, cudaStream_t stre
   return cudaErrorInvalidValue;
 }
 
-// Rows of a piece.
+// Rows of a piece: few where there are few, for the SMs' sake.
 int piece_rows(int64_t T) { return T <= 8192 ? 16 : kMaxPiece; }
 
 struct EmbedWs {
