@@ -314,14 +314,9 @@ struct Deep {
   }
   // Sum of weights, without recentring.
   __device__ __forceinline__ u64 weights_of(const float (&v)[kVec], uint32_t shift) const {
-    const PairScale scale = pair_scale(st.pw.kh, st.pw.kl, kPow2Magic);
     u64 t = 0;
 #pragma unroll
-    for (int i = 0; i < kVec; i += 2) {
-      u64 a, b;
-      weights_of_two(v[i], v[i + 1], scale, shift, table.t, a, b);
-      t += a + b;
-    }
+    for (int i = 0; i < kVec; ++i) t += weight_at(v[i], st.pw.kh, st.pw.kl, shift, table.t);
     return t;
   }
   // The border by bins: the last kept token before which there are less than k tokens, or (kMass)
@@ -399,7 +394,6 @@ struct Deep {
     const float z_lo = M - (static_cast<float>(hi) + 0.51f) / per;
 
     // ---- the weights of all, of those above in each part, and the tokens within
-    const PairScale scale2 = pair_scale(st.pw.kh, st.pw.kl, kPow2Magic);
     u64 mine = 0;
     float count = 0.f;  // of those above
     for (int q = warp; q < kParts; q += kWarps) {
@@ -410,19 +404,14 @@ struct Deep {
         E::unpack(x, v);
         if (!whole) drop(v, id_of(j, 0), zc);
         bool some = false;
-        if (kMass) {
-#pragma unroll
-          for (int i = 0; i < kVec; i += 2) {
-            u64 w0, w1;
-            weights_of_two(v[i], v[i + 1], scale2, shift, table.t, w0, w1);
-            mine += w0 + w1;
-            if (v[i] >= z_hi) above += w0;
-            if (v[i + 1] >= z_hi) above += w1;
-          }
-        }
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           const bool over = v[i] >= z_hi;
+          if (kMass) {
+            const u64 w = weight_at(v[i], st.pw.kh, st.pw.kl, shift, table.t);
+            mine += w;
+            if (over) above += w;
+          }
           if (over) count += 1.f;
           some |= !over && v[i] >= z_lo;
         }

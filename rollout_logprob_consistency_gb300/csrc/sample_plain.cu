@@ -118,14 +118,9 @@ struct Sampler {
 
   // Sum of weights, without recentring.
   __device__ __forceinline__ u64 weights_of(const float (&v)[kVec], uint32_t shift) const {
-    const PairScale scale = pair_scale(st.pw.kh, st.pw.kl, kPow2Magic);
     u64 t = 0;
 #pragma unroll
-    for (int i = 0; i < kVec; i += 2) {
-      u64 a, b;
-      weights_of_two(v[i], v[i + 1], scale, shift, sh.table.t, a, b);
-      t += a + b;
-    }
+    for (int i = 0; i < kVec; ++i) t += weight_at(v[i], st.pw.kh, st.pw.kl, shift, sh.table.t);
     return t;
   }
   // The draw, f and one being the kept tokens' weights; f counts them in n.
