@@ -1038,11 +1038,18 @@ tim_status tim_verify(const void* target, int64_t target_ld_seq, int64_t target_
     return TIM_ERR_SHAPE;
   if ((s = check_settings(*params)) != TIM_OK) return s;
   if (draft_params != nullptr && (s = check_settings(*draft_params)) != TIM_OK) return s;
+  // what the launches still read while they write results
   const size_t ids = static_cast<size_t>(B) * static_cast<size_t>(N) * 4;
-  const size_t all = ids + static_cast<size_t>(B) * 4;
-  if (meet(draft_ids, ids, out_ids, all) || meet(draft_ids, ids, out_logprob, all) ||
-      meet(draft_ids, ids, out_accepted, static_cast<size_t>(B) * 4))
-    return TIM_ERR_INVALID_ARG;
+  const size_t seqs = static_cast<size_t>(B) * 4, all = ids + seqs;
+  const void* const out[3] = {out_ids, out_logprob, out_accepted};
+  const size_t out_bytes[3] = {all, all, seqs};
+  for (int i = 0; i < 3; ++i) {
+    if (meet(draft_ids, ids, out[i], out_bytes[i]) || meet(uniform, ids, out[i], out_bytes[i]) ||
+        meet(uniform_draw, seqs, out[i], out_bytes[i]))
+      return TIM_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out_bytes[i], out[j], out_bytes[j])) return TIM_ERR_INVALID_ARG;
+  }
   if ((s = check_workspace(workspace, workspace_bytes, verify_bytes(B, N))) != TIM_OK) return s;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;

@@ -104,7 +104,10 @@ __device__ __forceinline__ bool wanted(const VerifyArgs& a, int64_t row) {
   bool all = true;
   for (int i = threadIdx.x & 31; i < n; i += 32) all = all && __ldg(ids + i) >= 0;
   all = __all_sync(0xFFFFFFFFu, all);
-  if (!a.in_rows) return all;
+  if (!a.in_rows) {
+    pdl_launch_dependents();  // the second launch may load its tables
+    return all;
+  }
   return __syncthreads_and(all && !refused_before(a, w)) != 0;
 }
 __device__ __forceinline__ bool in_range(float u) { return u >= 0.f && u < 1.f; }
@@ -516,8 +519,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_finish_kernel(const Verify
   const raw* const draft = static_cast<const raw*>(a.draft.logits) + b * a.draft.ld_seq;
   const float tau = settings_of(a, b, true).tau, draft_tau = settings_of(a, b, false).tau;
   cluster_arrive();
-  if (tid < 32) gather_drafts<kDtype>(a, b, writes, sh);
   load_tables(sh.fine, tid, kThreads);
+  pdl_wait();
+  if (tid < 32) gather_drafts<kDtype>(a, b, writes, sh);
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
   const int n = sh.n, refused = sh.refused;
@@ -585,7 +589,21 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t stream, int num_sms) {
     sample_list_kernel<kDtype, 128, VerifyArgs><<<g, 128, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_clusters(verify_finish_kernel<kDtype>, a.B, a.cluster, kThreads, 0, stream, a);
+  // Where all rows run at once the second launch comes up beside them and waits for their end.
+  if (a.B * a.cluster > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.in_rows ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, verify_finish_kernel<kDtype>, a);
 }
 
 struct VerifyWs {

@@ -150,7 +150,8 @@ def _verify(tim, **kw):
     (dict(s=(1.0, 0, 0.0, 0.0)), ARG), (dict(s=(1.0, 0, 1.0, 1.5)), ARG), (dict(q=(1e7, 0, 1.0, 0.0)), ARG),
     (dict(q=(1.0, 0, 1.0, -1.0)), ARG), (dict(rows=(P + 1, None, None, None)), ARG), (dict(out=None), ARG),
     (dict(lp=None), ARG), (dict(n=None), ARG), (dict(n=P + 2), ARG), (dict(out=FAR[2] + 44), ARG),
-    (dict(lp=FAR[2] - 60), ARG), (dict(n=FAR[2]), ARG), (dict(ws=None), WORKSPACE), (dict(ws=P + 8), WORKSPACE),
+    (dict(lp=FAR[2] - 60), ARG), (dict(n=FAR[2]), ARG), (dict(out=FAR[3] - 4), ARG), (dict(lp=FAR[3] + 44), ARG),
+    (dict(n=FAR[4] + 12), ARG), (dict(out=FAR[4]), ARG), (dict(lp=FAR[5] + 60), ARG), (dict(n=FAR[6] - 12), ARG), (dict(ws=None), WORKSPACE), (dict(ws=P + 8), WORKSPACE),
     (dict(nbytes=1024 + 4 * 7 * 32), WORKSPACE)])
 def test_verify_refusals(tim, kw, code):
     assert _verify(tim, **kw) == code
