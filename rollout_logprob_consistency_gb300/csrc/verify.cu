@@ -48,7 +48,7 @@ struct alignas(16) VerifyRow {
 };
 
 // What is decided of a draft: ln p of the token, and the code of a position that cannot be decided.
-struct Judged {
+struct Decision {
   float logprob;
   int code;
 };
@@ -65,7 +65,7 @@ struct VerifyArgs {
   const float* uniform_draw;
   tim_sample_params target_set, draft_set;
   VerifyRow* rows;    // B (N + 1) of the target, B N of the draft
-  Judged* judged;     // B N
+  Decision* decided;     // B N
   uint32_t* refused;  // B: the first position that ends a sequence, all ones at first
   uint32_t* done;     // B N: finished rows of a position, less one at first
   int32_t* out_ids;
@@ -159,14 +159,14 @@ __device__ __forceinline__ VerifyRow read_row(const VerifyRow* p) {
 
 // Whether the draft of a position whose rows are finished is accepted.
 template <int kDtype>
-__device__ __forceinline__ Judged judge(const VerifyArgs& a, int64_t b, int j, bool& accepted) {
+__device__ __forceinline__ Decision decide_draft(const VerifyArgs& a, int64_t b, int j, bool& accepted) {
   using E = Elem<kDtype>;
   using raw = typename E::raw;
   const int64_t at = b * a.N + j;
   const int id = __ldg(a.ids + at);
   const VerifyRow p = read_row(a.rows + b * (a.N + 1) + j);
   const float u = __ldg(a.uniform + at);
-  Judged r = {0.f, p.bad};
+  Decision r = {0.f, p.bad};
   accepted = false;
   if (id >= a.V) r.code = TIM_ERR_TOKEN_RANGE;
   if (r.code == 0 && !in_range(u)) r.code = TIM_ERR_INVALID_ARG;
@@ -201,7 +201,7 @@ __device__ __noinline__ void finished(const VerifyArgs& a, int64_t b, int j) {
     __threadfence();
   }
   bool accepted;
-  a.judged[at] = judge<kDtype>(a, b, j, accepted);
+  a.decided[at] = decide_draft<kDtype>(a, b, j, accepted);
   if (!accepted) atomicMin(a.refused + b, static_cast<uint32_t>(j));
 }
 
@@ -483,16 +483,16 @@ __device__ __forceinline__ void gather_drafts(const VerifyArgs& a, int64_t b, bo
     // up to the end of the drafts or the first that was refused
     const unsigned ends = __ballot_sync(0xFFFFFFFFu, id < 0 || static_cast<uint32_t>(j) >= known);
     const int end = ends != 0 ? __ffs(ends) - 1 : 32;
-    Judged r = {0.f, 0};
+    Decision r = {0.f, 0};
     bool accepted = false;
     if (lane < end && a.in_rows) {
-      r = a.judged[b * a.N + j];
+      r = a.decided[b * a.N + j];
       accepted = true;
     } else if (lane < end) {
-      r = judge<kDtype>(a, b, j, accepted);
+      r = decide_draft<kDtype>(a, b, j, accepted);
     } else if (lane == end) {
       if (id >= 0)
-        r = a.judged[b * a.N + j];
+        r = a.decided[b * a.N + j];
       else
         r.code = id < -1 ? TIM_ERR_TOKEN_RANGE : a.rows[b * (a.N + 1) + j].bad;
     }
@@ -616,14 +616,14 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t stream, int num_sms) {
 }
 
 struct VerifyWs {
-  size_t rows_off, judged_off, counts_off, counts, total;
+  size_t rows_off, decided_off, counts_off, counts, total;
 };
 VerifyWs verify_ws(int64_t B, int32_t N) {
   const size_t b = static_cast<size_t>(B), n = static_cast<size_t>(N);
   VerifyWs w;
   w.rows_off = 1024;
-  w.judged_off = w.rows_off + b * (2 * n + 1) * sizeof(VerifyRow);
-  w.counts_off = w.judged_off + b * n * sizeof(Judged);
+  w.decided_off = w.rows_off + b * (2 * n + 1) * sizeof(VerifyRow);
+  w.counts_off = w.decided_off + b * n * sizeof(Decision);
   w.counts = b * (n + 1) * 4;
   w.total = align_up(w.counts_off + w.counts, 1024);
   return w;
@@ -653,7 +653,7 @@ cudaError_t launch_verify(const VerifyMatrix& target, const VerifyMatrix& draft,
   uint8_t* const mem = static_cast<uint8_t*>(ws);
   a.dtype = dtype;
   a.rows = reinterpret_cast<VerifyRow*>(mem + w.rows_off);
-  a.judged = reinterpret_cast<Judged*>(mem + w.judged_off);
+  a.decided = reinterpret_cast<Decision*>(mem + w.decided_off);
   a.refused = reinterpret_cast<uint32_t*>(mem + w.counts_off);
   a.done = a.refused + B;
   a.out_ids = out_ids;
