@@ -1077,8 +1077,9 @@ def embed(table, ids, scale: float = 1.0, *, out=None, workspace: Optional[Works
     V, d, code, ld = _logits_args(table, "table")
     dev = table.device
     _need(ids, torch.int32, "ids", 1)
-    T = ids.shape[0]
-    i = _vector(ids, torch.int32, T, dev, "ids")
+    T, i = ids.shape[0], ids.data_ptr()
+    if ids.device != dev:
+        raise ValueError(f"ids must be on {dev}")
     ldo = d if out is None else _matrix(out, T, d, code, dev, "out")
 
     def call(sp):
