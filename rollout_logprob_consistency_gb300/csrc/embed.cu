@@ -13,8 +13,8 @@
 // call gives the same bits.  The table's gradient is zeroed by the rest of the sort's launch, which
 // has eight SMs' work otherwise; with `accumulate` it is added to.
 //
-// 32768 tokens of 4096 bf16 into 151936 rows take 200 to 219 us for sort and zeros (1.24 GB, 5.7 to 6.2
-// TB/s; the sort alone 18), 61 for the pieces and 9 for the joins.  Zeroing only the rows without a token, in
+// 32768 tokens of 4096 bf16 into 151936 rows take 187 to 196 us for sort and zeros (1.24 GB, 6.4 to
+// 6.6 TB/s; the sort alone 18), 61 for the pieces and 9 for the joins.  Zeroing only the rows without a token, in
 // the launch of the pieces, took 302 + 18 + 11.
 #include "embed_sort.cuh"
 #include <type_traits>
