@@ -135,6 +135,7 @@ def test_many_sequences(tim, B):
     import torch
     p = _problem(B, 3, 3001, "bf16", B)
     for kw in (dict(), dict(temperature=0.7, top_k=50, top_p=0.95), dict(top_p=0.97), dict(top_k=2000, top_p=0.9)):
+        _check(tim, {**p, "draft": None}, kw, least=B - 1)
         whole = _check(tim, p, kw, least=B - 1)
         b = B // 2
         one = _call(tim, {k: v[b:b + 1] for k, v in p.items()}, kw)
