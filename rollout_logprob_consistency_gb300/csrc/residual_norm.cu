@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, kResident<kVecs, kThreads>)
     }
     if (pre || post) block_sum(s1, scratch1);
     const float r2 = pre ? rsqrtf(s1[0] * inv_d + b.eps) : 0.f;
-    const float c2 = pre ? r2 * r2 * r2 * inv_d * s1[1] : 0.f;
+    // r^2 and r^3 alone may leave fp32's range where the gradient is well within it
+    const float c2 = pre ? r2 * (inv_d * s1[1]) * r2 : 0.f;
     const float r1 = post ? rsqrtf(s1[2] * inv_d + b.eps) : 1.f;
     const float by_row = b.scale * row_gate;  // all of the gate that is not an element's own
     if (by_token) row_gate = gate_at(row + gridDim.x);
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kVecs, kThreads>)
         load2(src.get(stage, 2, k), u);
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) {
-          H[k][i] = fma2(r2s, H[k][i], fma2(c2s, v[i], w[i]));
+          H[k][i] = fma2(r2s, fma2(c2s, v[i], H[k][i]), w[i]);
           acc_pre[k][i] = fma2(mul2(u[i], v[i]), r2s, acc_pre[k][i]);
         }
       } else {
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kVecs, kThreads>)
     float q[1] = {tqs.x + tqs.y};
     if (post || by_token) block_sum(q, scratch2);
     if (by_token && threadIdx.x == 0) static_cast<float*>(a.out_dgate)[row] = b.scale * r1 * q[0];
-    const float c1 = post ? by_row * r1 * r1 * r1 * inv_d * q[0] : 0.f;
+    const float c1 = post ? r1 * (inv_d * q[0]) * r1 : 0.f;
     const F2 c1s = f2(-c1, -c1);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kVecs, kThreads>)
         F2 u[kHalf];
         load2(src.get(stage, 0, k), u);
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) H[k][i] = fma2(by_r1, H[k][i], mul2(c1s, u[i]));
+        for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(by_r1, fma2(c1s, u[i], H[k][i]));
       } else {
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) H[k][i] = mul2(by_r1, H[k][i]);

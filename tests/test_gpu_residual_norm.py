@@ -233,6 +233,22 @@ def test_zero_and_nonfinite_rows(tim):
     assert bool(h2[2].isnan().all()) and bool(y2[3].isnan().any())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,pad", [(64, 0), (1000, 3), (4096, 0), (4096, 3), (16384, 0)])
+@pytest.mark.parametrize("size", [1e15, 1e-15])
+def test_gradients_of_rows_far_from_one(tim, dtype, d, pad, size):
+    """The gradient of a row of size s is of size 1 / s, its projection onto the row among it; 1 / s^3 is out
+    of fp32's range for these."""
+    for gate in GATES:
+        p = _problem(3, d, dtype, gate, True, True, d, pad)
+        p["h"].mul_(size)
+        p["x"].mul_(size)
+        _backward(tim, p, p["h"], 0.5, 0.0, dh=False)
+        _backward(tim, p, p["h"], 0.5, 0.0)
+        for post in (False, True):
+            _forward(tim, {**p, "gamma_post": p["gamma_post"] if post else None}, 0.5, 0.0)
+
+
 def test_differences(tim):
     """The gradient in fp32 against central differences of the formula in 64 bits."""
     T, d, scale, eps = 3, 5, 0.7, 1e-3
