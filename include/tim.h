@@ -798,8 +798,9 @@ tim_status tim_embed_backward(const void *dy, int32_t dtype, int64_t ldy, const 
  * The gate g is none (1), one number a row (TIM_GATE_TOKEN, [T], stride ld_gate), a
  * channel (TIM_GATE_CHANNEL, [d]) or an element (TIM_GATE_ELEMENT, [T, d]).  h' is the
  * hidden state that tim_logprob takes, y the next block's input.  Sums are fp32, in an
- * order that depends on d and on whether rows lie on 16-byte boundaries: a row's bits do
- * not depend on the batch.  Infinite and NaN values go through to their row's results; the
+ * order that depends on d and on whether all of the call's rows and gammas are whole 16-byte
+ * vectors (addresses, strides and d multiples of 16 bytes): a row's bits do not depend on the
+ * other rows or on T.  Infinite and NaN values go through to their row's results; the
  * mean of the squares has to lie within fp32's range.
  *
  * tim_residual_norm_backward: from the gradients dh of out_h and dy of out_y (either may be
@@ -821,7 +822,7 @@ tim_status tim_embed_backward(const void *dy, int32_t dtype, int64_t ldy, const 
  * 1 <= T <= 2^31 - 1, 1 <= d <= TIM_RESIDUAL_MAX_D; scale finite, eps finite and >= 0.
  * h is read with dy alone (and may be NULL without).
  * Outputs must not meet inputs or one another, but out_h may be residual itself and
- * out_y the block's output (same address and stride).
+ * out_y the block's output (same address and, with more than one row, stride).
  * workspace   of the backward: tim_residual_norm_backward_workspace_size(T, d) bytes, which
  *             serve smaller T too.
  * Errors: TIM_ERR_INVALID_ARG, TIM_ERR_SHAPE, TIM_ERR_WORKSPACE,

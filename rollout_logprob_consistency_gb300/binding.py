@@ -991,6 +991,18 @@ def _matrix(t, T, d, code, dev, name):
     return ld
 
 
+def _norm_rows(t, ld):
+    """The row stride ``ld`` of a matrix of the residual update; of one row alone the tensor's own too.
+    What order a row's sums are taken in depends on whether the strides are whole vectors, and a row
+    is to give the same bits alone as among the others of its matrices."""
+    own = t.stride(0)
+    return own if t.shape[0] == 1 and ld <= own <= 2 ** 31 else ld
+
+
+def _norm_matrix(t, T, d, code, dev, name):
+    return _norm_rows(t, _matrix(t, T, d, code, dev, name))
+
+
 def verify_workspace_size(B: int, N: int) -> int:
     """Bytes of the workspace of ``verify`` for B sequences of up to N drafts."""
     return int(lib().tim_verify_workspace_size(int(B), int(N)))
@@ -1191,6 +1203,7 @@ GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ELEMENT = range(4)
 def _block_args(block, gamma, gamma_post, gate, scale, eps):
     torch = _torch()
     T, d, code, ld = _logits_args(block, "block")
+    ld = _norm_rows(block, ld)
     dev, dtype = block.device, block.dtype
     b = _Block(T, d, code, block.data_ptr(), ld, None, None, 0, GATE_NONE, scale, None, eps, 0)
     if gamma is not None:
@@ -1212,7 +1225,7 @@ def _block_args(block, gamma, gamma_post, gate, scale, eps):
             raise ValueError("gate must have a number of its own for each row")
     else:
         b.gate_kind = GATE_ELEMENT
-        b.ld_gate = _matrix(gate, T, d, code, dev, "gate")
+        b.ld_gate = _norm_matrix(gate, T, d, code, dev, "gate")
     return b, T, d, code, dev
 
 
@@ -1229,12 +1242,12 @@ def residual_norm(residual, block, gamma, eps: float, *, gamma_post=None, gate=N
     y ``block`` themselves."""
     torch = _torch()
     b, T, d, code, dev = _block_args(block, gamma, gamma_post, gate, scale, eps)
-    ldr = _matrix(residual, T, d, code, dev, "residual")
+    ldr = _norm_matrix(residual, T, d, code, dev, "residual")
     ldh = ldy = d
     if out is not None:
-        ldh = _matrix(out[0], T, d, code, dev, "out h")
+        ldh = _norm_matrix(out[0], T, d, code, dev, "out h")
         if gamma is not None:
-            ldy = _matrix(out[1], T, d, code, dev, "out y")
+            ldy = _norm_matrix(out[1], T, d, code, dev, "out y")
 
     def call(sp):
         if out is not None:
@@ -1269,20 +1282,20 @@ def residual_norm_backward(h, block, dh, dy, gamma, eps: float, *, gamma_post=No
     b, T, d, code, dev = _block_args(block, gamma, gamma_post, gate, scale, eps)
     if dy is not None and gamma is None:
         raise ValueError("dy without gamma")
-    ldh = _matrix(h, T, d, code, dev, "h") if dy is not None else d
-    ldy = _matrix(dy, T, d, code, dev, "dy") if dy is not None else d
-    ldd = _matrix(dh, T, d, code, dev, "dh") if dh is not None else d
+    ldh = _norm_matrix(h, T, d, code, dev, "h") if dy is not None else d
+    ldy = _norm_matrix(dy, T, d, code, dev, "dy") if dy is not None else d
+    ldd = _norm_matrix(dh, T, d, code, dev, "dh") if dh is not None else d
     ldr = ldb = ldg = d
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is not None:
-        ldr = _matrix(out[0], T, d, code, dev, "out dresidual")
-        ldb = _matrix(out[1], T, d, code, dev, "out dblock")
+        ldr = _norm_matrix(out[0], T, d, code, dev, "out dresidual")
+        ldb = _norm_matrix(out[1], T, d, code, dev, "out dblock")
         for t, given, name in ((out[2], gamma, "dgamma"), (out[3], gamma_post, "dgamma_post")):
             if given is not None:
                 _vector(t, f32, d, dev, "out " + name)
         if b.gate_kind == GATE_ELEMENT:
-            ldg = _matrix(out[4], T, d, code, dev, "out dgate")
+            ldg = _norm_matrix(out[4], T, d, code, dev, "out dgate")
         elif b.gate_kind != GATE_NONE:
             _need(out[4], f32, "out dgate")
             if out[4].shape != gate.shape or out[4].device != dev:

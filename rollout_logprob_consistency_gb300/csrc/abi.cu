@@ -1123,7 +1123,8 @@ tim_status tim_residual_norm(const tim_block* b, const void* residual, int64_t l
   if (b->gamma != nullptr) out[1] = span(b, out_y, ld_y);
   for (int o = 0; o < 2; ++o)
     for (int i = 0; i < 5; ++i)
-      if (meet(out[o], in[i]) && !(i == o && out[o].p == in[i].p && out[o].ld == in[i].ld))
+      if (meet(out[o], in[i]) &&
+          !(i == o && out[o].p == in[i].p && (out[o].ld == in[i].ld || b->T == 1)))
         return TIM_ERR_INVALID_ARG;
   if (meet(out[0], out[1])) return TIM_ERR_INVALID_ARG;
   if ((s = check_device(nullptr)) != TIM_OK) return s;

@@ -8,8 +8,9 @@
 // stored h' computes (tim_logprob's final norm among them).
 //
 // Memory's: a row is read once into registers and its one or two sums are taken by the CTA that
-// holds it.  How a row is split over threads depends on d alone, so a row's bits do not depend on
-// the batch.
+// holds it.  How a row is split over threads depends on d and on whether all of the call's rows are whole
+// 16-byte vectors (addresses, strides and d alike; see Cols): a row's bits do not depend on the other
+// rows or on their number, but a copy of it at another alignment may differ in the last one.
 #include "residual_norm.cuh"
 
 #include <algorithm>

@@ -303,3 +303,26 @@ def test_a_workspace_of_another_device_is_refused(monkeypatch, op):
             binding.embed_backward(z, ids, 10, workspace=ws, check=False)
         else:
             binding.residual_norm_backward(z, z, z, None, None, 1e-6, workspace=ws)
+
+
+def test_one_row_keeps_its_strides(monkeypatch):
+    """Whether rows are whole vectors is decided from the strides, and decides the order of a row's sums."""
+    torch = pytest.importorskip("torch")
+    got = []
+
+    class Lib:
+        @staticmethod
+        def tim_residual_norm(b, r, ldr, h, ldh, y, ldy, sp):
+            got.append((b._obj.ld_block, b._obj.ld_gate, ldr, ldh, ldy))
+            return 0
+
+    monkeypatch.setattr(binding, "lib", lambda: Lib)
+    monkeypatch.setattr(binding, "_type_code", lambda t, name: 0)
+    monkeypatch.setattr(binding, "_vector", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(binding, "_run", lambda dev, stream, call: call(None))
+    x, gamma = torch.zeros(4, 11)[:, :8], torch.zeros(8)
+    for n in (4, 1):
+        out = (torch.zeros(n, 12)[:, :8], torch.zeros(n, 13)[:, :8])
+        binding.residual_norm(x[:n], x[:n], gamma, 1e-6, gate=x[:n], out=out)
+    binding.residual_norm(*(x.as_strided((1, 8), (s, 1)) for s in (5, 2 ** 31 + 1)), gamma, 1e-6)
+    assert got == [(11, 11, 11, 12, 13)] * 2 + [(8, 0, 8, 8, 8)]

@@ -215,6 +215,37 @@ def test_rows_do_not_depend_on_the_batch(tim):
     assert all(torch.equal(a, b) for a, b in zip(whole, again))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("offset,pad", [(0, 3), (3, 5), (0, 8), (2, 6)])
+def test_rows_of_padded_matrices_do_not_depend_on_the_batch(tim, dtype, offset, pad):
+    """A row alone lies at a 16-byte boundary here and there; its strides are still its matrices'."""
+    import torch
+    for d, gate in ((264, "channel"), (4096, "element")):
+        p = _problem(40, d, dtype, gate, True, True, 14, pad, offset)
+        kw = dict(gamma_post=p["gamma_post"], scale=0.5)
+        h, y = tim.residual_norm(p["h"], p["x"], p["gamma"], 1e-6, gate=p["gate"], **kw)
+        whole = tim.residual_norm_backward(p["h"], p["x"], p["dh"], p["dy"], p["gamma"], 1e-6, gate=p["gate"], **kw)
+        for i in range(40):
+            s = slice(i, i + 1)
+            g = p["gate"] if gate == "channel" else p["gate"][s]
+            one = tim.residual_norm(p["h"][s], p["x"][s], p["gamma"], 1e-6, gate=g, **kw)
+            assert torch.equal(one[0], h[s]) and torch.equal(one[1], y[s]), i
+            part = tim.residual_norm_backward(p["h"][s], p["x"][s], p["dh"][s], p["dy"][s], p["gamma"], 1e-6,
+                                              gate=g, **kw)
+            assert torch.equal(part[0], whole[0][s]) and torch.equal(part[1], whole[1][s]), i
+
+
+def test_one_row_in_place_by_views_of_other_strides(tim):
+    import torch
+    p = _problem(1, 264, "bf16", "none", True, True, 23, pad=8)
+    want = _forward(tim, p, 0.5, 1e-6)
+    h, x = p["h"], p["x"]
+    got = tim.residual_norm(h, x, p["gamma"], 1e-6, gamma_post=p["gamma_post"], scale=0.5,
+                            out=(h.as_strided((1, 264), (264, 1)), x.as_strided((1, 264), (300, 1))))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert got[0].data_ptr() == h.data_ptr() and got[1].data_ptr() == x.data_ptr()
+
+
 def test_zero_and_nonfinite_rows(tim):
     """A row of zeros under a norm (eps alone below the root); a NaN or infinite row leaves the others."""
     import torch
