@@ -800,8 +800,9 @@ tim_status tim_embed_backward(const void *dy, int32_t dtype, int64_t ldy, const 
  * hidden state that tim_logprob takes, y the next block's input.  Sums are fp32, in an
  * order that depends on d and on whether all of the call's rows and gammas are whole 16-byte
  * vectors (addresses, strides and d multiples of 16 bytes): a row's bits do not depend on the
- * other rows or on T.  Infinite and NaN values go through to their row's results; the
- * mean of the squares has to lie within fp32's range.
+ * other rows or on T.  Infinite and NaN values go through to their row's results.  The sum of
+ * a row's squares has to be below 2^128: a norm makes zeros of finite rows beyond, and they
+ * take no part in its gradients.  Without eps their mean has to be 2^-126 at least.
  *
  * tim_residual_norm_backward: from the gradients dh of out_h and dy of out_y (either may be
  * NULL: zeros), with h = out_h and the rounding of h' passed straight through,

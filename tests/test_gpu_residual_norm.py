@@ -280,6 +280,38 @@ def test_gradients_of_rows_far_from_one(tim, dtype, d, pad, size):
             _forward(tim, {**p, "gamma_post": p["gamma_post"] if post else None}, 0.5, 0.0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 4096, 16384])
+def test_rows_at_the_ends_of_the_range_of_their_squares(tim, dtype, d):
+    """Right while the sum of the squares lies below 2^128 and their mean at 2^-126 or above; finite rows
+    beyond the one are zeros under the norm and take no part in its gradients."""
+    import torch
+    p = _problem(4, d, dtype, "none", True, True, 31)
+    root = math.sqrt(d)
+    signs = torch.where(p["h"] < 0, -1.0, 1.0).to(p["h"].dtype)
+    for size in (2.0 ** 63 / root, 2.0 ** -62.5):
+        q = {**p, "h": signs * size, "x": signs.flip(0) * size}
+        _forward(tim, {**q, "gamma_post": None}, 0.5, 0.0)
+        # so that dh and the norm's part of dresidual are of one size, and dblock is within the range
+        q["dy"], q["dh"] = p["dy"] * min(size, 1.0), p["dh"] * (min(size, 1.0) / size)
+        _backward(tim, q, q["h"], 0.5, 0.0)
+    far = {**p, "h": p["h"].clone(), "x": p["x"].clone()}
+    far["h"][2] = signs[2] * (2.0 ** 66 / root)
+    far["x"][2] = signs[2] * (2.0 ** 66 / root)
+    h, y = tim.residual_norm(far["h"], far["x"], p["gamma"], 1e-6, gamma_post=p["gamma_post"])
+    assert torch.equal(h[2], far["h"][2]) and not bool(y[2].any())
+    got = tim.residual_norm_backward(h, far["x"], p["dh"], p["dy"], p["gamma"], 1e-6, gamma_post=p["gamma_post"])
+    assert torch.equal(got[0][2], p["dh"][2]) and not bool(got[1][2].any())
+    keep = [0, 1, 3]
+    part = {k: v[keep] if v is not None and v.dim() == 2 else v for k, v in p.items()}
+    hk, yk = _forward(tim, part, 1.0, 1e-6)
+    assert torch.equal(h[keep], hk) and torch.equal(y[keep], yk)
+    want = _backward(tim, part, hk, 1.0, 1e-6)
+    assert torch.equal(got[0][keep], want[0]) and torch.equal(got[1][keep], want[1])
+    # the sums over rows: one row more of zeros, which a CTA of its own leaves
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+
+
 def test_differences(tim):
     """The gradient in fp32 against central differences of the formula in 64 bits."""
     T, d, scale, eps = 3, 5, 0.7, 1e-3
