@@ -732,8 +732,8 @@ tim_status tim_distill_backward(const void *logits, int32_t dtype, int64_t ld, i
  *                in [0, 1).
  * params         as of tim_sample with row_* [B], a setting a sequence; draft_params those
  *                the drafter drew with, NULL: the same.
- * out_*          int32 [B, N + 1], float32 [B, N + 1], int32 [B]; must not meet draft_ids,
- *                the uniform numbers or one another.
+ * out_*          int32 [B, N + 1], float32 [B, N + 1], int32 [B]; must not meet the logits,
+ *                draft_ids, the uniform numbers, the settings, the workspace or one another.
  * workspace      tim_verify_workspace_size(B, N) bytes, which serve smaller B and N and
  *                the other operators on logits too; zero-initialised once.
  * Errors: as tim_sample.  Via tim_status_sync: TIM_ERR_TOKEN_RANGE (an id below -1 or

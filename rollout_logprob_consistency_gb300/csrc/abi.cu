@@ -296,6 +296,29 @@ tim_status check_settings(const tim_sample_params& p) {
   return TIM_OK;
 }
 
+// The settings that are arrays, n numbers each.
+struct Settings {
+  const void* rows[4];
+};
+Settings row_settings(const tim_sample_params& p) {
+  return Settings{{p.row_temperature, p.row_top_k, p.row_top_p, p.row_min_p}};
+}
+// Whether n bytes at p meet any of the arrays, of `bytes` each.
+bool meet(const void* p, size_t n, const Settings& s, size_t bytes) {
+  for (const void* r : s.rows)
+    if (r != nullptr && meet(p, n, r, bytes)) return true;
+  return false;
+}
+
+// Bytes from the first row of sequence 0 to behind row n - 1 of sequence B - 1.
+size_t extent(const VerifyMatrix& m, int64_t B, int64_t n, int32_t V, int32_t dtype) {
+  const unsigned __int128 e = static_cast<unsigned __int128>(B - 1) * static_cast<uint64_t>(m.ld_seq) +
+                              static_cast<unsigned __int128>(n - 1) * static_cast<uint64_t>(m.ld_pos) +
+                              static_cast<uint64_t>(V);
+  const unsigned __int128 room = UINTPTR_MAX - reinterpret_cast<uintptr_t>(m.logits);
+  return static_cast<size_t>(std::min(e * dtype_bytes(dtype), room));
+}
+
 tim_status check_drafts(int64_t B, int32_t N) {
   if (N < 1 || N > TIM_VERIFY_MAX_DRAFTS || B < 1 || B > ((1 << 28) - 1) / (2 * N + 1))
     return TIM_ERR_SHAPE;
@@ -1038,26 +1061,30 @@ tim_status tim_verify(const void* target, int64_t target_ld_seq, int64_t target_
     return TIM_ERR_SHAPE;
   if ((s = check_settings(*params)) != TIM_OK) return s;
   if (draft_params != nullptr && (s = check_settings(*draft_params)) != TIM_OK) return s;
-  // what the launches still read while they write results
+  // what the launches still read, or keep between them, while they write results
+  const VerifyMatrix p{target, target_ld_seq, target_ld_pos}, q{draft, draft_ld_seq, draft_ld_pos};
+  const tim_sample_params& q_params = draft_params != nullptr ? *draft_params : *params;
   const size_t ids = static_cast<size_t>(B) * static_cast<size_t>(N) * 4;
-  const size_t seqs = static_cast<size_t>(B) * 4, all = ids + seqs;
+  const size_t seqs = static_cast<size_t>(B) * 4, all = ids + seqs, kept = verify_bytes(B, N);
   const void* const out[3] = {out_ids, out_logprob, out_accepted};
   const size_t out_bytes[3] = {all, all, seqs};
   for (int i = 0; i < 3; ++i) {
     if (meet(draft_ids, ids, out[i], out_bytes[i]) || meet(uniform, ids, out[i], out_bytes[i]) ||
-        meet(uniform_draw, seqs, out[i], out_bytes[i]))
+        meet(uniform_draw, seqs, out[i], out_bytes[i]) ||
+        meet(out[i], out_bytes[i], row_settings(*params), seqs) ||
+        meet(out[i], out_bytes[i], row_settings(q_params), seqs) ||
+        meet(out[i], out_bytes[i], target, extent(p, B, N + 1, V, dtype)) ||
+        (draft != nullptr && meet(out[i], out_bytes[i], draft, extent(q, B, N, V, dtype))) ||
+        (workspace != nullptr && meet(out[i], out_bytes[i], workspace, kept)))
       return TIM_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (meet(out[i], out_bytes[i], out[j], out_bytes[j])) return TIM_ERR_INVALID_ARG;
   }
-  if ((s = check_workspace(workspace, workspace_bytes, verify_bytes(B, N))) != TIM_OK) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, kept)) != TIM_OK) return s;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;
-  return from_cuda(launch_verify(VerifyMatrix{target, target_ld_seq, target_ld_pos},
-                                 VerifyMatrix{draft, draft_ld_seq, draft_ld_pos}, dtype, B, N, V,
-                                 draft_ids, uniform, uniform_draw, *params,
-                                 draft_params != nullptr ? *draft_params : *params, out_ids,
-                                 out_logprob, out_accepted, workspace,
+  return from_cuda(launch_verify(p, q, dtype, B, N, V, draft_ids, uniform, uniform_draw, *params,
+                                 q_params, out_ids, out_logprob, out_accepted, workspace,
                                  reinterpret_cast<cudaStream_t>(stream), sms));
 }
 

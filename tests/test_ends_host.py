@@ -326,3 +326,41 @@ def test_one_row_keeps_its_strides(monkeypatch):
         binding.residual_norm(x[:n], x[:n], gamma, 1e-6, gate=x[:n], out=out)
     binding.residual_norm(*(x.as_strided((1, 8), (s, 1)) for s in (5, 2 ** 31 + 1)), gamma, 1e-6)
     assert got == [(11, 11, 11, 12, 13)] * 2 + [(8, 0, 8, 8, 8)]
+
+
+FREE = P * 40  # meets nothing of _verify's
+
+
+@pytest.mark.parametrize("out,size", [("out", 64), ("lp", 64), ("n", 16)])
+@pytest.mark.parametrize("what", ["target", "draft", "temperature", "top_k", "top_p", "min_p", "draft's", "workspace"])
+def test_verify_refuses_results_over_what_it_still_reads(tim, out, size, what):
+    """Other sequences' CTAs read it while one writes.  B = 4, N = 3: 16 ids and logprobs, 4 counts."""
+    def call(at):
+        if what == "target":
+            return _verify(tim, target=FREE, **{out: at})
+        if what == "draft":
+            return _verify(tim, draft=FREE, **{out: at})
+        if what == "workspace":
+            return _verify(tim, ws=FREE, **{out: at})
+        i = 0 if what == "draft's" else ("temperature", "top_k", "top_p", "min_p").index(what)
+        rows = tuple(FREE if j == i else None for j in range(4))
+        if what != "draft's":
+            return _verify(tim, rows=rows, **{out: at})
+        a = dict(out=FAR[5], lp=FAR[6], n=FAR[7])
+        a[out] = at
+        p, q = binding._SampleParams(*OFF, *(None,) * 4), binding._SampleParams(*OFF, *rows)
+        return tim.lib().tim_verify(FAR[0], 256, 64, FAR[1], 192, 64, 1, 4, 3, 64, FAR[2], FAR[3], FAR[4],
+                                    ctypes.byref(p), ctypes.byref(q), a["out"], a["lp"], a["n"], FAR[8], 1 << 20, None)
+
+    # bytes: 3 sequence strides of 512 (384 of the draft's) and 3 (2) positions of 128, and the last row's;
+    # 4 settings; the workspace's status and its rows
+    end = {"target": 3 * 512 + 3 * 128 + 128, "draft": 3 * 384 + 2 * 128 + 128,
+           "workspace": tim.verify_workspace_size(4, 3)}.get(what, 16)
+    for at in (FREE, FREE + end - 4, FREE - size + 4):
+        assert call(at) == ARG, at - FREE
+
+
+def test_verify_rows_far_apart_do_not_wrap(tim):
+    """Strides whose extent is beyond 64 bits: whatever lies above the matrix's address is its."""
+    far = 1 << 40
+    assert _verify(tim, B=1 << 25, ts=far, tp=far, ds=far, dp=far) == ARG
