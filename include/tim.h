@@ -766,10 +766,11 @@ tim_status tim_verify(const void *target, int64_t target_ld_seq, int64_t target_
  * other tokens (on where the sorted batch is cut).
  *
  * table        [V, d] of dtype, row stride ld >= d;  out [T, d] of dtype, row stride ldo;
- *              must not meet table.
+ *              must not meet table, ids or the workspace.
  * dy           [T, d] of dtype, row stride ldy;  out_dtable [V, d] contiguous, of
- *              out_dtype (TIM_F32 or dtype); must not meet dy.  In 16 bits a row is rounded
- *              once a call; with more than 131072 tokens, once every so many.
+ *              out_dtype (TIM_F32 or dtype); must not meet dy, ids or the workspace.  In 16
+ *              bits a row is rounded once a call; with more than 131072 tokens, once every so
+ *              many.
  * T >= 1 (up to 2^31 - 1), 1 <= V <= 2^31 - 256, 1 <= d <= 65536, strides up to 2^31;
  * scale finite.  Any element-aligned address; rows of whole 16-byte vectors are faster.
  * workspace    tim_embed: 1024 bytes; tim_embed_backward: tim_embed_backward_workspace_size
@@ -822,7 +823,8 @@ tim_status tim_embed_backward(const void *dy, int32_t dtype, int64_t ldy, const 
  * aligned address (whole 16-byte vectors are faster); gammas [d] of dtype.
  * 1 <= T <= 2^31 - 1, 1 <= d <= TIM_RESIDUAL_MAX_D; scale finite, eps finite and >= 0.
  * h is read with dy alone (and may be NULL without).
- * Outputs must not meet inputs or one another, but out_h may be residual itself and
+ * Outputs must not meet inputs, the workspace or one another (matrices count from their first
+ * element to behind their last, what lies between rows too), but out_h may be residual itself and
  * out_y the block's output (same address and, with more than one row, stride).
  * workspace   of the backward: tim_residual_norm_backward_workspace_size(T, d) bytes, which
  *             serve smaller T too.

@@ -1095,8 +1095,9 @@ tim_status tim_embed(const void* table, int32_t dtype, int64_t ld, const int32_t
   if (s != TIM_OK) return s;
   if ((s = check_matrix(table, dtype, ld, d)) != TIM_OK) return s;
   if ((s = check_matrix(out, dtype, ldo, d)) != TIM_OK) return s;
-  if (meet(table, extent(ld, V, d, dtype), out, extent(ldo, T, d, dtype)) ||
-      meet(ids, static_cast<size_t>(T) * 4, out, extent(ldo, T, d, dtype)))
+  const size_t written = extent(ldo, T, d, dtype);
+  if (meet(table, extent(ld, V, d, dtype), out, written) ||
+      meet(ids, static_cast<size_t>(T) * 4, out, written) || meet(workspace, 1024, out, written))
     return TIM_ERR_INVALID_ARG;
   if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
   if ((s = check_device(nullptr)) != TIM_OK) return s;
@@ -1121,7 +1122,8 @@ tim_status tim_embed_backward(const void* dy, int32_t dtype, int64_t ldy, const 
   if (accumulate != 0 && accumulate != 1) return TIM_ERR_INVALID_ARG;
   const size_t table = extent(d, V, d, out_dtype);
   if (meet(dy, extent(ldy, T, d, dtype), out_dtable, table) ||
-      meet(ids, static_cast<size_t>(T) * 4, out_dtable, table))
+      meet(ids, static_cast<size_t>(T) * 4, out_dtable, table) ||
+      meet(workspace, embed_backward_bytes(T, d), out_dtable, table))
     return TIM_ERR_INVALID_ARG;
   if ((s = check_workspace(workspace, workspace_bytes, embed_backward_bytes(T, d))) != TIM_OK)
     return s;
@@ -1199,6 +1201,7 @@ tim_status tim_residual_norm_backward(const tim_block* b, const void* h, int64_t
   in[4] = gate_span(b);
   in[5] = row_span(b, b->gamma);
   in[6] = row_span(b, b->gamma_post);
+  const Span scratch{workspace, residual_norm_backward_bytes(b->T, b->d), 0};
   const size_t sums = static_cast<size_t>(b->d) * 4;
   out[0] = span(b, out_dresidual, ld_dresidual);
   out[1] = span(b, out_dblock, ld_dblock);
@@ -1217,10 +1220,9 @@ tim_status tim_residual_norm_backward(const tim_block* b, const void* h, int64_t
       if (meet(out[o], in[i])) return TIM_ERR_INVALID_ARG;
     for (int i = 0; i < o; ++i)
       if (meet(out[o], out[i])) return TIM_ERR_INVALID_ARG;
+    if (meet(out[o], scratch)) return TIM_ERR_INVALID_ARG;
   }
-  if ((s = check_workspace(workspace, workspace_bytes, residual_norm_backward_bytes(b->T, b->d))) !=
-      TIM_OK)
-    return s;
+  if ((s = check_workspace(workspace, workspace_bytes, scratch.bytes)) != TIM_OK) return s;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;
   NormGradArgs a = {};

@@ -364,3 +364,14 @@ def test_verify_rows_far_apart_do_not_wrap(tim):
     """Strides whose extent is beyond 64 bits: whatever lies above the matrix's address is its."""
     far = 1 << 40
     assert _verify(tim, B=1 << 25, ts=far, tp=far, ds=far, dp=far) == ARG
+
+
+def test_results_over_the_workspace_are_refused(tim):
+    """It holds the status, the sorted tokens and the sums that the launches hand on."""
+    assert all(_embed(tim, ws=FREE, out=at) == ARG for at in (FREE, FREE + 1020, FREE - 8 * 64 * 2 + 2))
+    end = tim.embed_backward_workspace_size(8, 100, 64)
+    assert all(_embed_backward(tim, ws=FREE, out=at) == ARG for at in (FREE, FREE + end - 4, FREE - 100 * 64 * 4 + 4))
+    end = tim.residual_norm_backward_workspace_size(8, 64)
+    for out, size in (("dr", 1024), ("db", 1024), ("dgate", 1024), ("dgamma", 256), ("dpost", 256)):
+        for at in (FREE, FREE + end - 4, FREE - size + 4):
+            assert _norm_backward(tim, ws=FREE, **{out: at}) == ARG, (out, at - FREE)
