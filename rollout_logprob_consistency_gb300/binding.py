@@ -991,6 +991,12 @@ def _matrix(t, T, d, code, dev, name):
     return ld
 
 
+def _i32_size(n):
+    """A size for the library's 32 bits: one that does not fit stays too large, where ctypes would keep its
+    low 32 bits."""
+    return min(max(int(n), -2 ** 31), 2 ** 31 - 1)
+
+
 def _norm_rows(t, ld):
     """The row stride ``ld`` of a matrix of the residual update; of one row alone the tensor's own too.
     What order a row's sums are taken in depends on whether the strides are whole vectors, and a row
@@ -1005,7 +1011,7 @@ def _norm_matrix(t, T, d, code, dev, name):
 
 def verify_workspace_size(B: int, N: int) -> int:
     """Bytes of the workspace of ``verify`` for B sequences of up to N drafts."""
-    return int(lib().tim_verify_workspace_size(int(B), int(N)))
+    return int(lib().tim_verify_workspace_size(int(B), _i32_size(N)))
 
 
 def _sequence_rows(t, B, n, V, dev, name):
@@ -1069,10 +1075,10 @@ def verify(target, draft_ids, uniform, uniform_draw, draft=None, temperature=1.0
                  torch.empty(B, dtype=i32, device=dev))
         ws = _sized_workspace(workspace, dev, stream, lambda: verify_workspace_size(B, N))
         _check(lib().tim_verify(target.data_ptr(), ts, tp,
-                                None if draft is None else draft.data_ptr(), ds, dp, code, B, N, V,
-                                draft_ids.data_ptr(), uniform.data_ptr(), u, _c.byref(p), q,
-                                o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(), ws.ptr, ws.nbytes,
-                                sp), "tim_verify")
+                                None if draft is None else draft.data_ptr(), ds, dp, code, B,
+                                _i32_size(N), _i32_size(V), draft_ids.data_ptr(), uniform.data_ptr(), u,
+                                _c.byref(p), q, o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr(),
+                                ws.ptr, ws.nbytes, sp), "tim_verify")
         if check:
             ws.check("tim_verify", stream)
         return o
@@ -1099,8 +1105,8 @@ def embed(table, ids, scale: float = 1.0, *, out=None, workspace: Optional[Works
         if o is None:
             o = torch.empty(T, d, dtype=table.dtype, device=dev)
         ws = _status_workspace(workspace, dev, stream)
-        _check(lib().tim_embed(table.data_ptr(), code, ld, i, T, V, d, scale, o.data_ptr(), ldo,
-                               ws.ptr, ws.nbytes, sp), "tim_embed")
+        _check(lib().tim_embed(table.data_ptr(), code, ld, i, T, _i32_size(V), _i32_size(d), scale,
+                               o.data_ptr(), ldo, ws.ptr, ws.nbytes, sp), "tim_embed")
         if check:
             ws.check("tim_embed", stream)
         return o
@@ -1110,7 +1116,7 @@ def embed(table, ids, scale: float = 1.0, *, out=None, workspace: Optional[Works
 
 def embed_backward_workspace_size(T: int, V: int, d: int) -> int:
     """Bytes of the workspace of ``embed_backward``; it serves ``embed`` too."""
-    return int(lib().tim_embed_backward_workspace_size(int(T), int(V), int(d)))
+    return int(lib().tim_embed_backward_workspace_size(int(T), _i32_size(V), _i32_size(d)))
 
 
 def embed_backward(dy, ids, V: int, scale: float = 1.0, *, dtype=None, out_dtable=None,
@@ -1141,8 +1147,8 @@ def embed_backward(dy, ids, V: int, scale: float = 1.0, *, dtype=None, out_dtabl
         if o is None:
             o = torch.empty(V, d, dtype=dtype, device=dev)
         ws = _sized_workspace(workspace, dev, stream, lambda: embed_backward_workspace_size(T, V, d))
-        _check(lib().tim_embed_backward(dy.data_ptr(), code, ld, i, T, V, d, scale, o.data_ptr(),
-                                        _DTYPE_CODES[dtype], int(bool(accumulate)), ws.ptr,
+        _check(lib().tim_embed_backward(dy.data_ptr(), code, ld, i, T, _i32_size(V), _i32_size(d), scale,
+                                        o.data_ptr(), _DTYPE_CODES[dtype], int(bool(accumulate)), ws.ptr,
                                         ws.nbytes, sp), "tim_embed_backward")
         if check:
             ws.check("tim_embed_backward", stream)
@@ -1205,7 +1211,7 @@ def _block_args(block, gamma, gamma_post, gate, scale, eps):
     T, d, code, ld = _logits_args(block, "block")
     ld = _norm_rows(block, ld)
     dev, dtype = block.device, block.dtype
-    b = _Block(T, d, code, block.data_ptr(), ld, None, None, 0, GATE_NONE, scale, None, eps, 0)
+    b = _Block(T, _i32_size(d), code, block.data_ptr(), ld, None, None, 0, GATE_NONE, scale, None, eps, 0)
     if gamma is not None:
         b.gamma = _vector(gamma, dtype, d, dev, "gamma")
     if gamma_post is not None:
@@ -1265,7 +1271,7 @@ def residual_norm(residual, block, gamma, eps: float, *, gamma_post=None, gate=N
 
 def residual_norm_backward_workspace_size(T: int, d: int) -> int:
     """Bytes of the workspace of ``residual_norm_backward``."""
-    return int(lib().tim_residual_norm_backward_workspace_size(int(T), int(d)))
+    return int(lib().tim_residual_norm_backward_workspace_size(int(T), _i32_size(d)))
 
 
 def residual_norm_backward(h, block, dh, dy, gamma, eps: float, *, gamma_post=None, gate=None,

@@ -375,3 +375,43 @@ def test_results_over_the_workspace_are_refused(tim):
     for out, size in (("dr", 1024), ("db", 1024), ("dgate", 1024), ("dgamma", 256), ("dpost", 256)):
         for at in (FREE, FREE + end - 4, FREE - size + 4):
             assert _norm_backward(tim, ws=FREE, **{out: at}) == ARG, (out, at - FREE)
+
+
+def test_sizes_beyond_32_bits_stay_too_large(tim, monkeypatch):
+    """The low 32 bits of 2^32 + 5 are a size that would be served, and the rest of the table left as it was."""
+    torch = pytest.importorskip("torch")
+    big, most = 2 ** 32 + 5, 2 ** 31 - 1
+    assert tim.verify_workspace_size(4, big) == 0 and tim.verify_workspace_size(4, big - 2 ** 33) == 0
+    assert tim.embed_backward_workspace_size(8, big, 8) == 0 and tim.embed_backward_workspace_size(8, 100, big) == 0
+    assert tim.residual_norm_backward_workspace_size(8, big) == 0
+    got = {}
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: got.__setitem__(name, a) or 0
+
+    def like(*shape):
+        return torch.empty(1).expand(*shape)
+
+    ws = types.SimpleNamespace(ptr=0, nbytes=1 << 20, buf=torch.zeros(1))
+    monkeypatch.setattr(binding, "lib", Lib)
+    monkeypatch.setattr(binding, "_type_code", lambda t, name: 0)
+    monkeypatch.setattr(binding, "_logits_args", lambda t, name: (*t.shape, 0, t.shape[1]))
+    monkeypatch.setattr(binding, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(binding, "_run", lambda dev, stream, call: call(None))
+    monkeypatch.setattr(binding, "_DTYPE_CODES", {torch.float32: 0})
+    kw = dict(workspace=ws, check=False)
+    ids = torch.zeros(4, dtype=torch.int32)
+    binding.embed_backward(like(4, 8), ids, big, out_dtable=like(big, 8), **kw)
+    assert got["tim_embed_backward"][5:7] == (most, 8)
+    binding.embed_backward(like(4, big), ids, 8, out_dtable=like(8, big), **kw)
+    assert got["tim_embed_backward"][5:7] == (8, most)
+    binding.embed(like(big, 8), ids, out=like(4, 8), **kw)
+    assert got["tim_embed"][5:7] == (most, 8)
+    binding.embed(like(8, big), ids, out=like(4, big), **kw)
+    assert got["tim_embed"][5:7] == (8, most)
+    monkeypatch.setattr(binding, "_sequence_rows", lambda t, *a: (0, 0, 0))
+    binding.verify(like(1, 4, big), ids[:3].view(1, 3), torch.zeros(1, 3), torch.zeros(1), **kw)
+    assert got["tim_verify"][7:10] == (1, 3, most)
+    binding.residual_norm(like(1, big), like(1, big), None, 1e-6, out=(like(1, big), None))
+    assert got["tim_residual_norm"][0]._obj.d == most
