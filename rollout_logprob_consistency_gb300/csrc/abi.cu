@@ -1074,13 +1074,14 @@ tim_status tim_verify(const void* target, int64_t target_ld_seq, int64_t target_
         meet(out[i], out_bytes[i], row_settings(*params), seqs) ||
         meet(out[i], out_bytes[i], row_settings(q_params), seqs) ||
         meet(out[i], out_bytes[i], target, extent(p, B, N + 1, V, dtype)) ||
-        (draft != nullptr && meet(out[i], out_bytes[i], draft, extent(q, B, N, V, dtype))) ||
-        (workspace != nullptr && meet(out[i], out_bytes[i], workspace, kept)))
+        (draft != nullptr && meet(out[i], out_bytes[i], draft, extent(q, B, N, V, dtype))))
       return TIM_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (meet(out[i], out_bytes[i], out[j], out_bytes[j])) return TIM_ERR_INVALID_ARG;
   }
   if ((s = check_workspace(workspace, workspace_bytes, kept)) != TIM_OK) return s;
+  for (int i = 0; i < 3; ++i)
+    if (meet(out[i], out_bytes[i], workspace, kept)) return TIM_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;
   return from_cuda(launch_verify(p, q, dtype, B, N, V, draft_ids, uniform, uniform_draw, *params,
@@ -1097,9 +1098,10 @@ tim_status tim_embed(const void* table, int32_t dtype, int64_t ld, const int32_t
   if ((s = check_matrix(out, dtype, ldo, d)) != TIM_OK) return s;
   const size_t written = extent(ldo, T, d, dtype);
   if (meet(table, extent(ld, V, d, dtype), out, written) ||
-      meet(ids, static_cast<size_t>(T) * 4, out, written) || meet(workspace, 1024, out, written))
+      meet(ids, static_cast<size_t>(T) * 4, out, written))
     return TIM_ERR_INVALID_ARG;
   if ((s = check_workspace(workspace, workspace_bytes, 1024)) != TIM_OK) return s;
+  if (meet(workspace, 1024, out, written)) return TIM_ERR_INVALID_ARG;
   if ((s = check_device(nullptr)) != TIM_OK) return s;
   return from_cuda(launch_embed(table, dtype, ld, ids, T, V, d, scale, out, ldo,
                                 static_cast<int*>(workspace),
@@ -1122,11 +1124,11 @@ tim_status tim_embed_backward(const void* dy, int32_t dtype, int64_t ldy, const 
   if (accumulate != 0 && accumulate != 1) return TIM_ERR_INVALID_ARG;
   const size_t table = extent(d, V, d, out_dtype);
   if (meet(dy, extent(ldy, T, d, dtype), out_dtable, table) ||
-      meet(ids, static_cast<size_t>(T) * 4, out_dtable, table) ||
-      meet(workspace, embed_backward_bytes(T, d), out_dtable, table))
+      meet(ids, static_cast<size_t>(T) * 4, out_dtable, table))
     return TIM_ERR_INVALID_ARG;
-  if ((s = check_workspace(workspace, workspace_bytes, embed_backward_bytes(T, d))) != TIM_OK)
-    return s;
+  const size_t kept = embed_backward_bytes(T, d);
+  if ((s = check_workspace(workspace, workspace_bytes, kept)) != TIM_OK) return s;
+  if (meet(workspace, kept, out_dtable, table)) return TIM_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;
   return from_cuda(launch_embed_backward(dy, dtype, ldy, ids, T, V, d, scale, out_dtable, out_dtype,
@@ -1201,7 +1203,6 @@ tim_status tim_residual_norm_backward(const tim_block* b, const void* h, int64_t
   in[4] = gate_span(b);
   in[5] = row_span(b, b->gamma);
   in[6] = row_span(b, b->gamma_post);
-  const Span scratch{workspace, residual_norm_backward_bytes(b->T, b->d), 0};
   const size_t sums = static_cast<size_t>(b->d) * 4;
   out[0] = span(b, out_dresidual, ld_dresidual);
   out[1] = span(b, out_dblock, ld_dblock);
@@ -1220,9 +1221,11 @@ tim_status tim_residual_norm_backward(const tim_block* b, const void* h, int64_t
       if (meet(out[o], in[i])) return TIM_ERR_INVALID_ARG;
     for (int i = 0; i < o; ++i)
       if (meet(out[o], out[i])) return TIM_ERR_INVALID_ARG;
-    if (meet(out[o], scratch)) return TIM_ERR_INVALID_ARG;
   }
+  const Span scratch{workspace, residual_norm_backward_bytes(b->T, b->d), 0};
   if ((s = check_workspace(workspace, workspace_bytes, scratch.bytes)) != TIM_OK) return s;
+  for (const Span& o : out)
+    if (meet(o, scratch)) return TIM_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = check_device(&sms)) != TIM_OK) return s;
   NormGradArgs a = {};

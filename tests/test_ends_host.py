@@ -415,3 +415,12 @@ def test_sizes_beyond_32_bits_stay_too_large(tim, monkeypatch):
     assert got["tim_verify"][7:10] == (1, 3, most)
     binding.residual_norm(like(1, big), like(1, big), None, 1e-6, out=(like(1, big), None))
     assert got["tim_residual_norm"][0]._obj.d == most
+
+
+def test_a_workspace_that_is_too_small_is_told_so(tim):
+    """Also where the bytes that it lacks are an output's."""
+    at = FREE + 1024
+    assert _verify(tim, ws=FREE, nbytes=1024, out=at) == WORKSPACE
+    assert _embed(tim, ws=FREE, nbytes=768, out=FREE + 768) == WORKSPACE
+    assert _embed_backward(tim, ws=FREE, nbytes=1024, out=at) == WORKSPACE
+    assert _norm_backward(tim, ws=FREE, nbytes=1024, dr=at) == WORKSPACE
