@@ -769,8 +769,7 @@ tim_status tim_verify(const void *target, int64_t target_ld_seq, int64_t target_
  *              must not meet table, ids or the workspace.
  * dy           [T, d] of dtype, row stride ldy;  out_dtable [V, d] contiguous, of
  *              out_dtype (TIM_F32 or dtype); must not meet dy, ids or the workspace.  In 16
- *              bits a row is rounded once a call; with more than 131072 tokens, once every so
- *              many.
+ *              bits a row is rounded once a call.
  * T >= 1 (up to 2^31 - 1), 1 <= V <= 2^31 - 256, 1 <= d <= 65536, strides up to 2^31;
  * scale finite.  Any element-aligned address; rows of whole 16-byte vectors are faster.
  * workspace    tim_embed: 1024 bytes; tim_embed_backward: tim_embed_backward_workspace_size

@@ -6,11 +6,11 @@
 // The lookup is memory's: distinct rows read, T rows written.
 //
 // The gradient is a sum over equal tokens, so the tokens are sorted first (embed_sort.cuh's one
-// launch: the order of equal ids is their order in the batch), and the sorted list is cut into
-// pieces of a fixed number of rows.  A piece's CTA walks its rows with a column vector a thread and
-// an fp32 running sum, writes the tokens that lie wholly within, and leaves the sums of the first and
-// the last where they go on beyond it; a second launch joins those in order.  No atomics: the same
-// call gives the same bits.  The table's gradient is zeroed by the rest of the sort's launch, which
+// launch for up to 131072 of them: the order of equal ids is their order in the batch), and the sorted
+// list is cut into pieces of a fixed number of rows.  A piece's CTA walks its rows with a column vector a
+// thread and an fp32 running sum, writes the tokens that lie wholly within, and leaves the sums of the
+// first and the last where they go on beyond it; a second launch joins those in order.  No atomics: the
+// same call gives the same bits.  The table's gradient is zeroed by the rest of the sort's launch, which
 // has eight SMs' work otherwise; with `accumulate` it is added to.
 //
 // 32768 tokens of 4096 bf16 into 151936 rows take 187 to 196 us for sort and zeros (1.24 GB, 6.4 to
@@ -123,7 +123,13 @@ cudaError_t launch_lookup(const LookupArgs& a, int64_t T, cudaStream_t stream) {
 
 constexpr int kGradThreads = 256;
 constexpr int kRows = 8;       // rows in flight
-constexpr int kMaxPiece = 64;
+constexpr int kMaxPiece = 64;  // rows of a piece, or of a step of a long one
+// Of a batch, whose first and last tokens' sums are kept.  131073 tokens of 2048 bf16, any of 151936, take
+// 273 us so and 285 with half as many; a frequent token's pieces are joined by one CTA, so that 262144 tokens of
+// which a tenth are alike take 571 us so and 464 with half as many.
+constexpr int kMaxPieces = 2 * kSortRows / kMaxPiece;
+
+constexpr uint32_t kNoId = 0xFFFFFFFFu;  // no token's, nor V
 
 struct GradArgs {
   const void* dy;
@@ -181,8 +187,9 @@ __device__ __forceinline__ void store_cols(typename Elem<kOut>::raw* p, const fl
   }
 }
 
-template <int kDtype, int kOut, int kVec>
-__global__ void __launch_bounds__(kGradThreads, 4) embed_grad_kernel(const GradArgs a) {
+// kLong: pieces of more than kMaxPiece rows, taken in steps of as many.
+template <int kDtype, int kOut, int kVec, bool kLong>
+__global__ void __launch_bounds__(kGradThreads, kLong ? 3 : 4) embed_grad_kernel(const GradArgs a) {
   using raw = typename Elem<kDtype>::raw;
   using raw_out = typename Elem<kOut>::raw;
   __shared__ uint32_t ids[kMaxPiece + 2], rows[kMaxPiece];
@@ -190,21 +197,14 @@ __global__ void __launch_bounds__(kGradThreads, 4) embed_grad_kernel(const GradA
   const uint32_t none = static_cast<uint32_t>(a.V);
   // a piece of the sorted list, a slice of the columns
   const int p = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kGradThreads + tid;
-  const int i0 = p * a.piece, len = min(a.piece, a.T - i0);
-  for (int i = tid; i < len + 2; i += kGradThreads) {
-    const int at = i0 - 1 + i;
-    ids[i] = at >= 0 && at < a.T ? __ldg(a.id + at) : 0xFFFFFFFFu;  // no token's
-    if (i < len) rows[i] = __ldg(a.row + i0 + i);
-  }
-  __syncthreads();
-  if (c >= n) return;
+  const int end = min(a.piece, a.T - p * a.piece) + p * a.piece;
   const raw* const dy = static_cast<const raw*>(a.dy) + c * kVec;
   float acc[kVec] = {};
-  uint32_t cur = ids[1];
+  uint32_t cur = 0, before = 0;
   bool first = true;
-  auto flush = [&](bool last) {
+  auto flush = [&](uint32_t next) {  // next: the id behind the piece, or none's
     if (cur >= none) return;
-    const bool from_before = first && ids[0] == cur, goes_on = last && ids[len + 1] == cur;
+    const bool from_before = first && before == cur, goes_on = next == cur;
     if (from_before || goes_on) {
       float* const to =
           a.partial + (static_cast<int64_t>(p) * 2 + (from_before ? 0 : 1)) * a.d + c * kVec;
@@ -215,32 +215,55 @@ __global__ void __launch_bounds__(kGradThreads, 4) embed_grad_kernel(const GradA
                              acc, a.scale, a.accumulate);
     }
   };
-  for (int r0 = 0; r0 < len; r0 += kRows) {
-    if (ids[1 + r0] >= none) {  // only such follow
-      flush(false);
+  auto walk = [&](int len) {
+    for (int r0 = 0; r0 < len; r0 += kRows) {
+      if (ids[1 + r0] >= none) {  // only such follow
+        flush(kNoId);
+        cur = none;
+        return;
+      }
+      Loaded<kDtype, kVec> v[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (r0 + k < len && ids[1 + r0 + k] < none)
+          v[k].load(dy + static_cast<int64_t>(rows[r0 + k]) * a.ld);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (r0 + k >= len) break;
+        const uint32_t id = ids[1 + r0 + k];
+        if (id != cur) {
+          flush(kNoId);
+          cur = id;
+          first = false;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+        }
+        if (id >= none) return;
+        v[k].add_to(acc);
+      }
+    }
+  };
+  for (int i0 = p * a.piece;;) {
+    const int len = kLong ? min(kMaxPiece, end - i0) : end - i0;
+    for (int i = tid; i < len + 2; i += kGradThreads) {
+      const int at = i0 - 1 + i;
+      ids[i] = at >= 0 && at < a.T ? __ldg(a.id + at) : kNoId;
+      if (i < len) rows[i] = __ldg(a.row + i0 + i);
+    }
+    __syncthreads();
+    if (!kLong && c >= n) return;
+    if (!kLong || i0 == p * a.piece) {
+      before = ids[0];
+      cur = ids[1];
+    }
+    if (!kLong || c < n) walk(len);
+    i0 += len;
+    if (!kLong || i0 == end || ids[len] >= none) {  // cur is none's in the last of these
+      if (!kLong || c < n) flush(ids[len + 1]);
       return;
     }
-    Loaded<kDtype, kVec> v[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (r0 + k < len && ids[1 + r0 + k] < none)
-        v[k].load(dy + static_cast<int64_t>(rows[r0 + k]) * a.ld);
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (r0 + k >= len) break;
-      const uint32_t id = ids[1 + r0 + k];
-      if (id != cur) {
-        flush(false);
-        cur = id;
-        first = false;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
-      }
-      if (id >= none) return;
-      v[k].add_to(acc);
-    }
+    __syncthreads();  // every thread has read this step's
   }
-  flush(true);
 }
 
 // The tokens whose rows lie in several pieces: the CTA of the piece where one begins adds its parts.
@@ -248,10 +271,11 @@ template <int kOut, int kVec>
 __global__ void __launch_bounds__(kGradThreads) embed_join_kernel(const GradArgs a) {
   using raw_out = typename Elem<kOut>::raw;
   const int p = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kGradThreads + threadIdx.x;
-  const int i0 = p * a.piece, i1 = i0 + a.piece;  // all but the last piece are whole
-  if (i1 >= a.T) return;
+  const int i0 = p * a.piece;
+  if (a.T - i0 <= a.piece) return;  // all but the last piece are whole
+  const int i1 = i0 + a.piece;
   const uint32_t id = __ldg(a.id + i1 - 1), next = __ldg(a.id + i1);
-  const uint32_t before = i0 > 0 ? __ldg(a.id + i0 - 1) : 0xFFFFFFFFu;
+  const uint32_t before = i0 > 0 ? __ldg(a.id + i0 - 1) : kNoId;
   if (id >= static_cast<uint32_t>(a.V) || next != id || before == id) return;  // or begins earlier
   if (c >= a.d / kVec) return;
   float acc[kVec];
@@ -286,8 +310,9 @@ cudaError_t launch_grad(const GradArgs& args, cudaStream_t stream) {
   GradArgs a = args;
   a.slices = (a.d / kVec + kGradThreads - 1) / kGradThreads;
   const int64_t work = static_cast<int64_t>(a.pieces) * a.slices;
-  embed_grad_kernel<kDtype, kOut, kVec>
-      <<<static_cast<unsigned>(work), kGradThreads, 0, stream>>>(a);
+  auto* const kernel = a.piece > kMaxPiece ? embed_grad_kernel<kDtype, kOut, kVec, true>
+                                           : embed_grad_kernel<kDtype, kOut, kVec, false>;
+  kernel<<<static_cast<unsigned>(work), kGradThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.pieces == 1) return e;
   embed_join_kernel<kOut, kVec><<<static_cast<unsigned>(work), kGradThreads, 0, stream>>>(a);
@@ -309,21 +334,26 @@ cudaError_t launch_grad_type(const GradArgs& a, int out_dtype, cudaStream_t stre
   return cudaErrorInvalidValue;
 }
 
-// Rows of a piece: few where there are few, for the SMs' sake.
-int piece_rows(int64_t T) { return T <= 8192 ? 16 : kMaxPiece; }
+// Rows of a piece: few where there are few, for the SMs' sake, and so many that kMaxPieces pieces do.
+int piece_rows(int64_t T) {
+  if (T <= 8192) return 16;
+  const int64_t steps = (T + kMaxPiece - 1) / kMaxPiece;
+  return static_cast<int>((steps + kMaxPieces - 1) / kMaxPieces) * kMaxPiece;
+}
 
 struct EmbedWs {
-  size_t id_off, row_off, partial_off, total;
+  size_t sorted_off[2], list, partial_off, total;  // a list: ids, then rows
 };
 EmbedWs embed_ws(int64_t T, int d) {
-  const int64_t n = std::min<int64_t>(T, kSortRows);
+  const size_t n = static_cast<size_t>(T);
   EmbedWs w;
-  w.id_off = 1024;
-  w.row_off = align_up(w.id_off + static_cast<size_t>(n) * 4, 1024);
-  w.partial_off = align_up(w.row_off + static_cast<size_t>(n) * 4, 1024);
-  // fewer tokens than n can have more pieces (a last batch, a smaller call with this workspace)
-  const size_t small = static_cast<size_t>((std::min<int64_t>(n, 8192) + 15) / 16);
-  const size_t large = static_cast<size_t>((n + kMaxPiece - 1) / kMaxPiece);
+  w.list = align_up(n * 4, 1024);
+  w.sorted_off[0] = 1024;
+  w.sorted_off[1] = w.sorted_off[0] + 2 * w.list;
+  w.partial_off = w.sorted_off[1] + (T > kSortRows ? 2 * w.list : 0);
+  // fewer tokens than n can have more pieces (a smaller call with this workspace)
+  const size_t small = (std::min<size_t>(n, 8192) + 15) / 16;
+  const size_t large = std::min<size_t>((n + kMaxPiece - 1) / kMaxPiece, kMaxPieces);
   w.total = align_up(w.partial_off + std::max(small, large) * 2 * static_cast<size_t>(d) * 4, 1024);
   return w;
 }
@@ -346,36 +376,32 @@ cudaError_t launch_embed_backward(const void* dy, int dtype, int64_t ld, const i
                                   void* ws, cudaStream_t stream, int num_sms) {
   const EmbedWs w = embed_ws(T, d);
   uint8_t* const b = static_cast<uint8_t*>(ws);
-  const int es = dtype == TIM_F32 ? 4 : 2;
-  // The sort takes kSortRows tokens at a time; more of them are added batch by batch.
-  for (int64_t t0 = 0; t0 < T; t0 += kSortRows) {
-    uint32_t* const id = reinterpret_cast<uint32_t*>(b + w.id_off);
-    uint32_t* const row = reinterpret_cast<uint32_t*>(b + w.row_off);
-    GradArgs a = {};
-    a.T = static_cast<int>(std::min<int64_t>(T - t0, kSortRows));
-    a.dy = static_cast<const uint8_t*>(dy) + t0 * ld * es;
-    a.ld = ld;
-    a.id = id;
-    a.row = row;
-    a.V = V;
-    a.d = d;
-    a.piece = piece_rows(a.T);
-    a.pieces = (a.T + a.piece - 1) / a.piece;
-    a.scale = scale;
-    a.out = out;
-    const bool zero = t0 == 0 && !accumulate;
-    a.accumulate = !zero;
-    a.partial = reinterpret_cast<float*>(b + w.partial_off);
-    cudaError_t e = launch_embed_sort(ids + t0, a.T, V, id, row, static_cast<int*>(ws), out,
-                                      zero ? static_cast<int64_t>(V) * d * (out_dtype == TIM_F32 ? 4 : 2) : 0,
-                                      num_sms, stream);
-    if (e != cudaSuccess) return e;
-    e = dtype == TIM_F32    ? launch_grad_type<TIM_F32>(a, out_dtype, stream)
-        : dtype == TIM_BF16 ? launch_grad_type<TIM_BF16>(a, out_dtype, stream)
-                            : launch_grad_type<TIM_F16>(a, out_dtype, stream);
-    if (e != cudaSuccess) return e;
+  Sorted sorted[2];
+  for (int i = 0; i < 2; ++i) {
+    sorted[i].id = reinterpret_cast<uint32_t*>(b + w.sorted_off[i]);
+    sorted[i].row = reinterpret_cast<uint32_t*>(b + w.sorted_off[i] + w.list);
   }
-  return cudaSuccess;
+  GradArgs a = {};
+  a.dy = dy;
+  a.ld = ld;
+  a.id = sorted[0].id;
+  a.row = sorted[0].row;
+  a.T = static_cast<int>(T);
+  a.V = V;
+  a.d = d;
+  a.piece = piece_rows(T);
+  a.pieces = static_cast<int>((T + a.piece - 1) / a.piece);
+  a.scale = scale;
+  a.out = out;
+  a.accumulate = accumulate;
+  a.partial = reinterpret_cast<float*>(b + w.partial_off);
+  const int64_t table = static_cast<int64_t>(V) * d * (out_dtype == TIM_F32 ? 4 : 2);
+  const cudaError_t e = launch_embed_sort(ids, a.T, V, sorted, static_cast<int*>(ws), out,
+                                          accumulate ? 0 : table, num_sms, stream);
+  if (e != cudaSuccess) return e;
+  return dtype == TIM_F32    ? launch_grad_type<TIM_F32>(a, out_dtype, stream)
+         : dtype == TIM_BF16 ? launch_grad_type<TIM_BF16>(a, out_dtype, stream)
+                             : launch_grad_type<TIM_F16>(a, out_dtype, stream);
 }
 
 }  // namespace tim

@@ -1,6 +1,8 @@
 // The tokens of a batch in the order of their ids, equal ids in the order of their rows: a radix sort in one
 // launch, by a cluster of CTAs that keep all of it in their shared memory.  The other clusters of
-// the launch, if there are any, zero the table's gradient meanwhile.
+// the launch, if there are any, zero the table's gradient meanwhile.  More tokens than a cluster holds are
+// sorted in runs, a cluster each, and the runs merged two by two, a launch a round: a token's place
+// is its own in its run and, by a binary search, how many of the other run go before it.
 //
 // A pass orders by 9 bits of the id, lowest first.  Every warp has 32 kItems tokens that follow one
 // another in the list and counts its digits, equal ones of a step ranked by lane; the counts of a
@@ -28,11 +30,12 @@ constexpr int kDigits = 1 << kDigitBits;
 struct SortArgs {
   const int32_t* ids;
   int T, V, passes;
-  uint32_t size;  // CTAs of the cluster
+  uint32_t size;  // CTAs of a cluster
+  uint32_t runs;  // of kSortRows tokens but for the last, a cluster each
   uint32_t* out_id;  // V: no token
   uint32_t* out_row;
   int* status;
-  uint8_t* zero;  // zero_bytes of it become 0, by all clusters but the first
+  uint8_t* zero;  // zero_bytes of it become 0, by the clusters behind the runs'
   int64_t zero_bytes;
 };
 
@@ -73,10 +76,13 @@ __global__ void __launch_bounds__(kSortThreads, kItems <= 4 ? 2 : 1) embed_sort_
   constexpr int kOfCta = kSortThreads * kItems;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank(), size = a.size;
-  if (blockIdx.x >= size) {
-    zero_share(a.zero, a.zero_bytes, blockIdx.x - size, gridDim.x - size);
+  const uint32_t run = blockIdx.x / size;
+  if (run >= a.runs) {
+    zero_share(a.zero, a.zero_bytes, blockIdx.x - a.runs * size, gridDim.x - a.runs * size);
     return;
   }
+  const uint32_t t0 = run * kSortRows;
+  const uint32_t T = min(static_cast<uint32_t>(a.T) - t0, static_cast<uint32_t>(kSortRows));
   const uint32_t first = warp * 32 * kItems + lane;        // of the CTA's tokens
   uint32_t id[kItems], row[kItems], place[kItems];
   bool bad = false;
@@ -84,8 +90,8 @@ __global__ void __launch_bounds__(kSortThreads, kItems <= 4 ? 2 : 1) embed_sort_
   for (int k = 0; k < kItems; ++k) {
     row[k] = rank * kOfCta + first + k * 32;
     id[k] = static_cast<uint32_t>(a.V);  // none, and beyond the end: last, in order
-    if (row[k] < static_cast<uint32_t>(a.T)) {
-      const int t = __ldg(a.ids + row[k]);
+    if (row[k] < T) {
+      const int t = __ldg(a.ids + t0 + row[k]);
       bad |= t < -1 || t >= a.V;
       if (t >= 0 && t < a.V) id[k] = static_cast<uint32_t>(t);
     }
@@ -156,9 +162,9 @@ __global__ void __launch_bounds__(kSortThreads, kItems <= 4 ? 2 : 1) embed_sort_
       const uint32_t digit = (id[k] >> shift) & (kDigits - 1);
       const uint32_t to = sh.base[digit] + mine[digit] + place[k];
       if (last) {
-        if (to < static_cast<uint32_t>(a.T)) {
-          a.out_id[to] = id[k];
-          a.out_row[to] = row[k];
+        if (to < T) {
+          a.out_id[t0 + to] = id[k];
+          a.out_row[t0 + to] = t0 + row[k];
         }
       } else {
         cluster_store(cluster_addr(&sh.item[to % kOfCta], to / kOfCta),
@@ -172,6 +178,32 @@ __global__ void __launch_bounds__(kSortThreads, kItems <= 4 ? 2 : 1) embed_sort_
   }
 }
 
+// Of two neighbouring runs of `len` one that is twice as long (a last run may be shorter, or alone).  Equal
+// ids of the first go before those of the second, so that rows stay in order.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads)
+    embed_merge_kernel(const uint32_t* id, const uint32_t* row, uint32_t T, uint32_t len,
+                       uint32_t* out_id, uint32_t* out_row) {
+  const uint32_t i = blockIdx.x * kMergeThreads + threadIdx.x;  // T < 2^31
+  if (i >= T) return;
+  const uint32_t first = i / len * len, a = (i / len & 1u) != 0 ? first - len : first;  // a + 2 len < 2^32
+  const uint32_t b = min(a + len, T), end = min(b + len, T);
+  const uint32_t v = __ldg(id + i);
+  const bool second = i >= b;
+  uint32_t lo = second ? a : b, hi = second ? b : end;
+  const uint32_t from = lo;
+  while (lo < hi) {  // the first of the other run that does not go before
+    const uint32_t mid = lo + (hi - lo) / 2, x = __ldg(id + mid);
+    if (second ? x <= v : x < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const uint32_t to = (second ? i - len : i) + (lo - from);
+  out_id[to] = v;
+  out_row[to] = __ldg(row + i);
+}
+
 template <int kItems>
 cudaError_t launch_sort(const SortArgs& a, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
@@ -180,15 +212,17 @@ cudaError_t launch_sort(const SortArgs& a, int num_sms, cudaStream_t stream) {
   // as many CTAs as an SM's threads take twice over, or as there are chunks
   const int64_t chunks = (a.zero_bytes + kZeroChunk - 1) / kZeroChunk;
   const int64_t others = std::min<int64_t>((chunks + a.size - 1) / a.size, 2 * num_sms / a.size);
-  return launch_clusters(embed_sort_kernel<kItems>, 1 + others, static_cast<int>(a.size), kSortThreads,
-                         sizeof(SortShared<kItems>), stream, a);
+  return launch_clusters(embed_sort_kernel<kItems>, a.runs + others, static_cast<int>(a.size),
+                         kSortThreads, sizeof(SortShared<kItems>), stream, a);
 }
 
-// The ids of T <= kSortRows tokens in order, and their rows; ids that are none, or out of range
-// (noted in the status word), as V at the end.
-cudaError_t launch_embed_sort(const int32_t* ids, int T, int V, uint32_t* out_id, uint32_t* out_row,
-                              int* status, void* zero, int64_t zero_bytes, int num_sms,
-                              cudaStream_t stream) {
+// The ids of T tokens in order, and their rows, in sorted[0] (sorted[1]: as much memory again, for more
+// than kSortRows); ids that are none, or out of range (noted in the status word), as V at the end.
+struct Sorted {
+  uint32_t *id, *row;
+};
+cudaError_t launch_embed_sort(const int32_t* ids, int T, int V, const Sorted (&sorted)[2], int* status,
+                              void* zero, int64_t zero_bytes, int num_sms, cudaStream_t stream) {
   int bits = 1;
   while (bits < 32 && (static_cast<uint32_t>(V) >> bits) != 0) ++bits;
   SortArgs a = {};
@@ -198,14 +232,26 @@ cudaError_t launch_embed_sort(const int32_t* ids, int T, int V, uint32_t* out_id
   a.passes = (bits + kDigitBits - 1) / kDigitBits;
   a.size = 1;
   while (a.size < kSortCluster && a.size * kSortThreads * 4 < static_cast<uint32_t>(T)) a.size *= 2;
-  a.out_id = out_id;
-  a.out_row = out_row;
+  a.runs = (static_cast<uint32_t>(T) + kSortRows - 1) / kSortRows;
+  int rounds = 0;
+  while ((1u << rounds) < a.runs) ++rounds;
+  int at = rounds & 1;  // so that the last round ends in sorted[0]
+  a.out_id = sorted[at].id;
+  a.out_row = sorted[at].row;
   a.status = status;
   a.zero = static_cast<uint8_t*>(zero);
   a.zero_bytes = zero_bytes;
-  return a.size * kSortThreads * 4 >= static_cast<uint32_t>(T)
-             ? launch_sort<4>(a, num_sms, stream)
-             : launch_sort<kSortItems>(a, num_sms, stream);
+  cudaError_t e = a.size * kSortThreads * 4 >= static_cast<uint32_t>(T)
+                      ? launch_sort<4>(a, num_sms, stream)
+                      : launch_sort<kSortItems>(a, num_sms, stream);
+  for (int r = 0; r < rounds && e == cudaSuccess; ++r, at ^= 1) {
+    embed_merge_kernel<<<(static_cast<unsigned>(T) + kMergeThreads - 1) / kMergeThreads, kMergeThreads, 0,
+                         stream>>>(sorted[at].id, sorted[at].row, static_cast<uint32_t>(T),
+                                   static_cast<uint32_t>(kSortRows) << r, sorted[at ^ 1].id,
+                                   sorted[at ^ 1].row);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 }  // namespace

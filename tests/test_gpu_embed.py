@@ -148,6 +148,70 @@ def test_long_batches(tim, T):
         assert torch.equal(got.double(), want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [131072, 131073, 262144, 270001, 700003])
+def test_long_batches_are_rounded_once(tim, dtype, T):
+    """Sums of small whole numbers are exact in fp32: in 16 bits too the result is the exact one rounded once,
+    whatever sorts a token's rows went through, and so is what is added to a table's own."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    for V, kind, d in ((151936, "zipf", 8), (90, "any", 3), (5, "one", 16)):
+        ids = _ids(T, V, T + d, kind)
+        if kind == "one":
+            ids = torch.where(torch.arange(T, device="cuda") % 3 == 0, ids, -1)
+            ids[T // 2:] = 4
+        dy = torch.randint(-8, 9, (T, d), generator=g, device="cuda").to(_dtype(dtype))
+        before = torch.randint(-900, 900, (V, d), generator=g, device="cuda").to(_dtype(dtype))
+        live = ids >= 0
+        want = torch.zeros(V, d, dtype=torch.float64, device="cuda")
+        want.index_add_(0, ids[live].long(), 0.5 * dy[live].double())
+        for out in {torch.float32, dy.dtype}:
+            got = tim.embed_backward(dy, ids, V, 0.5, dtype=out)
+            assert torch.equal(got, want.to(out)), (V, kind, out)
+            to = before.to(out, copy=True)
+            got = tim.embed_backward(dy, ids, V, 0.5, out_dtable=to, accumulate=True)
+            assert torch.equal(got, (before.double() + want).to(out)), (V, kind, out)
+
+
+@pytest.mark.parametrize("T", [140000, 300000])
+def test_long_batches_in_any_type_and_address(tim, T):
+    for dtype in ("f32", "bf16", "f16"):
+        for V, d, pad, offset, kind in ((300, 24, 3, 1, "zipf"), (1000, 264, 0, 0, "any"), (3, 40, 0, 0, "one")):
+            if T > 200000 and d > 100:
+                continue
+            dy, ids = _tensor(T, d, dtype, T + d, pad, offset), _ids(T, V, T, kind)
+            _check_grad(tim, dy, ids, V, 0.3)
+            _check_grad(tim, dy, ids, V, 0.3, dtype=dy.dtype)
+
+
+def test_long_batches_are_added_in_the_order_of_their_rows(tim):
+    """Rows of one token in every sort: 1, 2^24 and -2^24 add up to 0 in this order alone.  Bad ids of any
+    sort are reported."""
+    import torch
+    T, V = 400000, 1000
+    ids = torch.arange(T, device="cuda").int() % (V - 1)
+    dy = torch.zeros(T, 8, device="cuda")
+    for at, x in ((1000, 1.0), (200000, 2.0 ** 24), (399999, -2.0 ** 24)):
+        ids[at] = V - 1
+        dy[at] = x
+    assert not bool(tim.embed_backward(dy, ids, V).any())
+    assert bool((tim.embed_backward(dy.flip(0), ids.flip(0).contiguous(), V)[V - 1] == 1).all())
+    dy = _tensor(T, 8, "f32", 6)
+    first = tim.embed_backward(dy, ids, V)
+    ws = tim.Workspace(tim.embed_backward_workspace_size(T, V, 8))
+    for _ in range(3):
+        small = tim.embed_backward(dy[:9000], ids[:9000], V, workspace=ws)  # it serves smaller calls between
+        assert torch.equal(first, tim.embed_backward(dy, ids, V, workspace=ws))
+        assert torch.equal(small, tim.embed_backward(dy[:9000], ids[:9000], V))
+    good = ids.clone()
+    for at in (5, 131072, 399998):
+        good[at], ids[at] = -1, V if at == 5 else -2
+    got = tim.embed_backward(dy, ids, V, workspace=ws, check=False)
+    with pytest.raises(tim.TimError, match="TIM_ERR_TOKEN_RANGE"):
+        ws.check()
+    assert torch.equal(got, tim.embed_backward(dy, good, V))
+
+
 def test_order_is_the_batchs(tim):
     """Equal tokens are added in the order of their rows, so the result does not change with the run,
     and the sum of 1, 2^24, -2^24 in that order is 0."""
