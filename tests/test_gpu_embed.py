@@ -388,3 +388,22 @@ def test_beyond_2_31_elements(tim):
     table[V - 1] = 0
     table[523300] = 0
     assert not bool(table.any())  # the others, token 0's among them, are 0
+
+
+@pytest.mark.slow
+def test_gradient_of_a_long_batch_beyond_2_31_elements(tim):
+    """Rows beyond 2^31 elements of dy, of tokens that lie in several sorts and in one."""
+    import torch
+    T, V, d = 600000, 5000, 4104
+    dy = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 3, 140000, 523300, T - 3, T - 1], device="cuda")
+    ids[at] = torch.tensor([4999, 7, 7, 7, 4999, 123], dtype=torch.int32, device="cuda")
+    dy[at] = torch.tensor([1, 2, 4, 8, 16, 32], dtype=torch.bfloat16, device="cuda")[:, None]
+    dy[1] = math.nan  # no token's
+    for out in (torch.bfloat16, torch.float32):
+        got = tim.embed_backward(dy, ids, V, 3.0, dtype=out)
+        for v, want in ((4999, 51.0), (7, 42.0), (123, 96.0)):
+            assert bool((got[v] == want).all()), (v, out)
+            got[v] = 0
+        assert not bool(got.any())

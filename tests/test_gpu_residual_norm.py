@@ -443,3 +443,30 @@ def test_beyond_2_31_elements(tim):
     ones = torch.ones(d, dtype=torch.bfloat16, device="cuda")
     tim.residual_norm(h, x, ones, 0.0, gate=gate, out=(h, x))
     assert torch.equal(h[:, ::4099], gate.expand(T, 4)) and bool((x == 1).all())
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("T,d", [(262200, 8192), (131100, 16384)])
+def test_gradients_beyond_2_31_elements(tim, T, d):
+    """With rows on their way to shared memory and without.  Of rows of ones under both norms, with dy = +1, -1,
+    +1, ..., dh = c and a gate of g: dresidual = c +- 1, dblock = +-g, dgate = d c."""
+    import torch
+    h, x, dy = (torch.ones(T, d, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    dy[:, 1::2] = -1
+    row = torch.arange(T, device="cuda").view(T, 1)
+    c, g = (row % 16).to(torch.bfloat16), (row % 127 + 1).to(torch.bfloat16)
+    dh = c.expand(T, d).contiguous()
+    ones = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    dres, dblock, dgamma, dpost, dgate = tim.residual_norm_backward(h, x, dh, dy, ones, 0.0, gamma_post=ones, gate=g)
+    for i in range(0, T, 1 << 15):
+        s = slice(i, i + (1 << 15))
+        assert torch.equal(dres[s], dh[s] + dy[s]) and torch.equal(dblock[s], g[s] * dy[s]), i
+    # r = 1 is off by four steps at most, a row's sum is one of whole numbers and exact, a sum over rows is
+    # that of a CTA's, one on every SM at least, and then of the CTAs'
+    assert bool(((dgate - d * c.float()).abs() <= 2.0 ** -20 * d * c.float()).all())
+    tol = (T / torch.cuda.get_device_properties(0).multi_processor_count + 70) * 2.0 ** -24
+    sign = dy[0].double()
+    assert bool(((dgamma.double() - T * sign).abs() <= tol * T).all())
+    cd, gd = c.double().view(T), g.double().view(T)
+    want, size = (gd * cd).sum() + sign * gd.sum(), (gd * (cd + 1)).sum()
+    assert bool(((dpost.double() - want).abs() <= tol * size).all())
