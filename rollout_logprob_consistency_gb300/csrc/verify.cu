@@ -660,10 +660,11 @@ cudaError_t launch_verify(const VerifyMatrix& target, const VerifyMatrix& draft,
   a.out_logprob = out_logprob;
   a.out_accepted = out_accepted;
   a.status = static_cast<int*>(ws);
-  // Eight CTAs a sequence while they all run in two rounds; four beyond: what is done once a CTA (the
-  // drafts, the tables) then weighs less.  151936 bf16 tokens, most drafts refused somewhere: 48 sequences
-  // 25 us with eight, 33 with four; 128 sequences 65 and 55 (two: 62).
-  a.cluster = kMaxCluster * B <= 4 * num_sms ? kMaxCluster : kMaxCluster / 2;
+  // Eight CTAs a sequence up to a third of the SMs, four beyond: what is done once a CTA (the drafts, the
+  // tables) then weighs less.  Both launches with eight and with four, 4 drafts, 151936 bf16 tokens, unfiltered:
+  // 24 sequences 95 us and 96, 48 123 and 133, 56 137 and 137, 64 145 and 139, 128 221 and 210 (in the
+  // second launch alone 65 and 55, two: 62); with top-k 50 and top-p 0.95 56 sequences 109 and 101.
+  a.cluster = 3 * B <= num_sms ? kMaxCluster : kMaxCluster / 2;
   // Rows that run all at once have nothing to gain from what the others say, and a chain less each.
   a.in_rows = B * (N + 1) + (draft_given(a) ? B * N : 0) > num_sms;
   if (a.in_rows) {

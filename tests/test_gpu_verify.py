@@ -146,6 +146,19 @@ def test_many_sequences(tim, B):
                 assert torch.equal(w[b:b + 1], o)
 
 
+def test_sequences_on_either_side_of_a_third_of_the_sms(tim):
+    """Where the second launch takes other numbers of CTAs a sequence: what they draw is the same."""
+    import torch
+    B = torch.cuda.get_device_properties(0).multi_processor_count // 3
+    p = _problem(B + 1, 3, 3001, "bf16", 5)
+    for kw in (dict(), dict(top_k=50, top_p=0.95), dict(temperature=0.7, min_p=0.02)):
+        for draft in (p["draft"], None):
+            q = {**p, "draft": draft}
+            more = _check(tim, q, kw, least=B - 1)
+            few = _check(tim, {k: v[:B] if v is not None else v for k, v in q.items()}, kw, least=B - 2)
+            assert torch.equal(more[0][:B], few[0]) and torch.equal(more[2][:B], few[2])
+
+
 @pytest.mark.parametrize("N", [31, 32, 33, 70])
 def test_many_drafts(tim, N):
     """A drafter that nearly agrees: accepted runs beyond the 32 positions that are looked at together."""
