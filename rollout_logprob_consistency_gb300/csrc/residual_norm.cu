@@ -4,8 +4,9 @@
 //   h' = h + scale g n                                          g: a gate a channel, a token, an element
 //   y  = h' / sqrt(mean h'^2 + eps) gamma                       the next block's input
 //
-// h' is rounded to its type before y is taken from it, so that y is what any later reader of the
-// stored h' computes (tim_logprob's final norm among them).
+// h' is rounded to its type before y is taken from it: y is the norm of the h' that is stored, which is
+// what a later reader of it has (tim_logprob's final norm sums in another order, so an element of its
+// own y in some thousand is a step of the type away from this one's).
 //
 // Memory's: a row is read once into registers and its one or two sums are taken by the CTA that
 // holds it.  How a row is split over threads depends on d and on whether all of the call's rows are whole
@@ -195,13 +196,18 @@ __global__ void __launch_bounds__(kThreads, 1) residual_norm_kernel(const NormAr
 // A CTA takes every gridDim-th row; the sums over its rows stay in registers, a thread's columns, and are
 // left in the workspace for residual_fold_kernel.
 //
-// 16384 rows of 4096 bf16 with both norms and a gate a token take 158 us, 5.1 TB/s, and the fold 4.5: the
-// instructions bound it (half the issue slots, 16 warps an SM), most of them the unpacking of 16-bit
-// numbers.
+// 16384 rows of 4096 bf16 with both norms and a gate a token take 158 us, 5.1 TB/s, and the fold 4.5.  Waiting
+// bounds it: with what a row keeps in registers 16 warps share an SM, and between a row's two sums over the
+// CTA they wait for exchanges and barriers and then for memory beside too few others (issue slots 48%
+// used, DRAM 62%; exchanges 1.9 and memory 1.7 of the stalled warps a cycle).
 //
 // kStages: the rows that are on their way to shared memory while one is worked on, copied by the
 // threads that will read them, so that they wait for their own copies alone.  0: rows are read where
-// they lie, each time they are needed.
+// they lie, each time they are needed: rows of more than 1024 vectors, for which an SM's shared memory would
+// not do (4096 rows of 16384 bf16 306 us where their bytes would take 119), and rows that are not whole
+// vectors (16384 rows of 4096 bf16 with a stride of 4099 1162 us).  Those kernels spill: more than 1024 vectors
+// 208 to 392 bytes a thread where they are whole (fp32 up to 2048 none) and 148 to 1480 where they are not, fewer
+// that are not whole 24 to 472 in 16 bits.
 
 // Where a row's four operands come from.
 template <int kDtype, bool kWide, int kVecs, int kThreads, int kStages>
@@ -507,8 +513,10 @@ bool wide(const tim_block& b) {
 template <int kN>
 using Int = std::integral_constant<int, kN>;
 
-// f(vectors of a thread, threads a row), by the row's vectors alone.  Two vectors from 512 on: the gradient
-// of rows of 4096 bf16 took 158 us so, 168 with one vector and twice the threads, 239 with four.
+// f(vectors of a thread, threads a row), by the row's vectors alone.  Two vectors beyond 256: the gradient
+// of rows of 4096 bf16 took 158 us so, 168 with one vector and twice the threads, 239 with four.  The
+// update itself takes 170 us so for 32768 rows of 4096 bf16, 215 with one and 164 with four; for 16384 of 8192
+// 217, 342 and 175; for 32768 of 2048, with one vector here, 102 and 86 with two.
 template <int kDtype, class F>
 cudaError_t with_split(int nvec, F&& f) {
   if (nvec <= 64) return f(Int<1>(), Int<64>());
