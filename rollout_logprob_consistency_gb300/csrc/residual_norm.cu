@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) residual_norm_kernel(const NormAr
 //
 // 16384 rows of 4096 bf16 with both norms and a gate a token take 158 us, 5.1 TB/s, and the fold 4.5.  Waiting
 // bounds it: with what a row keeps in registers 16 warps share an SM, and between a row's two sums over the
-// CTA they wait for exchanges and barriers and then for memory beside too few others (issue slots 48%
-// used, DRAM 62%; exchanges 1.9 and memory 1.7 of the stalled warps a cycle).
+// CTA they wait beside too few others (issue slots 47% used, DRAM 62%; stalled for shared memory and exchanges
+// 1.8 warps a cycle issued, for memory 1.7, for fixed latencies 1.6, at barriers 0.5).
 //
 // kStages: the rows that are on their way to shared memory while one is worked on, copied by the
 // threads that will read them, so that they wait for their own copies alone.  0: rows are read where

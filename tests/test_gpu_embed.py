@@ -358,6 +358,39 @@ def test_graph_replay_streams_and_two_calls_at_once(tim):
     assert all(torch.equal(x, want[n]) for n in range(2) for x in got[n])
 
 
+def test_long_batch_replayed_and_on_another_stream(tim):
+    """Several sorts and their merges in a captured graph, whose inputs change between replays."""
+    import torch
+    T, V, d = 300000, 4000, 24
+    dy, ids, grad = _tensor(T, d, "bf16", 2).contiguous(), _ids(T, V, 3), torch.zeros(V, d, device="cuda")
+    ws = tim.Workspace(tim.embed_backward_workspace_size(T, V, d))
+
+    def step():
+        tim.embed_backward(dy, ids, V, 3.0, out_dtable=grad, workspace=ws, check=False)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        ids.copy_(_ids(T, V, 50 + seed, "zipf" if seed == 1 else "any"))
+        dy.copy_(_tensor(T, d, "bf16", 60 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        assert torch.equal(grad, tim.embed_backward(dy, ids, V, 3.0, stream=side))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    cases = [(ids, dy), (_ids(T, V, 99), _tensor(T, d, "bf16", 98))]
+    want = [tim.embed_backward(g, i, V) for i, g in cases]
+    torch.cuda.synchronize()
+    got = [[tim.embed_backward(g, i, V, stream=streams[n], check=False) for n, (i, g) in enumerate(cases)]
+           for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for pair in got for x, w in zip(pair, want))
+
+
 def test_tied_to_the_head(tim):
     """The other half of a tied matrix's gradient, added to the head's."""
     import torch
